@@ -23,7 +23,8 @@ EXPORTS = ("hs_record_bytes", "hs_pool_create", "hs_pool_destroy", "hs_pool_rese
            "hs_append_writethrough", "hs_resolve", "hs_sparse_attn", "hs_stats", "hs_read_state",
            "hs_read_buffer", "hs_read_history", "hs_sparse_attn_noalloc", "hs_append_resolve",
            "hs_resolve_range", "hs_sparse_attn_range", "hs_reserve", "hs_release", "hs_host_usage",
-           "hs_device_usage", "hs_debug_stall_next")
+           "hs_device_usage", "hs_debug_stall_next", "hs_rope_turns", "hs_append_rotated",
+           "hs_tree_attn_workspace", "hs_tree_attn", "hs_pool_tree_attn", "hs_keep_path")
 
 
 class hs_config(ctypes.Structure):
@@ -61,6 +62,60 @@ class hs_totals(ctypes.Structure):
         ("host_bytes", ctypes.c_uint64),
         ("error_bits", ctypes.c_uint32),
         ("resolves", ctypes.c_uint32),
+    ]
+
+
+class hs_paged_kv(ctypes.Structure):
+    _fields_ = [
+        ("d_pages", ctypes.c_void_p),
+        ("d_table", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_tokens", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("d_err", ctypes.c_void_p),
+        ("cuda_device", ctypes.c_int32),
+    ]
+
+
+class hs_append_args(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("d_cu", ctypes.c_void_p),
+        ("d_start", ctypes.c_void_p),
+        ("d_rope_pos", ctypes.c_void_p),
+        ("d_k", ctypes.c_void_p),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("d_v", ctypes.c_void_p),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("d_turns", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_offset", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("d_q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("d_q_out", ctypes.c_void_p),
+        ("q_out_token_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("q_dim", ctypes.c_int32),
+    ]
+
+
+class hs_tree_args(ctypes.Structure):
+    _fields_ = [
+        ("d_q", ctypes.c_void_p),
+        ("d_len", ctypes.c_void_p),
+        ("d_locs", ctypes.c_void_p),
+        ("top_k", ctypes.c_int32),
+        ("d_mask", ctypes.c_void_p),
+        ("d_nodes", ctypes.c_void_p),
+        ("nodes", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("d_out", ctypes.c_void_p),
+        ("d_workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -108,6 +163,12 @@ def load(build_if_missing: bool = False):
             "hs_host_usage": (I, [P, P, P, P]),
             "hs_device_usage": (I, [P, P, P, P]),
             "hs_debug_stall_next": (I, [P, I]),
+            "hs_rope_turns": (I, [P, I, P]),
+            "hs_append_rotated": (I, [P, P, P, P]),
+            "hs_tree_attn_workspace": (I64, [P, I, I]),
+            "hs_tree_attn": (I, [P, P, P, P]),
+            "hs_pool_tree_attn": (I, [P, I, P, P, P]),
+            "hs_keep_path": (I, [P, P, P, P, I, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -1,0 +1,289 @@
+// Attention for a tree of drafted tokens over a cache.
+//
+// For node i of request r and query head h, over the context's entries and the nodes that i sees:
+//   s_e = scale <q, K(e)>,  o = sum_e 2^(s_e log2(e) - m) V(e) / sum_e 2^(s_e log2(e) - m).
+// A context record serves all T nodes and all query heads of its KV head, so the cache is read once:
+// at few rows (nodes x query heads of a KV head) device memory bounds it, at many the tensor cores.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "hs_paged.cuh"
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct TreeArgs {
+  PagedRows kv;             // paged form; err is the pool's error word in the pool's form
+  const uint64_t* slot_pt;  // pool form: [R][slot_pages] device address of each buffer page, else null
+  const int32_t* slot_cap;  // [R] slots a buffer holds
+  int slot_pages, slot_shift;
+  const uint8_t* draft;     // pool form: [R][T][rec]
+  const uint16_t* q;        // [R][T][Hq][dqk]
+  const int64_t* len;       // [R], paged form
+  const int32_t* locs;      // [R][k] or null
+  const uint64_t* mask;     // [R][T][words]
+  const int32_t* nodes;     // [R] or null
+  uint16_t* out;            // [R][T][Hq][dv]
+  int R, T, k, words, Hq, Hkv, dqk, dv;
+  int kstride, voff;        // values: KV head g's key at g * kstride, its value voff further on
+  float qscale;             // scale * log2(e)
+};
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *(const uint32_t*)&v;
+}
+
+// context length (paged form); a negative one becomes one behind which no node has a position either
+__device__ __forceinline__ int64_t context_of(const TreeArgs& a, int r, uint32_t* bad) {
+  if (a.len == nullptr) return 0;
+  const int64_t n = a.len[r];
+  if (n < 0) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return n < 0 ? -(1ll << 40) : n;
+}
+// the nodes in use
+__device__ __forceinline__ int nodes_of(const TreeArgs& a, int r, uint32_t* bad) {
+  if (a.nodes == nullptr) return a.T;
+  const int n = a.nodes[r];
+  if (n < 0 || n > a.T) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return min(max(n, 0), a.T);
+}
+// entries of the context of request r: its positions or its list
+__device__ __forceinline__ int64_t entries_of(const TreeArgs& a, int r, int64_t len, uint32_t* bad) {
+  if (a.locs != nullptr) return a.k;
+  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_tokens;
+  if (len > cap) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return max((int64_t)0, min(len, cap));
+}
+
+// record of context entry e, or null (padding, or bad with a bit raised)
+__device__ __forceinline__ const uint8_t* entry_record(const TreeArgs& a, int r, int64_t e, uint32_t* bad) {
+  int64_t p = e;
+  if (a.locs != nullptr) {
+    p = a.locs[(int64_t)r * a.k + e];
+    if (p == -1) return nullptr;
+  }
+  if (a.slot_pt != nullptr) {
+    if (p < 0 || p >= a.slot_cap[r]) {
+      *bad |= (uint32_t)HS_DEVERR_LOC;
+      return nullptr;
+    }
+    return hs_slot_addr(a.slot_pt + (int64_t)r * a.slot_pages, a.slot_shift, a.kv.rec, (int)p);
+  }
+  const int64_t row = paged_row(a.kv, r, p, (uint32_t)HS_DEVERR_LOC, bad);
+  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
+}
+__device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, int64_t len, int j, uint32_t* bad) {
+  if (a.draft != nullptr) return a.draft + ((int64_t)r * a.T + j) * a.kv.rec;
+  const int64_t row = paged_row(a.kv, r, len + j, (uint32_t)HS_DEVERR_LOC, bad);
+  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
+}
+
+// Any shape: a CTA per (node, query head, request), its four warps take the entries in turn and merge
+// their running maxima, sums and accumulators at the end.  A lane holds every 32nd group of 8 values of
+// a head (head dims up to 576 = 72 groups: at most three).
+constexpr int kAnyWarps = 4, kAnyGroups = 3;
+
+__global__ void __launch_bounds__(kAnyWarps * 32) k_tree_any(TreeArgs a) {
+  __shared__ float s_acc[kAnyWarps][kAnyGroups * 32 * 8];
+  __shared__ float s_m[kAnyWarps], s_l[kAnyWarps];
+  hs_pdl_wait();
+  const int t = blockIdx.x / a.Hq, h = blockIdx.x - t * a.Hq, r = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t bad = 0u;
+  const int64_t len = context_of(a, r, &bad);
+  const int nn = nodes_of(a, r, &bad);
+  const int64_t n = entries_of(a, r, len, &bad);
+  if (t >= nn) {
+    if (threadIdx.x == 0) report(a.kv.err, bad);
+    return;
+  }
+  const int kg = a.dqk / 8, vg = a.dv / 8;
+  const int64_t koff = (int64_t)(h / (a.Hq / a.Hkv)) * a.kstride;
+  const int64_t row = ((int64_t)r * a.T + t) * a.Hq + h;
+  float q[kAnyGroups][8], acc[kAnyGroups][8];
+#pragma unroll
+  for (int x = 0; x < kAnyGroups; ++x) {
+    const int gi = lane + 32 * x;
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (gi < kg) u = *(const uint4*)(a.q + row * a.dqk + 8 * gi);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[x][2 * i] = lo(w[i]);
+      q[x][2 * i + 1] = hi(w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[x][i] = 0.f;
+  }
+  const uint64_t* mask = a.mask + ((int64_t)r * a.T + t) * a.words;
+  float m = -INFINITY, l = 0.f;
+  for (int64_t e = warp; e < n + nn; e += kAnyWarps) {
+    const uint8_t* rec;
+    if (e < n) {
+      rec = entry_record(a, r, e, &bad);
+    } else {
+      const int j = (int)(e - n);
+      if (((mask[j >> 6] >> (j & 63)) & 1ull) == 0ull) continue;
+      rec = node_record(a, r, len, j, &bad);
+    }
+    if (rec == nullptr) continue;
+    const uint16_t* kp = (const uint16_t*)rec + koff;
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < kAnyGroups; ++x) {
+      const int gi = lane + 32 * x;
+      if (gi < kg) {
+        const uint4 u = *(const uint4*)(kp + 8 * gi);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s = fmaf(q[x][2 * i], lo(w[i]), s);
+          s = fmaf(q[x][2 * i + 1], hi(w[i]), s);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s *= a.qscale;
+    if (s == -INFINITY) continue;  // weight 0 whatever the maximum
+    // NaN scores go on: fmaxf keeps the maximum, the weight is NaN
+    const float mn = fmaxf(m, s);
+    const float al = m == mn ? 1.f : exp2f(m - mn), p = exp2f(s - mn);
+    m = mn;
+    l = l * al + p;
+#pragma unroll
+    for (int x = 0; x < kAnyGroups; ++x) {
+      const int gi = lane + 32 * x;
+      if (gi < vg) {
+        const uint4 u = *(const uint4*)(kp + a.voff + 8 * gi);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[x][2 * i] = fmaf(p, lo(w[i]), acc[x][2 * i] * al);
+          acc[x][2 * i + 1] = fmaf(p, hi(w[i]), acc[x][2 * i + 1] * al);
+        }
+      }
+    }
+  }
+  report(a.kv.err, bad);
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int x = 0; x < kAnyGroups; ++x)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_acc[warp][(lane + 32 * x) * 8 + i] = acc[x][i];
+  __syncthreads();
+  float M = -INFINITY, L = 0.f, wt[kAnyWarps];
+#pragma unroll
+  for (int w = 0; w < kAnyWarps; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+  for (int w = 0; w < kAnyWarps; ++w) {
+    wt[w] = s_m[w] == -INFINITY ? (s_l[w] == 0.f ? 0.f : NAN) : exp2f(s_m[w] - M);  // NaN scores alone: NaN
+    L += wt[w] * s_l[w];
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  for (int d = 2 * threadIdx.x; d < a.dv; d += 2 * kAnyWarps * 32) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) {
+      x = fmaf(wt[w], s_acc[w][d], x);
+      y = fmaf(wt[w], s_acc[w][d + 1], y);
+    }
+    *(uint32_t*)(a.out + row * a.dv + d) = pack(x * inv, y * inv);
+  }
+}
+
+int check_tree(const hs_config* c, const hs_tree_args* g) {
+  if (g == nullptr) return HS_ERR_ARG;
+  if (g->d_q == nullptr || g->d_mask == nullptr || g->d_out == nullptr) return HS_ERR_ARG;
+  if (!hs_aligned(g->d_q, 16) || !hs_aligned(g->d_out, 16) || !hs_aligned(g->d_mask, 8) || !hs_aligned(g->d_locs, 4) ||
+      !hs_aligned(g->d_nodes, 4) || !hs_aligned(g->d_len, 8) || !hs_aligned(g->d_workspace, 16))
+    return HS_ERR_ARG;
+  if (g->nodes < 1 || g->nodes > HS_MAX_TREE_NODES) return HS_ERR_ARG;
+  if (!isfinite(g->scale)) return HS_ERR_ARG;
+  return HS_OK;
+}
+
+TreeArgs tree_args(const hs_config* c, const hs_tree_args* g) {
+  TreeArgs a{};
+  a.q = (const uint16_t*)g->d_q;
+  a.locs = g->d_locs;
+  a.mask = g->d_mask;
+  a.nodes = g->d_nodes;
+  a.out = (uint16_t*)g->d_out;
+  a.R = c->num_requests;
+  a.T = g->nodes;
+  a.words = (g->nodes + 63) / 64;
+  a.Hq = c->num_q_heads;
+  a.Hkv = c->num_kv_heads;
+  a.dqk = c->head_dim_qk;
+  a.dv = c->head_dim_v;
+  if (c->layout == HS_LAYOUT_GQA) {
+    a.kstride = c->head_dim_qk + c->head_dim_v;
+    a.voff = c->head_dim_qk;
+  }
+  a.qscale = g->scale * kLog2e;
+  return a;
+}
+
+int launch_tree(const TreeArgs& a, cudaStream_t st) {
+  const cudaError_t e = hs_launch_pdl(k_tree_any, dim3(a.T * a.Hq, a.R), dim3(kAnyWarps * 32), 0, st, a);
+  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int cuda_device) {
+  const int rc = hs_check_shape(cfg);
+  if (rc != HS_OK) return rc;
+  if (nodes < 1 || nodes > HS_MAX_TREE_NODES || cuda_device < 0) return HS_ERR_ARG;
+  return 0;
+}
+
+extern "C" int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_tree_args* args, void* stream) {
+  int rc = hs_check_shape(cfg);
+  if (rc == HS_OK) rc = hs_check_paged(cfg, kv);
+  if (rc == HS_OK) rc = check_tree(cfg, args);
+  if (rc != HS_OK) return rc;
+  if (args->d_len == nullptr || (args->d_locs != nullptr && args->top_k < 1)) return HS_ERR_ARG;
+  HsOnDevice on(kv->cuda_device);
+  if (!on.ok) return HS_ERR_CUDA;
+  TreeArgs a = tree_args(cfg, args);
+  a.kv = hs_paged_rows(cfg, kv);
+  a.len = args->d_len;
+  a.k = args->d_locs != nullptr ? args->top_k : 0;
+  return launch_tree(a, (cudaStream_t)stream);
+}
+
+extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const void* d_draft,
+                                 void* stream) {
+  if (pool == nullptr) return HS_ERR_ARG;
+  const hs_config& c = pool->cfg;
+  int rc = hs_check_shape(&c);
+  if (rc == HS_OK) rc = check_tree(&c, args);
+  if (rc != HS_OK) return rc;
+  if (layer < 0 || layer >= c.num_layers || args->d_locs == nullptr || d_draft == nullptr || !hs_aligned(d_draft, 16))
+    return HS_ERR_ARG;
+  if (c.fetch_in_attention != 0) return HS_ERR_CONFIG;
+  HsOnDevice on(pool->device);
+  if (!on.ok) return HS_ERR_CUDA;
+  TreeArgs a = tree_args(&c, args);
+  a.kv.rec = pool->rec;
+  a.kv.err = pool->err_global;
+  a.slot_pt = pool->slot_table + (int64_t)layer * c.num_requests * pool->slot_pages;
+  a.slot_cap = pool->slot_cap + (int64_t)layer * c.num_requests;
+  a.slot_pages = pool->slot_pages;
+  a.slot_shift = pool->slot_shift;
+  a.draft = (const uint8_t*)d_draft;
+  a.k = c.top_k;
+  pool->last_res_layer = -1;  // an attention after this one waits for the whole stream
+  return launch_tree(a, (cudaStream_t)stream);
+}

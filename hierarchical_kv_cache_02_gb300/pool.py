@@ -96,6 +96,39 @@ def _dev_tensor(t, dtype, shape, name, device):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _tree_nodes(q) -> int:
+    import torch
+
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [R][T][Hq][Dqk]")
+    return int(q.shape[1])
+
+
+def _tree_args(lib, c_cfg, cfg, device, q, T, mask, nodes, out, scale, stream):
+    """Check and marshal what both forms of the tree attention take; returns the C arguments, the
+    output and the workspace.  The workspace is this call's own, allocated on the stream that uses it."""
+    import torch
+
+    R, words = cfg.num_requests, (T + 63) // 64
+    qp = _dev_tensor(q, torch.bfloat16, (R, T, cfg.num_q_heads, cfg.head_dim_qk), "q", device)
+    mp = _dev_tensor(mask, torch.int64, (R, T, words), "mask", device)
+    np_ = None if nodes is None else _dev_tensor(nodes, torch.int32, (R,), "nodes", device)
+    need = lib.hs_tree_attn_workspace(ctypes.byref(c_cfg), T, device)
+    if need < 0:
+        raise HsError("hs_tree_attn_workspace", int(need))
+    ws = None
+    if out is None or need > 0:
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty((R, T, cfg.num_q_heads, cfg.head_dim_v), dtype=torch.bfloat16, device=f"cuda:{device}")
+            if need > 0:
+                ws = torch.empty((need,), dtype=torch.uint8, device=f"cuda:{device}")
+    op = _dev_tensor(out, torch.bfloat16, (R, T, cfg.num_q_heads, cfg.head_dim_v), "out", device)
+    s = cfg.default_scale if scale is None else float(scale)
+    args = _lib.hs_tree_args(qp, None, None, 0, mp, np_, T, s, op, ws.data_ptr() if ws is not None else None, need)
+    return args, out, ws
+
+
 class HsPool:
     """One pool: host history, hot buffers and metadata for R requests x L layers."""
 
@@ -240,6 +273,24 @@ class HsPool:
         s = c.default_scale if scale is None else float(scale)
         _check("hs_sparse_attn", self.lib.hs_sparse_attn(self._h, int(layer), qp, lp, kvp, int(rows),
                                                          ctypes.c_float(s), op, _stream_ptr(stream, self.device)))
+        return out
+
+    def tree_attn(self, layer: int, q, locs, draft, mask, nodes=None, out=None, scale=None, stream=None):
+        """Attention of T drafted tokens a request over the resolved slots of `layer` and each other.
+        q bf16 [R][T][Hq][Dqk]; locs int32 [R][k] (what resolve returned, shared by a request's nodes);
+        draft bf16 [R][T][record_elems], the nodes' records (rotated, in no pool yet); mask int64
+        [R][T][ceil(T/64)] (see tree_mask); nodes: int32 [R] nodes in use, rows behind them are left as
+        they were.  out: bf16 [R][T][Hq][Dv].  Not for pools with fetch_in_attention = 1."""
+        import torch
+
+        c = self.cfg
+        T = _tree_nodes(q)
+        lo = _dev_tensor(locs, torch.int32, (c.num_requests, c.top_k), "locs", self.device)
+        d = _dev_tensor(draft, torch.bfloat16, (c.num_requests, T, c.record_elems), "draft", self.device)
+        args, out, _ws = _tree_args(self.lib, self._c, c, self.device, q, T, mask, nodes, out, scale, stream)
+        args.d_locs, args.top_k = lo, c.top_k
+        _check("hs_pool_tree_attn", self.lib.hs_pool_tree_attn(self._h, int(layer), ctypes.byref(args), d,
+                                                               _stream_ptr(stream, self.device)))
         return out
 
     # -- counters and inspection (synchronous) --------------------------------------

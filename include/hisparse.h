@@ -366,6 +366,133 @@ int hs_release(hs_pool* pool, int req);
 enum { HS_STALL_ATTN = 1, HS_STALL_RESOLVE = 2, HS_STALL_FETCH = 4 };
 int hs_debug_stall_next(hs_pool* pool, int kernels);
 
+/*
+ * Speculative decoding over a cache: the T drafted tokens ("nodes") of a request form a tree that hangs
+ * from its last token.  Three operators go round in a loop: append the drafts' records (rotated) behind
+ * the context, attend all nodes at once over the context and each other, keep the accepted path.  The
+ * summary has no counterpart; they stand beside hs_append_writethrough, hs_sparse_attn and
+ * hs_sparse_attn_noalloc.
+ *
+ * They work on a cache that the caller keeps in device memory in pages, or (hs_pool_tree_attn) on a
+ * pool's hot buffers.  Records have the layouts of hs_config; of the hs_config these calls read only
+ * num_requests (<= 65535), layout, num_q_heads, num_kv_heads, head_dim_qk and head_dim_v (head dims:
+ * multiples of 8, at most 576).  No call allocates or synchronises; all are CAPTURABLE.  `stream`
+ * belongs to kv->cuda_device; the current device does not matter.
+ */
+typedef struct {
+  void* d_pages;          /* bf16 [num_pages][page_tokens][record], 16-byte aligned */
+  const int32_t* d_table; /* [num_requests][max_pages]: position p of request r is row p % page_tokens of
+                             page d_table[r][p / page_tokens].  NULL: request r owns the pages
+                             [r * max_pages, (r + 1) * max_pages) in order */
+  int64_t num_pages;      /* num_pages * page_tokens <= 2^31 - 1 */
+  int32_t page_tokens;    /* >= 1, any number */
+  int32_t max_pages;      /* pages of a request: positions [0, max_pages * page_tokens) */
+  uint32_t* d_err;        /* device word that errors only the device sees are OR'ed into, or NULL */
+  int32_t cuda_device;
+} hs_paged_kv;
+
+/*
+ * Rotation tables.  The angle of position a for rotary pair j is a * inv_freq[j]; h_turns[j] =
+ * inv_freq[j] / (2 pi) mod 1 as a 64-bit binary fraction, correctly rounded, so that a * h_turns[j] mod
+ * 2^64 is the angle in turns with an error of a * 2^-65: far positions turn as exactly as near ones.  Host
+ * arrays of n; errors: HS_ERR_ARG (NULL, n < 0, a frequency that is not below 2^32 in magnitude).
+ */
+int hs_rope_turns(const double* h_inv_freq, int n, uint64_t* h_turns);
+
+typedef struct {
+  int32_t num_tokens;         /* N >= 0 rows of the token arrays */
+  const int32_t* d_cu;        /* [num_requests + 1] ascending: tokens [cu[r], cu[r+1]) belong to request r;
+                                 tokens outside [cu[0], cu[num_requests]) are padding: nothing is read or
+                                 written for them */
+  const int64_t* d_start;     /* [num_requests]: token t of request r is stored at position start[r] + t - cu[r] */
+  const int64_t* d_rope_pos;  /* [N] position whose angle a token gets (a drafted node: its depth), or NULL:
+                                 the position where it is stored */
+  const void* d_k;            /* bf16 [N][num_kv_heads][head_dim_qk]; MLA: the latent */
+  int64_t k_token_stride, k_head_stride; /* in values; strides and addresses: multiples of 16 bytes */
+  const void* d_v;            /* GQA: bf16 [N][num_kv_heads][head_dim_v]; MLA: NULL */
+  int64_t v_token_stride, v_head_stride;
+  const uint64_t* d_turns;    /* [rotary_dim / 2] of hs_rope_turns, device; NULL when rotary_dim = 0 */
+  int32_t rotary_dim;         /* rotated values of a head, a multiple of 16; 0: nothing is rotated */
+  int32_t rotary_offset;      /* the first of them in K, a multiple of 8 (MLA: usually head_dim_v) */
+  int32_t interleaved;        /* 0: value j turns with j + rotary_dim / 2; 1: value 2j with 2j + 1 */
+  const void* d_q;            /* bf16 [N][num_q_heads][q_dim], or NULL: no queries */
+  int64_t q_token_stride, q_head_stride;
+  void* d_q_out;              /* the queries rotated; may be d_q itself with the same strides */
+  int64_t q_out_token_stride, q_out_head_stride;
+  int32_t q_dim;              /* head_dim_qk (rotated at rotary_offset, the rest copied) or rotary_dim
+                                 (all of it rotated) */
+} hs_append_args;
+
+/*
+ * Append to a paged cache with the rotation applied on the way: every token's key (its rotary part
+ * turned by its position) and value become the record at its position; queries are turned in the same
+ * launch.  Records of a call go to distinct positions by construction; pages that two requests share
+ * must not be written by two of them in one call.  A position outside [0, max_pages * page_tokens) sets
+ * HS_DEVERR_APPEND, a table entry outside [0, num_pages) HS_DEVERR_PAGE; that record is skipped (its
+ * query is still rotated).  The sines and cosines are within 1e-6 for positions below 2^40, products
+ * and sums are 32-bit, results are rounded once to bf16.  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_CUDA.
+ */
+int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, const hs_append_args* args, void* stream);
+
+#define HS_MAX_TREE_NODES 256
+
+typedef struct {
+  const void* d_q;         /* bf16 [num_requests][nodes][num_q_heads][head_dim_qk], 16-byte aligned */
+  const int64_t* d_len;    /* [num_requests] context length; node j is the record at position len + j */
+  const int32_t* d_locs;   /* NULL: the context is every position [0, len).  Else [num_requests][top_k]
+                              positions, -1 = padding, in any order: only those */
+  int32_t top_k;           /* with d_locs: 1 <= top_k; ignored without */
+  const uint64_t* d_mask;  /* [num_requests][nodes][ceil(nodes / 64)]: bit j of node i's words is set when
+                              i sees node j (itself included).  Any pattern is accepted */
+  const int32_t* d_nodes;  /* [num_requests] nodes in use (0 .. nodes), or NULL: all of them.  Output rows
+                              behind them are left as they were */
+  int32_t nodes;           /* T, 1 .. HS_MAX_TREE_NODES */
+  float scale;
+  void* d_out;             /* bf16 [num_requests][nodes][num_q_heads][head_dim_v], 16-byte aligned */
+  void* d_workspace;       /* hs_tree_attn_workspace bytes, 16-byte aligned; used by this call alone until
+                              it is done: calls that may overlap need one each */
+  int64_t workspace_bytes;
+} hs_tree_args;
+
+/* Bytes of workspace a tree attention of `nodes` nodes needs on `cuda_device`, whatever the lengths (0 is
+ * possible); negative: an hs_status. */
+int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int cuda_device);
+
+/*
+ * Attention of a tree of drafted tokens over a paged cache: for request r, node i and query head h,
+ *   out[r][i][h] = sum_e softmax_e(scale * <q[r][i][h], K(e)>) V(e)
+ * over the context's entries and the nodes j that i sees.  Every context record is read once for all
+ * nodes and all query heads of its KV head.  Nothing visible gives zeros.  What a node does not see has no
+ * influence on it, whatever its values (NaN and infinities included).  Positions outside
+ * [0, max_pages * page_tokens) set HS_DEVERR_LOC, bad table entries HS_DEVERR_PAGE: such
+ * entries are not seen.  A len < 0 sets HS_DEVERR_LOC and leaves neither context nor nodes (a list is still
+ * read); a node count outside [0, nodes] sets it and is clamped.  Scores, softmax sums and accumulators
+ * are 32-bit; the weights enter the value product as bf16 for the shapes on the tensor cores, and the
+ * output is rounded once to bf16.  The order of the sums depends on the lengths alone: equal calls give
+ * equal bits.  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH (workspace too small), HS_ERR_CUDA.
+ */
+int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_tree_args* args, void* stream);
+
+/*
+ * The same over the hot buffers of a layer: args->d_locs are the slots that hs_resolve published
+ * ([num_requests][cfg.top_k]; args->top_k and d_len are ignored), shared by all nodes of a request, and
+ * d_draft (bf16 [num_requests][nodes][record], device, 16-byte aligned) holds the nodes' records, which
+ * are in no pool yet.  Slots outside the buffer set HS_DEVERR_LOC (hs_stats).  Pools with
+ * fetch_in_attention = 1 are refused (HS_ERR_CONFIG): their misses are copied by hs_sparse_attn alone.
+ */
+int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const void* d_draft, void* stream);
+
+/*
+ * Keep the accepted path of a tree: for i in [0, count[r]) the record at position len[r] + i becomes the
+ * one that was at position len[r] + path[r][i] before the call.  d_path int32 [num_requests][path_len],
+ * node numbers with path[r][i] >= i (the nodes of a path ascend, so this holds for every tree whose
+ * parents come first); another entry sets HS_DEVERR_LOC and is skipped, as is one whose position is
+ * outside the cache; a count outside [0, path_len] sets HS_DEVERR_LOC and is clamped.  d_len int64, d_count
+ * int32 [num_requests].  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_CUDA.
+ */
+int hs_keep_path(const hs_config* cfg, const hs_paged_kv* kv, const int64_t* d_len, const int32_t* d_path, int path_len,
+                 const int32_t* d_count, void* stream);
+
 /* Host memory of the pool: pages mapped in some table, pages on the free list, pinned bytes held. */
 int hs_host_usage(hs_pool* pool, int64_t* pages_in_use, int64_t* pages_free, int64_t* bytes_pinned);
 
