@@ -4,6 +4,10 @@
 
 #include "hs_internal.cuh"
 
+// positions of a request, and entries of a list, at most: the kernels count entries, rounded up to
+// whole tiles, in 32 bits
+constexpr int32_t kMaxPositions = INT32_MAX - 65535;
+
 struct PagedRows {
   uint8_t* base;         // [num_pages][page_tokens][rec]
   const int32_t* table;  // [R][max_pages] or null: the identity
@@ -65,6 +69,7 @@ inline int hs_check_paged(const hs_config* c, const hs_paged_kv* kv) {
   if (!hs_aligned(kv->d_table, 4) || !hs_aligned(kv->d_err, 4)) return HS_ERR_ARG;
   if (kv->num_pages < 1 || kv->page_tokens < 1 || kv->max_pages < 1 || kv->cuda_device < 0) return HS_ERR_ARG;
   if (kv->num_pages > (int64_t)INT32_MAX / kv->page_tokens) return HS_ERR_ARG;
+  if (kv->max_pages > kMaxPositions / kv->page_tokens) return HS_ERR_ARG;
   if (kv->d_table == nullptr && (int64_t)c->num_requests * kv->max_pages > kv->num_pages) return HS_ERR_ARG;
   return HS_OK;
 }

@@ -4,85 +4,13 @@
 //   s_e = scale <q, K(e)>,  o = sum_e 2^(s_e log2(e) - m) V(e) / sum_e 2^(s_e log2(e) - m).
 // A context record serves all T nodes and all query heads of its KV head, so the cache is read once:
 // at few rows (nodes x query heads of a KV head) device memory bounds it, at many the tensor cores.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
-#include "hs_paged.cuh"
+#include "hs_tree.cuh"
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct TreeArgs {
-  PagedRows kv;             // paged form; err is the pool's error word in the pool's form
-  const uint64_t* slot_pt;  // pool form: [R][slot_pages] device address of each buffer page, else null
-  const int32_t* slot_cap;  // [R] slots a buffer holds
-  int slot_pages, slot_shift;
-  const uint8_t* draft;     // pool form: [R][T][rec]
-  const uint16_t* q;        // [R][T][Hq][dqk]
-  const int64_t* len;       // [R], paged form
-  const int32_t* locs;      // [R][k] or null
-  const uint64_t* mask;     // [R][T][words]
-  const int32_t* nodes;     // [R] or null
-  uint16_t* out;            // [R][T][Hq][dv]
-  int R, T, k, words, Hq, Hkv, dqk, dv;
-  int kstride, voff;        // values: KV head g's key at g * kstride, its value voff further on
-  float qscale;             // scale * log2(e)
-};
-
-__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *(const uint32_t*)&v;
-}
-
-// context length (paged form); a negative one becomes one behind which no node has a position either
-__device__ __forceinline__ int64_t context_of(const TreeArgs& a, int r, uint32_t* bad) {
-  if (a.len == nullptr) return 0;
-  const int64_t n = a.len[r];
-  if (n < 0) *bad |= (uint32_t)HS_DEVERR_LOC;
-  return n < 0 ? -(1ll << 40) : n;
-}
-// the nodes in use
-__device__ __forceinline__ int nodes_of(const TreeArgs& a, int r, uint32_t* bad) {
-  if (a.nodes == nullptr) return a.T;
-  const int n = a.nodes[r];
-  if (n < 0 || n > a.T) *bad |= (uint32_t)HS_DEVERR_LOC;
-  return min(max(n, 0), a.T);
-}
-// entries of the context of request r: its positions or its list
-__device__ __forceinline__ int64_t entries_of(const TreeArgs& a, int r, int64_t len, uint32_t* bad) {
-  if (a.locs != nullptr) return a.k;
-  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_tokens;
-  if (len > cap) *bad |= (uint32_t)HS_DEVERR_LOC;
-  return max((int64_t)0, min(len, cap));
-}
-
-// record of context entry e, or null (padding, or bad with a bit raised)
-__device__ __forceinline__ const uint8_t* entry_record(const TreeArgs& a, int r, int64_t e, uint32_t* bad) {
-  int64_t p = e;
-  if (a.locs != nullptr) {
-    p = a.locs[(int64_t)r * a.k + e];
-    if (p == -1) return nullptr;
-  }
-  if (a.slot_pt != nullptr) {
-    if (p < 0 || p >= a.slot_cap[r]) {
-      *bad |= (uint32_t)HS_DEVERR_LOC;
-      return nullptr;
-    }
-    return hs_slot_addr(a.slot_pt + (int64_t)r * a.slot_pages, a.slot_shift, a.kv.rec, (int)p);
-  }
-  const int64_t row = paged_row(a.kv, r, p, (uint32_t)HS_DEVERR_LOC, bad);
-  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
-}
-__device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, int64_t len, int j, uint32_t* bad) {
-  if (a.draft != nullptr) return a.draft + ((int64_t)r * a.T + j) * a.kv.rec;
-  const int64_t row = paged_row(a.kv, r, len + j, (uint32_t)HS_DEVERR_LOC, bad);
-  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
-}
 
 // Any shape: a CTA per (node, query head, request), its four warps take the entries in turn and merge
 // their running maxima, sums and accumulators at the end.  A lane holds every 32nd group of 8 values of
@@ -234,7 +162,29 @@ TreeArgs tree_args(const hs_config* c, const hs_tree_args* g) {
   return a;
 }
 
-int launch_tree(const TreeArgs& a, cudaStream_t st) {
+int num_sms_of(int device) {
+  static int sms[64];  // the same value whoever writes it
+  if (device < 0) return 0;
+  if (device < 64 && sms[device] > 0) return sms[device];
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (device < 64) sms[device] = n;
+  return n;
+}
+
+// The tensor-core kernel where the shape and the tensor maps allow it, else the one for any shape.
+int launch_tree(const hs_config* c, const hs_tree_args* g, const TreeArgs& a, const hs_tree_pool_rows* pool, int device,
+                cudaStream_t st) {
+  const int sms = num_sms_of(device);
+  if (sms < 1) return HS_ERR_CUDA;
+  const hs_tree_plan p = hs_tree_gqa_plan(c, g->nodes, sms);
+  if (p.usable && (pool == nullptr || pool->rows <= (int64_t)INT32_MAX)) {
+    if (g->d_workspace == nullptr || g->workspace_bytes < p.workspace) return HS_ERR_SCRATCH;
+    return hs_tree_gqa_launch(c, g, &a, pool, sms, st);
+  }
   const cudaError_t e = hs_launch_pdl(k_tree_any, dim3(a.T * a.Hq, a.R), dim3(kAnyWarps * 32), 0, st, a);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
@@ -245,7 +195,9 @@ extern "C" int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int c
   const int rc = hs_check_shape(cfg);
   if (rc != HS_OK) return rc;
   if (nodes < 1 || nodes > HS_MAX_TREE_NODES || cuda_device < 0) return HS_ERR_ARG;
-  return 0;
+  const int sms = num_sms_of(cuda_device);
+  if (sms < 1) return HS_ERR_CUDA;
+  return hs_tree_gqa_plan(cfg, nodes, sms).workspace;
 }
 
 extern "C" int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_tree_args* args, void* stream) {
@@ -253,14 +205,15 @@ extern "C" int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const h
   if (rc == HS_OK) rc = hs_check_paged(cfg, kv);
   if (rc == HS_OK) rc = check_tree(cfg, args);
   if (rc != HS_OK) return rc;
-  if (args->d_len == nullptr || (args->d_locs != nullptr && args->top_k < 1)) return HS_ERR_ARG;
+  if (args->d_len == nullptr || (args->d_locs != nullptr && (args->top_k < 1 || args->top_k > kMaxPositions)))
+    return HS_ERR_ARG;
   HsOnDevice on(kv->cuda_device);
   if (!on.ok) return HS_ERR_CUDA;
   TreeArgs a = tree_args(cfg, args);
   a.kv = hs_paged_rows(cfg, kv);
   a.len = args->d_len;
   a.k = args->d_locs != nullptr ? args->top_k : 0;
-  return launch_tree(a, (cudaStream_t)stream);
+  return launch_tree(cfg, args, a, nullptr, kv->cuda_device, (cudaStream_t)stream);
 }
 
 extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const void* d_draft,
@@ -285,5 +238,6 @@ extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* a
   a.draft = (const uint8_t*)d_draft;
   a.k = c.top_k;
   pool->last_res_layer = -1;  // an attention after this one waits for the whole stream
-  return launch_tree(a, (cudaStream_t)stream);
+  const hs_tree_pool_rows rows = hs_pool_rows(pool);
+  return launch_tree(&c, args, a, &rows, pool->device, (cudaStream_t)stream);
 }

@@ -1,0 +1,326 @@
+// Tree attention: arguments, record lookups and the division of the work, shared by its kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "hs_paged.cuh"
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct TreeArgs {
+  PagedRows kv;             // paged form; err is the pool's error word in the pool's form
+  const uint64_t* slot_pt;  // pool form: [R][slot_pages] device address of each buffer page, else null
+  const int32_t* slot_cap;  // [R] slots a buffer holds
+  int slot_pages, slot_shift;
+  const uint8_t* draft;     // pool form: [R][T][rec]
+  const uint16_t* q;        // [R][T][Hq][dqk]
+  const int64_t* len;       // [R], paged form
+  const int32_t* locs;      // [R][k] or null
+  const uint64_t* mask;     // [R][T][words]
+  const int32_t* nodes;     // [R] or null
+  uint16_t* out;            // [R][T][Hq][dv]
+  int R, T, k, words, Hq, Hkv, dqk, dv;
+  int kstride, voff;        // values: KV head g's key at g * kstride, its value voff further on
+  float qscale;             // scale * log2(e)
+};
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *(const uint32_t*)&v;
+}
+
+// context length (paged form); a negative one becomes one behind which no node has a position either
+__device__ __forceinline__ int64_t context_of(const TreeArgs& a, int r, uint32_t* bad) {
+  if (a.len == nullptr) return 0;
+  const int64_t n = a.len[r];
+  if (n < 0) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return n < 0 ? -(1ll << 40) : n;
+}
+// the nodes in use
+__device__ __forceinline__ int nodes_of(const TreeArgs& a, int r, uint32_t* bad) {
+  if (a.nodes == nullptr) return a.T;
+  const int n = a.nodes[r];
+  if (n < 0 || n > a.T) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return min(max(n, 0), a.T);
+}
+// entries of the context of request r: its positions or its list
+__device__ __forceinline__ int64_t entries_of(const TreeArgs& a, int r, int64_t len, uint32_t* bad) {
+  if (a.locs != nullptr) return a.k;
+  const int64_t cap = (int64_t)a.kv.max_pages * a.kv.page_tokens;
+  if (len > cap) *bad |= (uint32_t)HS_DEVERR_LOC;
+  return max((int64_t)0, min(len, cap));
+}
+
+// record of context entry e, or null (padding, or bad with a bit raised)
+__device__ __forceinline__ const uint8_t* entry_record(const TreeArgs& a, int r, int64_t e, uint32_t* bad) {
+  int64_t p = e;
+  if (a.locs != nullptr) {
+    p = a.locs[(int64_t)r * a.k + e];
+    if (p == -1) return nullptr;
+  }
+  if (a.slot_pt != nullptr) {
+    if (p < 0 || p >= a.slot_cap[r]) {
+      *bad |= (uint32_t)HS_DEVERR_LOC;
+      return nullptr;
+    }
+    return hs_slot_addr(a.slot_pt + (int64_t)r * a.slot_pages, a.slot_shift, a.kv.rec, (int)p);
+  }
+  const int64_t row = paged_row(a.kv, r, p, (uint32_t)HS_DEVERR_LOC, bad);
+  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
+}
+__device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, int64_t len, int j, uint32_t* bad) {
+  if (a.draft != nullptr) return a.draft + ((int64_t)r * a.T + j) * a.kv.rec;
+  const int64_t row = paged_row(a.kv, r, len + j, (uint32_t)HS_DEVERR_LOC, bad);
+  return row < 0 ? nullptr : a.kv.base + row * a.kv.rec;
+}
+
+// ---- division of the work among the CTAs of the tensor-core kernels ---------------------------------
+//
+// A request's entries are its context, padded to a multiple of 4, then its nodes; they are cut into tiles
+// of TT.  An item is the work of one accumulator over all tiles of a request (a KV head and one or two
+// groups of nodes, or a slice of the value dims); the tiles of all items of all requests form one
+// sequence, request by request and item by item, of which every worker takes an equal, contiguous
+// share.  Lengths live on the device alone, so each CTA finds its share itself.  A worker's portion of
+// an item that does not hold all its tiles becomes a partial: slot 0 of the worker when the portion
+// starts inside the item, else slot 1 (a worker has at most one of each); k_tree_combine joins them.
+
+constexpr int kPortions = 14;  // portions a round of a CTA holds per worker
+constexpr int kWindow = 16;    // requests a round looks at per worker
+
+struct Portion {
+  int r, item, t0, t1;  // tiles [t0, t1) of the item
+  int n, len, nn;       // context entries, position of node 0 (negative: the nodes have none), nodes in use
+};
+
+struct PlanState {  // shared memory
+  Portion port[2][kPortions];
+  long long off[2], left[2];  // tiles into request cur, tiles still to take
+  int cur[2], nport[2];
+  int wn[2][kWindow], wlen[2][kWindow];
+  short wnn[2][kWindow];
+  long long scan[16];
+};
+
+struct WorkSplit {
+  int items;             // per request
+  int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA
+  long long* prefix;     // [R + 1] tiles (of one item) before each request, written by CTA 0
+  float *part, *ml;      // [workers][2 slots][rows][dims], [workers][2][rows][2]: maximum (base 2) and sum
+  int rows;              // accumulator rows of a portion
+};
+
+template <int TT>
+__device__ __forceinline__ long long tiles_of(int n, int nn) {
+  return nn == 0 ? 0 : (((long long)n + 3) / 4 * 4 + nn + TT - 1) / TT;
+}
+__device__ __forceinline__ void request_of(const TreeArgs& a, int r, int* n, int* len, int* nn, uint32_t* bad) {
+  const int64_t l = context_of(a, r, bad);
+  *nn = nodes_of(a, r, bad);
+  *n = (int)entries_of(a, r, l, bad);
+  *len = l > INT32_MAX ? -1 - HS_MAX_TREE_NODES : (int)max(l, (int64_t)(-1 - HS_MAX_TREE_NODES));
+}
+__device__ __forceinline__ long long split_at(long long total, int w, int workers) { return total * w / workers; }
+
+// Where each worker of this CTA starts.  Every thread of the CTA calls it.
+template <int TT>
+__device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
+  const int each = (a.R + nthr - 1) / nthr, r0 = min(tid * each, a.R), r1 = min(r0 + each, a.R);
+  uint32_t bad = 0u;
+  long long mine = 0;
+  int n, len, nn;
+  for (int r = r0; r < r1; ++r) {
+    request_of(a, r, &n, &len, &nn, &bad);
+    mine += tiles_of<TT>(n, nn);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s->scan[warp] = incl;
+  __syncthreads();
+  long long base = 0, total = 0;
+  for (int w = 0; w < (nthr >> 5); ++w) {
+    if (w == warp) base = total;
+    total += s->scan[w];
+  }
+  base += incl - mine;
+  const long long W = total * ws.items;
+  const int workers = (int)gridDim.x * ws.groups;
+  if (blockIdx.x == 0) {
+    report(a.kv.err, bad);
+    long long run = base;
+    for (int r = r0; r < r1; ++r) {
+      ws.prefix[r] = run;
+      request_of(a, r, &n, &len, &nn, &bad);
+      run += tiles_of<TT>(n, nn);
+    }
+    if (tid == 0) ws.prefix[a.R] = total;
+  }
+  for (int g = 0; g < 2; ++g) {
+    const int w = g * (int)gridDim.x + (int)blockIdx.x;
+    const long long s0 = g < ws.groups ? split_at(W, w, workers) : 0, s1 = g < ws.groups ? split_at(W, w + 1, workers) : 0;
+    if (tid == 0) s->left[g] = s1 - s0;
+    if (s1 > s0 && s0 >= base * ws.items && s0 < (base + mine) * ws.items) {  // true in one thread
+      long long off = s0 - base * ws.items;
+      int r = r0;
+      for (; r < r1; ++r) {
+        request_of(a, r, &n, &len, &nn, &bad);
+        const long long all = tiles_of<TT>(n, nn) * ws.items;
+        if (off < all) break;
+        off -= all;
+      }
+      s->cur[g] = r;
+      s->off[g] = off;
+    }
+  }
+  __syncthreads();
+}
+
+// The next portions of each worker; false when no worker has any left.  Every thread calls it.
+template <int TT>
+__device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
+  if (s->left[0] <= 0 && s->left[1] <= 0) return false;  // the same in every thread: written before a barrier
+  const int tid = threadIdx.x;
+  if (tid < 2 * kWindow) {
+    const int g = tid / kWindow, i = tid - g * kWindow;
+    if (s->left[g] > 0 && s->cur[g] + i < a.R) {
+      uint32_t bad = 0u;
+      int n, len, nn;
+      request_of(a, s->cur[g] + i, &n, &len, &nn, &bad);
+      s->wn[g][i] = n;
+      s->wlen[g][i] = len;
+      s->wnn[g][i] = (short)nn;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 || tid == 32) {
+    const int g = tid >> 5;
+    long long left = s->left[g], off = s->off[g];
+    int np = 0, i = 0;
+    const int cur = s->cur[g];
+    while (left > 0 && np < kPortions && i < kWindow && cur + i < a.R) {
+      const int n = s->wn[g][i], nn = s->wnn[g][i];
+      const long long T = tiles_of<TT>(n, nn);
+      if (off >= T * ws.items) {
+        off -= T * ws.items;
+        ++i;
+        continue;
+      }
+      Portion p;
+      p.r = cur + i;
+      p.item = (int)(off / T);
+      p.t0 = (int)(off - p.item * T);
+      p.t1 = (int)min(T, p.t0 + left);
+      p.n = n;
+      p.len = s->wlen[g][i];
+      p.nn = nn;
+      s->port[g][np++] = p;
+      left -= p.t1 - p.t0;
+      off += p.t1 - p.t0;
+    }
+    s->nport[g] = np;
+    s->left[g] = cur + i < a.R ? left : 0;
+    s->off[g] = off;
+    s->cur[g] = cur + i;
+  }
+  __syncthreads();
+  return true;
+}
+
+// bits j0 .. j0 + 31 of a node's visibility among the nn nodes in use (bits before 0 are clear)
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int nn, int j0) {
+  if (j0 <= -32 || j0 >= nn) return 0u;
+  const int s = max(j0, 0), w = s >> 6, b = s & 63;
+  uint64_t x = m[w] >> b;
+  if (b > 32 && w + 1 < words) x |= m[w + 1] << (64 - b);
+  uint32_t v = (uint32_t)x;
+  if (nn - s < 32) v &= (1u << (nn - s)) - 1u;
+  return v << (s - j0);
+}
+
+// ---- joining the partials of an item -------------------------------------------------------------
+
+struct CombineArgs {
+  const int32_t* nodes;
+  uint16_t* out;
+  WorkSplit ws;
+  int R, T, Hq, dv, workers;
+  int G, MT, per;  // rows of a node, nodes of a 128-row tile, tiles of an item
+  int np, nslice;  // items: (KV head * np + tile group) * nslice + slice
+};
+
+// One warp per accumulator row, DV dims; items that one worker held whole are written by it.
+template <int DV>
+__global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = DV / 64;  // float2 per lane
+  const int item = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
+  const long long p0 = c.ws.prefix[r], T = c.ws.prefix[r + 1] - p0, W = c.ws.prefix[c.R] * c.ws.items;
+  if (T == 0) return;
+  const long long a = p0 * c.ws.items + item * T;
+  const int wf = (int)(((a + 1) * c.workers - 1) / W), wl = (int)(((a + T) * c.workers - 1) / W);
+  if (wf == wl) return;
+  const int row = blockIdx.z * 8 + (threadIdx.x >> 5), x = row & 127;
+  const int slice = item % c.nslice, hp = item / c.nslice, h = hp / c.np, mt = (hp % c.np) * c.per + (row >> 7);
+  const int t = mt * c.MT + x / c.G;
+  int nn = c.T;
+  if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
+  if (row >= c.ws.rows || x >= c.G * c.MT || t >= nn) return;
+  auto slot_row = [&](int w) { return ((long long)w * 2 + (w == wf ? 1 : 0)) * c.ws.rows + row; };
+  auto empty = [&](int w) { return W < c.workers && split_at(W, w, c.workers) == split_at(W, w + 1, c.workers); };
+  float M = -INFINITY;
+  for (int w = wf + lane; w <= wl; w += 32)
+    if (!empty(w)) M = fmaxf(M, c.ws.ml[slot_row(w) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float2 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float2(0.f, 0.f);
+  float L = 0.f;
+  for (int w0 = wf; w0 <= wl; w0 += 32) {
+    float wt = 0.f, lw = 0.f;
+    if (w0 + lane <= wl && !empty(w0 + lane)) {
+      const float2 ml = *(const float2*)(c.ws.ml + slot_row(w0 + lane) * 2);
+      // nothing seen: no part in the result; NaN scores alone: NaN
+      wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2f(ml.x - M);
+      lw = wt * ml.y;
+    }
+    const int cnt = min(32, wl - w0 + 1);
+    for (int i = 0; i < cnt; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wt, i);
+      L += __shfl_sync(0xffffffffu, lw, i);
+      if (wi == 0.f) continue;
+      const float2* p = (const float2*)(c.ws.part + slot_row(w0 + i) * DV);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 u = p[lane + 32 * v];
+        acc[v].x = fmaf(wi, u.x, acc[v].x);
+        acc[v].y = fmaf(wi, u.y, acc[v].y);
+      }
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t* o = (uint32_t*)(c.out + (((int64_t)r * c.T + t) * c.Hq + (int64_t)h * c.G + x % c.G) * c.dv + slice * DV);
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[lane + 32 * v] = pack(acc[v].x * inv, acc[v].y * inv);
+}
+
+}  // namespace
+
+// ---- host ------------------------------------------------------------------------------------------
+
+// Launch plans of the tensor-core kernels.  `usable`: the shape is theirs.
+struct hs_tree_plan {
+  bool usable;
+  int64_t workspace;
+};
+hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms);
+int hs_tree_gqa_launch(const hs_config* c, const hs_tree_args* g, const void* tree_args, const hs_tree_pool_rows* pool,
+                       int num_sms, cudaStream_t st);

@@ -1,0 +1,688 @@
+// Tree attention over GQA records on the 5th-generation tensor cores.
+//
+// Rows of an accumulator are (node, query head of one KV head) pairs: MT = 128 / G nodes of G heads.  Per
+// tile of 128 entries S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128), both tcgen05.mma with the
+// accumulators in tensor memory; the weights P go back to tensor memory over their scores and enter the
+// second product from there.  Two softmax warpgroups, a thread per row, each with its own S and O:
+//   one tile of rows (T <= MT): each group is a worker of its own with its own share of the entries, so
+//     that one group's softmax runs beside the other's products;
+//   more rows: the groups take two tiles of rows over the same entries, which are loaded once for both.
+// Records are gathered by TMA (four rows of 64 values an instruction, 128-byte swizzled; 16 or 32 rows when a
+// dense context's pages allow) into a ring of K and V tiles, four producer warps a tile.
+// Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
+// of one tile of rows 0.54 us at the tensor cores' rate.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "hs_tc.cuh"
+#include "hs_tree.cuh"
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kProducers = 4;
+constexpr int kWarpMma = 8, kWarpProd = 9;
+constexpr int kThreads = (kWarpProd + kProducers) * 32;
+constexpr int kMaskRing = 8;   // tiles of validity bits per group: more than the ring can run ahead
+constexpr float kLazy = 8.f;   // log2 headroom before the running maximum is raised
+constexpr size_t kSmemCap = 227 * 1024;
+
+template <int D>
+struct Shape {
+  static constexpr int kCh = D / 64;                 // 64-value (128-byte) column blocks
+  static constexpr int kBlk = kTile * 128;           // bytes of one block of a tile
+  static constexpr int kSlot = kCh * kBlk;           // a K or V tile; also a Q tile
+  static constexpr int kRing = D == 128 ? 5 : 11;
+  static constexpr size_t kDyn = (size_t)(2 + kRing) * kSlot + 1024;
+};
+
+struct TcArgs {
+  TreeArgs a;
+  WorkSplit ws;
+  int G, MT, np, shared;   // np: row tiles (shared: pairs of them) of a KV head
+  int nmt;                 // row tiles of a KV head
+  int seg;                 // dense contexts whose pages hold multiples of it: rows per box (32 or 16), else 0
+  int ctx_rows, draft_rows;  // extents of the record maps: a row index there reads zeros
+  const uint8_t* pool_base;  // pool form: its buffer pages are rows of one array
+  int64_t pool_page_bytes, pool_page_slots;
+};
+
+struct Control {
+  PlanState plan;
+  __align__(8) uint64_t full[11], empty[11];
+  uint64_t qfull[2], s[2], p[2], pv[2], v[2], mask[2][kMaskRing];
+  uint64_t fin;
+  uint32_t valid[2][kMaskRing][4];
+  int vslot[2];
+  uint32_t tmem, abort;
+};
+
+// one OR over the threads of a named barrier
+__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)x)
+      : "memory");
+  return r != 0u;
+}
+
+__device__ __forceinline__ bool bad_pair(uint32_t w) {  // an infinity or NaN among two bf16
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t good_pair(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tree_gqa(const TcArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap ctxmap,
+               const __grid_constant__ CUtensorMap segmap, const __grid_constant__ CUtensorMap draftmap) {
+  using C = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Control ct;
+  const TreeArgs& a = c.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t q_u = smem_u32(smem), ring_u = q_u + 2 * C::kSlot;
+  volatile uint32_t* abort = &ct.abort;
+  if (tid == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&ct.full[i], kProducers);
+      mbar_init(&ct.empty[i], 1u);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&ct.qfull[g], 1u);
+      mbar_init(&ct.s[g], 1u);
+      mbar_init(&ct.p[g], 128u);
+      mbar_init(&ct.pv[g], 1u);
+      mbar_init(&ct.v[g], 1u);
+      for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[g][i], kProducers);
+    }
+    mbar_init(&ct.fin, 1u);
+    ct.abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ct.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the only kernel that may start early is this call's own combine, which waits for this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  plan_start<kTile>(a, c.ws, &ct.plan);
+  tc_fence_after();
+  const uint32_t tb = ct.tmem;
+  // tensor memory: per group 128 columns of scores (their first 64 become the weights), then D of O
+  const uint32_t t_s[2] = {tb, tb + 128u}, t_o[2] = {tb + 256u, tb + 256u + (uint32_t)D};
+
+  // counters that run on through the rounds, each used by one role
+  int seq = 0;                      // ring loads (producers: issued; products: consumed)
+  int tiles[2] = {0, 0};            // tiles of each group (products), or of a group's K loads (producers)
+  int nq[2] = {0, 0};               // portions of each group
+  int nt = 0, nv = 0, nm = 0;       // softmax: tiles, tiles with nodes, tiles of the mask ring
+  int sent = 0;                     // producers: ring loads issued; first softmax thread: query loads
+  bool ok = true;
+  uint32_t bad = 0u;
+
+  while (plan_round<kTile>(a, c.ws, &ct.plan)) {
+    const int ng = c.shared ? 1 : 2;  // portion lists
+    const Portion* list[2] = {ct.plan.port[0], ct.plan.port[c.shared ? 0 : 1]};
+    const int count[2] = {ct.plan.nport[0], c.shared ? ct.plan.nport[0] : ct.plan.nport[1]};
+    // whether group g takes part in an item: the last pair of row tiles may be a single one
+    auto present = [&](int g, const Portion& p) { return !c.shared || 2 * (p.item % c.np) + g < c.nmt; };
+
+    if (warp >= kWarpProd) {
+      // ---------------- producers: a quarter of every tile each ----------------
+      const int pw = warp - kWarpProd, ch = lane >> 3, i4 = lane & 7;
+      auto load = [&](const Portion& P, int tile, bool val, int g) {
+        const int slot = seq % C::kRing;
+        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
+        const int e0 = tile * kTile + 32 * pw, e = e0 + 4 * i4;
+        const int h = P.item / c.np;
+        const bool boxed = c.seg != 0 && e0 + 32 <= P.n;
+        int row[4];
+        uint32_t ok4 = 0u;
+        bool draft = false;
+        if (boxed) {
+          // one lane per box: lanes 0 .. 32 / seg - 1 of each column block
+          const int b = i4 * c.seg;
+          row[0] = c.ctx_rows;
+          if (b < 32) {
+            const int64_t x = paged_row(a.kv, P.r, e0 + b, (uint32_t)HS_DEVERR_LOC, &bad);
+            if (x >= 0) {
+              row[0] = (int)x;
+              ok4 = (c.seg == 32 ? 0xffffffffu : 0xffffu) << b;
+            }
+          }
+        } else {
+          draft = e >= n4;
+          const int oob = draft ? c.draft_rows : c.ctx_rows;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            int64_t y = -1;
+            if (draft) {
+              const int j = e - n4 + x;
+              if (j < P.nn)
+                y = a.draft != nullptr ? (int64_t)P.r * a.T + j
+                                       : paged_row(a.kv, P.r, (int64_t)P.len + j, (uint32_t)HS_DEVERR_LOC, &bad);
+            } else if (e + x < P.n) {
+              int64_t p = e + x;
+              if (a.locs != nullptr) p = a.locs[(int64_t)P.r * a.k + p];
+              if (a.locs != nullptr && p == -1) {
+              } else if (a.slot_pt != nullptr) {
+                if (p < 0 || p >= a.slot_cap[P.r]) {
+                  bad |= (uint32_t)HS_DEVERR_LOC;
+                } else {
+                  const uint64_t page = a.slot_pt[(int64_t)P.r * a.slot_pages + (p >> a.slot_shift)];
+                  y = (int64_t)((page - (uint64_t)(uintptr_t)c.pool_base) / (uint64_t)c.pool_page_bytes) * c.pool_page_slots +
+                      (p & ((1 << a.slot_shift) - 1));
+                }
+              } else {
+                y = paged_row(a.kv, P.r, p, (uint32_t)HS_DEVERR_LOC, &bad);
+              }
+            }
+            row[x] = y >= 0 ? (int)y : oob;
+            if (y >= 0) ok4 |= 1u << (4 * i4 + x);
+          }
+        }
+        if (ok && seq >= C::kRing) ok = warp_wait(&ct.empty[slot], (uint32_t)((seq / C::kRing - 1) & 1), abort);
+        if (ok) {
+          if (lane == 0) mbar_arrive_expect_tx(&ct.full[slot], (uint32_t)(32 * D * 2));
+          __syncwarp();
+          const int x0 = h * a.kstride + (val ? a.voff : 0) + 64 * ch;
+          const uint32_t dst = ring_u + (uint32_t)(slot * C::kSlot + ch * C::kBlk + 32 * pw * 128);
+          if (ch < C::kCh) {
+            if (boxed) {
+              if (i4 * c.seg < 32)
+                tma_load_2d(dst + (uint32_t)(i4 * c.seg * 128), &segmap, x0, row[0], &ct.full[slot]);
+            } else {
+              tma_gather4(dst + (uint32_t)(4 * i4 * 128), draft ? &draftmap : &ctxmap, x0, row, &ct.full[slot]);
+            }
+          }
+          sent = seq + 1;
+          if (!val) {
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) ok4 |= __shfl_xor_sync(0xffffffffu, ok4, o);
+            const int m = tiles[g] % kMaskRing;
+            if (lane == 0) {
+              ct.valid[g][m][pw] = ok4;
+              mbar_arrive(&ct.mask[g][m]);
+            }
+          }
+        }
+        if (!val) ++tiles[g];
+        ++seq;
+      };
+      // the order of the products below
+      int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
+      for (int g = 0; g < ng; ++g) kt[g] = vt[g] = count[g] > 0 ? list[g][0].t0 : 0;
+      auto step = [&](int g, int (&pi)[2], int (&ti)[2], bool val) {
+        load(list[g][pi[g]], ti[g], val, g);
+        if (++ti[g] == list[g][pi[g]].t1) {
+          ++pi[g];
+          if (pi[g] < count[g]) ti[g] = list[g][pi[g]].t0;
+        }
+      };
+      for (int g = 0; g < ng; ++g)
+        if (kp[g] < count[g]) step(g, kp, kt, false);
+      for (bool more = true; more;) {
+        more = false;
+        for (int g = 0; g < ng; ++g) {
+          if (vp[g] >= count[g]) continue;
+          more = true;
+          step(g, vp, vt, true);
+          if (kp[g] < count[g]) step(g, kp, kt, false);
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ---------------- products: S_0(0), S_1(0), then O_g(i), S_g(i+1) by turns ----------------
+      const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0), id_o = umma_idesc_bf16(128, D, 0, 1);
+      const uint64_t dq0 = umma_sdesc(q_u, 16, 1024, 2), dk0 = umma_sdesc(ring_u, 16, 1024, 2);
+      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
+      const uint64_t dv0 = umma_sdesc(ring_u, C::kBlk, 1024, 2);
+      constexpr uint64_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
+      int kslot = 0, vslot = 0;  // shared: the slots both groups use
+      auto take = [&]() {
+        const int slot = seq % C::kRing;
+        if (ok) ok = warp_wait(&ct.full[slot], (uint32_t)((seq / C::kRing) & 1), abort);
+        tc_fence_after();
+        ++seq;
+        return slot;
+      };
+      auto score = [&](int g, const Portion& P, int tile, bool last_user) {
+        if (tile == P.t0) {  // this portion's queries
+          if (ok) ok = warp_wait(&ct.qfull[g], (uint32_t)(nq[g] & 1), abort);
+          ++nq[g];
+        }
+        // the weights of the tile before share these columns: their product has to be complete
+        if (ok && tiles[g] > 0) ok = warp_wait(&ct.pv[g], (uint32_t)((tiles[g] - 1) & 1), abort);
+        tc_fence_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int b = 0; b < C::kCh; ++b)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16(t_s[g], dq0 + (uint64_t)g * kSlotStep + b * kBlkStep + 2 * ks,
+                        dk0 + (uint64_t)kslot * kSlotStep + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
+          umma_commit(&ct.s[g]);
+          if (last_user) umma_commit(&ct.empty[kslot]);
+        }
+        __syncwarp();
+      };
+      auto value = [&](int g, const Portion& P, int tile, bool last_user) {
+        if (ok) ok = warp_wait(&ct.p[g], (uint32_t)(tiles[g] & 1), abort);
+        tc_fence_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16_ta(t_o[g], t_s[g] + 8u * ks, dv0 + (uint64_t)vslot * kSlotStep + 128 * ks, id_o,
+                         (tile != P.t0 || ks != 0) ? 1u : 0u);
+          umma_commit(&ct.pv[g]);
+          if (last_user) umma_commit(&ct.empty[vslot]);
+        }
+        __syncwarp();
+        ++tiles[g];
+      };
+      int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
+      for (int g = 0; g < 2; ++g) kt[g] = vt[g] = count[g] > 0 ? list[g][0].t0 : 0;
+      auto advance = [&](int g, int (&pi)[2], int (&ti)[2]) {
+        if (++ti[g] == list[g][pi[g]].t1) {
+          ++pi[g];
+          if (pi[g] < count[g]) ti[g] = list[g][pi[g]].t0;
+        }
+      };
+      auto do_score = [&](int g) {
+        if (kp[g] >= count[g]) return;
+        const Portion& P = list[g][kp[g]];
+        if (!c.shared || g == 0) kslot = take();
+        if (present(g, P)) score(g, P, kt[g], !c.shared || g == 1 || !present(1, P));
+        advance(g, kp, kt);
+      };
+      do_score(0);
+      do_score(1);
+      for (bool more = true; more;) {
+        more = false;
+        for (int g = 0; g < 2; ++g) {
+          if (vp[g] >= count[g]) continue;
+          more = true;
+          const Portion& P = list[g][vp[g]];
+          if (!c.shared || g == 0) {
+            vslot = take();
+            // nodes among the entries: the softmax looks at their values first (both groups together, so
+            // both are told before the first one's weights are waited for)
+            if (lane == 0 && (vt[g] + 1) * (long long)kTile > (long long)(((unsigned)P.n + 3u) & ~3u)) {
+              for (int x = g; x < (c.shared ? 2 : g + 1); ++x) {
+                if (!present(x, P)) continue;
+                ct.vslot[x] = vslot;
+                mbar_arrive(&ct.v[x]);
+              }
+            }
+            __syncwarp();
+          }
+          if (present(g, P)) value(g, P, vt[g], !c.shared || g == 1 || !present(1, P));
+          advance(g, vp, vt);
+          do_score(g);
+        }
+      }
+    } else {
+      // ---------------- softmax: group g, thread = row = TMEM lane ----------------
+      const int g = warp >> 2, row = tid & 127;
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t ts = t_s[g] + lane_base, to = t_o[g] + lane_base;
+      const int lt = row / c.G, hq = row - lt * c.G;
+      auto load_q = [&](const Portion& P) {  // by the group's first thread
+        ++sent;
+        mbar_arrive_expect_tx(&ct.qfull[g], (uint32_t)(C::kCh * c.G * c.MT * 128));
+        const int h = P.item / c.np, mt = c.shared ? 2 * (P.item % c.np) + g : 0;
+        for (int b = 0; b < C::kCh; ++b)
+          tma_load_4d(q_u + (uint32_t)(g * C::kSlot + b * C::kBlk), &qmap, 64 * b, h * c.G, mt * c.MT, P.r, &ct.qfull[g]);
+      };
+      auto next_present = [&](int i) {
+        while (i < count[g] && !present(g, list[g][i])) ++i;
+        return i;
+      };
+      if (row == 0) {
+        const int i = next_present(0);
+        if (i < count[g]) load_q(list[g][i]);
+      }
+      for (int pi = 0; pi < count[g]; ++pi) {
+        const Portion P = list[g][pi];
+        if (!present(g, P)) {
+          nm += P.t1 - P.t0;
+          continue;
+        }
+        const bool both = c.shared && present(1, P);
+        const int h = P.item / c.np, mt = c.shared ? 2 * (P.item % c.np) + g : 0, t = mt * c.MT + lt;
+        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
+        const bool row_ok = row < c.G * c.MT && t < P.nn;
+        const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+        const uint64_t* mw = a.mask + ((int64_t)P.r * a.T + (row_ok ? t : 0)) * a.words;
+        float m = -INFINITY, l = 0.f;
+        bool dirty = false;  // a node's value is infinite or NaN
+        for (int tile = P.t0; tile < P.t1; ++tile) {
+          const int j0 = (int)((long long)tile * kTile - n4);  // node of the tile's first entry
+          const bool nodes = j0 + kTile > 0;
+          if (ok) ok = mbar_wait_bounded(&ct.s[g], (uint32_t)(nt & 1), abort);
+          tc_fence_after();
+          if (row == 0 && tile == P.t1 - 1) {  // the last scores of the portion are done: the next one's queries
+            const int i = next_present(pi + 1);
+            if (i < count[g] && ok) load_q(list[g][i]);
+          }
+          const int mg = c.shared ? 0 : g;
+          if (ok) ok = mbar_wait_bounded(&ct.mask[mg][nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
+          ok = __all_sync(0xffffffffu, ok);
+          uint32_t w[4];
+          bool full = !nodes;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            w[x] = ct.valid[mg][nm % kMaskRing][x];
+            full = full && w[x] == 0xffffffffu;
+          }
+          if (nodes) {
+            // entries that are nodes: valid ones that this row sees
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int jw = j0 + 32 * x;
+              const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
+              w[x] &= ctx | (row_ok ? mask_bits(mw, a.words, P.nn, jw) : 0u);
+            }
+            if (ok) ok = mbar_wait_bounded(&ct.v[g], (uint32_t)(nv & 1), abort);
+            ok = __all_sync(0xffffffffu, ok);
+            ++nv;
+            bool d = false;
+            if (ok && j0 + row >= 0 && j0 + row < P.nn) {
+              const int vs = ct.vslot[g];
+              for (int b = both ? g : 0; b < C::kCh; b += both ? 2 : 1) {
+                uint4* vr = (uint4*)(smem + 2 * C::kSlot + vs * C::kSlot + b * C::kBlk + row * 128);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  uint4 u = vr[x];
+                  if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
+                    d = true;
+                    u = make_uint4(good_pair(u.x), good_pair(u.y), good_pair(u.z), good_pair(u.w));
+                    vr[x] = u;
+                  }
+                }
+              }
+            }
+            if (d) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (bar_or(both ? 3 : 1 + g, both ? 256 : 128, d)) dirty = true;
+          }
+          ++nm;
+          ++nt;
+          if (ok && warp_ok) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              float v[32];
+              tmem_ld32(ts + 32u * x, v);
+              const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
+              if (full) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[j] * a.qscale);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, (wx >> j) & 1u ? v[j] * a.qscale : -INFINITY);
+              }
+            }
+            const bool raise = mx > m + kLazy;
+            if (__any_sync(0xffffffffu, raise)) {
+              const float mn = raise ? mx : m;
+              const float al = (mn == m || m == -INFINITY) ? 1.f : fast_exp2(m - mn);
+              m = mn;
+              l *= al;
+              if (tile != P.t0) {
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                  float o[32];
+                  tmem_ld32(to + 32u * x, o);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] *= al;
+                  tmem_st32(to + 32u * x, o);
+                }
+              }
+            }
+            const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 0
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              float v[32];
+              tmem_ld32(ts + 32u * x, v);
+              const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float p0 = fast_exp2(fmaf(v[2 * j], a.qscale, -base)), p1 = fast_exp2(fmaf(v[2 * j + 1], a.qscale, -base));
+                if (!full) {
+                  p0 = (wx >> (2 * j)) & 1u ? p0 : 0.f;
+                  p1 = (wx >> (2 * j + 1)) & 1u ? p1 : 0.f;
+                }
+                pk[j] = pack_bf16(p0, p1);
+                sum0 += lo(pk[j]);  // the rounded weights, as the product takes them
+                sum1 += hi(pk[j]);
+              }
+              tmem_st16(ts + 16u * x, pk);
+            }
+            l += sum0 + sum1;
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          mbar_arrive(&ct.p[g]);
+        }
+        // the portion's result: complete, or a partial
+        if (ok) ok = mbar_wait_bounded(&ct.pv[g], (uint32_t)((nt - 1) & 1), abort);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        if (ok && warp_ok) {
+          const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
+          const int wk = (c.shared ? 0 : g) * (int)gridDim.x + (int)blockIdx.x;
+          const long long prow = ((long long)wk * 2 + (P.t0 > 0 ? 0 : 1)) * c.ws.rows + (c.shared ? 128 * g : 0) + row;
+          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32];
+            tmem_ld32(to + 32u * x, o);
+            if (dirty && row_ok) {
+              // values left out of the product (they would have reached every row): into the rows that see them
+              for (int j = max(0, P.t0 * kTile - n4); j < min((long long)P.nn, (long long)P.t1 * kTile - n4); ++j) {
+                if (((mw[j >> 6] >> (j & 63)) & 1ull) == 0ull) continue;
+                const uint8_t* rec = node_record(a, P.r, P.len, j, &bad);
+                if (rec == nullptr) continue;
+                const uint32_t* vr = (const uint32_t*)rec + ((int64_t)h * a.kstride + a.voff + 32 * x) / 2;
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const uint32_t u = vr[y];
+                  if ((u & 0x7f80u) == 0x7f80u) o[2 * y] += lo(u);
+                  if ((u & 0x7f800000u) == 0x7f800000u) o[2 * y + 1] += hi(u);
+                }
+              }
+            }
+            if (row_ok) {
+              if (whole) {
+                uint4* dst = (uint4*)(a.out + (((int64_t)P.r * a.T + t) * a.Hq + (int64_t)h * c.G + hq) * D + 32 * x);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv), pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                                      pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+              } else {
+                float4* dst = (float4*)(c.ws.part + prow * D + 32 * x);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              }
+            }
+          }
+          if (row_ok && !whole) *(float2*)(c.ws.ml + prow * 2) = make_float2(m, l);
+        }
+        tc_fence_before();
+      }
+    }
+    if (!ok) *abort = 1u;
+    __syncwarp();
+  }
+  if (!ok) {
+    *abort = 1u;
+    if (lane == 0) report(a.kv.err, (uint32_t)HS_DEVERR_TIMEOUT);
+  }
+  report(a.kv.err, bad);
+  // after a wait that gave up, copies and products may still be in flight: they end before the CTA does
+  volatile uint32_t never = 0u;
+  if (warp == kWarpMma) {
+    if (elect_one()) umma_commit(&ct.fin);
+    __syncwarp();
+    warp_wait(&ct.fin, 0u, &never);
+  }
+  __syncthreads();
+  if (*abort != 0u && lane == 0) {
+    const uint64_t t0 = global_ns();
+    if (warp >= kWarpProd) {
+      for (int i = max(0, sent - C::kRing); i < sent; ++i)
+        while (!mbar_try_wait(&ct.full[i % C::kRing], (uint32_t)((i / C::kRing) & 1)) && global_ns() - t0 < 1000000000ull) {
+        }
+    } else if ((warp & 3) == 0 && warp < kWarpMma && sent > 0) {
+      while (!mbar_try_wait(&ct.qfull[warp >> 2], (uint32_t)((sent - 1) & 1)) && global_ns() - t0 < 1000000000ull) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+
+struct Plan {
+  int D, G, MT, nmt, shared, np, items, rows, workers;
+};
+
+bool plan_of(const hs_config* c, int T, int sms, Plan* p) {
+  if (c->layout != HS_LAYOUT_GQA || c->head_dim_qk != c->head_dim_v) return false;
+  if (c->head_dim_qk != 64 && c->head_dim_qk != 128) return false;
+  p->D = c->head_dim_qk;
+  p->G = c->num_q_heads / c->num_kv_heads;
+  if (p->G > 128) return false;
+  p->MT = 128 / p->G < T ? 128 / p->G : T;
+  p->nmt = (T + p->MT - 1) / p->MT;
+  p->shared = p->nmt > 1;
+  p->np = p->shared ? (p->nmt + 1) / 2 : 1;
+  p->items = c->num_kv_heads * p->np;
+  p->rows = p->shared ? 256 : p->G * p->MT;
+  p->workers = p->shared ? sms : 2 * sms;
+  return true;
+}
+
+int64_t part_floats(const Plan& p) { return (int64_t)p.workers * 2 * p.rows * p.D; }
+
+bool encode(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
+            const cuuint32_t* box) {
+  const EncodeFn fn = tensor_map_encoder();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  memset(m, 0, sizeof(*m));
+  return fn != nullptr && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(base), size, stride, box,
+                             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The shared-memory limit of a kernel, raised once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, bool* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = hs_raise_smem_limit(kern, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int D>
+cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& ctx, const CUtensorMap& seg,
+                   const CUtensorMap& draft, const CombineArgs& cb, cudaStream_t st) {
+  static_assert(Shape<D>::kDyn + sizeof(Control) <= kSmemCap, "shared memory of a CTA");
+  static bool done[64];
+  cudaError_t e = allow_smem(k_tree_gqa<D>, Shape<D>::kDyn, done);
+  if (e != cudaSuccess) return e;
+  e = hs_launch_pdl(k_tree_gqa<D>, dim3(sms), dim3(kThreads), Shape<D>::kDyn, st, c, q, ctx, seg, draft);
+  if (e != cudaSuccess) return e;
+  return hs_launch_pdl(k_tree_combine<D>, dim3(p.items, c.a.R, (p.rows + 7) / 8), dim3(256), 0, st, cb);
+}
+
+}  // namespace
+
+hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms) {
+  Plan p;
+  hs_tree_plan r = {plan_of(c, nodes, num_sms, &p), 0};
+  if (r.usable)
+    r.workspace = (int64_t)((c->num_requests + 1) * sizeof(int64_t) + 15) / 16 * 16 +
+                  (part_floats(p) + (int64_t)p.workers * 2 * p.rows * 2) * (int64_t)sizeof(float);
+  return r;
+}
+
+int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* tree_args, const hs_tree_pool_rows* pool,
+                       int num_sms, cudaStream_t st) {
+  Plan p;
+  if (!plan_of(cfg, g->nodes, num_sms, &p)) return HS_ERR_CONFIG;
+  TcArgs c{};
+  c.a = *(const TreeArgs*)tree_args;
+  c.G = p.G;
+  c.MT = p.MT;
+  c.np = p.np;
+  c.shared = p.shared;
+  c.nmt = p.nmt;
+  uint8_t* w = (uint8_t*)g->d_workspace;
+  c.ws.items = p.items;
+  c.ws.groups = p.shared ? 1 : 2;
+  c.ws.rows = p.rows;
+  c.ws.prefix = (long long*)w;
+  c.ws.part = (float*)(w + (int64_t)((cfg->num_requests + 1) * sizeof(int64_t) + 15) / 16 * 16);
+  c.ws.ml = c.ws.part + part_floats(p);
+  const cuuint64_t rec = (cuuint64_t)c.a.kv.rec;
+  const uint8_t* base = c.a.kv.base;
+  int64_t rows = c.a.kv.num_pages * c.a.kv.page_tokens;
+  if (pool != nullptr) {
+    base = pool->base;
+    rows = pool->rows;
+    c.pool_base = pool->base;
+    c.pool_page_bytes = pool->page_bytes;
+    c.pool_page_slots = pool->page_slots;
+  } else if (c.a.locs == nullptr) {
+    c.seg = c.a.kv.page_tokens % 32 == 0 ? 32 : (c.a.kv.page_tokens % 16 == 0 ? 16 : 0);
+  }
+  c.ctx_rows = (int)rows;
+  c.draft_rows = pool != nullptr ? cfg->num_requests * g->nodes : (int)rows;
+  CUtensorMap qm, ctx, seg, draft;
+  const cuuint64_t size[2] = {rec / 2, (cuuint64_t)rows}, stride[1] = {rec};
+  const cuuint32_t box[2] = {64, 1}, sbox[2] = {64, (cuuint32_t)(c.seg != 0 ? c.seg : 1)};
+  const cuuint64_t dsize[2] = {rec / 2, (cuuint64_t)c.draft_rows};
+  const cuuint64_t row = (cuuint64_t)p.D * 2;
+  const cuuint64_t qsize[4] = {(cuuint64_t)p.D, (cuuint64_t)cfg->num_q_heads, (cuuint64_t)g->nodes, (cuuint64_t)cfg->num_requests};
+  const cuuint64_t qstride[3] = {row, row * cfg->num_q_heads, row * cfg->num_q_heads * g->nodes};
+  const cuuint32_t qbox[4] = {64, (cuuint32_t)p.G, (cuuint32_t)p.MT, 1};
+  if (!encode(&ctx, base, 2, size, stride, box) || !encode(&seg, base, 2, size, stride, sbox) ||
+      !encode(&draft, pool != nullptr ? (const void*)c.a.draft : (const void*)base, 2, dsize, stride, box) ||
+      !encode(&qm, c.a.q, 4, qsize, qstride, qbox))
+    return HS_ERR_CUDA;
+  CombineArgs cb{};
+  cb.nodes = c.a.nodes;
+  cb.out = c.a.out;
+  cb.ws = c.ws;
+  cb.R = c.a.R;
+  cb.T = c.a.T;
+  cb.Hq = c.a.Hq;
+  cb.dv = p.D;
+  cb.workers = p.workers;
+  cb.G = p.G;
+  cb.MT = p.MT;
+  cb.per = p.shared ? 2 : 1;
+  cb.np = p.np;
+  cb.nslice = 1;
+  const cudaError_t e = p.D == 128 ? launch<128>(c, p, num_sms, qm, ctx, seg, draft, cb, st)
+                                   : launch<64>(c, p, num_sms, qm, ctx, seg, draft, cb, st);
+  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}

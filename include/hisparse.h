@@ -386,7 +386,8 @@ typedef struct {
                              [r * max_pages, (r + 1) * max_pages) in order */
   int64_t num_pages;      /* num_pages * page_tokens <= 2^31 - 1 */
   int32_t page_tokens;    /* >= 1, any number */
-  int32_t max_pages;      /* pages of a request: positions [0, max_pages * page_tokens) */
+  int32_t max_pages;      /* pages of a request: positions [0, max_pages * page_tokens), at
+                             most 2^31 - 65536 */
   uint32_t* d_err;        /* device word that errors only the device sees are OR'ed into, or NULL */
   int32_t cuda_device;
 } hs_paged_kv;
@@ -441,7 +442,7 @@ typedef struct {
   const int64_t* d_len;    /* [num_requests] context length; node j is the record at position len + j */
   const int32_t* d_locs;   /* NULL: the context is every position [0, len).  Else [num_requests][top_k]
                               positions, -1 = padding, in any order: only those */
-  int32_t top_k;           /* with d_locs: 1 <= top_k; ignored without */
+  int32_t top_k;           /* with d_locs: 1 .. 2^31 - 65536; ignored without */
   const uint64_t* d_mask;  /* [num_requests][nodes][ceil(nodes / 64)]: bit j of node i's words is set when
                               i sees node j (itself included).  Any pattern is accepted */
   const int32_t* d_nodes;  /* [num_requests] nodes in use (0 .. nodes), or NULL: all of them.  Output rows
