@@ -1057,15 +1057,6 @@ constexpr int kUTmemO = 128;               // first TMEM column of O^T (after th
 constexpr float kULazy = 8.f;              // log2 headroom before the max is raised
 constexpr size_t kUSmem = (size_t)kUQ + kUP + (size_t)kURing * kUSlot + 1024;  // + 1 KB alignment
 
-// 16-byte cp.async; src_bytes = 0 writes zeros (nothing is read)
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-// one arrival on *bar once every cp.async this thread issued before has landed
-__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // barrier of one softmax warpgroup (ids 1 and 2; 0 is __syncthreads)
 __device__ __forceinline__ void wg_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 

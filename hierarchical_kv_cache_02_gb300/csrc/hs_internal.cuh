@@ -206,11 +206,6 @@ void hs_attn_workspace(const hs_config* cfg, int num_sms, size_t* floats, int* m
 bool hs_attn_supported(const hs_config* cfg);
 bool hs_attn_can_fetch(const hs_config* cfg);  // the attention can take over the miss fetch
 int hs_attn_prepare(const hs_config* cfg, int num_sms);
-struct hs_tree_pool_rows {  // the device cache pool as one array of records
-  const uint8_t* base;
-  int64_t rows, page_bytes, page_slots;
-};
-hs_tree_pool_rows hs_pool_rows(const hs_pool* pool);
 int hs_resolve_prepare(hs_pool* pool);
 size_t hs_resolve_smem_bytes(const hs_config* cfg);
 // Dynamic shared memory of a resolve CTA at most: 227 KB less the kernel's static shared memory

@@ -602,11 +602,6 @@ extern "C" int hs_device_usage(hs_pool* pool, int64_t* pages_in_use, int64_t* pa
   return HS_OK;
 }
 
-hs_tree_pool_rows hs_pool_rows(const hs_pool* p) {
-  const hs_dev_pages& d = *p->dev;
-  return {p->buf, d.total_pages * d.page_slots, d.page_bytes, d.page_slots};
-}
-
 extern "C" int hs_debug_stall_next(hs_pool* pool, int kernels) {
   if (pool == nullptr || (kernels & ~(HS_STALL_ATTN | HS_STALL_RESOLVE | HS_STALL_FETCH)) != 0) return HS_ERR_ARG;
   pool->debug_stall |= kernels;

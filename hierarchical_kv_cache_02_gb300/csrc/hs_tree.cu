@@ -175,15 +175,14 @@ int num_sms_of(int device) {
   return n;
 }
 
-// The tensor-core kernel where the shape and the tensor maps allow it, else the one for any shape.
-int launch_tree(const hs_config* c, const hs_tree_args* g, const TreeArgs& a, const hs_tree_pool_rows* pool, int device,
-                cudaStream_t st) {
+// The tensor-core kernel for the shapes it takes, else the one for any shape.
+int launch_tree(const hs_config* c, const hs_tree_args* g, const TreeArgs& a, int device, cudaStream_t st) {
   const int sms = num_sms_of(device);
   if (sms < 1) return HS_ERR_CUDA;
   const hs_tree_plan p = hs_tree_gqa_plan(c, g->nodes, sms);
-  if (p.usable && (pool == nullptr || pool->rows <= (int64_t)INT32_MAX)) {
+  if (p.usable) {
     if (g->d_workspace == nullptr || g->workspace_bytes < p.workspace) return HS_ERR_SCRATCH;
-    return hs_tree_gqa_launch(c, g, &a, pool, sms, st);
+    return hs_tree_gqa_launch(c, g, &a, sms, st);
   }
   const cudaError_t e = hs_launch_pdl(k_tree_any, dim3(a.T * a.Hq, a.R), dim3(kAnyWarps * 32), 0, st, a);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
@@ -213,7 +212,7 @@ extern "C" int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const h
   a.kv = hs_paged_rows(cfg, kv);
   a.len = args->d_len;
   a.k = args->d_locs != nullptr ? args->top_k : 0;
-  return launch_tree(cfg, args, a, nullptr, kv->cuda_device, (cudaStream_t)stream);
+  return launch_tree(cfg, args, a, kv->cuda_device, (cudaStream_t)stream);
 }
 
 extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const void* d_draft,
@@ -238,6 +237,5 @@ extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* a
   a.draft = (const uint8_t*)d_draft;
   a.k = c.top_k;
   pool->last_res_layer = -1;  // an attention after this one waits for the whole stream
-  const hs_tree_pool_rows rows = hs_pool_rows(pool);
-  return launch_tree(&c, args, a, &rows, pool->device, (cudaStream_t)stream);
+  return launch_tree(&c, args, a, pool->device, (cudaStream_t)stream);
 }

@@ -123,7 +123,22 @@ __device__ __forceinline__ void request_of(const TreeArgs& a, int r, int* n, int
   *n = (int)entries_of(a, r, l, bad);
   *len = l > INT32_MAX ? -1 - HS_MAX_TREE_NODES : (int)max(l, (int64_t)(-1 - HS_MAX_TREE_NODES));
 }
-__device__ __forceinline__ long long split_at(long long total, int w, int workers) { return total * w / workers; }
+// Shares of `total` tiles: the first total % workers workers take one more than the others.
+struct Shares {
+  long long per, more;  // more: workers with per + 1
+  __device__ __forceinline__ Shares(long long total, int workers) {
+    per = div_small(total, workers);
+    more = total - per * workers;
+  }
+  __device__ __forceinline__ static long long div_small(long long x, long long y) {  // x >= 0, y > 0
+    return ((unsigned long long)x | (unsigned long long)y) >> 32 == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+  }
+  __device__ __forceinline__ long long start(int w) const { return w * per + min((long long)w, more); }
+  __device__ __forceinline__ int worker(long long x) const {  // the one that holds tile x
+    const long long big = more * (per + 1);
+    return (int)(x < big ? div_small(x, per + 1) : more + div_small(x - big, per));
+  }
+};
 
 // Where each worker of this CTA starts.  Every thread of the CTA calls it.
 template <int TT>
@@ -132,7 +147,7 @@ __device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& w
   const int each = (a.R + nthr - 1) / nthr, r0 = min(tid * each, a.R), r1 = min(r0 + each, a.R);
   uint32_t bad = 0u;
   long long mine = 0;
-  int n, len, nn;
+  int n = 0, len = 0, nn = 0;
   for (int r = r0; r < r1; ++r) {
     request_of(a, r, &n, &len, &nn, &bad);
     mine += tiles_of<TT>(n, nn);
@@ -151,27 +166,35 @@ __device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& w
     total += s->scan[w];
   }
   base += incl - mine;
-  const long long W = total * ws.items;
-  const int workers = (int)gridDim.x * ws.groups;
+  const Shares sh(total * ws.items, (int)gridDim.x * ws.groups);
+  if (a.R <= kWindow) {  // the requests fit a round's window: looked at once, here
+    if (tid < a.R) {
+      for (int g = 0; g < 2; ++g) {
+        s->wn[g][tid] = n;
+        s->wlen[g][tid] = len;
+        s->wnn[g][tid] = (short)nn;
+      }
+    }
+  }
   if (blockIdx.x == 0) {
     report(a.kv.err, bad);
     long long run = base;
     for (int r = r0; r < r1; ++r) {
       ws.prefix[r] = run;
-      request_of(a, r, &n, &len, &nn, &bad);
+      if (each > 1) request_of(a, r, &n, &len, &nn, &bad);
       run += tiles_of<TT>(n, nn);
     }
     if (tid == 0) ws.prefix[a.R] = total;
   }
   for (int g = 0; g < 2; ++g) {
     const int w = g * (int)gridDim.x + (int)blockIdx.x;
-    const long long s0 = g < ws.groups ? split_at(W, w, workers) : 0, s1 = g < ws.groups ? split_at(W, w + 1, workers) : 0;
+    const long long s0 = g < ws.groups ? sh.start(w) : 0, s1 = g < ws.groups ? sh.start(w + 1) : 0;
     if (tid == 0) s->left[g] = s1 - s0;
     if (s1 > s0 && s0 >= base * ws.items && s0 < (base + mine) * ws.items) {  // true in one thread
       long long off = s0 - base * ws.items;
       int r = r0;
       for (; r < r1; ++r) {
-        request_of(a, r, &n, &len, &nn, &bad);
+        if (each > 1) request_of(a, r, &n, &len, &nn, &bad);
         const long long all = tiles_of<TT>(n, nn) * ws.items;
         if (off < all) break;
         off -= all;
@@ -188,7 +211,8 @@ template <int TT>
 __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
   if (s->left[0] <= 0 && s->left[1] <= 0) return false;  // the same in every thread: written before a barrier
   const int tid = threadIdx.x;
-  if (tid < 2 * kWindow) {
+  const bool all = a.R <= kWindow;  // then the window starts at request 0 and is there already
+  if (!all && tid < 2 * kWindow) {
     const int g = tid / kWindow, i = tid - g * kWindow;
     if (s->left[g] > 0 && s->cur[g] + i < a.R) {
       uint32_t bad = 0u;
@@ -200,11 +224,11 @@ __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& w
     }
   }
   __syncthreads();
-  if (tid == 0 || tid == 32) {
+  if ((tid == 0 || tid == 32) && s->left[tid >> 5] > 0) {
     const int g = tid >> 5;
     long long left = s->left[g], off = s->off[g];
-    int np = 0, i = 0;
-    const int cur = s->cur[g];
+    int np = 0, i = all ? s->cur[g] : 0;
+    const int cur = all ? 0 : s->cur[g];
     while (left > 0 && np < kPortions && i < kWindow && cur + i < a.R) {
       const int n = s->wn[g][i], nn = s->wnn[g][i];
       const long long T = tiles_of<TT>(n, nn);
@@ -215,7 +239,7 @@ __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& w
       }
       Portion p;
       p.r = cur + i;
-      p.item = (int)(off / T);
+      p.item = (int)Shares::div_small(off, T);
       p.t0 = (int)(off - p.item * T);
       p.t1 = (int)min(T, p.t0 + left);
       p.n = n;
@@ -226,9 +250,11 @@ __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& w
       off += p.t1 - p.t0;
     }
     s->nport[g] = np;
-    s->left[g] = cur + i < a.R ? left : 0;
+    s->left[g] = cur + i < a.R ? left : 0;  // lengths that change under the call must not keep it going
     s->off[g] = off;
     s->cur[g] = cur + i;
+  } else if (tid == 0 || tid == 32) {
+    s->nport[tid >> 5] = 0;
   }
   __syncthreads();
   return true;
@@ -262,10 +288,11 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = DV / 64;  // float2 per lane
   const int item = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
-  const long long p0 = c.ws.prefix[r], T = c.ws.prefix[r + 1] - p0, W = c.ws.prefix[c.R] * c.ws.items;
+  const long long p0 = c.ws.prefix[r], T = c.ws.prefix[r + 1] - p0;
   if (T == 0) return;
+  const Shares sh(c.ws.prefix[c.R] * c.ws.items, c.workers);
   const long long a = p0 * c.ws.items + item * T;
-  const int wf = (int)(((a + 1) * c.workers - 1) / W), wl = (int)(((a + T) * c.workers - 1) / W);
+  const int wf = sh.worker(a), wl = sh.worker(a + T - 1);
   if (wf == wl) return;
   const int row = blockIdx.z * 8 + (threadIdx.x >> 5), x = row & 127;
   const int slice = item % c.nslice, hp = item / c.nslice, h = hp / c.np, mt = (hp % c.np) * c.per + (row >> 7);
@@ -274,10 +301,9 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
   if (row >= c.ws.rows || x >= c.G * c.MT || t >= nn) return;
   auto slot_row = [&](int w) { return ((long long)w * 2 + (w == wf ? 1 : 0)) * c.ws.rows + row; };
-  auto empty = [&](int w) { return W < c.workers && split_at(W, w, c.workers) == split_at(W, w + 1, c.workers); };
   float M = -INFINITY;
   for (int w = wf + lane; w <= wl; w += 32)
-    if (!empty(w)) M = fmaxf(M, c.ws.ml[slot_row(w) * 2]);
+    M = fmaxf(M, c.ws.ml[slot_row(w) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float2 acc[V];
@@ -286,13 +312,14 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   float L = 0.f;
   for (int w0 = wf; w0 <= wl; w0 += 32) {
     float wt = 0.f, lw = 0.f;
-    if (w0 + lane <= wl && !empty(w0 + lane)) {
+    if (w0 + lane <= wl) {
       const float2 ml = *(const float2*)(c.ws.ml + slot_row(w0 + lane) * 2);
       // nothing seen: no part in the result; NaN scores alone: NaN
       wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2f(ml.x - M);
       lw = wt * ml.y;
     }
     const int cnt = min(32, wl - w0 + 1);
+#pragma unroll 4
     for (int i = 0; i < cnt; ++i) {
       const float wi = __shfl_sync(0xffffffffu, wt, i);
       L += __shfl_sync(0xffffffffu, lw, i);
@@ -322,5 +349,4 @@ struct hs_tree_plan {
   int64_t workspace;
 };
 hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms);
-int hs_tree_gqa_launch(const hs_config* c, const hs_tree_args* g, const void* tree_args, const hs_tree_pool_rows* pool,
-                       int num_sms, cudaStream_t st);
+int hs_tree_gqa_launch(const hs_config* c, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st);

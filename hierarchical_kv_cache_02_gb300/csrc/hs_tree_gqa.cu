@@ -7,8 +7,9 @@
 //   one tile of rows (T <= MT): each group is a worker of its own with its own share of the entries, so
 //     that one group's softmax runs beside the other's products;
 //   more rows: the groups take two tiles of rows over the same entries, which are loaded once for both.
-// Records are gathered by TMA (four rows of 64 values an instruction, 128-byte swizzled; 16 or 32 rows when a
-// dense context's pages allow) into a ring of K and V tiles, four producer warps a tile.
+// Four producer warps fill a ring of K and V tiles (128-byte swizzled): a dense context in boxes of 16 or 32 rows
+// by TMA where its pages allow, everything else row by row in 16-byte copies (TMA's gather of four rows measured
+// slower: its instructions leave a warp one lane at a time, 75 ns each).
 // Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
 // of one tile of rows 0.54 us at the tensor cores' rate.
 #include <cuda_runtime.h>
@@ -44,9 +45,8 @@ struct TcArgs {
   int G, MT, np, shared;   // np: row tiles (shared: pairs of them) of a KV head
   int nmt;                 // row tiles of a KV head
   int seg;                 // dense contexts whose pages hold multiples of it: rows per box (32 or 16), else 0
-  int ctx_rows, draft_rows;  // extents of the record maps: a row index there reads zeros
-  const uint8_t* pool_base;  // pool form: its buffer pages are rows of one array
-  int64_t pool_page_bytes, pool_page_slots;
+  int negate;              // the scale is negative: qscale is its magnitude, the scores' products are negated
+  int ctx_rows;            // rows of the cache: a box that starts there reads zeros
 };
 
 struct Control {
@@ -80,8 +80,7 @@ __device__ __forceinline__ uint32_t good_pair(uint32_t w) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tree_gqa(const TcArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap ctxmap,
-               const __grid_constant__ CUtensorMap segmap, const __grid_constant__ CUtensorMap draftmap) {
+    k_tree_gqa(const TcArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap) {
   using C = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Control ct;
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort = &ct.abort;
   if (tid == 0) {
     for (int i = 0; i < C::kRing; ++i) {
-      mbar_init(&ct.full[i], kProducers);
+      mbar_init(&ct.full[i], kProducers * 32);
       mbar_init(&ct.empty[i], 1u);
     }
     for (int g = 0; g < 2; ++g) {
@@ -111,6 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ct.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kWarpProd && lane == 0) {
+    prefetch_map(&qmap);
+    if (c.seg != 0) prefetch_map(&segmap);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the only kernel that may start early is this call's own combine, which waits for this one
@@ -139,80 +142,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto present = [&](int g, const Portion& p) { return !c.shared || 2 * (p.item % c.np) + g < c.nmt; };
 
     if (warp >= kWarpProd) {
-      // ---------------- producers: a quarter of every tile each ----------------
-      const int pw = warp - kWarpProd, ch = lane >> 3, i4 = lane & 7;
+      // ---------------- producers: 32 entries of every tile each ----------------
+      // Lane y looks up entry y of the warp's 32 in three steps, each a tile ahead of the next, so that the
+      // latencies of the list and of the page table stay out of the way: A the position (a list entry), B the
+      // page, C the record.
+      const int pw = warp - kWarpProd, crow = lane >> 3, cch = lane & 7;
+      // what an entry is: 0 nothing, 1 context, 2 a node in the cache, 3 a node among the drafts
+      struct Look {
+        int kind, r, p;
+        uint64_t page;
+      };
+      Look la[2], lb[2];
+      int ap[2] = {0, 0}, at[2] = {0, 0}, now_row[2];
+      uint64_t now[2];
+      auto look_a = [&](int g) {  // the list's position
+        Look& l = la[g];
+        l.kind = 0;
+        if (ap[g] >= count[g]) return;
+        const Portion& P = list[g][ap[g]];
+        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u), e = at[g] * kTile + 32 * pw + lane;
+        l.r = P.r;
+        if (e < P.n) {
+          l.kind = 1;
+          l.p = a.locs != nullptr ? a.locs[(int64_t)P.r * a.k + e] : e;
+        } else if (e >= n4 && e - n4 < P.nn) {
+          l.kind = a.draft != nullptr ? 3 : 2;
+          l.p = a.draft != nullptr ? e - n4 : P.len + (e - n4);
+        }
+        if (++at[g] == P.t1) {
+          ++ap[g];
+          if (ap[g] < count[g]) at[g] = list[g][ap[g]].t0;
+        }
+      };
+      auto look_b = [&](int g) {  // its page; p becomes the place in the page
+        Look& l = lb[g];
+        l = la[g];
+        if (l.kind == 0 || l.kind == 3) return;
+        if (l.kind == 1 && a.locs != nullptr && l.p == -1) {
+          l.kind = 0;
+        } else if (a.slot_pt != nullptr) {
+          if (l.p < 0 || l.p >= a.slot_cap[l.r]) {
+            bad |= (uint32_t)HS_DEVERR_LOC;
+            l.kind = 0;
+          } else {
+            l.page = a.slot_pt[(int64_t)l.r * a.slot_pages + (l.p >> a.slot_shift)];
+            l.p &= (1 << a.slot_shift) - 1;
+          }
+        } else if (l.p < 0 || l.p >= a.kv.max_pages * a.kv.page_tokens) {
+          bad |= (uint32_t)HS_DEVERR_LOC;
+          l.kind = 0;
+        } else {
+          const unsigned pg = (unsigned)l.p / (unsigned)a.kv.page_tokens;
+          l.p -= (int)(pg * (unsigned)a.kv.page_tokens);
+          l.page = a.kv.table != nullptr ? (uint64_t)(int64_t)a.kv.table[(int64_t)l.r * a.kv.max_pages + pg]
+                                         : (uint64_t)((int64_t)l.r * a.kv.max_pages + pg);
+        }
+      };
+      auto look_c = [&](int g) {  // the record's address (0: none); its row in the cache for the boxes
+        const Look& l = lb[g];
+        now[g] = 0ull;
+        now_row[g] = c.ctx_rows;
+        if (l.kind == 0) return;
+        if (l.kind == 3) {
+          now[g] = (uint64_t)(uintptr_t)a.draft + (uint64_t)((int64_t)l.r * a.T + l.p) * (uint64_t)a.kv.rec;
+        } else if (a.slot_pt != nullptr) {
+          now[g] = l.page + (uint64_t)l.p * (uint64_t)a.kv.rec;
+        } else if (l.page < (uint64_t)a.kv.num_pages) {
+          now_row[g] = (int)l.page * a.kv.page_tokens + l.p;
+          now[g] = (uint64_t)(uintptr_t)a.kv.base + (uint64_t)now_row[g] * (uint64_t)a.kv.rec;
+        } else {
+          bad |= (uint32_t)HS_DEVERR_PAGE;
+        }
+      };
       auto load = [&](const Portion& P, int tile, bool val, int g) {
         const int slot = seq % C::kRing;
-        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
-        const int e0 = tile * kTile + 32 * pw, e = e0 + 4 * i4;
-        const int h = P.item / c.np;
-        const bool boxed = c.seg != 0 && e0 + 32 <= P.n;
-        int row[4];
-        uint32_t ok4 = 0u;
-        bool draft = false;
-        if (boxed) {
-          // one lane per box: lanes 0 .. 32 / seg - 1 of each column block
-          const int b = i4 * c.seg;
-          row[0] = c.ctx_rows;
-          if (b < 32) {
-            const int64_t x = paged_row(a.kv, P.r, e0 + b, (uint32_t)HS_DEVERR_LOC, &bad);
-            if (x >= 0) {
-              row[0] = (int)x;
-              ok4 = (c.seg == 32 ? 0xffffffffu : 0xffffu) << b;
-            }
-          }
-        } else {
-          draft = e >= n4;
-          const int oob = draft ? c.draft_rows : c.ctx_rows;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            int64_t y = -1;
-            if (draft) {
-              const int j = e - n4 + x;
-              if (j < P.nn)
-                y = a.draft != nullptr ? (int64_t)P.r * a.T + j
-                                       : paged_row(a.kv, P.r, (int64_t)P.len + j, (uint32_t)HS_DEVERR_LOC, &bad);
-            } else if (e + x < P.n) {
-              int64_t p = e + x;
-              if (a.locs != nullptr) p = a.locs[(int64_t)P.r * a.k + p];
-              if (a.locs != nullptr && p == -1) {
-              } else if (a.slot_pt != nullptr) {
-                if (p < 0 || p >= a.slot_cap[P.r]) {
-                  bad |= (uint32_t)HS_DEVERR_LOC;
-                } else {
-                  const uint64_t page = a.slot_pt[(int64_t)P.r * a.slot_pages + (p >> a.slot_shift)];
-                  y = (int64_t)((page - (uint64_t)(uintptr_t)c.pool_base) / (uint64_t)c.pool_page_bytes) * c.pool_page_slots +
-                      (p & ((1 << a.slot_shift) - 1));
-                }
-              } else {
-                y = paged_row(a.kv, P.r, p, (uint32_t)HS_DEVERR_LOC, &bad);
-              }
-            }
-            row[x] = y >= 0 ? (int)y : oob;
-            if (y >= 0) ok4 |= 1u << (4 * i4 + x);
-          }
+        const bool boxed = c.seg != 0 && tile * kTile + 32 * pw + 32 <= P.n;
+        if (!val) {
+          look_c(g);
+          look_b(g);
+          look_a(g);
         }
         if (ok && seq >= C::kRing) ok = warp_wait(&ct.empty[slot], (uint32_t)((seq / C::kRing - 1) & 1), abort);
         if (ok) {
-          if (lane == 0) mbar_arrive_expect_tx(&ct.full[slot], (uint32_t)(32 * D * 2));
-          __syncwarp();
-          const int x0 = h * a.kstride + (val ? a.voff : 0) + 64 * ch;
-          const uint32_t dst = ring_u + (uint32_t)(slot * C::kSlot + ch * C::kBlk + 32 * pw * 128);
-          if (ch < C::kCh) {
-            if (boxed) {
-              if (i4 * c.seg < 32)
-                tma_load_2d(dst + (uint32_t)(i4 * c.seg * 128), &segmap, x0, row[0], &ct.full[slot]);
-            } else {
-              tma_gather4(dst + (uint32_t)(4 * i4 * 128), draft ? &draftmap : &ctxmap, x0, row, &ct.full[slot]);
+          const int x0 = P.item / c.np * a.kstride + (val ? a.voff : 0);
+          const uint32_t dst = ring_u + (uint32_t)(slot * C::kSlot + 32 * pw * 128);
+          if (boxed) {
+            if (lane == 0) mbar_arrive_expect_tx(&ct.full[slot], (uint32_t)(32 * D * 2));
+            else mbar_arrive(&ct.full[slot]);
+            const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row[g], (box * c.seg) & 31);
+            if (box * c.seg < 32 && (lane & 3) < C::kCh)
+              tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + 64 * (lane & 3), row,
+                          &ct.full[slot]);
+          } else {
+            // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 4 * i + crow;
+              const uint64_t src = __shfl_sync(0xffffffffu, now[g], row);
+              const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4));
+#pragma unroll
+              for (int b = 0; b < C::kCh; ++b)
+                cp_async16_zfill(to + b * C::kBlk, (const void*)(uintptr_t)(src != 0ull ? src + 2 * (x0 + 64 * b) + 16 * cch : (uint64_t)(uintptr_t)a.q),
+                                 src != 0ull ? 16u : 0u);
             }
+            cp_async_arrive_noinc(&ct.full[slot]);
           }
           sent = seq + 1;
           if (!val) {
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) ok4 |= __shfl_xor_sync(0xffffffffu, ok4, o);
+            const uint32_t word = __ballot_sync(0xffffffffu, now[g] != 0ull);
             const int m = tiles[g] % kMaskRing;
             if (lane == 0) {
-              ct.valid[g][m][pw] = ok4;
+              ct.valid[g][m][pw] = word;
               mbar_arrive(&ct.mask[g][m]);
             }
           }
@@ -222,7 +262,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // the order of the products below
       int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
-      for (int g = 0; g < ng; ++g) kt[g] = vt[g] = count[g] > 0 ? list[g][0].t0 : 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        kt[g] = vt[g] = at[g] = count[g] > 0 ? list[g][0].t0 : 0;
+        if (g < ng) look_a(g);
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g >= ng) continue;
+        look_b(g);
+        look_a(g);
+      }
       auto step = [&](int g, int (&pi)[2], int (&ti)[2], bool val) {
         load(list[g][pi[g]], ti[g], val, g);
         if (++ti[g] == list[g][pi[g]].t1) {
@@ -230,12 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pi[g] < count[g]) ti[g] = list[g][pi[g]].t0;
         }
       };
-      for (int g = 0; g < ng; ++g)
-        if (kp[g] < count[g]) step(g, kp, kt, false);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (g < ng && kp[g] < count[g]) step(g, kp, kt, false);
       for (bool more = true; more;) {
         more = false;
-        for (int g = 0; g < ng; ++g) {
-          if (vp[g] >= count[g]) continue;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g >= ng || vp[g] >= count[g]) continue;
           more = true;
           step(g, vp, vt, true);
           if (kp[g] < count[g]) step(g, kp, kt, false);
@@ -243,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kWarpMma) {
       // ---------------- products: S_0(0), S_1(0), then O_g(i), S_g(i+1) by turns ----------------
-      const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0), id_o = umma_idesc_bf16(128, D, 0, 1);
+      const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
       const uint64_t dq0 = umma_sdesc(q_u, 16, 1024, 2), dk0 = umma_sdesc(ring_u, 16, 1024, 2);
       // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
       const uint64_t dv0 = umma_sdesc(ring_u, C::kBlk, 1024, 2);
@@ -252,6 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto take = [&]() {
         const int slot = seq % C::kRing;
         if (ok) ok = warp_wait(&ct.full[slot], (uint32_t)((seq / C::kRing) & 1), abort);
+        // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_after();
         ++seq;
         return slot;
@@ -291,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tiles[g];
       };
       int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
+#pragma unroll
       for (int g = 0; g < 2; ++g) kt[g] = vt[g] = count[g] > 0 ? list[g][0].t0 : 0;
       auto advance = [&](int g, int (&pi)[2], int (&ti)[2]) {
         if (++ti[g] == list[g][pi[g]].t1) {
@@ -309,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       do_score(1);
       for (bool more = true; more;) {
         more = false;
+#pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (vp[g] >= count[g]) continue;
           more = true;
@@ -399,9 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool d = false;
             if (ok && j0 + row >= 0 && j0 + row < P.nn) {
               const int vs = ct.vslot[g];
+#pragma unroll 1
               for (int b = both ? g : 0; b < C::kCh; b += both ? 2 : 1) {
                 uint4* vr = (uint4*)(smem + 2 * C::kSlot + vs * C::kSlot + b * C::kBlk + row * 128);
-#pragma unroll
+#pragma unroll 2
                 for (int x = 0; x < 8; ++x) {
                   uint4 u = vr[x];
                   if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
@@ -418,20 +475,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nm;
           ++nt;
           if (ok && warp_ok) {
+            // The loops stay loops: unrolled further, fetching the instructions costs more than it saves.
             float mx = -INFINITY;
 #pragma unroll 1
             for (int x = 0; x < 4; ++x) {
               float v[32];
               tmem_ld32(ts + 32u * x, v);
-              const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
-              if (full) {
+              if (!full) {
+                const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[j] * a.qscale);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, (wx >> j) & 1u ? v[j] * a.qscale : -INFINITY);
+                for (int j = 0; j < 32; ++j) v[j] = (wx >> j) & 1u ? v[j] : -INFINITY;
               }
+              float y = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
+                y = fmaxf(fmaxf(y, v[j + 2]), v[j + 3]);
+              }
+              mx = fmaxf(mx, y);
             }
+            mx *= a.qscale;  // positive: a negative scale is in the products' sign
             const bool raise = mx > m + kLazy;
             if (__any_sync(0xffffffffu, raise)) {
               const float mn = raise ? mx : m;
@@ -455,16 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 4; ++x) {
               float v[32];
               tmem_ld32(ts + 32u * x, v);
-              const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fast_exp2(fmaf(v[j], a.qscale, -base));
+              if (!full) {
+                const uint32_t wx = x == 0 ? w[0] : x == 1 ? w[1] : x == 2 ? w[2] : w[3];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = (wx >> j) & 1u ? v[j] : 0.f;
+              }
               uint32_t pk[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                float p0 = fast_exp2(fmaf(v[2 * j], a.qscale, -base)), p1 = fast_exp2(fmaf(v[2 * j + 1], a.qscale, -base));
-                if (!full) {
-                  p0 = (wx >> (2 * j)) & 1u ? p0 : 0.f;
-                  p1 = (wx >> (2 * j + 1)) & 1u ? p1 : 0.f;
-                }
-                pk[j] = pack_bf16(p0, p1);
+                pk[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
                 sum0 += lo(pk[j]);  // the rounded weights, as the product takes them
                 sum1 += hi(pk[j]);
               }
@@ -539,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
+  if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
     if (warp >= kWarpProd) {
@@ -602,13 +667,13 @@ cudaError_t allow_smem(K kern, size_t bytes, bool* done) {
 }
 
 template <int D>
-cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& ctx, const CUtensorMap& seg,
-                   const CUtensorMap& draft, const CombineArgs& cb, cudaStream_t st) {
+cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& seg, const CombineArgs& cb,
+                   cudaStream_t st) {
   static_assert(Shape<D>::kDyn + sizeof(Control) <= kSmemCap, "shared memory of a CTA");
   static bool done[64];
   cudaError_t e = allow_smem(k_tree_gqa<D>, Shape<D>::kDyn, done);
   if (e != cudaSuccess) return e;
-  e = hs_launch_pdl(k_tree_gqa<D>, dim3(sms), dim3(kThreads), Shape<D>::kDyn, st, c, q, ctx, seg, draft);
+  e = hs_launch_pdl(k_tree_gqa<D>, dim3(sms), dim3(kThreads), Shape<D>::kDyn, st, c, q, seg);
   if (e != cudaSuccess) return e;
   return hs_launch_pdl(k_tree_combine<D>, dim3(p.items, c.a.R, (p.rows + 7) / 8), dim3(256), 0, st, cb);
 }
@@ -624,8 +689,7 @@ hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms) {
   return r;
 }
 
-int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* tree_args, const hs_tree_pool_rows* pool,
-                       int num_sms, cudaStream_t st) {
+int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st) {
   Plan p;
   if (!plan_of(cfg, g->nodes, num_sms, &p)) return HS_ERR_CONFIG;
   TcArgs c{};
@@ -642,32 +706,25 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.ws.prefix = (long long*)w;
   c.ws.part = (float*)(w + (int64_t)((cfg->num_requests + 1) * sizeof(int64_t) + 15) / 16 * 16);
   c.ws.ml = c.ws.part + part_floats(p);
-  const cuuint64_t rec = (cuuint64_t)c.a.kv.rec;
-  const uint8_t* base = c.a.kv.base;
-  int64_t rows = c.a.kv.num_pages * c.a.kv.page_tokens;
-  if (pool != nullptr) {
-    base = pool->base;
-    rows = pool->rows;
-    c.pool_base = pool->base;
-    c.pool_page_bytes = pool->page_bytes;
-    c.pool_page_slots = pool->page_slots;
-  } else if (c.a.locs == nullptr) {
-    c.seg = c.a.kv.page_tokens % 32 == 0 ? 32 : (c.a.kv.page_tokens % 16 == 0 ? 16 : 0);
+  if (c.a.qscale < 0.f) {
+    c.negate = 1;
+    c.a.qscale = -c.a.qscale;
   }
-  c.ctx_rows = (int)rows;
-  c.draft_rows = pool != nullptr ? cfg->num_requests * g->nodes : (int)rows;
-  CUtensorMap qm, ctx, seg, draft;
-  const cuuint64_t size[2] = {rec / 2, (cuuint64_t)rows}, stride[1] = {rec};
-  const cuuint32_t box[2] = {64, 1}, sbox[2] = {64, (cuuint32_t)(c.seg != 0 ? c.seg : 1)};
-  const cuuint64_t dsize[2] = {rec / 2, (cuuint64_t)c.draft_rows};
+  CUtensorMap qm, seg;
+  memset(&seg, 0, sizeof(seg));
+  if (c.a.slot_pt == nullptr && c.a.locs == nullptr) {
+    const int pt = c.a.kv.page_tokens;
+    c.seg = pt % 32 == 0 ? 32 : pt % 16 == 0 ? 16 : 0;
+    c.ctx_rows = (int)(c.a.kv.num_pages * pt);
+    const cuuint64_t rec = (cuuint64_t)c.a.kv.rec, size[2] = {rec / 2, (cuuint64_t)c.ctx_rows}, stride[1] = {rec};
+    const cuuint32_t box[2] = {64, (cuuint32_t)c.seg};
+    if (c.seg != 0 && !encode(&seg, c.a.kv.base, 2, size, stride, box)) c.seg = 0;
+  }
   const cuuint64_t row = (cuuint64_t)p.D * 2;
   const cuuint64_t qsize[4] = {(cuuint64_t)p.D, (cuuint64_t)cfg->num_q_heads, (cuuint64_t)g->nodes, (cuuint64_t)cfg->num_requests};
   const cuuint64_t qstride[3] = {row, row * cfg->num_q_heads, row * cfg->num_q_heads * g->nodes};
   const cuuint32_t qbox[4] = {64, (cuuint32_t)p.G, (cuuint32_t)p.MT, 1};
-  if (!encode(&ctx, base, 2, size, stride, box) || !encode(&seg, base, 2, size, stride, sbox) ||
-      !encode(&draft, pool != nullptr ? (const void*)c.a.draft : (const void*)base, 2, dsize, stride, box) ||
-      !encode(&qm, c.a.q, 4, qsize, qstride, qbox))
-    return HS_ERR_CUDA;
+  if (!encode(&qm, c.a.q, 4, qsize, qstride, qbox)) return HS_ERR_CUDA;
   CombineArgs cb{};
   cb.nodes = c.a.nodes;
   cb.out = c.a.out;
@@ -682,7 +739,6 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   cb.per = p.shared ? 2 : 1;
   cb.np = p.np;
   cb.nslice = 1;
-  const cudaError_t e = p.D == 128 ? launch<128>(c, p, num_sms, qm, ctx, seg, draft, cb, st)
-                                   : launch<64>(c, p, num_sms, qm, ctx, seg, draft, cb, st);
+  const cudaError_t e = p.D == 128 ? launch<128>(c, p, num_sms, qm, seg, cb, st) : launch<64>(c, p, num_sms, qm, seg, cb, st);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
