@@ -119,11 +119,24 @@ __device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, ui
                "l"(a), "l"(b), "r"(id), "r"(acc)
                : "memory");
 }
-// the same with A in tensor memory (K-major: 32-bit columns of two bf16 each)
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-               "r"(a), "l"(b), "r"(id), "r"(acc)
+// The same products for operands that are all 128-byte swizzled with 1 KB between groups of 8 rows (what K-major
+// operands, and MN-major ones whose LBO is in the low word, have in common): only the low words of the
+// descriptors vary, so only these are passed.  A from shared memory, or from tensor memory (K-major: 32-bit
+// columns of two bf16 each).
+constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t umma_sdesc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void umma_bf16_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+               "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kSdescHi)
+               : "memory");
+}
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "mov.b64 y, {%2, %5};\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+               "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kSdescHi)
                : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -171,6 +184,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The same with a limit of tries instead of a time (a try suspends the thread for a while; 2^22 of them take
+// a good part of a second at the least), for kernels whose code size counts.
+__device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
 
 // bounded wait of a whole warp: lane 0 waits, the result is the warp's
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {

@@ -88,11 +88,12 @@ __device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, 
 // an item that does not hold all its tiles becomes a partial: slot 0 of the worker when the portion
 // starts inside the item, else slot 1 (a worker has at most one of each); k_tree_combine joins them.
 
-constexpr int kPortions = 14;  // portions a round of a CTA holds per worker
+constexpr int kPortions = 10;  // portions a round of a CTA holds per worker
 constexpr int kWindow = 16;    // requests a round looks at per worker
 
 struct Portion {
-  int r, item, t0, t1;  // tiles [t0, t1) of the item
+  int r, t0, t1;        // tiles [t0, t1) of an item of request r
+  int head, pair;       // the item: head * np + pair
   int n, len, nn;       // context entries, position of node 0 (negative: the nodes have none), nodes in use
 };
 
@@ -106,7 +107,7 @@ struct PlanState {  // shared memory
 };
 
 struct WorkSplit {
-  int items;             // per request
+  int items, np;         // per request; of them per KV head
   int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA
   long long* prefix;     // [R + 1] tiles (of one item) before each request, written by CTA 0
   float *part, *ml;      // [workers][2 slots][rows][dims], [workers][2][rows][2]: maximum (base 2) and sum
@@ -140,69 +141,72 @@ struct Shares {
   }
 };
 
-// Where each worker of this CTA starts.  Every thread of the CTA calls it.
+// Where each worker of this CTA starts.  Every thread of the CTA calls it.  (Here and in the kernels code
+// size counts: a CTA fetches every instruction anew, and lives for some tens of microseconds.)
 template <int TT>
 __device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   const int each = (a.R + nthr - 1) / nthr, r0 = min(tid * each, a.R), r1 = min(r0 + each, a.R);
   uint32_t bad = 0u;
-  long long mine = 0;
-  int n = 0, len = 0, nn = 0;
-  for (int r = r0; r < r1; ++r) {
-    request_of(a, r, &n, &len, &nn, &bad);
-    mine += tiles_of<TT>(n, nn);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s->scan[warp] = incl;
-  __syncthreads();
-  long long base = 0, total = 0;
-  for (int w = 0; w < (nthr >> 5); ++w) {
-    if (w == warp) base = total;
-    total += s->scan[w];
-  }
-  base += incl - mine;
-  const Shares sh(total * ws.items, (int)gridDim.x * ws.groups);
-  if (a.R <= kWindow) {  // the requests fit a round's window: looked at once, here
-    if (tid < a.R) {
-      for (int g = 0; g < 2; ++g) {
-        s->wn[g][tid] = n;
-        s->wlen[g][tid] = len;
-        s->wnn[g][tid] = (short)nn;
-      }
-    }
-  }
-  if (blockIdx.x == 0) {
-    report(a.kv.err, bad);
-    long long run = base;
+  long long mine = 0, run = 0, s0[2] = {-1, -1};
+  // the first pass counts each thread's tiles, the second finds the places among them
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int n = 0, len = 0, nn = 0;
+    long long T = mine;  // one request a thread: known from the first pass
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      ws.prefix[r] = run;
-      if (each > 1) request_of(a, r, &n, &len, &nn, &bad);
-      run += tiles_of<TT>(n, nn);
-    }
-    if (tid == 0) ws.prefix[a.R] = total;
-  }
-  for (int g = 0; g < 2; ++g) {
-    const int w = g * (int)gridDim.x + (int)blockIdx.x;
-    const long long s0 = g < ws.groups ? sh.start(w) : 0, s1 = g < ws.groups ? sh.start(w + 1) : 0;
-    if (tid == 0) s->left[g] = s1 - s0;
-    if (s1 > s0 && s0 >= base * ws.items && s0 < (base + mine) * ws.items) {  // true in one thread
-      long long off = s0 - base * ws.items;
-      int r = r0;
-      for (; r < r1; ++r) {
-        if (each > 1) request_of(a, r, &n, &len, &nn, &bad);
-        const long long all = tiles_of<TT>(n, nn) * ws.items;
-        if (off < all) break;
-        off -= all;
+      if (pass == 0 || each > 1) {
+        request_of(a, r, &n, &len, &nn, &bad);
+        T = tiles_of<TT>(n, nn);
       }
-      s->cur[g] = r;
-      s->off[g] = off;
+      if (pass == 0) {
+        mine += T;
+        if (a.R <= kWindow) {  // the requests fit a round's window: they stay there
+          s->wn[0][r] = s->wn[1][r] = n;
+          s->wlen[0][r] = s->wlen[1][r] = len;
+          s->wnn[0][r] = s->wnn[1][r] = (short)nn;
+        }
+      } else {
+        if (blockIdx.x == 0) ws.prefix[r] = run;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const long long off = s0[g] - run * ws.items;
+          if (s0[g] >= 0 && off >= 0 && off < T * ws.items) {
+            s->cur[g] = r;
+            s->off[g] = off;
+          }
+        }
+        run += T;
+      }
+    }
+    if (pass == 0) {
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s->scan[warp] = incl;
+      __syncthreads();
+      long long total = 0;
+      for (int w = 0; w < (nthr >> 5); ++w) {
+        if (w == warp) run = total;
+        total += s->scan[w];
+      }
+      run += incl - mine;
+      const Shares sh(total * ws.items, (int)gridDim.x * ws.groups);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int w = g * (int)gridDim.x + (int)blockIdx.x;
+        const long long x = sh.start(w), left = g < ws.groups ? sh.start(w + 1) - x : 0;
+        if (left > 0) s0[g] = x;
+        if (tid == 0) s->left[g] = left;
+      }
+      if (blockIdx.x == 0 && tid == 0) ws.prefix[a.R] = total;
     }
   }
+  if (blockIdx.x == 0) report(a.kv.err, bad);
   __syncthreads();
 }
 
@@ -239,8 +243,10 @@ __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& w
       }
       Portion p;
       p.r = cur + i;
-      p.item = (int)Shares::div_small(off, T);
-      p.t0 = (int)(off - p.item * T);
+      const int item = (int)Shares::div_small(off, T);
+      p.head = item / ws.np;
+      p.pair = item - p.head * ws.np;
+      p.t0 = (int)(off - item * T);
       p.t1 = (int)min(T, p.t0 + left);
       p.n = n;
       p.len = s->wlen[g][i];

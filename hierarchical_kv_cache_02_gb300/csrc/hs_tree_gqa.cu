@@ -78,6 +78,58 @@ __device__ __forceinline__ uint32_t good_pair(uint32_t w) {
   return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
 }
 
+template <typename T>
+__device__ __forceinline__ void swap_both(T& x, T& y) {
+  const T z = x;
+  x = y;
+  y = z;
+}
+__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  bool w = true;
+  if ((threadIdx.x & 31) == 0) w = mbar_wait_small(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+}
+
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// A place in a portion list, with what is needed of the portion.
+struct Cursor {
+  const Portion* list;
+  int count, p, t, t0, t1, nodes_from;  // nodes_from: the first tile that holds nodes
+  bool pairs;                           // shared: both groups take part (the last pair of row tiles may be single)
+  __device__ __forceinline__ void fetch(const TcArgs& c) {
+    if (p >= count) return;
+    const Portion& P = list[p];
+    t = t0 = P.t0;
+    t1 = P.t1;
+    nodes_from = (int)(((unsigned)P.n + 3u) & ~3u) / kTile;
+    pairs = !c.shared || 2 * P.pair + 1 < c.nmt;
+  }
+  __device__ __forceinline__ void open(const Portion* l, int n, const TcArgs& c) {
+    list = l;
+    count = n;
+    p = 0;
+    fetch(c);
+  }
+  __device__ __forceinline__ bool left() const { return p < count; }
+  __device__ __forceinline__ void next(const TcArgs& c) {
+    if (++t == t1) {
+      ++p;
+      fetch(c);
+    }
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tree_gqa(const TcArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap) {
@@ -122,24 +174,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan_start<kTile>(a, c.ws, &ct.plan);
   tc_fence_after();
   const uint32_t tb = ct.tmem;
-  // tensor memory: per group 128 columns of scores (their first 64 become the weights), then D of O
-  const uint32_t t_s[2] = {tb, tb + 128u}, t_o[2] = {tb + 256u, tb + 256u + (uint32_t)D};
+  // tensor memory: 128 columns of scores a group (their first 64 become the weights), then D of O a group
 
-  // counters that run on through the rounds, each used by one role
-  int seq = 0;                      // ring loads (producers: issued; products: consumed)
-  int tiles[2] = {0, 0};            // tiles of each group (products), or of a group's K loads (producers)
-  int nq[2] = {0, 0};               // portions of each group
-  int nt = 0, nv = 0, nm = 0;       // softmax: tiles, tiles with nodes, tiles of the mask ring
-  int sent = 0;                     // producers: ring loads issued; first softmax thread: query loads
+  // state that runs on through the rounds, each used by one role
+  Ring<C::kRing> ring;             // producers and products
+  int tiles0 = 0, tiles1 = 0;      // producers: tiles of each group loaded; products: finished
+  int portions0 = 0, portions1 = 0;  // products: portions of each group begun
+  int nt = 0, nv = 0, nm = 0;      // softmax: tiles, tiles with nodes, tiles of the mask ring
+  int sent = 0;                    // producers: ring loads issued; first softmax thread: query loads
   bool ok = true;
   uint32_t bad = 0u;
 
   while (plan_round<kTile>(a, c.ws, &ct.plan)) {
     const int ng = c.shared ? 1 : 2;  // portion lists
-    const Portion* list[2] = {ct.plan.port[0], ct.plan.port[c.shared ? 0 : 1]};
-    const int count[2] = {ct.plan.nport[0], c.shared ? ct.plan.nport[0] : ct.plan.nport[1]};
     // whether group g takes part in an item: the last pair of row tiles may be a single one
-    auto present = [&](int g, const Portion& p) { return !c.shared || 2 * (p.item % c.np) + g < c.nmt; };
+    auto present = [&](int g, const Portion& p) { return !c.shared || 2 * p.pair + g < c.nmt; };
+    auto count_of = [&](int g) { return ct.plan.nport[g < ng ? g : 0]; };
+    auto list_of = [&](int g) -> const Portion* { return ct.plan.port[g < ng ? g : 0]; };
+    // The groups take turns: the products O_g(i) then S_g(i + 1), in the first turn S_g(0) alone; the ring's loads
+    // K_g(i), V_g(i).  (Values loaded right behind their keys: the lookups and addresses serve both, and a
+    // head's key and value are neighbours in memory.)
 
     if (warp >= kWarpProd) {
       // ---------------- producers: 32 entries of every tile each ----------------
@@ -152,270 +206,271 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kind, r, p;
         uint64_t page;
       };
-      Look la[2], lb[2];
-      int ap[2] = {0, 0}, at[2] = {0, 0}, now_row[2];
-      uint64_t now[2];
-      auto look_a = [&](int g) {  // the list's position
-        Look& l = la[g];
-        l.kind = 0;
-        if (ap[g] >= count[g]) return;
-        const Portion& P = list[g][ap[g]];
-        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u), e = at[g] * kTile + 32 * pw + lane;
-        l.r = P.r;
-        if (e < P.n) {
-          l.kind = 1;
-          l.p = a.locs != nullptr ? a.locs[(int64_t)P.r * a.k + e] : e;
-        } else if (e >= n4 && e - n4 < P.nn) {
-          l.kind = a.draft != nullptr ? 3 : 2;
-          l.p = a.draft != nullptr ? e - n4 : P.len + (e - n4);
-        }
-        if (++at[g] == P.t1) {
-          ++ap[g];
-          if (ap[g] < count[g]) at[g] = list[g][ap[g]].t0;
-        }
+      struct Ahead {
+        Look la, lb;
+        int ap, at, row;  // cursor of step A; the record's row, for the boxes
+        uint64_t now;     // the record's address, 0: none
+        bool begun;
       };
-      auto look_b = [&](int g) {  // its page; p becomes the place in the page
-        Look& l = lb[g];
-        l = la[g];
-        if (l.kind == 0 || l.kind == 3) return;
-        if (l.kind == 1 && a.locs != nullptr && l.p == -1) {
-          l.kind = 0;
-        } else if (a.slot_pt != nullptr) {
-          if (l.p < 0 || l.p >= a.slot_cap[l.r]) {
+      Ahead ahead0 = {}, ahead1 = {};  // two variables, never exchanged: a move would wait for a load on its way
+      Cursor k0, k1;
+      k0.open(list_of(0), count_of(0), c);
+      k1.open(list_of(1), ng > 1 ? count_of(1) : 0, c);
+      ahead0.at = k0.t;
+      ahead1.at = k1.t;
+      auto look = [&](Ahead& mine) {
+        {  // C
+          const Look& l = mine.lb;
+          mine.now = 0ull;
+          mine.row = c.ctx_rows;
+          if (l.kind == 3) {
+            mine.now = (uint64_t)(uintptr_t)a.draft + (uint64_t)((int64_t)l.r * a.T + l.p) * (uint64_t)a.kv.rec;
+          } else if (l.kind != 0 && a.slot_pt != nullptr) {
+            mine.now = l.page + (uint64_t)l.p * (uint64_t)a.kv.rec;
+          } else if (l.kind != 0 && l.page < (uint64_t)a.kv.num_pages) {
+            mine.row = (int)l.page * a.kv.page_tokens + l.p;
+            mine.now = (uint64_t)(uintptr_t)a.kv.base + (uint64_t)mine.row * (uint64_t)a.kv.rec;
+          } else if (l.kind != 0) {
+            bad |= (uint32_t)HS_DEVERR_PAGE;
+          }
+        }
+        {  // B; p becomes the place in the page
+          Look& l = mine.lb;
+          l = mine.la;
+          const int most = a.slot_pt != nullptr ? (l.kind == 1 ? a.slot_cap[l.r] : 0) : a.kv.max_pages * a.kv.page_tokens;
+          if (l.kind == 1 && a.locs != nullptr && l.p == -1) l.kind = 0;
+          if ((l.kind == 1 || l.kind == 2) && (unsigned)l.p >= (unsigned)most) {
             bad |= (uint32_t)HS_DEVERR_LOC;
             l.kind = 0;
-          } else {
-            l.page = a.slot_pt[(int64_t)l.r * a.slot_pages + (l.p >> a.slot_shift)];
-            l.p &= (1 << a.slot_shift) - 1;
           }
-        } else if (l.p < 0 || l.p >= a.kv.max_pages * a.kv.page_tokens) {
-          bad |= (uint32_t)HS_DEVERR_LOC;
+          if (l.kind == 1 || l.kind == 2) {
+            if (a.slot_pt != nullptr) {
+              l.page = a.slot_pt[(int64_t)l.r * a.slot_pages + (l.p >> a.slot_shift)];
+              l.p &= (1 << a.slot_shift) - 1;
+            } else {
+              const unsigned pg = (unsigned)l.p / (unsigned)a.kv.page_tokens;
+              l.p -= (int)(pg * (unsigned)a.kv.page_tokens);
+              l.page = a.kv.table != nullptr ? (uint64_t)(int64_t)a.kv.table[(int64_t)l.r * a.kv.max_pages + pg]
+                                             : (uint64_t)((int64_t)l.r * a.kv.max_pages + pg);
+            }
+          }
+        }
+        {  // A
+          Look& l = mine.la;
           l.kind = 0;
-        } else {
-          const unsigned pg = (unsigned)l.p / (unsigned)a.kv.page_tokens;
-          l.p -= (int)(pg * (unsigned)a.kv.page_tokens);
-          l.page = a.kv.table != nullptr ? (uint64_t)(int64_t)a.kv.table[(int64_t)l.r * a.kv.max_pages + pg]
-                                         : (uint64_t)((int64_t)l.r * a.kv.max_pages + pg);
+          l.r = 0;
+          if (mine.ap < k0.count) {
+            const Portion& P = k0.list[mine.ap];
+            const int n4 = (int)(((unsigned)P.n + 3u) & ~3u), e = mine.at * kTile + 32 * pw + lane;
+            l.r = P.r;
+            if (e < P.n) {
+              l.kind = 1;
+              l.p = a.locs != nullptr ? a.locs[(int64_t)P.r * a.k + e] : e;
+            } else if (e >= n4 && e - n4 < P.nn) {
+              l.kind = a.draft != nullptr ? 3 : 2;
+              l.p = a.draft != nullptr ? e - n4 : P.len + (e - n4);
+            }
+            if (++mine.at == P.t1) {
+              ++mine.ap;
+              if (mine.ap < k0.count) mine.at = k0.list[mine.ap].t0;
+            }
+          }
         }
       };
-      auto look_c = [&](int g) {  // the record's address (0: none); its row in the cache for the boxes
-        const Look& l = lb[g];
-        now[g] = 0ull;
-        now_row[g] = c.ctx_rows;
-        if (l.kind == 0) return;
-        if (l.kind == 3) {
-          now[g] = (uint64_t)(uintptr_t)a.draft + (uint64_t)((int64_t)l.r * a.T + l.p) * (uint64_t)a.kv.rec;
-        } else if (a.slot_pt != nullptr) {
-          now[g] = l.page + (uint64_t)l.p * (uint64_t)a.kv.rec;
-        } else if (l.page < (uint64_t)a.kv.num_pages) {
-          now_row[g] = (int)l.page * a.kv.page_tokens + l.p;
-          now[g] = (uint64_t)(uintptr_t)a.kv.base + (uint64_t)now_row[g] * (uint64_t)a.kv.rec;
-        } else {
-          bad |= (uint32_t)HS_DEVERR_PAGE;
-        }
-      };
-      auto load = [&](const Portion& P, int tile, bool val, int g) {
-        const int slot = seq % C::kRing;
-        const bool boxed = c.seg != 0 && tile * kTile + 32 * pw + 32 <= P.n;
-        if (!val) {
-          look_c(g);
-          look_b(g);
-          look_a(g);
-        }
-        if (ok && seq >= C::kRing) ok = warp_wait(&ct.empty[slot], (uint32_t)((seq / C::kRing - 1) & 1), abort);
-        if (ok) {
-          const int x0 = P.item / c.np * a.kstride + (val ? a.voff : 0);
-          const uint32_t dst = ring_u + (uint32_t)(slot * C::kSlot + 32 * pw * 128);
-          if (boxed) {
-            if (lane == 0) mbar_arrive_expect_tx(&ct.full[slot], (uint32_t)(32 * D * 2));
-            else mbar_arrive(&ct.full[slot]);
-            const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row[g], (box * c.seg) & 31);
-            if (box * c.seg < 32 && (lane & 3) < C::kCh)
-              tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + 64 * (lane & 3), row,
-                          &ct.full[slot]);
+      // one tile a turn, the groups by turns: k0 is the group at hand, exchanged with the other after its turn
+      int g = 0;
+      for (int idle = 0; idle < ng;) {
+        ++idle;
+        if (k0.left()) {
+          idle = 0;
+          const Portion& P = k0.list[k0.p];
+          if (g == 0) {
+#pragma unroll 1
+            for (int x = ahead0.begun ? 0 : 2; x >= 0; --x) look(ahead0);
+            ahead0.begun = true;
           } else {
-            // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = 4 * i + crow;
-              const uint64_t src = __shfl_sync(0xffffffffu, now[g], row);
-              const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4));
-#pragma unroll
-              for (int b = 0; b < C::kCh; ++b)
-                cp_async16_zfill(to + b * C::kBlk, (const void*)(uintptr_t)(src != 0ull ? src + 2 * (x0 + 64 * b) + 16 * cch : (uint64_t)(uintptr_t)a.q),
-                                 src != 0ull ? 16u : 0u);
-            }
-            cp_async_arrive_noinc(&ct.full[slot]);
+#pragma unroll 1
+            for (int x = ahead1.begun ? 0 : 2; x >= 0; --x) look(ahead1);
+            ahead1.begun = true;
           }
-          sent = seq + 1;
-          if (!val) {
-            const uint32_t word = __ballot_sync(0xffffffffu, now[g] != 0ull);
-            const int m = tiles[g] % kMaskRing;
-            if (lane == 0) {
-              ct.valid[g][m][pw] = word;
-              mbar_arrive(&ct.mask[g][m]);
+          const uint64_t now = g == 0 ? ahead0.now : ahead1.now;
+          const int now_row = g == 0 ? ahead0.row : ahead1.row;
+          const bool boxed = c.seg != 0 && k0.t * kTile + 32 * pw + 32 <= P.n;
+          const int x0 = P.head * a.kstride;
+#pragma unroll 1
+          for (int val = 0; val < 2; ++val) {
+            if (ok) ok = warp_wait_small(&ct.empty[ring.slot], ring.phase ^ 1u, abort);
+            if (ok) {
+              const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 32 * pw * 128);
+              uint64_t* full = &ct.full[ring.slot];
+              if (boxed) {
+                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(32 * D * 2));
+                else mbar_arrive(full);
+                const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row, (box * c.seg) & 31);
+                if (box * c.seg < 32 && (lane & 3) < C::kCh)
+                  tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + val * D + 64 * (lane & 3),
+                              row, full);
+              } else {
+                // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
+                const int off = 2 * (x0 + val * D) + 16 * cch;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int row = 4 * i + crow;
+                  const uint64_t src = __shfl_sync(0xffffffffu, now, row);
+                  const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+                  const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + off : (const uint8_t*)a.q;
+#pragma unroll
+                  for (int b = 0; b < C::kCh; ++b) cp_async16_zfill(to + b * C::kBlk, src != 0ull ? from + 128 * b : from, n);
+                }
+                cp_async_arrive_noinc(full);
+              }
+              ++sent;
             }
+            ring.next();
           }
+          const uint32_t word = __ballot_sync(0xffffffffu, now != 0ull);
+          int& n = g == 0 ? tiles0 : tiles1;
+          if (ok && lane == 0) {
+            ct.valid[g][n % kMaskRing][pw] = word;
+            mbar_arrive(&ct.mask[g][n % kMaskRing]);
+          }
+          ++n;
+          k0.next(c);
         }
-        if (!val) ++tiles[g];
-        ++seq;
-      };
-      // the order of the products below
-      int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        kt[g] = vt[g] = at[g] = count[g] > 0 ? list[g][0].t0 : 0;
-        if (g < ng) look_a(g);
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g >= ng) continue;
-        look_b(g);
-        look_a(g);
-      }
-      auto step = [&](int g, int (&pi)[2], int (&ti)[2], bool val) {
-        load(list[g][pi[g]], ti[g], val, g);
-        if (++ti[g] == list[g][pi[g]].t1) {
-          ++pi[g];
-          if (pi[g] < count[g]) ti[g] = list[g][pi[g]].t0;
-        }
-      };
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (g < ng && kp[g] < count[g]) step(g, kp, kt, false);
-      for (bool more = true; more;) {
-        more = false;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (g >= ng || vp[g] >= count[g]) continue;
-          more = true;
-          step(g, vp, vt, true);
-          if (kp[g] < count[g]) step(g, kp, kt, false);
+        if (ng > 1) {
+          swap_both(k0, k1);
+          g ^= 1;
         }
       }
     } else if (warp == kWarpMma) {
-      // ---------------- products: S_0(0), S_1(0), then O_g(i), S_g(i+1) by turns ----------------
-      const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
-      const uint64_t dq0 = umma_sdesc(q_u, 16, 1024, 2), dk0 = umma_sdesc(ring_u, 16, 1024, 2);
-      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
-      const uint64_t dv0 = umma_sdesc(ring_u, C::kBlk, 1024, 2);
-      constexpr uint64_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
-      int kslot = 0, vslot = 0;  // shared: the slots both groups use
-      auto take = [&]() {
-        const int slot = seq % C::kRing;
-        if (ok) ok = warp_wait(&ct.full[slot], (uint32_t)((seq / C::kRing) & 1), abort);
-        // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        tc_fence_after();
-        ++seq;
-        return slot;
-      };
-      auto score = [&](int g, const Portion& P, int tile, bool last_user) {
-        if (tile == P.t0) {  // this portion's queries
-          if (ok) ok = warp_wait(&ct.qfull[g], (uint32_t)(nq[g] & 1), abort);
-          ++nq[g];
-        }
-        // the weights of the tile before share these columns: their product has to be complete
-        if (ok && tiles[g] > 0) ok = warp_wait(&ct.pv[g], (uint32_t)((tiles[g] - 1) & 1), abort);
-        tc_fence_after();
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int b = 0; b < C::kCh; ++b)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_bf16(t_s[g], dq0 + (uint64_t)g * kSlotStep + b * kBlkStep + 2 * ks,
-                        dk0 + (uint64_t)kslot * kSlotStep + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
-          umma_commit(&ct.s[g]);
-          if (last_user) umma_commit(&ct.empty[kslot]);
-        }
-        __syncwarp();
-      };
-      auto value = [&](int g, const Portion& P, int tile, bool last_user) {
-        if (ok) ok = warp_wait(&ct.p[g], (uint32_t)(tiles[g] & 1), abort);
-        tc_fence_after();
-        if (ok && elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_bf16_ta(t_o[g], t_s[g] + 8u * ks, dv0 + (uint64_t)vslot * kSlotStep + 128 * ks, id_o,
-                         (tile != P.t0 || ks != 0) ? 1u : 0u);
-          umma_commit(&ct.pv[g]);
-          if (last_user) umma_commit(&ct.empty[vslot]);
-        }
-        __syncwarp();
-        ++tiles[g];
-      };
-      int kp[2] = {0, 0}, kt[2], vp[2] = {0, 0}, vt[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) kt[g] = vt[g] = count[g] > 0 ? list[g][0].t0 : 0;
-      auto advance = [&](int g, int (&pi)[2], int (&ti)[2]) {
-        if (++ti[g] == list[g][pi[g]].t1) {
-          ++pi[g];
-          if (pi[g] < count[g]) ti[g] = list[g][pi[g]].t0;
-        }
-      };
-      auto do_score = [&](int g) {
-        if (kp[g] >= count[g]) return;
-        const Portion& P = list[g][kp[g]];
-        if (!c.shared || g == 0) kslot = take();
-        if (present(g, P)) score(g, P, kt[g], !c.shared || g == 1 || !present(1, P));
-        advance(g, kp, kt);
-      };
-      do_score(0);
-      do_score(1);
-      for (bool more = true; more;) {
-        more = false;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (vp[g] >= count[g]) continue;
-          more = true;
-          const Portion& P = list[g][vp[g]];
-          if (!c.shared || g == 0) {
-            vslot = take();
-            // nodes among the entries: the softmax looks at their values first (both groups together, so
-            // both are told before the first one's weights are waited for)
-            if (lane == 0 && (vt[g] + 1) * (long long)kTile > (long long)(((unsigned)P.n + 3u) & ~3u)) {
-              for (int x = g; x < (c.shared ? 2 : g + 1); ++x) {
-                if (!present(x, P)) continue;
-                ct.vslot[x] = vslot;
-                mbar_arrive(&ct.v[x]);
+      // ---------------- products: one thread, so that nothing waits for a warp's agreement ----------------
+      if (lane == 0) {
+        const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
+        const uint32_t dq0 = umma_sdesc_lo(q_u, 16), dk0 = umma_sdesc_lo(ring_u, 16);
+        // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
+        const uint32_t dv0 = umma_sdesc_lo(ring_u, C::kBlk);
+        constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
+        auto land = [&](const Ring<C::kRing>& at) {
+          if (ok) ok = mbar_wait_small(&ct.full[at.slot], at.phase, abort);
+          // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        };
+        int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
+        Ring<C::kRing> v0, v1;  // where the values of the tile in hand are: of the group at hand, of the other
+        Cursor k0, k1, p0, p1;  // next scores and next values of the group at hand, of the other
+        const int n0 = count_of(0), n1 = count_of(1);
+        k0.open(list_of(0), n0, c);
+        k1.open(list_of(1), n1, c);
+        p0 = k0;
+        p1 = k1;
+        int due0 = 0, due1 = 0, g = 0;  // scores done whose values are not
+        for (int idle = 0; idle < 2;) {
+          ++idle;
+          const uint32_t ts = tb + 128u * g, to = tb + 256u + (uint32_t)(D * g);
+          int done = g == 0 ? tiles0 : tiles1;  // tiles of this group finished
+          if (due0 > 0) {
+            idle = 0;
+            const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
+            if (!c.shared || g == 0) {
+              land(v0);
+              vslot = v0.slot;
+              // nodes among the entries: the softmax looks at their values first (both groups together, so
+              // both are told before the first one's weights are waited for)
+              if (p0.t >= p0.nodes_from) {
+                ct.vslot[g] = v0.slot;
+                mbar_arrive(&ct.v[g]);
+                if (c.shared && p0.pairs) {
+                  ct.vslot[1] = v0.slot;
+                  mbar_arrive(&ct.v[1]);
+                }
               }
             }
-            __syncwarp();
+            if (here) {
+              if (ok) ok = mbar_wait_small(&ct.p[g], (uint32_t)(done & 1), abort);
+              tc_fence_after();
+              if (ok) {
+                const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) umma_bf16_ta(to, ts + 8u * ks, dv + 128 * ks, id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
+                umma_commit(&ct.pv[g]);
+                if (last_user) umma_commit(&ct.empty[vslot]);
+              }
+              ++done;
+            }
+            --due0;
+            p0.next(c);
           }
-          if (present(g, P)) value(g, P, vt[g], !c.shared || g == 1 || !present(1, P));
-          advance(g, vp, vt);
-          do_score(g);
+          if (k0.left()) {
+            idle = 0;
+            const bool here = g == 0 || k0.pairs, last_user = !c.shared || g == 1 || !k0.pairs;
+            if (!c.shared || g == 0) {
+              land(ring);
+              kslot = ring.slot;
+              ring.next();
+              v0 = ring;
+              ring.next();
+            }
+            if (here) {
+              if (k0.t == k0.t0) {  // this portion's queries
+                int& q = g == 0 ? portions0 : portions1;
+                if (ok) ok = mbar_wait_small(&ct.qfull[g], (uint32_t)(q & 1), abort);
+                ++q;
+              }
+              // the weights of the tile before share these columns: their product has to be complete
+              if (ok && done > 0) ok = mbar_wait_small(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+              tc_fence_after();
+              if (ok) {
+                const uint32_t dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)kslot * kSlotStep;
+#pragma unroll
+                for (int b = 0; b < C::kCh; ++b)
+#pragma unroll
+                  for (int ks = 0; ks < 4; ++ks)
+                    umma_bf16_lo(ts, dq + b * kBlkStep + 2 * ks, dk + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
+                umma_commit(&ct.s[g]);
+                if (last_user) umma_commit(&ct.empty[kslot]);
+              }
+            }
+            ++due0;
+            k0.next(c);
+          }
+          if (g == 0) tiles0 = done;
+          else tiles1 = done;
+          swap_both(k0, k1);
+          swap_both(p0, p1);
+          swap_both(due0, due1);
+          swap_both(v0, v1);
+          g ^= 1;
         }
       }
+      __syncwarp();
     } else {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
       const int g = warp >> 2, row = tid & 127;
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t ts = t_s[g] + lane_base, to = t_o[g] + lane_base;
+      const uint32_t ts = tb + 128u * g + lane_base, to = tb + 256u + (uint32_t)(D * g) + lane_base;
       const int lt = row / c.G, hq = row - lt * c.G;
       auto load_q = [&](const Portion& P) {  // by the group's first thread
         ++sent;
         mbar_arrive_expect_tx(&ct.qfull[g], (uint32_t)(C::kCh * c.G * c.MT * 128));
-        const int h = P.item / c.np, mt = c.shared ? 2 * (P.item % c.np) + g : 0;
+        const int h = P.head, mt = c.shared ? 2 * P.pair + g : 0;
         for (int b = 0; b < C::kCh; ++b)
           tma_load_4d(q_u + (uint32_t)(g * C::kSlot + b * C::kBlk), &qmap, 64 * b, h * c.G, mt * c.MT, P.r, &ct.qfull[g]);
       };
-      auto next_present = [&](int i) {
-        while (i < count[g] && !present(g, list[g][i])) ++i;
-        return i;
+      const Portion* list = list_of(g);
+      const int count = count_of(g);
+      auto next_q = [&](int i) {  // the queries of the next portion this group takes part in
+        while (i < count && !present(g, list[i])) ++i;
+        if (i < count) load_q(list[i]);
       };
-      if (row == 0) {
-        const int i = next_present(0);
-        if (i < count[g]) load_q(list[g][i]);
-      }
-      for (int pi = 0; pi < count[g]; ++pi) {
-        const Portion P = list[g][pi];
+      for (int pi = 0; pi < count; ++pi) {
+        const Portion P = list[pi];
+        if (pi == 0 && row == 0 && ok) next_q(0);
         if (!present(g, P)) {
           nm += P.t1 - P.t0;
           continue;
         }
         const bool both = c.shared && present(1, P);
-        const int h = P.item / c.np, mt = c.shared ? 2 * (P.item % c.np) + g : 0, t = mt * c.MT + lt;
+        const int h = P.head, mt = c.shared ? 2 * P.pair + g : 0, t = mt * c.MT + lt;
         const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
         const bool row_ok = row < c.G * c.MT && t < P.nn;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -425,14 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tile = P.t0; tile < P.t1; ++tile) {
           const int j0 = (int)((long long)tile * kTile - n4);  // node of the tile's first entry
           const bool nodes = j0 + kTile > 0;
-          if (ok) ok = mbar_wait_bounded(&ct.s[g], (uint32_t)(nt & 1), abort);
+          if (ok) ok = mbar_wait_small(&ct.s[g], (uint32_t)(nt & 1), abort);
           tc_fence_after();
           if (row == 0 && tile == P.t1 - 1) {  // the last scores of the portion are done: the next one's queries
-            const int i = next_present(pi + 1);
-            if (i < count[g] && ok) load_q(list[g][i]);
+            if (ok) next_q(pi + 1);
           }
           const int mg = c.shared ? 0 : g;
-          if (ok) ok = mbar_wait_bounded(&ct.mask[mg][nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
+          if (ok) ok = mbar_wait_small(&ct.mask[mg][nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
           ok = __all_sync(0xffffffffu, ok);
           uint32_t w[4];
           bool full = !nodes;
@@ -449,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
               w[x] &= ctx | (row_ok ? mask_bits(mw, a.words, P.nn, jw) : 0u);
             }
-            if (ok) ok = mbar_wait_bounded(&ct.v[g], (uint32_t)(nv & 1), abort);
+            if (ok) ok = mbar_wait_small(&ct.v[g], (uint32_t)(nv & 1), abort);
             ok = __all_sync(0xffffffffu, ok);
             ++nv;
             bool d = false;
@@ -541,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ct.p[g]);
         }
         // the portion's result: complete, or a partial
-        if (ok) ok = mbar_wait_bounded(&ct.pv[g], (uint32_t)((nt - 1) & 1), abort);
+        if (ok) ok = mbar_wait_small(&ct.pv[g], (uint32_t)((nt - 1) & 1), abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok && warp_ok) {
@@ -598,15 +652,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after a wait that gave up, copies and products may still be in flight: they end before the CTA does
   volatile uint32_t never = 0u;
   if (warp == kWarpMma) {
-    if (elect_one()) umma_commit(&ct.fin);
+    if (lane == 0) {  // the thread whose products they are
+      umma_commit(&ct.fin);
+      mbar_wait_bounded(&ct.fin, 0u, &never);
+    }
     __syncwarp();
-    warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
   if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
     if (warp >= kWarpProd) {
+#pragma unroll 1
       for (int i = max(0, sent - C::kRing); i < sent; ++i)
         while (!mbar_try_wait(&ct.full[i % C::kRing], (uint32_t)((i / C::kRing) & 1)) && global_ns() - t0 < 1000000000ull) {
         }
@@ -701,6 +758,7 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.nmt = p.nmt;
   uint8_t* w = (uint8_t*)g->d_workspace;
   c.ws.items = p.items;
+  c.ws.np = p.np;
   c.ws.groups = p.shared ? 1 : 2;
   c.ws.rows = p.rows;
   c.ws.prefix = (long long*)w;

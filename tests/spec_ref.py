@@ -19,8 +19,9 @@ def sees(mask, r, i, j):
     return (int(mask[r][i][j // 64]) >> (j % 64)) & 1 == 1
 
 
-def tree(cfg, context_rows, node_rows, q, mask, nodes, scale):
-    """context_rows[r], node_rows[r]: [n][record] tensors; q [R][T][Hq][Dqk]; mask, nodes host lists.
+def tree(cfg, context_rows, node_rows, q, mask, nodes, scale, only=None):
+    """context_rows[r], node_rows[r]: [n][record] tensors; q [R][T][Hq][Dqk]; mask, nodes host lists;
+    only: the (request, node, head) triples to compute, the others get no bound.
 
     Returns (out, bound) in float64, [R][T][Hq][Dv].  The bound, per value:
       - the output's rounding: 2^-8 |o|;
@@ -53,6 +54,9 @@ def tree(cfg, context_rows, node_rows, q, mask, nodes, scale):
             qq = q[r, :nn, h].double()
             # values that a node does not see (NaN among them) have no part in anything
             for i in range(nn):
+                if only is not None and (r, i, h) not in only:
+                    bound[r, i, h] = math.inf
+                    continue
                 if not bool(ok[i].any()):
                     continue
                 kk, vv = k[ok[i]], v[ok[i]]

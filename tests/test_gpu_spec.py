@@ -53,7 +53,7 @@ def random_tree(R, T, seed):
                         for _ in range(R)])
 
 
-def check_tree(cfg, kv, lens, T, mask, locs=None, nodes=None, seed=0, q=None, scale=None):
+def check_tree(cfg, kv, lens, T, mask, locs=None, nodes=None, seed=0, q=None, scale=None, only=None):
     R = cfg.num_requests
     if q is None:
         q = randn((R, T, cfg.num_q_heads, cfg.head_dim_qk), seed + 77)
@@ -67,7 +67,8 @@ def check_tree(cfg, kv, lens, T, mask, locs=None, nodes=None, seed=0, q=None, sc
     ctx = [flat_rows(kv, r, [p for p in (locs[r].tolist() if locs is not None else range(lens[r])) if p >= 0])
            for r in range(R)]
     node = [flat_rows(kv, r, range(lens[r], lens[r] + nn[r])) for r in range(R)]
-    want, bound = ref.tree(cfg, ctx, node, q, mask.tolist(), nn, cfg.default_scale if scale is None else scale)
+    want, bound = ref.tree(cfg, ctx, node, q, mask.tolist(), nn, cfg.default_scale if scale is None else scale,
+                           only=only)
     ref.assert_tree(out, want, bound, nn, before)
     return q, out
 
@@ -106,6 +107,33 @@ def test_tree_over_a_dense_context(cfg, T, lens, page, table):
     cfg = cfg()
     kv = make_cache(cfg, max(lens) + T, page, seed=T + sum(lens), table=table)
     check_tree(cfg, kv, lens, T, tree_mask(random_tree(cfg.num_requests, T, seed=T)), seed=T)
+
+
+@pytest.mark.parametrize("cfg,T,most", [(gqa(5), 7, 9000), (gqa(5), 70, 5000), (gqa(5, 40, 8), 77, 3000), (gqa(40, 2, 2, 64), 1, 700),
+                                        (gqa(5, 32, 8, 64), 40, 6000), (gqa(300, 4, 2), 2, 200), (gqa(700, 2, 1), 2, 90),
+                                        (mla(5), 3, 9000), (mla(60), 2, 300)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_tree_with_many_tiles_and_requests_a_worker(cfg, T, most, listed):
+    """Workers that walk through many tiles, several items and many requests, empty ones among them; every
+    (request, node, head) is compared for a sample of them."""
+    R, Hq = cfg.num_requests, cfg.num_q_heads
+    g = torch.Generator().manual_seed(T)
+    lens = [int(x) for x in torch.randint(0, most, (R,), generator=g)]
+    lens[0] = most
+    nodes = [T if r % 3 else int(torch.randint(0, T + 1, (1,), generator=g)) for r in range(R)]
+    nodes[0] = T
+    kv = make_cache(cfg, most + T, 16, seed=T)
+    locs = None
+    if listed:
+        k = min(most, 1500)
+        locs = torch.full((R, k), -1, dtype=torch.int32)
+        for r in range(R):
+            p = torch.randperm(lens[r] + 1, generator=g)[:k] if r % 4 else torch.arange(0)
+            locs[r, :len(p)] = p.to(torch.int32)
+        locs = locs.to(DEV)
+    pick = torch.randint(0, 10**9, (150, 3), generator=g).tolist()
+    only = {(a % R, b % T, c % Hq) for a, b, c in pick} | {(0, T - 1, Hq - 1), (R - 1, 0, 0)}
+    check_tree(cfg, kv, lens, T, tree_mask(random_tree(R, T, seed=T)), locs=locs, nodes=nodes, seed=T, only=only)
 
 
 @pytest.mark.parametrize("cfg,T,k", [(gqa(3), 8, 300), (gqa(2, 14, 2), 19, 1), (gqa(2, 8, 8, 64), 3, 129),
