@@ -179,10 +179,11 @@ int num_sms_of(int device) {
 int launch_tree(const hs_config* c, const hs_tree_args* g, const TreeArgs& a, int device, cudaStream_t st) {
   const int sms = num_sms_of(device);
   if (sms < 1) return HS_ERR_CUDA;
-  const hs_tree_plan p = hs_tree_gqa_plan(c, g->nodes, sms);
+  const bool mla = c->layout == HS_LAYOUT_MLA;
+  const hs_tree_plan p = mla ? hs_tree_mla_plan(c, g->nodes, sms) : hs_tree_gqa_plan(c, g->nodes, sms);
   if (p.usable) {
     if (g->d_workspace == nullptr || g->workspace_bytes < p.workspace) return HS_ERR_SCRATCH;
-    return hs_tree_gqa_launch(c, g, &a, sms, st);
+    return mla ? hs_tree_mla_launch(c, g, &a, sms, st) : hs_tree_gqa_launch(c, g, &a, sms, st);
   }
   const cudaError_t e = hs_launch_pdl(k_tree_any, dim3(a.T * a.Hq, a.R), dim3(kAnyWarps * 32), 0, st, a);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
@@ -196,7 +197,7 @@ extern "C" int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int c
   if (nodes < 1 || nodes > HS_MAX_TREE_NODES || cuda_device < 0) return HS_ERR_ARG;
   const int sms = num_sms_of(cuda_device);
   if (sms < 1) return HS_ERR_CUDA;
-  return hs_tree_gqa_plan(cfg, nodes, sms).workspace;
+  return (cfg->layout == HS_LAYOUT_MLA ? hs_tree_mla_plan(cfg, nodes, sms) : hs_tree_gqa_plan(cfg, nodes, sms)).workspace;
 }
 
 extern "C" int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_tree_args* args, void* stream) {

@@ -3,7 +3,10 @@
 
 #include <cuda_bf16.h>
 
+#include <string.h>
+
 #include "hs_paged.cuh"
+#include "hs_tc.cuh"
 
 namespace {
 
@@ -266,6 +269,121 @@ __device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& w
   return true;
 }
 
+// A producer lane's lookups of its entry of each tile of a portion list, in three steps, each a tile ahead of
+// the next, so that the latencies of the list and of the page table stay out of the way: A the position (a
+// list entry), B the page, C the record.
+struct Lookahead {
+  // what an entry is: 0 nothing, 1 context, 2 a node in the cache, 3 a node among the drafts
+  struct Look {
+    int kind, r, p, head;
+    uint64_t page;
+  } la, lb;
+  int ap, at, row;  // place of step A; the record's row, for copies in boxes (rows_end: none)
+  uint64_t now;     // the record's address, 0: none
+  bool begun;
+
+  // One tile further; after the first three calls `now` and `row` are those of the first tile.  `mine`: the
+  // lane's entry in a tile; `lines`: 128-byte lines of the record (from the portion's KV head on) to bring
+  // into L2 now, a tile before they are copied.
+  __device__ __forceinline__ void step(const TreeArgs& a, const Portion* list, int count, int tile, int mine, int rows_end,
+                                       int lines, uint32_t* bad) {
+    {  // C
+      const Look& l = lb;
+      now = 0ull;
+      row = rows_end;
+      if (l.kind == 3) {
+        now = (uint64_t)(uintptr_t)a.draft + (uint64_t)((int64_t)l.r * a.T + l.p) * (uint64_t)a.kv.rec;
+      } else if (l.kind != 0 && a.slot_pt != nullptr) {
+        now = l.page + (uint64_t)l.p * (uint64_t)a.kv.rec;
+      } else if (l.kind != 0 && l.page < (uint64_t)a.kv.num_pages) {
+        row = (int)l.page * a.kv.page_tokens + l.p;
+        now = (uint64_t)(uintptr_t)a.kv.base + (uint64_t)row * (uint64_t)a.kv.rec;
+      } else if (l.kind != 0) {
+        *bad |= (uint32_t)HS_DEVERR_PAGE;
+      }
+      if (now != 0ull) {
+#pragma unroll 1
+        for (int x = 0; x < lines; ++x)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(now + (uint64_t)(2 * l.head + 128 * x)));
+      }
+    }
+    {  // B; p becomes the place in the page
+      Look& l = lb;
+      l = la;
+      const int most = a.slot_pt != nullptr ? (l.kind == 1 ? a.slot_cap[l.r] : 0) : a.kv.max_pages * a.kv.page_tokens;
+      if (l.kind == 1 && a.locs != nullptr && l.p == -1) l.kind = 0;
+      if ((l.kind == 1 || l.kind == 2) && (unsigned)l.p >= (unsigned)most) {
+        *bad |= (uint32_t)HS_DEVERR_LOC;
+        l.kind = 0;
+      }
+      if (l.kind == 1 || l.kind == 2) {
+        if (a.slot_pt != nullptr) {
+          l.page = a.slot_pt[(int64_t)l.r * a.slot_pages + (l.p >> a.slot_shift)];
+          l.p &= (1 << a.slot_shift) - 1;
+        } else {
+          const unsigned pg = (unsigned)l.p / (unsigned)a.kv.page_tokens;
+          l.p -= (int)(pg * (unsigned)a.kv.page_tokens);
+          l.page = a.kv.table != nullptr ? (uint64_t)(int64_t)a.kv.table[(int64_t)l.r * a.kv.max_pages + pg]
+                                         : (uint64_t)((int64_t)l.r * a.kv.max_pages + pg);
+        }
+      }
+    }
+    {  // A
+      Look& l = la;
+      l.kind = 0;
+      l.r = 0;
+      if (ap < count) {
+        const Portion& P = list[ap];
+        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u), e = at * tile + mine;
+        l.r = P.r;
+        l.head = P.head * a.kstride;
+        if (e < P.n) {
+          l.kind = 1;
+          l.p = a.locs != nullptr ? a.locs[(int64_t)P.r * a.k + e] : e;
+        } else if (e >= n4 && e - n4 < P.nn) {
+          l.kind = a.draft != nullptr ? 3 : 2;
+          l.p = a.draft != nullptr ? e - n4 : P.len + (e - n4);
+        }
+        if (++at == P.t1) {
+          ++ap;
+          if (ap < count) at = list[ap].t0;
+        }
+      }
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void swap_both(T& x, T& y) {
+  const T z = x;
+  x = y;
+  y = z;
+}
+__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  bool w = true;
+  if ((threadIdx.x & 31) == 0) w = mbar_wait_small(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+}
+
+// one OR over the threads of a named barrier
+__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)x)
+      : "memory");
+  return r != 0u;
+}
+
+__device__ __forceinline__ bool bad_pair(uint32_t w) {  // an infinity or NaN among two bf16
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t good_pair(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+
 // bits j0 .. j0 + 31 of a node's visibility among the nn nodes in use (bits before 0 are clear)
 __device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int nn, int j0) {
   if (j0 <= -32 || j0 >= nn) return 0u;
@@ -283,9 +401,10 @@ struct CombineArgs {
   const int32_t* nodes;
   uint16_t* out;
   WorkSplit ws;
-  int R, T, Hq, dv, workers;
-  int G, MT, per;  // rows of a node, nodes of a 128-row tile, tiles of an item
-  int np, nslice;  // items: (KV head * np + tile group) * nslice + slice
+  int R, T, Hq, workers;
+  int G, MT, per;  // rows of a node, nodes of a 128-row tile, row tiles of an item
+  int np;          // items: KV head * np + group of row tiles
+  int flat;        // a shared latent: item i holds the rows [flat i, flat (i + 1)) of all node x head rows
 };
 
 // One warp per accumulator row, DV dims; items that one worker held whole are written by it.
@@ -301,11 +420,12 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   const int wf = sh.worker(a), wl = sh.worker(a + T - 1);
   if (wf == wl) return;
   const int row = blockIdx.z * 8 + (threadIdx.x >> 5), x = row & 127;
-  const int slice = item % c.nslice, hp = item / c.nslice, h = hp / c.np, mt = (hp % c.np) * c.per + (row >> 7);
-  const int t = mt * c.MT + x / c.G;
+  const int mt = c.flat ? 0 : (item % c.np) * c.per + (row >> 7);
+  const int t = c.flat ? (item * c.flat + row) / c.Hq : mt * c.MT + x / c.G;
+  const int h = c.flat ? (item * c.flat + row) % c.Hq : item / c.np * c.G + x % c.G;
   int nn = c.T;
   if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
-  if (row >= c.ws.rows || x >= c.G * c.MT || t >= nn) return;
+  if (row >= c.ws.rows || (!c.flat && x >= c.G * c.MT) || t >= nn) return;
   auto slot_row = [&](int w) { return ((long long)w * 2 + (w == wf ? 1 : 0)) * c.ws.rows + row; };
   float M = -INFINITY;
   for (int w = wf + lane; w <= wl; w += 32)
@@ -340,9 +460,30 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t* o = (uint32_t*)(c.out + (((int64_t)r * c.T + t) * c.Hq + (int64_t)h * c.G + x % c.G) * c.dv + slice * DV);
+  uint32_t* o = (uint32_t*)(c.out + (((int64_t)r * c.T + t) * c.Hq + h) * DV);
 #pragma unroll
   for (int v = 0; v < V; ++v) o[lane + 32 * v] = pack(acc[v].x * inv, acc[v].y * inv);
+}
+
+bool encode(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
+            const cuuint32_t* box) {
+  const EncodeFn fn = tensor_map_encoder();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  memset(m, 0, sizeof(*m));
+  return fn != nullptr && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(base), size, stride, box,
+                             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The shared-memory limit of a kernel, raised once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, bool* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = hs_raise_smem_limit(kern, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
 }
 
 }  // namespace
@@ -355,4 +496,6 @@ struct hs_tree_plan {
   int64_t workspace;
 };
 hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms);
+hs_tree_plan hs_tree_mla_plan(const hs_config* c, int nodes, int num_sms);
+int hs_tree_mla_launch(const hs_config* c, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st);
 int hs_tree_gqa_launch(const hs_config* c, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st);

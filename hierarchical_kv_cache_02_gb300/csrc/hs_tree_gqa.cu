@@ -59,37 +59,6 @@ struct Control {
   uint32_t tmem, abort;
 };
 
-// one OR over the threads of a named barrier
-__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)x)
-      : "memory");
-  return r != 0u;
-}
-
-__device__ __forceinline__ bool bad_pair(uint32_t w) {  // an infinity or NaN among two bf16
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-__device__ __forceinline__ uint32_t good_pair(uint32_t w) {
-  return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
-}
-
-template <typename T>
-__device__ __forceinline__ void swap_both(T& x, T& y) {
-  const T z = x;
-  x = y;
-  y = z;
-}
-__device__ __forceinline__ bool warp_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
-  bool w = true;
-  if ((threadIdx.x & 31) == 0) w = mbar_wait_small(bar, parity, abort);
-  return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
-}
-
 template <int N>
 struct Ring {
   int slot = 0;
@@ -197,85 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kWarpProd) {
       // ---------------- producers: 32 entries of every tile each ----------------
-      // Lane y looks up entry y of the warp's 32 in three steps, each a tile ahead of the next, so that the
-      // latencies of the list and of the page table stay out of the way: A the position (a list entry), B the
-      // page, C the record.
+      // lane y looks up entry y of the warp's 32
       const int pw = warp - kWarpProd, crow = lane >> 3, cch = lane & 7;
-      // what an entry is: 0 nothing, 1 context, 2 a node in the cache, 3 a node among the drafts
-      struct Look {
-        int kind, r, p;
-        uint64_t page;
-      };
-      struct Ahead {
-        Look la, lb;
-        int ap, at, row;  // cursor of step A; the record's row, for the boxes
-        uint64_t now;     // the record's address, 0: none
-        bool begun;
-      };
-      Ahead ahead0 = {}, ahead1 = {};  // two variables, never exchanged: a move would wait for a load on its way
+      Lookahead ahead0 = {}, ahead1 = {};  // two variables, never exchanged: a move would wait for a load on its way
       Cursor k0, k1;
       k0.open(list_of(0), count_of(0), c);
       k1.open(list_of(1), ng > 1 ? count_of(1) : 0, c);
       ahead0.at = k0.t;
       ahead1.at = k1.t;
-      auto look = [&](Ahead& mine) {
-        {  // C
-          const Look& l = mine.lb;
-          mine.now = 0ull;
-          mine.row = c.ctx_rows;
-          if (l.kind == 3) {
-            mine.now = (uint64_t)(uintptr_t)a.draft + (uint64_t)((int64_t)l.r * a.T + l.p) * (uint64_t)a.kv.rec;
-          } else if (l.kind != 0 && a.slot_pt != nullptr) {
-            mine.now = l.page + (uint64_t)l.p * (uint64_t)a.kv.rec;
-          } else if (l.kind != 0 && l.page < (uint64_t)a.kv.num_pages) {
-            mine.row = (int)l.page * a.kv.page_tokens + l.p;
-            mine.now = (uint64_t)(uintptr_t)a.kv.base + (uint64_t)mine.row * (uint64_t)a.kv.rec;
-          } else if (l.kind != 0) {
-            bad |= (uint32_t)HS_DEVERR_PAGE;
-          }
-        }
-        {  // B; p becomes the place in the page
-          Look& l = mine.lb;
-          l = mine.la;
-          const int most = a.slot_pt != nullptr ? (l.kind == 1 ? a.slot_cap[l.r] : 0) : a.kv.max_pages * a.kv.page_tokens;
-          if (l.kind == 1 && a.locs != nullptr && l.p == -1) l.kind = 0;
-          if ((l.kind == 1 || l.kind == 2) && (unsigned)l.p >= (unsigned)most) {
-            bad |= (uint32_t)HS_DEVERR_LOC;
-            l.kind = 0;
-          }
-          if (l.kind == 1 || l.kind == 2) {
-            if (a.slot_pt != nullptr) {
-              l.page = a.slot_pt[(int64_t)l.r * a.slot_pages + (l.p >> a.slot_shift)];
-              l.p &= (1 << a.slot_shift) - 1;
-            } else {
-              const unsigned pg = (unsigned)l.p / (unsigned)a.kv.page_tokens;
-              l.p -= (int)(pg * (unsigned)a.kv.page_tokens);
-              l.page = a.kv.table != nullptr ? (uint64_t)(int64_t)a.kv.table[(int64_t)l.r * a.kv.max_pages + pg]
-                                             : (uint64_t)((int64_t)l.r * a.kv.max_pages + pg);
-            }
-          }
-        }
-        {  // A
-          Look& l = mine.la;
-          l.kind = 0;
-          l.r = 0;
-          if (mine.ap < k0.count) {
-            const Portion& P = k0.list[mine.ap];
-            const int n4 = (int)(((unsigned)P.n + 3u) & ~3u), e = mine.at * kTile + 32 * pw + lane;
-            l.r = P.r;
-            if (e < P.n) {
-              l.kind = 1;
-              l.p = a.locs != nullptr ? a.locs[(int64_t)P.r * a.k + e] : e;
-            } else if (e >= n4 && e - n4 < P.nn) {
-              l.kind = a.draft != nullptr ? 3 : 2;
-              l.p = a.draft != nullptr ? e - n4 : P.len + (e - n4);
-            }
-            if (++mine.at == P.t1) {
-              ++mine.ap;
-              if (mine.ap < k0.count) mine.at = k0.list[mine.ap].t0;
-            }
-          }
-        }
+      auto look = [&](Lookahead& l) {
+        l.step(a, k0.list, k0.count, kTile, 32 * pw + lane, c.ctx_rows, c.seg == 0 ? 2 * C::kCh : 0, &bad);
       };
       // one tile a turn, the groups by turns: k0 is the group at hand, exchanged with the other after its turn
       int g = 0;
@@ -284,57 +184,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k0.left()) {
           idle = 0;
           const Portion& P = k0.list[k0.p];
-          if (g == 0) {
+          // the lookups of the group's next tile follow the copies of this one
 #pragma unroll 1
-            for (int x = ahead0.begun ? 0 : 2; x >= 0; --x) look(ahead0);
-            ahead0.begun = true;
-          } else {
+          for (int behind = 0; behind < 2; ++behind) {
+            if (g == 0) {
 #pragma unroll 1
-            for (int x = ahead1.begun ? 0 : 2; x >= 0; --x) look(ahead1);
-            ahead1.begun = true;
-          }
-          const uint64_t now = g == 0 ? ahead0.now : ahead1.now;
-          const int now_row = g == 0 ? ahead0.row : ahead1.row;
-          const bool boxed = c.seg != 0 && k0.t * kTile + 32 * pw + 32 <= P.n;
-          const int x0 = P.head * a.kstride;
+              for (int x = behind ? 1 : ahead0.begun ? 0 : 3; x > 0; --x) look(ahead0);
+              ahead0.begun = true;
+            } else {
 #pragma unroll 1
-          for (int val = 0; val < 2; ++val) {
-            if (ok) ok = warp_wait_small(&ct.empty[ring.slot], ring.phase ^ 1u, abort);
-            if (ok) {
-              const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 32 * pw * 128);
-              uint64_t* full = &ct.full[ring.slot];
-              if (boxed) {
-                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(32 * D * 2));
-                else mbar_arrive(full);
-                const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row, (box * c.seg) & 31);
-                if (box * c.seg < 32 && (lane & 3) < C::kCh)
-                  tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + val * D + 64 * (lane & 3),
-                              row, full);
-              } else {
-                // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
-                const int off = 2 * (x0 + val * D) + 16 * cch;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int row = 4 * i + crow;
-                  const uint64_t src = __shfl_sync(0xffffffffu, now, row);
-                  const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4)), n = src != 0ull ? 16u : 0u;
-                  const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + off : (const uint8_t*)a.q;
-#pragma unroll
-                  for (int b = 0; b < C::kCh; ++b) cp_async16_zfill(to + b * C::kBlk, src != 0ull ? from + 128 * b : from, n);
-                }
-                cp_async_arrive_noinc(full);
-              }
-              ++sent;
+              for (int x = behind ? 1 : ahead1.begun ? 0 : 3; x > 0; --x) look(ahead1);
+              ahead1.begun = true;
             }
-            ring.next();
+            if (behind) break;
+            const uint64_t now = g == 0 ? ahead0.now : ahead1.now;
+            const int now_row = g == 0 ? ahead0.row : ahead1.row;
+            const bool boxed = c.seg != 0 && k0.t * kTile + 32 * pw + 32 <= P.n;
+            const int x0 = P.head * a.kstride;
+#pragma unroll 1
+            for (int val = 0; val < 2; ++val) {
+              if (ok) ok = warp_wait_small(&ct.empty[ring.slot], ring.phase ^ 1u, abort);
+              if (ok) {
+                const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 32 * pw * 128);
+                uint64_t* full = &ct.full[ring.slot];
+                if (boxed) {
+                  if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(32 * D * 2));
+                  else mbar_arrive(full);
+                  const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row, (box * c.seg) & 31);
+                  if (box * c.seg < 32 && (lane & 3) < C::kCh)
+                    tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + val * D + 64 * (lane & 3),
+                                row, full);
+                } else {
+                  // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
+                  const int off = 2 * (x0 + val * D) + 16 * cch;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + crow;
+                    const uint64_t src = __shfl_sync(0xffffffffu, now, row);
+                    const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+                    const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + off : (const uint8_t*)a.q;
+#pragma unroll
+                    for (int b = 0; b < C::kCh; ++b) cp_async16_zfill(to + b * C::kBlk, src != 0ull ? from + 128 * b : from, n);
+                  }
+                  cp_async_arrive_noinc(full);
+                }
+                ++sent;
+              }
+              ring.next();
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, now != 0ull);
+            int& n = g == 0 ? tiles0 : tiles1;
+            if (ok && lane == 0) {
+              ct.valid[g][n % kMaskRing][pw] = word;
+              mbar_arrive(&ct.mask[g][n % kMaskRing]);
+            }
+            ++n;
           }
-          const uint32_t word = __ballot_sync(0xffffffffu, now != 0ull);
-          int& n = g == 0 ? tiles0 : tiles1;
-          if (ok && lane == 0) {
-            ct.valid[g][n % kMaskRing][pw] = word;
-            mbar_arrive(&ct.mask[g][n % kMaskRing]);
-          }
-          ++n;
           k0.next(c);
         }
         if (ng > 1) {
@@ -702,27 +607,6 @@ bool plan_of(const hs_config* c, int T, int sms, Plan* p) {
 
 int64_t part_floats(const Plan& p) { return (int64_t)p.workers * 2 * p.rows * p.D; }
 
-bool encode(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
-            const cuuint32_t* box) {
-  const EncodeFn fn = tensor_map_encoder();
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  memset(m, 0, sizeof(*m));
-  return fn != nullptr && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(base), size, stride, box,
-                             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The shared-memory limit of a kernel, raised once per device.
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, bool* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
-  e = hs_raise_smem_limit(kern, (int)bytes);
-  if (e == cudaSuccess && dev < 64) done[dev] = true;
-  return e;
-}
-
 template <int D>
 cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& seg, const CombineArgs& cb,
                    cudaStream_t st) {
@@ -790,13 +674,11 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   cb.R = c.a.R;
   cb.T = c.a.T;
   cb.Hq = c.a.Hq;
-  cb.dv = p.D;
   cb.workers = p.workers;
   cb.G = p.G;
   cb.MT = p.MT;
   cb.per = p.shared ? 2 : 1;
   cb.np = p.np;
-  cb.nslice = 1;
   const cudaError_t e = p.D == 128 ? launch<128>(c, p, num_sms, qm, seg, cb, st) : launch<64>(c, p, num_sms, qm, seg, cb, st);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }

@@ -1,0 +1,502 @@
+// Tree attention over shared-latent records (576 values, the first 512 of them V) on the 5th-generation tensor
+// cores.
+//
+// The rows of a request are its (node, query head) pairs one after the other; an item is 64 of them, whatever the
+// head count.  A CTA holds their queries in shared memory (72 KB) and two tiles of 64 records (72 KB each): a
+// latent is key and value at once, so a tile is loaded once and stays from the scores to the value product.
+// Per tile S = Q K^T (64 x 64 x 576) and O += P V (64 x 512 x 64).  An accumulator of 64 rows takes 16 of every 32
+// lanes of tensor memory, so O's two halves of 256 dims share columns (lanes 0-15 and 16-31 of each
+// quarter), and so do the scores of even and odd tiles.  The scores of the next tile are issued before the
+// value product of the one at hand, so the softmax (one warpgroup, a thread per row) runs beside them.
+// 128 rows with half of the dims in an accumulator would use the tensor cores better, but their queries leave
+// 80 KB for records: not enough to load one tile while the values of another wait for its weights.
+// What bounds it: at full rate the products of a tile take 2176 cycles of a 64-row accumulator.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "hs_tc.cuh"
+#include "hs_tree.cuh"
+
+namespace {
+
+constexpr int kTile = 64, kRows = 64, kDim = 576, kValue = 512;
+constexpr int kChunks = kDim / 64, kParts = 3;    // 128-byte column blocks of a tile; a third of them to a barrier
+constexpr int kBlk = 64 * 128;                    // bytes of one block of 64 rows
+constexpr int kBuf = kChunks * kBlk;              // a tile; also the queries
+constexpr int kProducers = 4, kWarpMma = 4, kWarpProd = 5;
+constexpr int kThreads = (kWarpProd + kProducers) * 32;
+constexpr int kMaskRing = 4;
+constexpr float kLazy = 8.f;                      // log2 headroom before the running maximum is raised
+constexpr size_t kDyn = 3 * (size_t)kBuf + kBlk + 1024;
+constexpr uint32_t kScores = 256;                 // first column of the scores, behind O's 256
+
+struct MlaArgs {
+  TreeArgs a;
+  WorkSplit ws;
+  int seg;       // dense contexts whose pages hold multiples of 16: rows per box (16), else 0
+  int ctx_rows;  // rows of the cache: a box that starts there reads zeros
+  int negate;    // the scale is negative: qscale is its magnitude, the scores' products are negated
+};
+
+struct MlaControl {
+  PlanState plan;
+  __align__(8) uint64_t full[2][kParts], empty[2];
+  uint64_t qfull, s[2], p, pv, mask[kMaskRing], fin;
+  uint32_t valid[kMaskRing][kProducers];
+  uint32_t tmem, abort;
+};
+static_assert(kDyn + sizeof(MlaControl) <= 227 * 1024, "shared memory of a CTA");
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tree_mla(const MlaArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ MlaControl ct;
+  const TreeArgs& a = c.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t q_u = smem_u32(smem), p_u = q_u + kBuf, buf_u = p_u + kBlk;
+  volatile uint32_t* abort = &ct.abort;
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      for (int i = 0; i < kParts; ++i) mbar_init(&ct.full[b][i], kProducers * 32);
+      mbar_init(&ct.empty[b], 1u);
+      mbar_init(&ct.s[b], 1u);
+    }
+    mbar_init(&ct.qfull, 1u);
+    mbar_init(&ct.p, 128u);
+    mbar_init(&ct.pv, 1u);
+    for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], kProducers);
+    mbar_init(&ct.fin, 1u);
+    ct.abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ct.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kWarpProd && lane == 0) {
+    prefetch_map(&qmap);
+    if (c.seg != 0) prefetch_map(&segmap);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the only kernel that may start early is this call's own combine, which waits for this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  plan_start<kTile>(a, c.ws, &ct.plan);
+  tc_fence_after();
+  const uint32_t tb = ct.tmem;
+
+  // state that runs on through the rounds
+  int nt = 0;                      // tiles so far, of each role
+  int nq = 0;                      // portions so far (products); query loads (first softmax thread)
+  int sent = 0;                    // producers: tiles whose copies were issued
+  bool ok = true;
+  uint32_t bad = 0u;
+
+  while (plan_round<kTile>(a, c.ws, &ct.plan)) {
+    const Portion* list = ct.plan.port[0];
+    const int count = ct.plan.nport[0];
+    if (warp >= kWarpProd) {
+      // ---------------- producers: 16 entries of every tile each, looked up by lanes 0-15 ----------------
+      const int pw = warp - kWarpProd, crow = lane >> 3, cch = lane & 7;
+      Lookahead ahead = {};
+      ahead.at = count > 0 ? list[0].t0 : 0;
+      int kp = 0, kt = ahead.at;
+#pragma unroll 1
+      for (int x = -2; kp < count; ++x) {
+        ahead.step(a, list, count, kTile, 16 * pw + (lane & 15), c.ctx_rows, c.seg == 0 && lane < 16 ? kChunks : 0, &bad);
+        if (x < 0) continue;  // the steps' head start
+        const Portion& P = list[kp];
+        const bool boxed = c.seg != 0 && kt * kTile + 16 * pw + 16 <= P.n;
+        const int b = nt & 1;
+        if (ok) ok = warp_wait_small(&ct.empty[b], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
+        if (ok) {
+          const uint32_t dst = buf_u + (uint32_t)(b * kBuf + 16 * pw * 128);
+          const int row = __shfl_sync(0xffffffffu, ahead.row, 0);
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            uint64_t* full = &ct.full[b][part];
+            const int ch0 = part * (kChunks / kParts);
+            if (boxed) {
+              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(kChunks / kParts * 16 * 128));
+              else mbar_arrive(full);
+              __syncwarp();
+              if (lane < kChunks / kParts)
+                tma_load_2d(dst + (uint32_t)((ch0 + lane) * kBlk), &segmap, 64 * (ch0 + lane), row, full);
+            } else {
+              // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int y = 4 * i + crow;
+                const uint64_t src = __shfl_sync(0xffffffffu, ahead.now, y);
+                const uint32_t to = dst + (uint32_t)(ch0 * kBlk + y * 128 + ((cch ^ (y & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+                const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + 128 * ch0 + 16 * cch : (const uint8_t*)a.q;
+#pragma unroll
+                for (int h = 0; h < kChunks / kParts; ++h) cp_async16_zfill(to + h * kBlk, src != 0ull ? from + 128 * h : from, n);
+              }
+              cp_async_arrive_noinc(full);
+            }
+          }
+          sent = nt + 1;
+        }
+        const uint32_t word = __ballot_sync(0xffffffffu, ahead.now != 0ull) & 0xffffu;
+        if (ok && lane == 0) {
+          ct.valid[nt % kMaskRing][pw] = word;
+          mbar_arrive(&ct.mask[nt % kMaskRing]);
+        }
+        ++nt;
+        if (++kt == P.t1) {
+          ++kp;
+          if (kp < count) kt = list[kp].t0;
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ---------------- products, by one thread: S(0), then S(i + 1), O(i) by turns ----------------
+      if (lane == 0) {
+        const uint32_t id_s = umma_idesc_bf16(kRows, kTile, 0, 0) | (c.negate ? kNegateA : 0u);
+        const uint32_t id_o = umma_idesc_bf16(kRows, 256, 0, 1);
+        const uint32_t dq = umma_sdesc_lo(q_u, 16), dk = umma_sdesc_lo(buf_u, 16), dp = umma_sdesc_lo(p_u, 16);
+        // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
+        const uint32_t dv = umma_sdesc_lo(buf_u, kBlk);
+        int kp = 0, kt = count > 0 ? list[0].t0 : 0, vp = 0, vt = kt, ks_done = nt;  // next scores, next values
+        while (vp < count) {
+          if (kp < count) {
+            const int b = ks_done & 1;
+            if (kt == list[kp].t0) {  // this portion's queries
+              if (ok) ok = mbar_wait_small(&ct.qfull, (uint32_t)(nq & 1), abort);
+              ++nq;
+            }
+            const uint32_t to = tb + kScores + ((uint32_t)(16 * b) << 16);
+#pragma unroll 1
+            for (int part = 0; part < kParts; ++part) {
+              if (ok) ok = mbar_wait_small(&ct.full[b][part], (uint32_t)((ks_done >> 1) & 1), abort);
+              // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              tc_fence_after();
+              if (ok) {
+                const uint32_t x = (uint32_t)(part * (kChunks / kParts)) * (kBlk >> 4);
+#pragma unroll
+                for (int h = 0; h < kChunks / kParts; ++h)
+#pragma unroll
+                  for (int ks = 0; ks < 4; ++ks)
+                    umma_bf16_lo(to, dq + x + h * (kBlk >> 4) + 2 * ks, dk + (uint32_t)(b * (kBuf >> 4)) + x + h * (kBlk >> 4) + 2 * ks,
+                                 id_s, (part | h | ks) != 0 ? 1u : 0u);
+              }
+            }
+            if (ok) umma_commit(&ct.s[b]);
+            ++ks_done;
+            if (++kt == list[kp].t1) {
+              ++kp;
+              if (kp < count) kt = list[kp].t0;
+            }
+            // one tile of scores ahead of the values, unless its queries differ: a portion's queries are
+            // replaced once its last scores are done
+            if (ks_done == nt + 1 && kp < count) continue;
+          }
+          const int b = nt & 1;
+          if (ok) ok = mbar_wait_small(&ct.p, (uint32_t)(nt & 1), abort);
+          tc_fence_after();
+          if (ok) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_lo(tb + ((uint32_t)(16 * h) << 16), dp + 2 * ks,
+                             dv + (uint32_t)(b * (kBuf >> 4) + 4 * h * (kBlk >> 4)) + 128 * ks, id_o,
+                             (vt != list[vp].t0 || ks != 0) ? 1u : 0u);
+            umma_commit(&ct.pv);
+            umma_commit(&ct.empty[b]);
+          }
+          ++nt;
+          if (++vt == list[vp].t1) {
+            ++vp;
+            if (vp < count) vt = list[vp].t0;
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------- softmax: thread = row (lane & 15) of the warp's 16 ----------------
+      // Lanes 0-15 hold the scores of even tiles and O's dims 0-255, lanes 16-31 those of odd tiles and
+      // dims 256-511; what a row's two lanes have to agree on goes from the one with the scores to both.
+      const int row = 16 * warp + (lane & 15), side = lane >> 4;
+      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+      auto load_q = [&](const Portion& P) {  // by the first thread
+        mbar_arrive_expect_tx(&ct.qfull, (uint32_t)kBuf);
+        const int r0 = (int)((int64_t)P.r * a.T * a.Hq + (int64_t)kRows * P.head);
+        for (int b = 0; b < kChunks; ++b) tma_load_2d(q_u + (uint32_t)(b * kBlk), &qmap, 64 * b, r0, &ct.qfull);
+        ++nq;
+      };
+      if (tid == 0 && count > 0 && ok) load_q(list[0]);
+      for (int pi = 0; pi < count; ++pi) {
+        const Portion P = list[pi];
+        const int flat = kRows * P.head + row, t = flat / a.Hq;
+        const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
+        const bool row_ok = t < P.nn;
+        const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+        const uint64_t* mw = a.mask + ((int64_t)P.r * a.T + (row_ok ? t : 0)) * a.words;
+        float m = -INFINITY, l = 0.f;
+        bool dirty = false;  // a node's value is infinite or NaN
+        for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
+          const int b = nt & 1;
+          const int j0 = (int)((long long)tile * kTile - n4);  // node of the tile's first entry
+          const bool nodes = j0 + kTile > 0;
+          if (ok) ok = mbar_wait_small(&ct.s[b], (uint32_t)((nt >> 1) & 1), abort);
+          tc_fence_after();
+          if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
+          if (ok) ok = mbar_wait_small(&ct.mask[nt % kMaskRing], (uint32_t)((nt / kMaskRing) & 1), abort);
+          ok = __all_sync(0xffffffffu, ok);
+          uint32_t w[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) w[x] = ct.valid[nt % kMaskRing][2 * x] | (ct.valid[nt % kMaskRing][2 * x + 1] << 16);
+          const bool full = !nodes && (w[0] & w[1]) == 0xffffffffu;
+          if (nodes) {
+            // entries that are nodes: valid ones that this row sees
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int jw = j0 + 32 * x;
+              const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
+              w[x] &= ctx | (row_ok ? mask_bits(mw, a.words, P.nn, jw) : 0u);
+            }
+            // infinite and NaN values would reach every row of the product: they are taken out here and
+            // added to the rows that see them at the end.  Their scores are done.
+            bool d = false;
+            const int y = tid & 63;
+            for (int i = 0; i < kParts; ++i)
+              if (ok) ok = mbar_wait_small(&ct.full[b][i], (uint32_t)((nt >> 1) & 1), abort);
+            if (ok && j0 + y >= 0 && j0 + y < P.nn) {
+#pragma unroll 1
+              for (int ch = tid >> 6; ch < kValue / 64; ch += 2) {
+                uint4* vr = (uint4*)(smem + kBuf + kBlk + b * kBuf + ch * kBlk + y * 128);
+#pragma unroll 2
+                for (int x = 0; x < 8; ++x) {
+                  uint4 u = vr[x];
+                  if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
+                    d = true;
+                    u = make_uint4(good_pair(u.x), good_pair(u.y), good_pair(u.z), good_pair(u.w));
+                    vr[x] = u;
+                  }
+                }
+              }
+            }
+            if (d) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (bar_or(1, 128, d)) dirty = true;
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          float sum = 0.f;
+          uint32_t pk[32];
+          if (ok && warp_ok) {
+            float v[64];
+            tmem_ld64(tb + lane_base + kScores, v);
+            if (!full) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] = (w[j >> 5] >> (j & 31)) & 1u ? v[j] : -INFINITY;
+            }
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+              mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
+              my = fmaxf(fmaxf(my, v[j + 2]), v[j + 3]);
+            }
+            mx = fmaxf(mx, my) * a.qscale;
+            mx = __shfl_sync(0xffffffffu, mx, (lane & 15) + 16 * b);
+            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
+            const bool raise = mx > m + kLazy;
+            const bool any = __any_sync(0xffffffffu, raise);
+            const float mo = m;
+            if (raise) m = mx;
+            const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 0
+            float s1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float p0 = fast_exp2(fmaf(v[2 * j], a.qscale, -base)), p1 = fast_exp2(fmaf(v[2 * j + 1], a.qscale, -base));
+              if (!full) {
+                p0 = (w[j >> 4] >> ((2 * j) & 31)) & 1u ? p0 : 0.f;
+                p1 = (w[j >> 4] >> ((2 * j + 1) & 31)) & 1u ? p1 : 0.f;
+              }
+              pk[j] = pack_bf16(p0, p1);
+              sum += lo(pk[j]);  // the rounded weights, as the product takes them
+              s1 += hi(pk[j]);
+            }
+            sum = __shfl_sync(0xffffffffu, sum + s1, (lane & 15) + 16 * b);
+            if (nt > 0) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (any) {
+              const float al = (m == mo || mo == -INFINITY) ? 1.f : fast_exp2(mo - m);
+              l *= al;
+              if (tile != P.t0 && ok) {
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                  float o[32];
+                  tmem_ld32(tb + lane_base + 32u * x, o);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] *= al;
+                  tmem_st32(tb + lane_base + 32u * x, o);
+                }
+              }
+            }
+            l += sum;
+            // P, K-major and swizzled like the queries: 64 entries are one 128-byte row
+            if (side == b) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                *(uint4*)(smem + kBuf + row * 128 + ((x ^ (row & 7)) << 4)) =
+                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          } else if (ok && nt > 0) {
+            ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);  // no phase of it may pass unseen
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          tc_fence_before();
+          mbar_arrive(&ct.p);
+        }
+        // the portion's result: complete, or a partial
+        if (ok) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        if (ok && warp_ok) {
+          const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
+          const long long prow = ((long long)blockIdx.x * 2 + (P.t0 > 0 ? 0 : 1)) * kRows + row;
+          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {
+            float o[32];
+            tmem_ld32(tb + lane_base + 32u * x, o);
+            const int dim = 256 * side + 32 * x;
+            if (dirty && row_ok) {
+              for (int j = max(0, P.t0 * kTile - n4); j < min((long long)P.nn, (long long)P.t1 * kTile - n4); ++j) {
+                if (((mw[j >> 6] >> (j & 63)) & 1ull) == 0ull) continue;
+                const uint8_t* rec = node_record(a, P.r, P.len, j, &bad);
+                if (rec == nullptr) continue;
+                const uint32_t* vr = (const uint32_t*)rec + dim / 2;
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const uint32_t u = vr[y];
+                  if ((u & 0x7f80u) == 0x7f80u) o[2 * y] += lo(u);
+                  if ((u & 0x7f800000u) == 0x7f800000u) o[2 * y + 1] += hi(u);
+                }
+              }
+            }
+            if (row_ok) {
+              if (whole) {
+                uint4* dst = (uint4*)(a.out + ((int64_t)P.r * a.T * a.Hq + flat) * kValue + dim);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv), pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                                      pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+              } else {
+                float4* dst = (float4*)(c.ws.part + prow * kValue + dim);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+              }
+            }
+          }
+          if (row_ok && !whole && side == 0) *(float2*)(c.ws.ml + prow * 2) = make_float2(m, l);
+        }
+        tc_fence_before();
+      }
+    }
+    if (!ok) *abort = 1u;
+    __syncwarp();
+  }
+  if (!ok) {
+    *abort = 1u;
+    if (lane == 0) report(a.kv.err, (uint32_t)HS_DEVERR_TIMEOUT);
+  }
+  report(a.kv.err, bad);
+  // after a wait that gave up, copies and products may still be in flight: they end before the CTA does
+  volatile uint32_t never = 0u;
+  if (warp == kWarpMma) {
+    if (lane == 0) {  // the thread whose products they are
+      umma_commit(&ct.fin);
+      mbar_wait_bounded(&ct.fin, 0u, &never);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (*abort != 0u && lane == 0) {
+    const uint64_t t0 = global_ns();
+    if (warp >= kWarpProd) {
+#pragma unroll 1
+      for (int i = max(0, sent - 2); i < sent; ++i)
+        for (int part = 0; part < kParts; ++part)
+          while (!mbar_try_wait(&ct.full[i & 1][part], (uint32_t)((i >> 1) & 1)) && global_ns() - t0 < 1000000000ull) {
+          }
+    } else if (warp == 0 && nq > 0) {
+      while (!mbar_try_wait(&ct.qfull, (uint32_t)((nq - 1) & 1)) && global_ns() - t0 < 1000000000ull) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+
+bool usable(const hs_config* c) {
+  return c->layout == HS_LAYOUT_MLA && c->head_dim_qk == kDim && c->head_dim_v == kValue &&
+         (int64_t)c->num_requests * HS_MAX_TREE_NODES * c->num_q_heads <= (int64_t)INT32_MAX;
+}
+int items_of(const hs_config* c, int T) { return (T * c->num_q_heads + kRows - 1) / kRows; }
+int64_t prefix_bytes(const hs_config* c) { return ((int64_t)(c->num_requests + 1) * (int64_t)sizeof(int64_t) + 15) / 16 * 16; }
+
+}  // namespace
+
+hs_tree_plan hs_tree_mla_plan(const hs_config* c, int nodes, int num_sms) {
+  hs_tree_plan r = {usable(c), 0};
+  if (r.usable) r.workspace = prefix_bytes(c) + (int64_t)num_sms * 2 * kRows * (kValue + 2) * (int64_t)sizeof(float);
+  return r;
+}
+
+int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st) {
+  MlaArgs c{};
+  c.a = *(const TreeArgs*)tree_args;
+  uint8_t* w = (uint8_t*)g->d_workspace;
+  c.ws.items = items_of(cfg, g->nodes);
+  c.ws.np = 1;
+  c.ws.groups = 1;
+  c.ws.rows = kRows;
+  c.ws.prefix = (long long*)w;
+  c.ws.part = (float*)(w + prefix_bytes(cfg));
+  c.ws.ml = c.ws.part + (int64_t)num_sms * 2 * kRows * kValue;
+  if (c.a.qscale < 0.f) {
+    c.negate = 1;
+    c.a.qscale = -c.a.qscale;
+  }
+  CUtensorMap qm, seg;
+  memset(&seg, 0, sizeof(seg));
+  const cuuint64_t rec = kDim * 2;
+  if (c.a.slot_pt == nullptr && c.a.locs == nullptr && c.a.kv.page_tokens % 16 == 0) {
+    c.seg = 16;
+    c.ctx_rows = (int)(c.a.kv.num_pages * c.a.kv.page_tokens);
+    const cuuint64_t size[2] = {kDim, (cuuint64_t)c.ctx_rows}, stride[1] = {rec};
+    const cuuint32_t box[2] = {64, 16};
+    if (!encode(&seg, c.a.kv.base, 2, size, stride, box)) c.seg = 0;
+  }
+  const cuuint64_t qsize[2] = {kDim, (cuuint64_t)cfg->num_requests * g->nodes * cfg->num_q_heads}, qstride[1] = {rec};
+  const cuuint32_t qbox[2] = {64, kRows};
+  if (!encode(&qm, c.a.q, 2, qsize, qstride, qbox)) return HS_ERR_CUDA;
+  CombineArgs cb{};
+  cb.nodes = c.a.nodes;
+  cb.out = c.a.out;
+  cb.ws = c.ws;
+  cb.R = c.a.R;
+  cb.T = c.a.T;
+  cb.Hq = c.a.Hq;
+  cb.workers = num_sms;
+  cb.flat = kRows;
+  static bool done[64];
+  cudaError_t e = allow_smem(k_tree_mla, kDyn, done);
+  if (e == cudaSuccess) e = hs_launch_pdl(k_tree_mla, dim3(num_sms), dim3(kThreads), kDyn, st, c, qm, seg);
+  if (e == cudaSuccess)
+    e = hs_launch_pdl(k_tree_combine<kValue>, dim3(c.ws.items, cfg->num_requests, kRows / 8), dim3(256), 0, st, cb);
+  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}

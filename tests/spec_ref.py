@@ -28,7 +28,7 @@ def tree(cfg, context_rows, node_rows, q, mask, nodes, scale, only=None):
       - each weight rounded to bf16, the normaliser summing the rounded weights: the weighted mean moves by
         at most 2^-8 in its numerator and its denominator, 2 * 2^-8 * A with A = sum p |V|;
       - a score is a 32-bit dot product of exact bf16 products: it is off by at most
-        (Dqk + 2) 2^-24 scale sum |q K|, and 2^x by 2^-21 relative (argument reduction and function): 2 A times both;
+        (Dqk + 2) 2^-24 |scale| sum |q K|, and 2^x by 2^-21 relative (argument reduction and function): 2 A times both;
       - sums of n weights and products in 32 bits: n 2^-24, likewise 2 A."""
     R, T, Hq, Dqk = q.shape
     Hkv, Dv = cfg.num_kv_heads, cfg.head_dim_v
@@ -64,7 +64,8 @@ def tree(cfg, context_rows, node_rows, q, mask, nodes, scale, only=None):
                 p = torch.softmax(s, dim=0)
                 out[r, i, h] = p @ vv
                 a = p @ vv.abs()
-                off = (Dqk + 2) * U_FP32 * scale * float((kk.abs() @ qq[i].abs()).max())
+                # |scale|: an error bound is a magnitude (a negative scale would lower it below the roundings')
+                off = (Dqk + 2) * U_FP32 * abs(scale) * float((kk.abs() @ qq[i].abs()).max())
                 w = U_BF16 + off + 2.0**-21 + vv.shape[0] * U_FP32
                 bound[r, i, h] = U_BF16 * out[r, i, h].abs() + 2 * w * (1 + w) * a * (1 + U_BF16)
     return out, bound
