@@ -207,6 +207,20 @@ __device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, 
   return false;
 }
 
+// A whole warp's wait whose result the compiler knows to be the same in all lanes.  The warp that issues the
+// products keeps to such values throughout: tcgen05.mma takes its operands from uniform registers, and where
+// they are not uniform to begin with each product costs their moves (57 cycles instead of 32 for one of
+// 64 x 64 x 16).
+__device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort != 0u)) return false;
+  }
+  return false;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // bounded wait of a whole warp: lane 0 waits, the result is the warp's
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
   bool w = true;

@@ -79,14 +79,14 @@ struct Cursor {
   __device__ __forceinline__ void fetch(const TcArgs& c) {
     if (p >= count) return;
     const Portion& P = list[p];
-    t = t0 = P.t0;
-    t1 = P.t1;
-    nodes_from = (int)(((unsigned)P.n + 3u) & ~3u) / kTile;
-    pairs = !c.shared || 2 * P.pair + 1 < c.nmt;
+    t = t0 = uniform(P.t0);
+    t1 = uniform(P.t1);
+    nodes_from = uniform((int)(((unsigned)P.n + 3u) & ~3u) / kTile);
+    pairs = !c.shared || 2 * uniform(P.pair) + 1 < c.nmt;
   }
   __device__ __forceinline__ void open(const Portion* l, int n, const TcArgs& c) {
     list = l;
-    count = n;
+    count = uniform(n);
     p = 0;
     fetch(c);
   }
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Control ct;
   const TreeArgs& a = c.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_u = smem_u32(smem), ring_u = q_u + 2 * C::kSlot;
   volatile uint32_t* abort = &ct.abort;
@@ -248,106 +248,106 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kWarpMma) {
-      // ---------------- products: one thread, so that nothing waits for a warp's agreement ----------------
-      if (lane == 0) {
-        const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
-        const uint32_t dq0 = umma_sdesc_lo(q_u, 16), dk0 = umma_sdesc_lo(ring_u, 16);
-        // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
-        const uint32_t dv0 = umma_sdesc_lo(ring_u, C::kBlk);
-        constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
-        auto land = [&](const Ring<C::kRing>& at) {
-          if (ok) ok = mbar_wait_small(&ct.full[at.slot], at.phase, abort);
-          // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        };
-        int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
-        Ring<C::kRing> v0, v1;  // where the values of the tile in hand are: of the group at hand, of the other
-        Cursor k0, k1, p0, p1;  // next scores and next values of the group at hand, of the other
-        const int n0 = count_of(0), n1 = count_of(1);
-        k0.open(list_of(0), n0, c);
-        k1.open(list_of(1), n1, c);
-        p0 = k0;
-        p1 = k1;
-        int due0 = 0, due1 = 0, g = 0;  // scores done whose values are not
-        for (int idle = 0; idle < 2;) {
-          ++idle;
-          const uint32_t ts = tb + 128u * g, to = tb + 256u + (uint32_t)(D * g);
-          int done = g == 0 ? tiles0 : tiles1;  // tiles of this group finished
-          if (due0 > 0) {
-            idle = 0;
-            const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
-            if (!c.shared || g == 0) {
-              land(v0);
-              vslot = v0.slot;
-              // nodes among the entries: the softmax looks at their values first (both groups together, so
-              // both are told before the first one's weights are waited for)
-              if (p0.t >= p0.nodes_from) {
-                ct.vslot[g] = v0.slot;
-                mbar_arrive(&ct.v[g]);
-                if (c.shared && p0.pairs) {
-                  ct.vslot[1] = v0.slot;
-                  mbar_arrive(&ct.v[1]);
-                }
+      // ---------------- products ----------------
+      const uint32_t tu = (uint32_t)uniform((int)tb);
+      const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
+      const uint32_t dq0 = (uint32_t)uniform((int)umma_sdesc_lo(q_u, 16)), dk0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, 16));
+      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
+      const uint32_t dv0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, C::kBlk));
+      constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
+      auto land = [&](const Ring<C::kRing>& at) {
+        if (ok) ok = uniform_wait(&ct.full[at.slot], at.phase, abort);
+        // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      };
+      int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
+      Ring<C::kRing> v0, v1;     // where the values of the tile in hand are: of the group at hand, of the other
+      Cursor k0, k1, p0, p1;     // next scores and next values of the group at hand, of the other
+      k0.open(list_of(0), count_of(0), c);
+      k1.open(list_of(1), count_of(1), c);
+      p0 = k0;
+      p1 = k1;
+      int due0 = 0, due1 = 0, g = 0;  // scores done whose values are not
+      for (int idle = 0; idle < 2;) {
+        ++idle;
+        const uint32_t ts = tu + 128u * g, to = tu + 256u + (uint32_t)(D * g);
+        int done = g == 0 ? tiles0 : tiles1;  // tiles of this group finished
+        if (due0 > 0) {
+          idle = 0;
+          const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
+          if (!c.shared || g == 0) {
+            land(v0);
+            vslot = v0.slot;
+            // nodes among the entries: the softmax looks at their values first (both groups together, so
+            // both are told before the first one's weights are waited for)
+            if (p0.t >= p0.nodes_from && lane == 0) {
+              ct.vslot[g] = v0.slot;
+              mbar_arrive(&ct.v[g]);
+              if (c.shared && p0.pairs) {
+                ct.vslot[1] = v0.slot;
+                mbar_arrive(&ct.v[1]);
               }
             }
-            if (here) {
-              if (ok) ok = mbar_wait_small(&ct.p[g], (uint32_t)(done & 1), abort);
-              tc_fence_after();
-              if (ok) {
-                const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) umma_bf16_ta(to, ts + 8u * ks, dv + 128 * ks, id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
-                umma_commit(&ct.pv[g]);
-                if (last_user) umma_commit(&ct.empty[vslot]);
-              }
-              ++done;
-            }
-            --due0;
-            p0.next(c);
+            __syncwarp();
           }
-          if (k0.left()) {
-            idle = 0;
-            const bool here = g == 0 || k0.pairs, last_user = !c.shared || g == 1 || !k0.pairs;
-            if (!c.shared || g == 0) {
-              land(ring);
-              kslot = ring.slot;
-              ring.next();
-              v0 = ring;
-              ring.next();
-            }
-            if (here) {
-              if (k0.t == k0.t0) {  // this portion's queries
-                int& q = g == 0 ? portions0 : portions1;
-                if (ok) ok = mbar_wait_small(&ct.qfull[g], (uint32_t)(q & 1), abort);
-                ++q;
-              }
-              // the weights of the tile before share these columns: their product has to be complete
-              if (ok && done > 0) ok = mbar_wait_small(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
-              tc_fence_after();
-              if (ok) {
-                const uint32_t dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)kslot * kSlotStep;
+          if (here) {
+            if (ok) ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
+            tc_fence_after();
+            if (ok && elect_one()) {
+              const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
 #pragma unroll
-                for (int b = 0; b < C::kCh; ++b)
-#pragma unroll
-                  for (int ks = 0; ks < 4; ++ks)
-                    umma_bf16_lo(ts, dq + b * kBlkStep + 2 * ks, dk + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
-                umma_commit(&ct.s[g]);
-                if (last_user) umma_commit(&ct.empty[kslot]);
-              }
+              for (int ks = 0; ks < 8; ++ks) umma_bf16_ta(to, ts + 8u * ks, dv + 128 * ks, id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
+              umma_commit(&ct.pv[g]);
+              if (last_user) umma_commit(&ct.empty[vslot]);
             }
-            ++due0;
-            k0.next(c);
+            __syncwarp();
+            ++done;
           }
-          if (g == 0) tiles0 = done;
-          else tiles1 = done;
-          swap_both(k0, k1);
-          swap_both(p0, p1);
-          swap_both(due0, due1);
-          swap_both(v0, v1);
-          g ^= 1;
+          --due0;
+          p0.next(c);
         }
+        if (k0.left()) {
+          idle = 0;
+          const bool here = g == 0 || k0.pairs, last_user = !c.shared || g == 1 || !k0.pairs;
+          if (!c.shared || g == 0) {
+            land(ring);
+            kslot = ring.slot;
+            ring.next();
+            v0 = ring;
+            ring.next();
+          }
+          if (here) {
+            if (k0.t == k0.t0) {  // this portion's queries
+              int& q = g == 0 ? portions0 : portions1;
+              if (ok) ok = uniform_wait(&ct.qfull[g], (uint32_t)(q & 1), abort);
+              ++q;
+            }
+            // the weights of the tile before share these columns: their product has to be complete
+            if (ok && done > 0) ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+            tc_fence_after();
+            if (ok && elect_one()) {
+              const uint32_t dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)kslot * kSlotStep;
+#pragma unroll
+              for (int b = 0; b < C::kCh; ++b)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_bf16_lo(ts, dq + b * kBlkStep + 2 * ks, dk + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
+              umma_commit(&ct.s[g]);
+              if (last_user) umma_commit(&ct.empty[kslot]);
+            }
+            __syncwarp();
+          }
+          ++due0;
+          k0.next(c);
+        }
+        if (g == 0) tiles0 = done;
+        else tiles1 = done;
+        swap_both(k0, k1);
+        swap_both(p0, p1);
+        swap_both(due0, due1);
+        swap_both(v0, v1);
+        g ^= 1;
       }
-      __syncwarp();
     } else {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
       const int g = warp >> 2, row = tid & 127;
@@ -557,11 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after a wait that gave up, copies and products may still be in flight: they end before the CTA does
   volatile uint32_t never = 0u;
   if (warp == kWarpMma) {
-    if (lane == 0) {  // the thread whose products they are
-      umma_commit(&ct.fin);
-      mbar_wait_bounded(&ct.fin, 0u, &never);
-    }
+    if (elect_one()) umma_commit(&ct.fin);  // by the thread whose products they are
     __syncwarp();
+    warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
   if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");

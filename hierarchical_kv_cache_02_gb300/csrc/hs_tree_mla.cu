@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ MlaControl ct;
   const TreeArgs& a = c.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t q_u = smem_u32(smem), p_u = q_u + kBuf, buf_u = p_u + kBlk;
   volatile uint32_t* abort = &ct.abort;
@@ -154,70 +154,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kWarpMma) {
-      // ---------------- products, by one thread: S(0), then S(i + 1), O(i) by turns ----------------
-      if (lane == 0) {
-        const uint32_t id_s = umma_idesc_bf16(kRows, kTile, 0, 0) | (c.negate ? kNegateA : 0u);
-        const uint32_t id_o = umma_idesc_bf16(kRows, 256, 0, 1);
-        const uint32_t dq = umma_sdesc_lo(q_u, 16), dk = umma_sdesc_lo(buf_u, 16), dp = umma_sdesc_lo(p_u, 16);
-        // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
-        const uint32_t dv = umma_sdesc_lo(buf_u, kBlk);
-        int kp = 0, kt = count > 0 ? list[0].t0 : 0, vp = 0, vt = kt, ks_done = nt;  // next scores, next values
-        while (vp < count) {
-          if (kp < count) {
-            const int b = ks_done & 1;
-            if (kt == list[kp].t0) {  // this portion's queries
-              if (ok) ok = mbar_wait_small(&ct.qfull, (uint32_t)(nq & 1), abort);
-              ++nq;
-            }
-            const uint32_t to = tb + kScores + ((uint32_t)(16 * b) << 16);
+      // ---------------- products: S(0), then S(i + 1), O(i) by turns ----------------
+      const uint32_t tu = (uint32_t)uniform((int)tb);
+      const uint32_t id_s = umma_idesc_bf16(kRows, kTile, 0, 0) | (c.negate ? kNegateA : 0u);
+      const uint32_t id_o = umma_idesc_bf16(kRows, 256, 0, 1);
+      const uint32_t dq = (uint32_t)uniform((int)umma_sdesc_lo(q_u, 16)), dk = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, 16));
+      const uint32_t dp = (uint32_t)uniform((int)umma_sdesc_lo(p_u, 16));
+      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
+      const uint32_t dv = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, kBlk));
+      const int n = uniform(count);
+      // the next scores' and the next values' place: portion, tiles left in it, whether it is its first tile
+      int kp = 0, kl = 0, vp = 0, vl = 0, ahead = 0;
+      bool kfirst = true, vfirst = true;
+      if (n > 0) kl = vl = uniform(list[0].t1 - list[0].t0);
+      while (vp < n) {
+        if (kp < n && ahead < 2) {  // up to one tile of scores ahead of the values
+          const int i = nt + ahead, b = i & 1;
+          if (kfirst) {  // this portion's queries
+            if (ok) ok = uniform_wait(&ct.qfull, (uint32_t)(nq & 1), abort);
+            ++nq;
+          }
+          const uint32_t to = tu + kScores + ((uint32_t)(16 * b) << 16);
+          uint32_t x = 0u, y = dk + (uint32_t)(b * (kBuf >> 4));
 #pragma unroll 1
-            for (int part = 0; part < kParts; ++part) {
-              if (ok) ok = mbar_wait_small(&ct.full[b][part], (uint32_t)((ks_done >> 1) & 1), abort);
-              // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              tc_fence_after();
-              if (ok) {
-                const uint32_t x = (uint32_t)(part * (kChunks / kParts)) * (kBlk >> 4);
+          for (int part = 0; part < kParts; ++part) {
+            if (ok) ok = uniform_wait(&ct.full[b][part], (uint32_t)((i >> 1) & 1), abort);
+            // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_after();
+            if (ok && elect_one()) {
 #pragma unroll
-                for (int h = 0; h < kChunks / kParts; ++h)
+              for (int h = 0; h < kChunks / kParts; ++h)
 #pragma unroll
-                  for (int ks = 0; ks < 4; ++ks)
-                    umma_bf16_lo(to, dq + x + h * (kBlk >> 4) + 2 * ks, dk + (uint32_t)(b * (kBuf >> 4)) + x + h * (kBlk >> 4) + 2 * ks,
-                                 id_s, (part | h | ks) != 0 ? 1u : 0u);
-              }
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_bf16_lo(to, dq + x + h * (kBlk >> 4) + 2 * ks, y + x + h * (kBlk >> 4) + 2 * ks, id_s,
+                               (part | h | ks) != 0 ? 1u : 0u);
+              if (part == kParts - 1) umma_commit(&ct.s[b]);
             }
-            if (ok) umma_commit(&ct.s[b]);
-            ++ks_done;
-            if (++kt == list[kp].t1) {
-              ++kp;
-              if (kp < count) kt = list[kp].t0;
-            }
-            // one tile of scores ahead of the values, unless its queries differ: a portion's queries are
-            // replaced once its last scores are done
-            if (ks_done == nt + 1 && kp < count) continue;
+            __syncwarp();
+            x += (uint32_t)(kChunks / kParts) * (kBlk >> 4);
           }
-          const int b = nt & 1;
-          if (ok) ok = mbar_wait_small(&ct.p, (uint32_t)(nt & 1), abort);
-          tc_fence_after();
-          if (ok) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_bf16_lo(tb + ((uint32_t)(16 * h) << 16), dp + 2 * ks,
-                             dv + (uint32_t)(b * (kBuf >> 4) + 4 * h * (kBlk >> 4)) + 128 * ks, id_o,
-                             (vt != list[vp].t0 || ks != 0) ? 1u : 0u);
-            umma_commit(&ct.pv);
-            umma_commit(&ct.empty[b]);
-          }
-          ++nt;
-          if (++vt == list[vp].t1) {
-            ++vp;
-            if (vp < count) vt = list[vp].t0;
-          }
+          ++ahead;
+          kfirst = --kl == 0;
+          if (kfirst && ++kp < n) kl = uniform(list[kp].t1 - list[kp].t0);
+          if (ahead == 1 && kp < n) continue;
         }
+        const int b = nt & 1;
+        if (ok) ok = uniform_wait(&ct.p, (uint32_t)(nt & 1), abort);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          const uint32_t y = dv + (uint32_t)(b * (kBuf >> 4));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16_lo(tu + ((uint32_t)(16 * h) << 16), dp + 2 * ks, y + 4 * h * (kBlk >> 4) + 128 * ks, id_o,
+                           (!vfirst || ks != 0) ? 1u : 0u);
+          umma_commit(&ct.pv);
+          umma_commit(&ct.empty[b]);
+        }
+        __syncwarp();
+        ++nt;
+        --ahead;
+        vfirst = --vl == 0;
+        if (vfirst && ++vp < n) vl = uniform(list[vp].t1 - list[vp].t0);
       }
-      __syncwarp();
     } else {
       // ---------------- softmax: thread = row (lane & 15) of the warp's 16 ----------------
       // Lanes 0-15 hold the scores of even tiles and O's dims 0-255, lanes 16-31 those of odd tiles and
@@ -412,11 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after a wait that gave up, copies and products may still be in flight: they end before the CTA does
   volatile uint32_t never = 0u;
   if (warp == kWarpMma) {
-    if (lane == 0) {  // the thread whose products they are
-      umma_commit(&ct.fin);
-      mbar_wait_bounded(&ct.fin, 0u, &never);
-    }
+    if (elect_one()) umma_commit(&ct.fin);  // by the thread whose products they are
     __syncwarp();
+    warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
   if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
