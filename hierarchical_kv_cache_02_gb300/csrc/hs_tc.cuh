@@ -219,6 +219,17 @@ __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity, vol
   }
   return false;
 }
+__device__ __forceinline__ bool uniform_test(uint64_t* bar, uint32_t parity) {  // no wait
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __any_sync(0xffffffffu, ok != 0u);
+}
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // bounded wait of a whole warp: lane 0 waits, the result is the warp's

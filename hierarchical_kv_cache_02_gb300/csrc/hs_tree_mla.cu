@@ -22,7 +22,11 @@
 namespace {
 
 constexpr int kTile = 64, kRows = 64, kDim = 576, kValue = 512;
-constexpr int kChunks = kDim / 64, kParts = 3;    // 128-byte column blocks of a tile; a third of them to a barrier
+constexpr int kChunks = kDim / 64;                // 128-byte column blocks of a tile
+// A tile's blocks come and go in two parts: 0-3, the values' first half, and 4-8.
+constexpr int kParts = 2;
+__device__ __forceinline__ int part_from(int part) { return 4 * part; }
+__device__ __forceinline__ int part_blocks(int part) { return 4 + part; }
 constexpr int kBlk = 64 * 128;                    // bytes of one block of 64 rows
 constexpr int kBuf = kChunks * kBlk;              // a tile; also the queries
 constexpr int kProducers = 4, kWarpMma = 4, kWarpProd = 5;
@@ -42,7 +46,7 @@ struct MlaArgs {
 
 struct MlaControl {
   PlanState plan;
-  __align__(8) uint64_t full[2][kParts], empty[2];
+  __align__(8) uint64_t full[2][kParts], empty[2][kParts];
   uint64_t qfull, s[2], p, pv, mask[kMaskRing], fin;
   uint32_t valid[kMaskRing][kProducers];
   uint32_t tmem, abort;
@@ -60,8 +64,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort = &ct.abort;
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
-      for (int i = 0; i < kParts; ++i) mbar_init(&ct.full[b][i], kProducers * 32);
-      mbar_init(&ct.empty[b], 1u);
+      for (int i = 0; i < kParts; ++i) {
+        mbar_init(&ct.full[b][i], kProducers * 32);
+        mbar_init(&ct.empty[b][i], 1u);
+      }
       mbar_init(&ct.s[b], 1u);
     }
     mbar_init(&ct.qfull, 1u);
@@ -92,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // state that runs on through the rounds
   int nt = 0;                      // tiles so far, of each role
   int nq = 0;                      // portions so far (products); query loads (first softmax thread)
-  int sent = 0;                    // producers: tiles whose copies were issued
+  int sent = 0;                    // producers: tile parts whose copies were issued
   bool ok = true;
   uint32_t bad = 0u;
 
@@ -107,40 +113,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kp = 0, kt = ahead.at;
 #pragma unroll 1
       for (int x = -2; kp < count; ++x) {
-        ahead.step(a, list, count, kTile, 16 * pw + (lane & 15), c.ctx_rows, c.seg == 0 && lane < 16 ? kChunks : 0, &bad);
+        ahead.step(a, list, count, kTile, 16 * pw + (lane & 15), c.ctx_rows, lane < 16 ? kChunks : 0, &bad);
         if (x < 0) continue;  // the steps' head start
         const Portion& P = list[kp];
         const bool boxed = c.seg != 0 && kt * kTile + 16 * pw + 16 <= P.n;
         const int b = nt & 1;
-        if (ok) ok = warp_wait_small(&ct.empty[b], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
-        if (ok) {
-          const uint32_t dst = buf_u + (uint32_t)(b * kBuf + 16 * pw * 128);
-          const int row = __shfl_sync(0xffffffffu, ahead.row, 0);
+        const uint32_t dst = buf_u + (uint32_t)(b * kBuf + 16 * pw * 128);
+        const int row = __shfl_sync(0xffffffffu, ahead.row, 0);
 #pragma unroll 1
-          for (int part = 0; part < kParts; ++part) {
-            uint64_t* full = &ct.full[b][part];
-            const int ch0 = part * (kChunks / kParts);
-            if (boxed) {
-              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(kChunks / kParts * 16 * 128));
-              else mbar_arrive(full);
-              __syncwarp();
-              if (lane < kChunks / kParts)
-                tma_load_2d(dst + (uint32_t)((ch0 + lane) * kBlk), &segmap, 64 * (ch0 + lane), row, full);
-            } else {
-              // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
+        for (int part = 0; part < kParts; ++part) {
+          if (ok) ok = warp_wait_small(&ct.empty[b][part], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
+          if (!ok) continue;
+          uint64_t* full = &ct.full[b][part];
+          const int ch0 = part_from(part), nch = part_blocks(part);
+          if (boxed) {
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nch * 16 * 128));
+            else mbar_arrive(full);
+            __syncwarp();
+            if (lane < nch) tma_load_2d(dst + (uint32_t)((ch0 + lane) * kBlk), &segmap, 64 * (ch0 + lane), row, full);
+          } else {
+            // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int y = 4 * i + crow;
-                const uint64_t src = __shfl_sync(0xffffffffu, ahead.now, y);
-                const uint32_t to = dst + (uint32_t)(ch0 * kBlk + y * 128 + ((cch ^ (y & 7)) << 4)), n = src != 0ull ? 16u : 0u;
-                const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + 128 * ch0 + 16 * cch : (const uint8_t*)a.q;
+            for (int i = 0; i < 4; ++i) {
+              const int y = 4 * i + crow;
+              const uint64_t src = __shfl_sync(0xffffffffu, ahead.now, y);
+              const uint32_t to = dst + (uint32_t)(ch0 * kBlk + y * 128 + ((cch ^ (y & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+              const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + 128 * ch0 + 16 * cch : (const uint8_t*)a.q;
 #pragma unroll
-                for (int h = 0; h < kChunks / kParts; ++h) cp_async16_zfill(to + h * kBlk, src != 0ull ? from + 128 * h : from, n);
-              }
-              cp_async_arrive_noinc(full);
+              for (int h = 0; h < 5; ++h)
+                if (h < nch) cp_async16_zfill(to + h * kBlk, src != 0ull ? from + 128 * h : from, n);
             }
+            cp_async_arrive_noinc(full);
           }
-          sent = nt + 1;
+          sent = 2 * nt + part + 1;
         }
         const uint32_t word = __ballot_sync(0xffffffffu, ahead.now != 0ull) & 0xffffu;
         if (ok && lane == 0) {
@@ -154,7 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kWarpMma) {
-      // ---------------- products: S(0), then S(i + 1), O(i) by turns ----------------
+      // ---------------- products ----------------
+      // S(i) waits for tile i's records, O(i) for its weights, and S(i + 2) takes the buffer that O(i) leaves.
+      // Whichever is ready is issued, values first: they set a buffer free.
       const uint32_t tu = (uint32_t)uniform((int)tb);
       const uint32_t id_s = umma_idesc_bf16(kRows, kTile, 0, 0) | (c.negate ? kNegateA : 0u);
       const uint32_t id_o = umma_idesc_bf16(kRows, 256, 0, 1);
@@ -163,20 +170,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
       const uint32_t dv = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, kBlk));
       const int n = uniform(count);
-      // the next scores' and the next values' place: portion, tiles left in it, whether it is its first tile
+      // the next scores' and the next values' place: portion, tiles left in it, whether it is its first tile;
+      // ahead: tiles whose scores were issued and whose values were not
       int kp = 0, kl = 0, vp = 0, vl = 0, ahead = 0;
       bool kfirst = true, vfirst = true;
       if (n > 0) kl = vl = uniform(list[0].t1 - list[0].t0);
       while (vp < n) {
-        if (kp < n && ahead < 2) {  // up to one tile of scores ahead of the values
+        bool scores = ahead == 0;
+        if (kp < n && ahead == 1) {
+          const int i = nt + 1;
+#pragma unroll 1
+          for (uint32_t x = 0; ok && x < (1u << 22); ++x) {
+            if (uniform_test(&ct.p, (uint32_t)(nt & 1))) break;
+            scores = uniform_test(&ct.full[i & 1][0], (uint32_t)((i >> 1) & 1));
+            if (scores) break;
+          }
+        }
+        if (scores) {
           const int i = nt + ahead, b = i & 1;
           if (kfirst) {  // this portion's queries
             if (ok) ok = uniform_wait(&ct.qfull, (uint32_t)(nq & 1), abort);
             ++nq;
           }
           const uint32_t to = tu + kScores + ((uint32_t)(16 * b) << 16);
-          uint32_t x = 0u, y = dk + (uint32_t)(b * (kBuf >> 4));
-#pragma unroll 1
+          const uint32_t y = dk + (uint32_t)(b * (kBuf >> 4));
+#pragma unroll
           for (int part = 0; part < kParts; ++part) {
             if (ok) ok = uniform_wait(&ct.full[b][part], (uint32_t)((i >> 1) & 1), abort);
             // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
@@ -184,20 +202,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (ok && elect_one()) {
 #pragma unroll
-              for (int h = 0; h < kChunks / kParts; ++h)
+              for (int h = 4 * part; h < 4 + 5 * part; ++h)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                  umma_bf16_lo(to, dq + x + h * (kBlk >> 4) + 2 * ks, y + x + h * (kBlk >> 4) + 2 * ks, id_s,
-                               (part | h | ks) != 0 ? 1u : 0u);
+                  umma_bf16_lo(to, dq + h * (kBlk >> 4) + 2 * ks, y + h * (kBlk >> 4) + 2 * ks, id_s, (h | ks) != 0 ? 1u : 0u);
               if (part == kParts - 1) umma_commit(&ct.s[b]);
             }
             __syncwarp();
-            x += (uint32_t)(kChunks / kParts) * (kBlk >> 4);
           }
           ++ahead;
           kfirst = --kl == 0;
           if (kfirst && ++kp < n) kl = uniform(list[kp].t1 - list[kp].t0);
-          if (ahead == 1 && kp < n) continue;
+          continue;
         }
         const int b = nt & 1;
         if (ok) ok = uniform_wait(&ct.p, (uint32_t)(nt & 1), abort);
@@ -205,13 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && elect_one()) {
           const uint32_t y = dv + (uint32_t)(b * (kBuf >> 4));
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               umma_bf16_lo(tu + ((uint32_t)(16 * h) << 16), dp + 2 * ks, y + 4 * h * (kBlk >> 4) + 128 * ks, id_o,
                            (!vfirst || ks != 0) ? 1u : 0u);
+            umma_commit(&ct.empty[b][h]);
+          }
           umma_commit(&ct.pv);
-          umma_commit(&ct.empty[b]);
         }
         __syncwarp();
         ++nt;
@@ -423,10 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t t0 = global_ns();
     if (warp >= kWarpProd) {
 #pragma unroll 1
-      for (int i = max(0, sent - 2); i < sent; ++i)
-        for (int part = 0; part < kParts; ++part)
-          while (!mbar_try_wait(&ct.full[i & 1][part], (uint32_t)((i >> 1) & 1)) && global_ns() - t0 < 1000000000ull) {
-          }
+      for (int i = max(0, sent - 4); i < sent; ++i)
+        while (!mbar_try_wait(&ct.full[(i >> 1) & 1][i & 1], (uint32_t)((i >> 2) & 1)) && global_ns() - t0 < 1000000000ull) {
+        }
     } else if (warp == 0 && nq > 0) {
       while (!mbar_try_wait(&ct.qfull, (uint32_t)((nq - 1) & 1)) && global_ns() - t0 < 1000000000ull) {
       }
