@@ -384,15 +384,34 @@ __device__ __forceinline__ uint32_t good_pair(uint32_t w) {
   return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
 }
 
-// bits j0 .. j0 + 31 of a node's visibility among the nn nodes in use (bits before 0 are clear)
-__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int nn, int j0) {
+// bits j0 .. j0 + 31 of a node's visibility among the nn nodes in use (bits before 0 are clear); first: the
+// first word of m, at hand
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, uint64_t first, int words, int nn, int j0) {
   if (j0 <= -32 || j0 >= nn) return 0u;
   const int s = max(j0, 0), w = s >> 6, b = s & 63;
-  uint64_t x = m[w] >> b;
+  uint64_t x = (w == 0 ? first : m[w]) >> b;
   if (b > 32 && w + 1 < words) x |= m[w + 1] << (64 - b);
   uint32_t v = (uint32_t)x;
   if (nn - s < 32) v &= (1u << (nn - s)) - 1u;
   return v << (s - j0);
+}
+
+// Takes infinite and NaN values out of the rows [y0, y1) of a tile of `blocks` 128-byte column blocks of `rows`
+// rows each (the swizzle moves bytes within a row's 128 only).  Thread `id` of `threads`; true: it found some.
+__device__ __forceinline__ bool clean_rows(uint8_t* tile, int rows, int blocks, int y0, int y1, int id, int threads) {
+  bool found = false;
+#pragma unroll 1
+  for (int i = id; i < (y1 - y0) * blocks * 8; i += threads) {
+    const int x = i & 7, z = i >> 3, b = z % blocks, y = y0 + z / blocks;
+    uint4* at = (uint4*)(tile + b * (rows * 128) + y * 128 + 16 * x);
+    const uint4 u = *at;
+    if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
+      found = true;
+      *at = make_uint4(good_pair(u.x), good_pair(u.y), good_pair(u.z), good_pair(u.w));
+    }
+  }
+  if (found) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return found;
 }
 
 // ---- joining the partials of an item -------------------------------------------------------------
@@ -489,6 +508,18 @@ cudaError_t allow_smem(K kern, size_t bytes, bool* done) {
 }  // namespace
 
 // ---- host ------------------------------------------------------------------------------------------
+
+// The workspace: the tiles before each request, then (32-byte aligned, whatever the workspace's alignment)
+// the partials and their statistics.
+inline int64_t hs_tree_workspace_bytes(const hs_config* c, int64_t workers, int64_t rows, int64_t dims) {
+  return (int64_t)(c->num_requests + 1) * (int64_t)sizeof(int64_t) + 64 + workers * 2 * rows * (dims + 2) * (int64_t)sizeof(float);
+}
+inline void hs_tree_workspace(void* w, const hs_config* c, int64_t workers, int64_t rows, int64_t dims, long long** prefix,
+                              float** part, float** ml) {
+  *prefix = (long long*)w;
+  *part = (float*)(((uintptr_t)(*prefix + c->num_requests + 1) + 31u) & ~(uintptr_t)31u);
+  *ml = *part + workers * 2 * rows * dims;
+}
 
 // Launch plans of the tensor-core kernels.  `usable`: the shape is theirs.
 struct hs_tree_plan {

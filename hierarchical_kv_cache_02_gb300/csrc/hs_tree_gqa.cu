@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_ok = row < c.G * c.MT && t < P.nn;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         const uint64_t* mw = a.mask + ((int64_t)P.r * a.T + (row_ok ? t : 0)) * a.words;
+        const uint64_t mfirst = mw[0];
         float m = -INFINITY, l = 0.f;
         bool dirty = false;  // a node's value is infinite or NaN
         for (int tile = P.t0; tile < P.t1; ++tile) {
@@ -406,29 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 4; ++x) {
               const int jw = j0 + 32 * x;
               const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
-              w[x] &= ctx | (row_ok ? mask_bits(mw, a.words, P.nn, jw) : 0u);
+              w[x] &= ctx | (row_ok ? mask_bits(mw, mfirst, a.words, P.nn, jw) : 0u);
             }
             if (ok) ok = mbar_wait_small(&ct.v[g], (uint32_t)(nv & 1), abort);
             ok = __all_sync(0xffffffffu, ok);
             ++nv;
-            bool d = false;
-            if (ok && j0 + row >= 0 && j0 + row < P.nn) {
-              const int vs = ct.vslot[g];
-#pragma unroll 1
-              for (int b = both ? g : 0; b < C::kCh; b += both ? 2 : 1) {
-                uint4* vr = (uint4*)(smem + 2 * C::kSlot + vs * C::kSlot + b * C::kBlk + row * 128);
-#pragma unroll 2
-                for (int x = 0; x < 8; ++x) {
-                  uint4 u = vr[x];
-                  if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
-                    d = true;
-                    u = make_uint4(good_pair(u.x), good_pair(u.y), good_pair(u.z), good_pair(u.w));
-                    vr[x] = u;
-                  }
-                }
-              }
-            }
-            if (d) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const bool d = ok && clean_rows(smem + 2 * C::kSlot + ct.vslot[g] * C::kSlot, kTile, C::kCh, max(0, -j0),
+                                            min(kTile, P.nn - j0), both ? tid : row, both ? 256 : 128);
             if (bar_or(both ? 3 : 1 + g, both ? 256 : 128, d)) dirty = true;
           }
           ++nm;
@@ -535,9 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv), pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
                                       pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
               } else {
-                float4* dst = (float4*)(c.ws.part + prow * D + 32 * x);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                for (int y = 0; y < 4; ++y) st_global_v8(c.ws.part + prow * D + 32 * x + 8 * y, o + 8 * y);
               }
             }
           }
@@ -603,8 +587,6 @@ bool plan_of(const hs_config* c, int T, int sms, Plan* p) {
   return true;
 }
 
-int64_t part_floats(const Plan& p) { return (int64_t)p.workers * 2 * p.rows * p.D; }
-
 template <int D>
 cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& seg, const CombineArgs& cb,
                    cudaStream_t st) {
@@ -622,9 +604,7 @@ cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q
 hs_tree_plan hs_tree_gqa_plan(const hs_config* c, int nodes, int num_sms) {
   Plan p;
   hs_tree_plan r = {plan_of(c, nodes, num_sms, &p), 0};
-  if (r.usable)
-    r.workspace = (int64_t)((c->num_requests + 1) * sizeof(int64_t) + 15) / 16 * 16 +
-                  (part_floats(p) + (int64_t)p.workers * 2 * p.rows * 2) * (int64_t)sizeof(float);
+  if (r.usable) r.workspace = hs_tree_workspace_bytes(c, p.workers, p.rows, p.D);
   return r;
 }
 
@@ -638,14 +618,11 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.np = p.np;
   c.shared = p.shared;
   c.nmt = p.nmt;
-  uint8_t* w = (uint8_t*)g->d_workspace;
   c.ws.items = p.items;
   c.ws.np = p.np;
   c.ws.groups = p.shared ? 1 : 2;
   c.ws.rows = p.rows;
-  c.ws.prefix = (long long*)w;
-  c.ws.part = (float*)(w + (int64_t)((cfg->num_requests + 1) * sizeof(int64_t) + 15) / 16 * 16);
-  c.ws.ml = c.ws.part + part_floats(p);
+  hs_tree_workspace(g->d_workspace, cfg, p.workers, p.rows, p.D, &c.ws.prefix, &c.ws.part, &c.ws.ml);
   if (c.a.qscale < 0.f) {
     c.negate = 1;
     c.a.qscale = -c.a.qscale;

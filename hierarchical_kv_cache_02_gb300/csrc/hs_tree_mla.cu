@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_ok = t < P.nn;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         const uint64_t* mw = a.mask + ((int64_t)P.r * a.T + (row_ok ? t : 0)) * a.words;
+        const uint64_t mfirst = mw[0];
         float m = -INFINITY, l = 0.f;
         bool dirty = false;  // a node's value is infinite or NaN
         for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
@@ -277,30 +278,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
               const int jw = j0 + 32 * x;
               const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
-              w[x] &= ctx | (row_ok ? mask_bits(mw, a.words, P.nn, jw) : 0u);
+              w[x] &= ctx | (row_ok ? mask_bits(mw, mfirst, a.words, P.nn, jw) : 0u);
             }
             // infinite and NaN values would reach every row of the product: they are taken out here and
             // added to the rows that see them at the end.  Their scores are done.
-            bool d = false;
-            const int y = tid & 63;
             for (int i = 0; i < kParts; ++i)
               if (ok) ok = mbar_wait_small(&ct.full[b][i], (uint32_t)((nt >> 1) & 1), abort);
-            if (ok && j0 + y >= 0 && j0 + y < P.nn) {
-#pragma unroll 1
-              for (int ch = tid >> 6; ch < kValue / 64; ch += 2) {
-                uint4* vr = (uint4*)(smem + kBuf + kBlk + b * kBuf + ch * kBlk + y * 128);
-#pragma unroll 2
-                for (int x = 0; x < 8; ++x) {
-                  uint4 u = vr[x];
-                  if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
-                    d = true;
-                    u = make_uint4(good_pair(u.x), good_pair(u.y), good_pair(u.z), good_pair(u.w));
-                    vr[x] = u;
-                  }
-                }
-              }
-            }
-            if (d) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const bool d = ok && clean_rows(smem + kBuf + kBlk + b * kBuf, kTile, kValue / 64, max(0, -j0), min(kTile, P.nn - j0), tid, 128);
             if (bar_or(1, 128, d)) dirty = true;
             ok = __all_sync(0xffffffffu, ok);
           }
@@ -408,9 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   dst[y] = make_uint4(pack_bf16(o[8 * y] * inv, o[8 * y + 1] * inv), pack_bf16(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
                                       pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
               } else {
-                float4* dst = (float4*)(c.ws.part + prow * kValue + dim);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                for (int y = 0; y < 4; ++y) st_global_v8(c.ws.part + prow * kValue + dim + 8 * y, o + 8 * y);
               }
             }
           }
@@ -461,27 +444,23 @@ bool usable(const hs_config* c) {
          (int64_t)c->num_requests * HS_MAX_TREE_NODES * c->num_q_heads <= (int64_t)INT32_MAX;
 }
 int items_of(const hs_config* c, int T) { return (T * c->num_q_heads + kRows - 1) / kRows; }
-int64_t prefix_bytes(const hs_config* c) { return ((int64_t)(c->num_requests + 1) * (int64_t)sizeof(int64_t) + 15) / 16 * 16; }
 
 }  // namespace
 
 hs_tree_plan hs_tree_mla_plan(const hs_config* c, int nodes, int num_sms) {
   hs_tree_plan r = {usable(c), 0};
-  if (r.usable) r.workspace = prefix_bytes(c) + (int64_t)num_sms * 2 * kRows * (kValue + 2) * (int64_t)sizeof(float);
+  if (r.usable) r.workspace = hs_tree_workspace_bytes(c, num_sms, kRows, kValue);
   return r;
 }
 
 int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* tree_args, int num_sms, cudaStream_t st) {
   MlaArgs c{};
   c.a = *(const TreeArgs*)tree_args;
-  uint8_t* w = (uint8_t*)g->d_workspace;
   c.ws.items = items_of(cfg, g->nodes);
   c.ws.np = 1;
   c.ws.groups = 1;
   c.ws.rows = kRows;
-  c.ws.prefix = (long long*)w;
-  c.ws.part = (float*)(w + prefix_bytes(cfg));
-  c.ws.ml = c.ws.part + (int64_t)num_sms * 2 * kRows * kValue;
+  hs_tree_workspace(g->d_workspace, cfg, num_sms, kRows, kValue, &c.ws.prefix, &c.ws.part, &c.ws.ml);
   if (c.a.qscale < 0.f) {
     c.negate = 1;
     c.a.qscale = -c.a.qscale;
