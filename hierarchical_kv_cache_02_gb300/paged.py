@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .pool import HsConfig, _check, _dev_tensor, _stream_ptr, _tree_args, _tree_nodes
+from .pool import HsConfig, _check, _dev_tensor, _fast_ptr, _fast_stream, _tree_args, _tree_nodes
 
 
 class RopeTable:
@@ -69,6 +69,12 @@ def _strided(t, n, heads, dim, name, device, written=False):
     """Pointer, token stride and head stride of a bf16 [n][heads][dim] view ([n][dim] when heads is 1)."""
     import torch
 
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (n, heads, dim) and t.get_device() == device:
+        ts, hs, vs = t.stride()
+        p = t.data_ptr()
+        if vs == 1 and n > 1 and heads > 1 and not (ts | hs | p >> 1) & 7 and (not written or (ts >= dim and hs >= dim)):
+            return p, ts, hs  # what most calls pass; the rest is looked at one by one
+
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda" or t.device.index != device:
@@ -104,6 +110,7 @@ class PagedKV:
         self.lib = _lib.load()
         self.cfg, self.device = cfg, pages.device.index
         self._c = cfg.to_c()
+        self._tree_sizes = {}
         R = cfg.num_requests
         p = _dev_tensor(pages, torch.bfloat16, (pages.shape[0], pages.shape[1], cfg.record_elems), "pages", self.device)
         t = None
@@ -143,9 +150,9 @@ class PagedKV:
             raise ValueError("a shared latent has no v" if mla else "v is missing")
         if v is not None:
             vp, vt, vh = _strided(v, N, c.num_kv_heads, c.head_dim_v, "v", self.device)
-        cup = _dev_tensor(cu, torch.int32, (c.num_requests + 1,), "cu", self.device)
-        sp = _dev_tensor(start, torch.int64, (c.num_requests,), "start", self.device)
-        rp = None if rope_pos is None else _dev_tensor(rope_pos, torch.int64, (N,), "rope_pos", self.device)
+        cup = _fast_ptr(cu, torch.int32, (c.num_requests + 1,), "cu", self.device)
+        sp = _fast_ptr(start, torch.int64, (c.num_requests,), "start", self.device)
+        rp = None if rope_pos is None else _fast_ptr(rope_pos, torch.int64, (N,), "rope_pos", self.device)
         turns, rd, il = None, 0, 0
         if rope is not None:
             if rope.device != self.device:
@@ -161,7 +168,7 @@ class PagedKV:
             if qd != c.head_dim_qk and (qd != rd or qd == 0):
                 raise ValueError("the last dim of q must be head_dim_qk or rotary_dim")
             if q_out is None:
-                with torch.cuda.stream(stream):
+                with torch.cuda.stream(stream):  # None: the current one
                     q_out = torch.empty((N, c.num_q_heads, qd), dtype=torch.bfloat16, device=q.device)
             qp, qt, qh = _strided(q, N, c.num_q_heads, qd, "q", self.device)
             op, ot, oh = _strided(q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
@@ -170,7 +177,7 @@ class PagedKV:
         a = _lib.hs_append_args(N, cup, sp, rp, kp, kt, kh, vp, vt, vh, turns, rd, int(rotary_offset), il, qp, qt, qh, op,
                                 ot, oh, qd)
         _check("hs_append_rotated", self.lib.hs_append_rotated(ctypes.byref(self._c), ctypes.byref(self._kv),
-                                                               ctypes.byref(a), _stream_ptr(stream, self.device)))
+                                                               ctypes.byref(a), _fast_stream(torch, stream, self.device)))
         return q_out
 
     def tree_attn(self, q, lens, mask, locs=None, nodes=None, out=None, scale=None, stream=None):
@@ -183,16 +190,17 @@ class PagedKV:
 
         c = self.cfg
         T = _tree_nodes(q)
-        lp = _dev_tensor(lens, torch.int64, (c.num_requests,), "lens", self.device)
-        args, out, _ws = _tree_args(self.lib, self._c, c, self.device, q, T, mask, nodes, out, scale, stream)
+        lp = _fast_ptr(lens, torch.int64, (c.num_requests,), "lens", self.device)
+        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, T, mask, nodes, out, scale,
+                                    stream)
         args.d_len = lp
         if locs is not None:
             if locs.dim() != 2 or locs.shape[1] < 1:
                 raise ValueError("locs must be [R][k] with k >= 1")
-            args.d_locs = _dev_tensor(locs, torch.int32, (c.num_requests, locs.shape[1]), "locs", self.device)
+            args.d_locs = _fast_ptr(locs, torch.int32, (c.num_requests, locs.shape[1]), "locs", self.device)
             args.top_k = int(locs.shape[1])
         _check("hs_tree_attn", self.lib.hs_tree_attn(ctypes.byref(self._c), ctypes.byref(self._kv), ctypes.byref(args),
-                                                     _stream_ptr(stream, self.device)))
+                                                     _fast_stream(torch, stream, self.device)))
         return out
 
     def keep_path(self, lens, path, count, stream=None):
@@ -203,11 +211,11 @@ class PagedKV:
         R = self.cfg.num_requests
         if not isinstance(path, torch.Tensor) or path.dim() != 2:
             raise ValueError("path must be a tensor [R][P]")
-        lp = _dev_tensor(lens, torch.int64, (R,), "lens", self.device)
-        pp = _dev_tensor(path, torch.int32, (R, path.shape[1]), "path", self.device)
-        cp = _dev_tensor(count, torch.int32, (R,), "count", self.device)
+        lp = _fast_ptr(lens, torch.int64, (R,), "lens", self.device)
+        pp = _fast_ptr(path, torch.int32, (R, path.shape[1]), "path", self.device)
+        cp = _fast_ptr(count, torch.int32, (R,), "count", self.device)
         _check("hs_keep_path", self.lib.hs_keep_path(ctypes.byref(self._c), ctypes.byref(self._kv), lp, pp,
-                                                     int(path.shape[1]), cp, _stream_ptr(stream, self.device)))
+                                                     int(path.shape[1]), cp, _fast_stream(torch, stream, self.device)))
 
     def errors(self, reset: bool = False) -> int:
         """The DEVERR_* bits that the calls so far recorded (synchronises the device)."""

@@ -104,26 +104,50 @@ def _tree_nodes(q) -> int:
     return int(q.shape[1])
 
 
-def _tree_args(lib, c_cfg, cfg, device, q, T, mask, nodes, out, scale, stream):
-    """Check and marshal what both forms of the tree attention take; returns the C arguments, the
-    output and the workspace.  The workspace is this call's own, allocated on the stream that uses it."""
-    import torch
+def _fast_ptr(t, dtype, shape, name, device):
+    """Address of a tensor that _dev_tensor accepts; whatever does not pass at first sight goes there."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev_tensor(t, dtype, shape, name, device).value
 
-    R, words = cfg.num_requests, (T + 63) // 64
-    qp = _dev_tensor(q, torch.bfloat16, (R, T, cfg.num_q_heads, cfg.head_dim_qk), "q", device)
-    mp = _dev_tensor(mask, torch.int64, (R, T, words), "mask", device)
-    np_ = None if nodes is None else _dev_tensor(nodes, torch.int32, (R,), "nodes", device)
-    need = lib.hs_tree_attn_workspace(ctypes.byref(c_cfg), T, device)
-    if need < 0:
-        raise HsError("hs_tree_attn_workspace", int(need))
+
+def _fast_stream(torch, stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _tree_args(torch, lib, c_cfg, cfg, device, sizes, q, T, mask, nodes, out, scale, stream):
+    """Check and marshal what both forms of the tree attention take; returns the C arguments, the
+    output and the workspace.  The workspace is this call's own, allocated on the stream that uses it;
+    `sizes` keeps its bytes by T."""
+    R, Hq = cfg.num_requests, cfg.num_q_heads
+    qp = _fast_ptr(q, torch.bfloat16, (R, T, Hq, cfg.head_dim_qk), "q", device)
+    mp = _fast_ptr(mask, torch.int64, (R, T, (T + 63) // 64), "mask", device)
+    np_ = None if nodes is None else _fast_ptr(nodes, torch.int32, (R,), "nodes", device)
+    need = sizes.get(T)
+    if need is None:
+        need = lib.hs_tree_attn_workspace(ctypes.byref(c_cfg), T, device)
+        if need < 0:
+            raise HsError("hs_tree_attn_workspace", int(need))
+        sizes[T] = need
     ws = None
-    if out is None or need > 0:
+    if stream is None:
+        if out is None:
+            out = torch.empty((R, T, Hq, cfg.head_dim_v), dtype=torch.bfloat16, device=q.device)
+        if need > 0:
+            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    else:
         with torch.cuda.stream(stream):
             if out is None:
-                out = torch.empty((R, T, cfg.num_q_heads, cfg.head_dim_v), dtype=torch.bfloat16, device=f"cuda:{device}")
+                out = torch.empty((R, T, Hq, cfg.head_dim_v), dtype=torch.bfloat16, device=q.device)
             if need > 0:
-                ws = torch.empty((need,), dtype=torch.uint8, device=f"cuda:{device}")
-    op = _dev_tensor(out, torch.bfloat16, (R, T, cfg.num_q_heads, cfg.head_dim_v), "out", device)
+                ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    op = _fast_ptr(out, torch.bfloat16, (R, T, Hq, cfg.head_dim_v), "out", device)
     s = cfg.default_scale if scale is None else float(scale)
     args = _lib.hs_tree_args(qp, None, None, 0, mp, np_, T, s, op, ws.data_ptr() if ws is not None else None, need)
     return args, out, ws
@@ -137,6 +161,7 @@ class HsPool:
         self.cfg = cfg
         self.device = int(device)
         self._c = cfg.to_c()
+        self._tree_sizes = {}
         h = ctypes.c_void_p()
         _check("hs_pool_create", self.lib.hs_pool_create(ctypes.byref(self._c), self.device, ctypes.byref(h)))
         self._h = h
@@ -285,12 +310,13 @@ class HsPool:
 
         c = self.cfg
         T = _tree_nodes(q)
-        lo = _dev_tensor(locs, torch.int32, (c.num_requests, c.top_k), "locs", self.device)
-        d = _dev_tensor(draft, torch.bfloat16, (c.num_requests, T, c.record_elems), "draft", self.device)
-        args, out, _ws = _tree_args(self.lib, self._c, c, self.device, q, T, mask, nodes, out, scale, stream)
+        lo = _fast_ptr(locs, torch.int32, (c.num_requests, c.top_k), "locs", self.device)
+        d = _fast_ptr(draft, torch.bfloat16, (c.num_requests, T, c.record_elems), "draft", self.device)
+        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, T, mask, nodes, out, scale,
+                                    stream)
         args.d_locs, args.top_k = lo, c.top_k
         _check("hs_pool_tree_attn", self.lib.hs_pool_tree_attn(self._h, int(layer), ctypes.byref(args), d,
-                                                               _stream_ptr(stream, self.device)))
+                                                               _fast_stream(torch, stream, self.device)))
         return out
 
     # -- counters and inspection (synchronous) --------------------------------------
