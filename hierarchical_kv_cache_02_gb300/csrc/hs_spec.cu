@@ -18,8 +18,20 @@ namespace {
 // The angle is reduced in integers: a * turns_j mod 2^64 is the fraction of a turn exactly, so far
 // positions lose nothing; its top 32 bits, as a signed number of half turns, go through sincospif.
 
+// A CTA takes a few tokens: their records' places and the sines and cosines, shared by all heads, first; then
+// units of two 16-byte vectors, two of them in flight per thread at 40 registers (six CTAs an SM).  Few tokens
+// spread over many CTAs, each with a share of every token's units.  16384 tokens of 32 + 8 + 8 heads of 128:
+// 67.5 us, 5.97 TB/s (four units in flight at 64 registers 73.6 us, one 68.1; 8 or 16 tokens a CTA 72 and 83 us, one 74).
+
 constexpr int kAppThreads = 256;
-constexpr int kAppTokens = 4;  // tokens of a CTA
+constexpr int kAppTokens = 4;   // tokens of a CTA at most
+constexpr int kAppFlight = 2;   // units a thread loads before it stores
+
+// i / d by a multiplication with ceil(2^32 / d): exact while i * d < 2^32
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1u ? i : __umulhi(i, m); }
+};
 
 struct AppendArgs {
   PagedRows kv;
@@ -30,8 +42,10 @@ struct AppendArgs {
   uint16_t* q_out;
   const uint64_t* turns;
   int64_t kts, khs, vts, vhs, qts, qhs, ots, ohs;  // strides in values
-  int R, N, Hkv, Hq, dqk, dv;                      // dv = 0: the record is the key alone (shared latent)
+  int R, N, dqk, dv;                               // dv = 0: the record is the key alone (shared latent)
   int half, k_off, q_off, q_dim, interleaved;      // half = rotary_dim / 2
+  int kn, vn, per_cta, tokens;                     // units of a token's keys and values, units and tokens of a CTA
+  Div all, kh, vh, qh, angles;                     // units of a token, of a head of each kind; pairs
 };
 
 struct Vec8 {
@@ -51,82 +65,71 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *(const uint32_t*)&v;
 }
 
-// Units of one head: each moves 8 or 16 values.  A half-form unit u < half / 8 turns values 8u.. with
-// their partners half further on; an interleaved unit u < half / 4 turns the four pairs of values 8u..;
-// the remaining units copy 8 values each.
-__device__ __forceinline__ int head_units(int dim, int half, int interleaved) {
-  return interleaved ? dim / 8 : dim / 8 - half / 8;
+// four neighbouring pairs (cs: 16-byte aligned, as a multiple of four pairs)
+__device__ __forceinline__ void turn(Vec8& v, const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float4 c = *(const float4*)(cs + i);
+    const float p0 = lo(v.w[i]), r0 = hi(v.w[i]), p1 = lo(v.w[i + 1]), r1 = hi(v.w[i + 1]);
+    v.w[i] = pack(p0 * c.x - r0 * c.y, r0 * c.x + p0 * c.y);
+    v.w[i + 1] = pack(p1 * c.z - r1 * c.w, r1 * c.z + p1 * c.w);
+  }
 }
 
-__device__ __forceinline__ void turn_unit(const uint16_t* src, uint16_t* dst, int u, int off, int half, int interleaved,
-                                          const float2* cs) {
-  if (interleaved) {
-    const int d = 8 * u;  // values in record order; the rotated ones are [off, off + 2 half)
-    Vec8 x = ld8(src + d);
-    const int j = (d - off) >> 1;
-    if (d >= off && j < half) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 c = cs[j + i];
-        const float a = lo(x.w[i]), b = hi(x.w[i]);
-        x.w[i] = pack(a * c.x - b * c.y, b * c.x + a * c.y);
-      }
-    }
-    st8(dst + d, x);
-    return;
-  }
-  if (u < half / 8) {
-    const int j = 8 * u;
-    Vec8 x = ld8(src + off + j), y = ld8(src + off + half + j);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 c0 = cs[j + 2 * i], c1 = cs[j + 2 * i + 1];
-      const float a0 = lo(x.w[i]), a1 = hi(x.w[i]), b0 = lo(y.w[i]), b1 = hi(y.w[i]);
-      x.w[i] = pack(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-      y.w[i] = pack(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
-    }
-    st8(dst + off + j, x);
-    st8(dst + off + half + j, y);
-    return;
-  }
-  int d = 8 * (u - half / 8);  // the values that are only copied: before and behind the rotated ones
-  if (d >= off) d += 2 * half;
-  st8(dst + d, ld8(src + d));
+// Units of one head, two vectors of 8 values each.  Half form: unit u < half / 8 turns values 8u.. with their
+// partners half further on; the rest of the head, before and behind the rotary values, is copied, two vectors a
+// unit.  Interleaved: unit u holds values 16u.., each vector turned when it is a rotary one.
+int head_units(int dim, int half, int interleaved) {
+  return interleaved ? (dim + 15) / 16 : half / 8 + (dim - 2 * half + 15) / 16;
 }
 
-__global__ void __launch_bounds__(kAppThreads) k_append_rotated(AppendArgs a) {
-  extern __shared__ float2 s_cs[];                 // [kAppTokens][half] cosine and sine of each pair
+// One unit: where it reads and writes, and how it turns.
+struct Unit {
+  const uint16_t* src;  // null: nothing to do
+  uint16_t* dst;
+  int second;           // values to the second vector, 0: none
+  int cs, cs2;          // first pair of each vector in the table of sines and cosines, -1: copied
+};
+
+__global__ void __launch_bounds__(kAppThreads, 6) k_append_rotated(AppendArgs a) {
+  extern __shared__ __align__(16) float2 s_cs[];   // [tokens][half] cosine and sine of each pair
   __shared__ int64_t s_row[kAppTokens], s_pos[kAppTokens];  // record row (-1: not stored), angle position
   __shared__ int s_live[kAppTokens];
   hs_pdl_wait();
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * kAppTokens, nt = min(kAppTokens, a.N - t0);
-  if (tid < nt) {
-    const int t = t0 + tid;
-    // the last request whose first token is not behind t
-    int x = 0, y = a.R;
-    while (y - x > 1) {
-      const int m = (x + y) >> 1;
-      if (a.cu[m] <= t) x = m;
-      else y = m;
+  const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.N - t0);
+  for (int w = tid >> 5; w < nt; w += kAppThreads / 32) {  // a warp a token
+    const int lane = tid & 31, t = t0 + w;
+    const int64_t given = a.rope_pos != nullptr ? a.rope_pos[t] : 0;
+    // the last request whose first token is not behind t: 32 places of the rest are looked at at a time
+    int x = 0, n = a.R;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, at = lane * step;
+      const bool before = at < n && a.cu[x + at] <= t;
+      const int c = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0);
+      x += c * step;
+      n = min(step, n - c * step);
     }
-    const int c0 = a.cu[x], c1 = a.cu[x + 1];
-    const bool live = c0 <= t && t < c1;
-    int64_t row = -1, pos = 0;
-    if (live) {
-      uint32_t bad = 0u;
-      pos = a.start[x] + (t - c0);
-      row = paged_row(a.kv, x, pos, (uint32_t)HS_DEVERR_APPEND, &bad);
-      report(a.kv.err, bad);
-      if (a.rope_pos != nullptr) pos = a.rope_pos[t];
+    if (lane == 0) {
+      const int c0 = a.cu[x], c1 = a.cu[x + 1];
+      const int64_t st = a.start[x];
+      const bool live = c0 <= t && t < c1;
+      int64_t row = -1, pos = 0;
+      if (live) {
+        uint32_t bad = 0u;
+        pos = st + (t - c0);
+        row = paged_row(a.kv, x, pos, (uint32_t)HS_DEVERR_APPEND, &bad);
+        if (blockIdx.y == 0) report(a.kv.err, bad);
+        if (a.rope_pos != nullptr) pos = given;
+      }
+      s_live[w] = live;
+      s_row[w] = row;
+      s_pos[w] = pos;
     }
-    s_live[tid] = live;
-    s_row[tid] = row;
-    s_pos[tid] = pos;
   }
   __syncthreads();
-  for (int i = tid; i < nt * a.half; i += kAppThreads) {
-    const int t = i / a.half, j = i - t * a.half;
+  for (uint32_t i = tid; i < (uint32_t)(nt * a.half); i += kAppThreads) {
+    const uint32_t t = a.angles(i), j = i - t * a.angles.d;
     const uint64_t turn = (uint64_t)s_pos[t] * a.turns[j];
     float s, c;
     sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
@@ -134,34 +137,87 @@ __global__ void __launch_bounds__(kAppThreads) k_append_rotated(AppendArgs a) {
   }
   __syncthreads();
   const int head_rec = a.dqk + a.dv;
-  // keys
-  const int ku = head_units(a.dqk, a.half, a.interleaved), kn = a.Hkv * ku;
-  for (int i = tid; i < nt * kn; i += kAppThreads) {
-    const int t = i / kn, w = i - t * kn, h = w / ku, u = w - h * ku;
-    if (s_row[t] < 0) continue;
-    turn_unit(a.k + (int64_t)(t0 + t) * a.kts + (int64_t)h * a.khs,
-              (uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + h * head_rec, u, a.k_off, a.half, a.interleaved,
-              s_cs + t * a.half);
-  }
-  // values
-  if (a.dv > 0) {
-    const int vu = a.dv / 8, vn = a.Hkv * vu;
-    for (int i = tid; i < nt * vn; i += kAppThreads) {
-      const int t = i / vn, w = i - t * vn, h = w / vu, u = w - h * vu;
-      if (s_row[t] < 0) continue;
-      st8((uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + h * head_rec + a.dqk + 8 * u,
-          ld8(a.v + (int64_t)(t0 + t) * a.vts + (int64_t)h * a.vhs + 8 * u));
+  const uint32_t end = min((uint32_t)(nt * (int)a.all.d), (blockIdx.y + 1) * (uint32_t)a.per_cta);
+  for (uint32_t i0 = blockIdx.y * (uint32_t)a.per_cta + tid; i0 < end; i0 += kAppFlight * kAppThreads) {
+    Unit un[kAppFlight];
+    Vec8 x[kAppFlight], y[kAppFlight];
+#pragma unroll
+    for (int f = 0; f < kAppFlight; ++f) {
+      const uint32_t i = i0 + f * kAppThreads;
+      Unit& n = un[f];
+      n.src = nullptr;
+      if (i >= end) continue;
+      const uint32_t t = a.tokens == 1 ? 0u : a.all(i), w = i - t * a.all.d;
+      const int64_t tok = t0 + (int)t;
+      int u, off, dim;
+      bool value = false;
+      if (w < (uint32_t)a.kn) {
+        if (s_row[t] < 0) continue;
+        const uint32_t h = a.kh(w);
+        u = (int)(w - h * a.kh.d);
+        off = a.k_off;
+        dim = a.dqk;
+        n.src = a.k + tok * a.kts + (int64_t)h * a.khs;
+        n.dst = (uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + (int)h * head_rec;
+      } else if (w < (uint32_t)(a.kn + a.vn)) {
+        if (s_row[t] < 0) continue;
+        const uint32_t v = w - a.kn, h = a.vh(v);
+        u = (int)(v - h * a.vh.d);
+        off = 0;
+        dim = a.dv;
+        value = true;
+        n.src = a.v + tok * a.vts + (int64_t)h * a.vhs;
+        n.dst = (uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + (int)h * head_rec + a.dqk;
+      } else {
+        if (!s_live[t]) continue;
+        const uint32_t v = w - a.kn - a.vn, h = a.qh(v);
+        u = (int)(v - h * a.qh.d);
+        off = a.q_off;
+        dim = a.q_dim;
+        n.src = a.q + tok * a.qts + (int64_t)h * a.qhs;
+        n.dst = a.q_out + tok * a.ots + (int64_t)h * a.ohs;
+      }
+      int d;  // the unit's first value
+      n.cs = n.cs2 = -1;
+      if (!value && a.interleaved) {
+        // d and off are multiples of 8: a vector is rotary or it is not
+        d = 16 * u;
+        n.second = d + 8 < dim ? 8 : 0;
+        const int j = (d - off) >> 1;
+        if (d >= off && j < a.half) n.cs = (int)t * a.half + j;
+        if (d + 8 >= off && j + 4 < a.half) n.cs2 = (int)t * a.half + j + 4;
+      } else if (!value && 8 * u < a.half) {
+        d = off + 8 * u;
+        n.second = a.half;
+        n.cs = (int)t * a.half + 8 * u;
+      } else {  // copied
+        const int gap = value ? 0 : 2 * a.half, from = value ? dim : off, v = 16 * u - (value ? 0 : 2 * a.half);
+        d = v + (v >= from ? gap : 0);
+        n.second = v + 8 < dim - gap ? v + 8 + (v + 8 >= from ? gap : 0) - d : 0;
+      }
+      n.src += d;
+      n.dst += d;
+      x[f] = ld8(n.src);
+      if (n.second != 0) y[f] = ld8(n.src + n.second);
     }
-  }
-  // queries
-  if (a.q != nullptr) {
-    const int qu = head_units(a.q_dim, a.half, a.interleaved), qn = a.Hq * qu;
-    for (int i = tid; i < nt * qn; i += kAppThreads) {
-      const int t = i / qn, w = i - t * qn, h = w / qu, u = w - h * qu;
-      if (!s_live[t]) continue;
-      turn_unit(a.q + (int64_t)(t0 + t) * a.qts + (int64_t)h * a.qhs,
-                a.q_out + (int64_t)(t0 + t) * a.ots + (int64_t)h * a.ohs, u, a.q_off, a.half, a.interleaved,
-                s_cs + t * a.half);
+#pragma unroll
+    for (int f = 0; f < kAppFlight; ++f) {
+      const Unit& n = un[f];
+      if (n.src == nullptr) continue;
+      if (!a.interleaved && n.cs >= 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 c = *(const float4*)&s_cs[n.cs + 2 * i];  // two pairs: cosine, sine, cosine, sine
+          const float a0 = lo(x[f].w[i]), a1 = hi(x[f].w[i]), b0 = lo(y[f].w[i]), b1 = hi(y[f].w[i]);
+          x[f].w[i] = pack(a0 * c.x - b0 * c.y, a1 * c.z - b1 * c.w);
+          y[f].w[i] = pack(b0 * c.x + a0 * c.y, b1 * c.z + a1 * c.w);
+        }
+      } else {
+        if (n.cs >= 0) turn(x[f], s_cs + n.cs);
+        if (n.cs2 >= 0) turn(y[f], s_cs + n.cs2);
+      }
+      st8(n.dst, x[f]);
+      if (n.second != 0) st8(n.dst + n.second, y[f]);
     }
   }
 }
@@ -178,42 +234,47 @@ constexpr int kKeepBatch = 8;  // records in flight per thread
 
 __global__ void __launch_bounds__(kKeepThreads) k_keep_path(PagedRows kv, const int64_t* len, const int32_t* path,
                                                             int path_len, const int32_t* count) {
+  __shared__ int64_t s_src[HS_MAX_TREE_NODES], s_dst[HS_MAX_TREE_NODES];  // source -1: stays
   hs_pdl_wait();
   const int r = blockIdx.y;
-  const int col = blockIdx.x * kKeepThreads + threadIdx.x;
-  const int cols = (int)(kv.rec / 16);
-  uint32_t bad = 0u;
   const int given = count[r];
-  const int n = min(max(given, 0), path_len);
-  if (n != given) bad |= (uint32_t)HS_DEVERR_LOC;
   const int64_t base = len[r];
+  const int n = min(max(given, 0), path_len);
+  uint32_t bad = n != given ? (uint32_t)HS_DEVERR_LOC : 0u;
+  for (int i = threadIdx.x; i < n; i += kKeepThreads) {
+    const int p = path[(int64_t)r * path_len + i];
+    int64_t src = -1, dst = -1;
+    if (p < i) {
+      bad |= (uint32_t)HS_DEVERR_LOC;
+    } else if (p > i) {
+      src = paged_row(kv, r, base + p, (uint32_t)HS_DEVERR_LOC, &bad);
+      dst = paged_row(kv, r, base + i, (uint32_t)HS_DEVERR_LOC, &bad);
+    } else {
+      paged_row(kv, r, base + p, (uint32_t)HS_DEVERR_LOC, &bad);  // stays where it is, but has to be somewhere
+    }
+    s_src[i] = dst < 0 ? -1 : src;
+    s_dst[i] = dst;
+  }
+  if (blockIdx.x == 0) report(kv.err, bad);
+  __syncthreads();
+  const int64_t col = ((int64_t)blockIdx.x * kKeepThreads + threadIdx.x) * 16;
+  if (col >= kv.rec) return;
   for (int i0 = 0; i0 < n; i0 += kKeepBatch) {
     uint4 v[kKeepBatch];
-    int64_t to[kKeepBatch];
-#pragma unroll
-    for (int x = 0; x < kKeepBatch; ++x) {
-      to[x] = -1;
-      if (i0 + x < n) {
-        const int p = path[(int64_t)r * path_len + i0 + x];
-        if (p < i0 + x) {
-          bad |= (uint32_t)HS_DEVERR_LOC;
-        } else {
-          const int64_t src = paged_row(kv, r, base + p, (uint32_t)HS_DEVERR_LOC, &bad);
-          to[x] = paged_row(kv, r, base + i0 + x, (uint32_t)HS_DEVERR_LOC, &bad);
-          if (src < 0 || src == to[x]) to[x] = -1;
-          if (to[x] >= 0 && col < cols) v[x] = *(const uint4*)(kv.base + src * kv.rec + (int64_t)col * 16);
-        }
-      }
-    }
 #pragma unroll
     for (int x = 0; x < kKeepBatch; ++x)
-      if (to[x] >= 0 && col < cols) *(uint4*)(kv.base + to[x] * kv.rec + (int64_t)col * 16) = v[x];
+      if (i0 + x < n && s_src[i0 + x] >= 0) v[x] = *(const uint4*)(kv.base + s_src[i0 + x] * kv.rec + col);
+#pragma unroll
+    for (int x = 0; x < kKeepBatch; ++x)
+      if (i0 + x < n && s_src[i0 + x] >= 0) *(uint4*)(kv.base + s_dst[i0 + x] * kv.rec + col) = v[x];
   }
-  if (threadIdx.x == 0) report(kv.err, bad);
 }
 
 // 2^256 / (2 pi), lowest word first
 constexpr uint64_t kOverTwoPi[4] = {0x7f9458eaf7aef158ull, 0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+
+constexpr int kSmsHint = 152;  // to size grids by
+constexpr int kMinCtas = 456;
 
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 
@@ -270,8 +331,11 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
     if (g.d_q_out == nullptr || !hs_aligned(g.d_q, 16) || !hs_aligned(g.d_q_out, 16) || !stride_ok(g.q_token_stride) ||
         !stride_ok(g.q_head_stride) || !stride_ok(g.q_out_token_stride) || !stride_ok(g.q_out_head_stride))
       return HS_ERR_ARG;
-    if ((g.q_out_token_stride == 0 && g.num_tokens > 1) || (g.q_out_head_stride == 0 && cfg->num_q_heads > 1))
-      return HS_ERR_ARG;  // every query would be written over the others
+    // no two queries may be written over each other: one stride has to step over all that the other spans
+    const int64_t n = g.num_tokens, hq = cfg->num_q_heads, ts = g.q_out_token_stride, hs = g.q_out_head_stride, d = g.q_dim;
+    const bool by_token = (hq == 1 || hs >= d) && (n == 1 || ts >= (hq - 1) * hs + d);
+    const bool by_head = (n == 1 || ts >= d) && (hq == 1 || hs >= (n - 1) * ts + d);
+    if (!by_token && !by_head) return HS_ERR_ARG;
     if (g.q_dim != cfg->head_dim_qk && (g.q_dim != g.rotary_dim || g.q_dim == 0)) return HS_ERR_ARG;
   }
   HsOnDevice on(kv->cuda_device);
@@ -296,8 +360,6 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
   a.ohs = g.q_out_head_stride;
   a.R = cfg->num_requests;
   a.N = g.num_tokens;
-  a.Hkv = cfg->num_kv_heads;
-  a.Hq = cfg->num_q_heads;
   a.dqk = cfg->head_dim_qk;
   a.dv = mla ? 0 : cfg->head_dim_v;
   a.half = g.rotary_dim / 2;
@@ -305,9 +367,29 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
   a.q_off = g.q_dim == cfg->head_dim_qk ? g.rotary_offset : 0;
   a.q_dim = g.q_dim;
   a.interleaved = g.interleaved;
-  const size_t smem = (size_t)kAppTokens * a.half * sizeof(float2);
-  const cudaError_t e = hs_launch_pdl(k_append_rotated, dim3((a.N + kAppTokens - 1) / kAppTokens), dim3(kAppThreads), smem,
-                                      (cudaStream_t)stream, a);
+  const int ku = head_units(a.dqk, a.half, a.interleaved), vu = (a.dv + 15) / 16;
+  const int qu = g.d_q != nullptr ? head_units(g.q_dim, a.half, a.interleaved) : 0;
+  a.kn = cfg->num_kv_heads * ku;
+  a.vn = cfg->num_kv_heads * vu;
+  const int units = a.kn + a.vn + cfg->num_q_heads * qu;
+  auto div = [](int d) { return Div{(uint32_t)(d > 0 ? d : 1), d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u}; };
+  a.all = div(units);
+  a.kh = div(ku);
+  a.vh = div(vu);
+  a.qh = div(qu);
+  a.angles = div(a.half);
+  // kAppTokens tokens a CTA while that leaves three CTAs an SM, fewer else; then every token's units are shared by
+  // several CTAs until the GPU is filled or a share is below a quarter of one round (16 tokens: 3.2 us; a CTA a token
+  // 6.2 us).  A CTA's units stay below 2^16 (see Div).
+  a.tokens = kAppTokens;
+  while (a.tokens > 1 && (a.N < kMinCtas * a.tokens || units * a.tokens >= 65536)) a.tokens >>= 1;
+  const int ctas = (a.N + a.tokens - 1) / a.tokens;
+  int shares = 1;
+  while (shares < 64 && (int64_t)ctas * shares < 2 * kSmsHint && units * a.tokens / shares > kAppFlight * kAppThreads / 4)
+    shares *= 2;
+  a.per_cta = (units * a.tokens + shares - 1) / shares;
+  const size_t smem = (size_t)a.tokens * a.half * sizeof(float2);
+  const cudaError_t e = hs_launch_pdl(k_append_rotated, dim3(ctas, shares), dim3(kAppThreads), smem, (cudaStream_t)stream, a);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 

@@ -72,7 +72,7 @@ def _strided(t, n, heads, dim, name, device, written=False):
     if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (n, heads, dim) and t.get_device() == device:
         ts, hs, vs = t.stride()
         p = t.data_ptr()
-        if vs == 1 and n > 1 and heads > 1 and not (ts | hs | p >> 1) & 7 and (not written or (ts >= dim and hs >= dim)):
+        if vs == 1 and n > 1 and heads > 1 and not (ts | hs | p >> 1) & 7 and (not written or ts >= (heads - 1) * hs + dim):
             return p, ts, hs  # what most calls pass; the rest is looked at one by one
 
     if not isinstance(t, torch.Tensor):
@@ -91,7 +91,8 @@ def _strided(t, n, heads, dim, name, device, written=False):
     ts, hs = st[0] if n > 1 else 0, st[1] if heads > 1 else 0
     if ts % 8 or hs % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: address and strides must be multiples of 16 bytes")
-    if written and ((n > 1 and ts < dim) or (heads > 1 and hs < dim)):
+    if written and ((n > 1 and ts < dim) or (heads > 1 and hs < dim) or
+                    (n > 1 and heads > 1 and ts < (heads - 1) * hs + dim and hs < (n - 1) * ts + dim)):
         raise ValueError(f"{name} must not overlap itself")
     return t.data_ptr(), ts, hs
 

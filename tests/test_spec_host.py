@@ -81,7 +81,8 @@ def test_bad_pages(lib, change):
     dict(rotary_dim=-16), dict(rotary_dim=144), dict(rotary_offset=72), dict(rotary_offset=4), dict(rotary_offset=-8),
     dict(interleaved=2), dict(d_turns=None), dict(d_turns=OK_PTR + 4), dict(d_q_out=None), dict(d_q=OK_PTR + 4),
     dict(d_q_out=OK_PTR + 2), dict(q_token_stride=7), dict(q_out_head_stride=12), dict(q_dim=96), dict(q_dim=0),
-    dict(q_out_token_stride=0), dict(q_out_head_stride=0)])
+    dict(q_out_token_stride=0), dict(q_out_head_stride=0), dict(q_out_token_stride=128), dict(q_out_token_stride=4032),
+    dict(q_out_token_stride=128, q_out_head_stride=384)])
 def test_bad_appends(lib, change):
     c, kv = shape(), paged()
     assert lib.hs_append_rotated(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(append(**change)), None) == _lib.HS_ERR_ARG
