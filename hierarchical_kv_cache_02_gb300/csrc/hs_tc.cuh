@@ -225,6 +225,17 @@ __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity, vol
   }
   return false;
 }
+// Two at once: their latencies overlap.
+__device__ __forceinline__ bool uniform_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                              volatile uint32_t* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
+    if (__any_sync(0xffffffffu, x && y)) return true;
+    if (__any_sync(0xffffffffu, *abort != 0u)) return false;
+  }
+  return false;
+}
 __device__ __forceinline__ bool uniform_test(uint64_t* bar, uint32_t parity) {  // no wait
   uint32_t ok;
   asm volatile(

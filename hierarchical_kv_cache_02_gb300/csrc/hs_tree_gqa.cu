@@ -275,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (due0 > 0) {
           idle = 0;
           const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
-          if (!c.shared || g == 0) {
+          if (!c.shared || g == 0) vslot = v0.slot;
+          // nodes among the entries: the softmax looks at their values first (both groups together, so both are
+          // told before the first one's weights are waited for)
+          if (p0.t >= p0.nodes_from && (!c.shared || g == 0)) {
             land(v0);
-            vslot = v0.slot;
-            // nodes among the entries: the softmax looks at their values first (both groups together, so
-            // both are told before the first one's weights are waited for)
-            if (p0.t >= p0.nodes_from && lane == 0) {
+            if (lane == 0) {
               ct.vslot[g] = v0.slot;
               mbar_arrive(&ct.v[g]);
               if (c.shared && p0.pairs) {
@@ -291,7 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (here) {
-            if (ok) ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
+            // the weights, and the values (shared: the first group's wait for these serves both)
+            if (!c.shared || g == 0) {
+              if (ok) ok = uniform_wait2(&ct.p[g], (uint32_t)(done & 1), &ct.full[v0.slot], v0.phase, abort);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as in land
+            } else if (ok) {
+              ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
+            }
             tc_fence_after();
             if (ok && elect_one()) {
               const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
@@ -309,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k0.left()) {
           idle = 0;
           const bool here = g == 0 || k0.pairs, last_user = !c.shared || g == 1 || !k0.pairs;
+          const Ring<C::kRing> k_at = ring;
           if (!c.shared || g == 0) {
-            land(ring);
             kslot = ring.slot;
             ring.next();
             v0 = ring;
@@ -322,8 +328,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ok) ok = uniform_wait(&ct.qfull[g], (uint32_t)(q & 1), abort);
               ++q;
             }
-            // the weights of the tile before share these columns: their product has to be complete
-            if (ok && done > 0) ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+            // the keys; and the weights of the tile before share these columns: their product has to be complete
+            if (!c.shared || g == 0) {
+              if (ok && done > 0)
+                ok = uniform_wait2(&ct.full[k_at.slot], k_at.phase, &ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+              else if (ok)
+                ok = uniform_wait(&ct.full[k_at.slot], k_at.phase, abort);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as in land
+            } else if (ok && done > 0) {
+              ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+            }
             tc_fence_after();
             if (ok && elect_one()) {
               const uint32_t dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)kslot * kSlotStep;
