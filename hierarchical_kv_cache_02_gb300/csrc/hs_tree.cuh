@@ -87,8 +87,9 @@ __device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, 
 // of TT.  An item is the work of one accumulator over all tiles of a request (a KV head and one or two
 // groups of nodes, or a slice of the value dims); the tiles of all items of all requests form one
 // sequence, request by request and item by item, of which every worker takes an equal, contiguous
-// share.  Lengths live on the device alone, so each CTA finds its share itself.  A worker's portion of
-// an item that does not hold all its tiles becomes a partial: slot 0 of the worker when the portion
+// share.  (Each item begins with kBegin units of no tile, which stand for what a portion costs beside its tiles:
+// loading its queries, storing its result.)  Lengths live on the device alone, so each CTA finds its share
+// itself.  A worker's portion of an item that does not hold all its tiles becomes a partial: slot 0 of the worker when the portion
 // starts inside the item, else slot 1 (a worker has at most one of each); k_tree_combine joins them.
 
 constexpr int kPortions = 10;  // portions a round of a CTA holds per worker
@@ -102,7 +103,7 @@ struct Portion {
 
 struct PlanState {  // shared memory
   Portion port[2][kPortions];
-  long long off[2], left[2];  // tiles into request cur, tiles still to take
+  long long off[2], left[2];  // units into request cur, units still to take
   int cur[2], nport[2];
   int wn[2][kWindow], wlen[2][kWindow];
   short wnn[2][kWindow];
@@ -112,8 +113,8 @@ struct PlanState {  // shared memory
 struct WorkSplit {
   int items, np;         // per request; of them per KV head
   int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA
-  long long* prefix;     // [R + 1] tiles (of one item) before each request, written by CTA 0
-  float *part, *ml;      // [workers][2 slots][rows][dims], [workers][2][rows][2]: maximum (base 2) and sum
+  long long* prefix;     // [R + 1] units (of one item) before each request, written by CTA 0
+  float *part, *ml;      // [workers][2 slots][dims / 8][rows][8], [workers][2][rows][2]: maximum (base 2) and sum
   int rows;              // accumulator rows of a portion
 };
 
@@ -144,43 +145,145 @@ struct Shares {
   }
 };
 
-// Where each worker of this CTA starts.  Every thread of the CTA calls it.  (Here and in the kernels code
-// size counts: a CTA fetches every instruction anew, and lives for some tens of microseconds.)
+constexpr int kBegin = 1;
 template <int TT>
-__device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
+__device__ __forceinline__ long long units_of(int n, int nn) {
+  return nn == 0 ? 0 : tiles_of<TT>(n, nn) + kBegin;
+}
+
+// Worker g's next portions, by one thread; window[i] is request first + i.
+template <int TT>
+__device__ __forceinline__ void plan_walk(const TreeArgs& a, const WorkSplit& ws, PlanState* s, int g, int first, int i,
+                                          long long off, long long left) {
+  int np = 0;
+#pragma unroll 1
+  while (left > 0 && np < kPortions && i < kWindow && first + i < a.R) {
+    const int n = s->wn[g][i], nn = s->wnn[g][i];
+    const long long U = units_of<TT>(n, nn);
+    if (off >= U * ws.items) {
+      off -= U * ws.items;
+      ++i;
+      continue;
+    }
+    const int item = (int)Shares::div_small(off, U);
+    const long long u0 = off - item * U, u1 = min(U, u0 + left);
+    left -= u1 - u0;
+    off += u1 - u0;
+    if (u1 <= kBegin) continue;  // nothing but the item's first units
+    Portion p;
+    p.r = first + i;
+    p.head = item / ws.np;
+    p.pair = item - p.head * ws.np;
+    p.t0 = (int)max(0ll, u0 - kBegin);
+    p.t1 = (int)(u1 - kBegin);
+    p.n = n;
+    p.len = s->wlen[g][i];
+    p.nn = nn;
+    s->port[g][np++] = p;
+  }
+  s->nport[g] = np;
+  s->left[g] = first + i < a.R ? left : 0;  // lengths that change under the call must not keep it going
+  s->off[g] = off;
+  s->cur[g] = first + i;
+}
+
+// The next portions of each worker; false when no worker has any left.  Every thread calls it.
+template <int TT>
+__device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
+  if (s->left[0] <= 0 && s->left[1] <= 0) return false;  // the same in every thread: written before a barrier
+  const int tid = threadIdx.x;
+  const bool all = a.R <= kWindow;  // then the window starts at request 0 and is there already
+  if (!all && tid < 2 * kWindow) {
+    const int g = tid / kWindow, i = tid - g * kWindow;
+    if (s->left[g] > 0 && s->cur[g] + i < a.R) {
+      uint32_t bad = 0u;
+      int n, len, nn;
+      request_of(a, s->cur[g] + i, &n, &len, &nn, &bad);
+      s->wn[g][i] = n;
+      s->wlen[g][i] = len;
+      s->wnn[g][i] = (short)nn;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 || tid == 32) {
+    const int g = tid >> 5, cur = s->cur[g];
+    if (s->left[g] > 0) plan_walk<TT>(a, ws, s, g, all ? 0 : cur, all ? cur : 0, s->off[g], s->left[g]);
+    else s->nport[g] = 0;
+  }
+  __syncthreads();
+  return true;
+}
+
+// Where each worker of this CTA starts, and its first portions; false when there is nothing to do.  Every
+// thread of the CTA calls it.  (Here and in the kernels code size counts: a CTA fetches every instruction
+// anew, and lives for some tens of microseconds.)
+template <int TT>
+__device__ __forceinline__ bool plan_start(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
+  if (a.R <= kWindow) {  // a lane a request: warp g finds worker g's place by itself
+    if (warp < 2) {
+      const int g = warp;
+      uint32_t bad = 0u;
+      int n = 0, len = 0, nn = 0;
+      if (lane < a.R) {
+        request_of(a, lane, &n, &len, &nn, &bad);
+        s->wn[g][lane] = n;
+        s->wlen[g][lane] = len;
+        s->wnn[g][lane] = (short)nn;
+      }
+      const int U = (int)units_of<TT>(n, nn);  // 16 requests of 2^31 entries: below 2^30
+      int incl = U;
+#pragma unroll
+      for (int o = 1; o < kWindow; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int total = __shfl_sync(0xffffffffu, incl, kWindow - 1);
+      const Shares sh((long long)total * ws.items, (int)gridDim.x * ws.groups);
+      const int w = g * (int)gridDim.x + (int)blockIdx.x;
+      const long long s0 = sh.start(w), left = g < ws.groups ? sh.start(w + 1) - s0 : 0;
+      const long long off = s0 - (long long)(incl - U) * ws.items;
+      const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < (long long)U * ws.items);
+      if (g == 0 && blockIdx.x == 0) {
+        if (lane < a.R) ws.prefix[lane] = incl - U;
+        if (lane == 0) ws.prefix[a.R] = total;
+        report(a.kv.err, bad);
+      }
+      const int r = here != 0u ? __ffs(here) - 1 : 0;
+      const long long at = __shfl_sync(0xffffffffu, off, r);
+      __syncwarp();
+      if (lane == 0) plan_walk<TT>(a, ws, s, g, 0, r, at, left);
+    }
+    __syncthreads();
+    return s->nport[0] + s->nport[1] > 0 || s->left[0] + s->left[1] > 0;
+  }
   const int each = (a.R + nthr - 1) / nthr, r0 = min(tid * each, a.R), r1 = min(r0 + each, a.R);
   uint32_t bad = 0u;
   long long mine = 0, run = 0, s0[2] = {-1, -1};
-  // the first pass counts each thread's tiles, the second finds the places among them
+  // the first pass counts each thread's units, the second finds the places among them
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     int n = 0, len = 0, nn = 0;
-    long long T = mine;  // one request a thread: known from the first pass
+    long long U = mine;  // one request a thread: known from the first pass
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       if (pass == 0 || each > 1) {
         request_of(a, r, &n, &len, &nn, &bad);
-        T = tiles_of<TT>(n, nn);
+        U = units_of<TT>(n, nn);
       }
       if (pass == 0) {
-        mine += T;
-        if (a.R <= kWindow) {  // the requests fit a round's window: they stay there
-          s->wn[0][r] = s->wn[1][r] = n;
-          s->wlen[0][r] = s->wlen[1][r] = len;
-          s->wnn[0][r] = s->wnn[1][r] = (short)nn;
-        }
+        mine += U;
       } else {
         if (blockIdx.x == 0) ws.prefix[r] = run;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const long long off = s0[g] - run * ws.items;
-          if (s0[g] >= 0 && off >= 0 && off < T * ws.items) {
+          if (s0[g] >= 0 && off >= 0 && off < U * ws.items) {
             s->cur[g] = r;
             s->off[g] = off;
           }
         }
-        run += T;
+        run += U;
       }
     }
     if (pass == 0) {
@@ -211,62 +314,7 @@ __device__ __forceinline__ void plan_start(const TreeArgs& a, const WorkSplit& w
   }
   if (blockIdx.x == 0) report(a.kv.err, bad);
   __syncthreads();
-}
-
-// The next portions of each worker; false when no worker has any left.  Every thread calls it.
-template <int TT>
-__device__ __forceinline__ bool plan_round(const TreeArgs& a, const WorkSplit& ws, PlanState* s) {
-  if (s->left[0] <= 0 && s->left[1] <= 0) return false;  // the same in every thread: written before a barrier
-  const int tid = threadIdx.x;
-  const bool all = a.R <= kWindow;  // then the window starts at request 0 and is there already
-  if (!all && tid < 2 * kWindow) {
-    const int g = tid / kWindow, i = tid - g * kWindow;
-    if (s->left[g] > 0 && s->cur[g] + i < a.R) {
-      uint32_t bad = 0u;
-      int n, len, nn;
-      request_of(a, s->cur[g] + i, &n, &len, &nn, &bad);
-      s->wn[g][i] = n;
-      s->wlen[g][i] = len;
-      s->wnn[g][i] = (short)nn;
-    }
-  }
-  __syncthreads();
-  if ((tid == 0 || tid == 32) && s->left[tid >> 5] > 0) {
-    const int g = tid >> 5;
-    long long left = s->left[g], off = s->off[g];
-    int np = 0, i = all ? s->cur[g] : 0;
-    const int cur = all ? 0 : s->cur[g];
-    while (left > 0 && np < kPortions && i < kWindow && cur + i < a.R) {
-      const int n = s->wn[g][i], nn = s->wnn[g][i];
-      const long long T = tiles_of<TT>(n, nn);
-      if (off >= T * ws.items) {
-        off -= T * ws.items;
-        ++i;
-        continue;
-      }
-      Portion p;
-      p.r = cur + i;
-      const int item = (int)Shares::div_small(off, T);
-      p.head = item / ws.np;
-      p.pair = item - p.head * ws.np;
-      p.t0 = (int)(off - item * T);
-      p.t1 = (int)min(T, p.t0 + left);
-      p.n = n;
-      p.len = s->wlen[g][i];
-      p.nn = nn;
-      s->port[g][np++] = p;
-      left -= p.t1 - p.t0;
-      off += p.t1 - p.t0;
-    }
-    s->nport[g] = np;
-    s->left[g] = cur + i < a.R ? left : 0;  // lengths that change under the call must not keep it going
-    s->off[g] = off;
-    s->cur[g] = cur + i;
-  } else if (tid == 0 || tid == 32) {
-    s->nport[tid >> 5] = 0;
-  }
-  __syncthreads();
-  return true;
+  return plan_round<TT>(a, ws, s);
 }
 
 // A producer lane's lookups of its entry of each tile of a portion list, in three steps, each a tile ahead of
@@ -426,63 +474,73 @@ struct CombineArgs {
   int flat;        // a shared latent: item i holds the rows [flat i, flat (i + 1)) of all node x head rows
 };
 
-// One warp per accumulator row, DV dims; items that one worker held whole are written by it.
+// A thread holds 8 dims of a row, neighbouring threads neighbouring rows; items that one worker held whole are
+// written by it.
 template <int DV>
 __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int V = DV / 64;  // float2 per lane
-  const int item = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31;
-  const long long p0 = c.ws.prefix[r], T = c.ws.prefix[r + 1] - p0;
-  if (T == 0) return;
-  const Shares sh(c.ws.prefix[c.R] * c.ws.items, c.workers);
-  const long long a = p0 * c.ws.items + item * T;
-  const int wf = sh.worker(a), wl = sh.worker(a + T - 1);
-  if (wf == wl) return;
-  const int row = blockIdx.z * 8 + (threadIdx.x >> 5), x = row & 127;
+  constexpr int kFlight = 4;  // partials in flight
+  const int item = blockIdx.x, r = blockIdx.y, idx = blockIdx.z * 256 + threadIdx.x;
+  const long long p0 = c.ws.prefix[r], U = c.ws.prefix[r + 1] - p0, total = c.ws.prefix[c.R];
+  int nn = c.T;
+  if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
+  if (U == 0) return;
+  const int rows = c.ws.rows, blk = idx / rows, row = idx - blk * rows, x = row & 127;
   const int mt = c.flat ? 0 : (item % c.np) * c.per + (row >> 7);
   const int t = c.flat ? (item * c.flat + row) / c.Hq : mt * c.MT + x / c.G;
   const int h = c.flat ? (item * c.flat + row) % c.Hq : item / c.np * c.G + x % c.G;
-  int nn = c.T;
-  if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
-  if (row >= c.ws.rows || (!c.flat && x >= c.G * c.MT) || t >= nn) return;
-  auto slot_row = [&](int w) { return ((long long)w * 2 + (w == wf ? 1 : 0)) * c.ws.rows + row; };
-  float M = -INFINITY;
-  for (int w = wf + lane; w <= wl; w += 32)
-    M = fmaxf(M, c.ws.ml[slot_row(w) * 2]);
+  if (blk >= DV / 8 || (!c.flat && x >= c.G * c.MT) || t >= nn) return;
+  const Shares sh(total * c.ws.items, c.workers);
+  const long long a = p0 * c.ws.items + item * U;
+  const int wf = sh.worker(a + kBegin), wl = sh.worker(a + U - 1);
+  if (wf == wl) return;
+  float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float2 acc[V];
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int w0 = wf; w0 <= wl; w0 += kFlight) {
+    float2 ml[kFlight];
+    float4 lo4[kFlight], hi4[kFlight];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = make_float2(0.f, 0.f);
-  float L = 0.f;
-  for (int w0 = wf; w0 <= wl; w0 += 32) {
-    float wt = 0.f, lw = 0.f;
-    if (w0 + lane <= wl) {
-      const float2 ml = *(const float2*)(c.ws.ml + slot_row(w0 + lane) * 2);
-      // nothing seen: no part in the result; NaN scores alone: NaN
-      wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2f(ml.x - M);
-      lw = wt * ml.y;
+    for (int j = 0; j < kFlight; ++j) {  // the last one again where there are no more
+      const int w = min(w0 + j, wl);
+      const long long slot = ((long long)w * 2 + (w == wf ? 1 : 0)) * rows;
+      const float4* p = (const float4*)(c.ws.part + slot * DV + ((long long)blk * rows + row) * 8);
+      ml[j] = *(const float2*)(c.ws.ml + (slot + row) * 2);
+      lo4[j] = p[0];
+      hi4[j] = p[1];
     }
-    const int cnt = min(32, wl - w0 + 1);
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wt, i);
-      L += __shfl_sync(0xffffffffu, lw, i);
-      if (wi == 0.f) continue;
-      const float2* p = (const float2*)(c.ws.part + slot_row(w0 + i) * DV);
+    float mn = M;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 u = p[lane + 32 * v];
-        acc[v].x = fmaf(wi, u.x, acc[v].x);
-        acc[v].y = fmaf(wi, u.y, acc[v].y);
-      }
+    for (int j = 0; j < kFlight; ++j) mn = fmaxf(mn, ml[j].x);
+    const float al = M == mn ? 1.f : exp2f(M - mn);
+    M = mn;
+    L *= al;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= al;
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      // nothing seen: no part in the result; NaN scores alone: NaN
+      const float wt = ml[j].x == -INFINITY ? (ml[j].y == 0.f ? 0.f : ml[j].y) : exp2f(ml[j].x - M);
+      if (w0 + j > wl || wt == 0.f) continue;
+      L = fmaf(wt, ml[j].y, L);
+      acc[0] = fmaf(wt, lo4[j].x, acc[0]);
+      acc[1] = fmaf(wt, lo4[j].y, acc[1]);
+      acc[2] = fmaf(wt, lo4[j].z, acc[2]);
+      acc[3] = fmaf(wt, lo4[j].w, acc[3]);
+      acc[4] = fmaf(wt, hi4[j].x, acc[4]);
+      acc[5] = fmaf(wt, hi4[j].y, acc[5]);
+      acc[6] = fmaf(wt, hi4[j].z, acc[6]);
+      acc[7] = fmaf(wt, hi4[j].w, acc[7]);
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t* o = (uint32_t*)(c.out + (((int64_t)r * c.T + t) * c.Hq + h) * DV);
-#pragma unroll
-  for (int v = 0; v < V; ++v) o[lane + 32 * v] = pack(acc[v].x * inv, acc[v].y * inv);
+  *(uint4*)(c.out + (((int64_t)r * c.T + t) * c.Hq + h) * DV + 8 * blk) =
+      make_uint4(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv), pack(acc[4] * inv, acc[5] * inv),
+                 pack(acc[6] * inv, acc[7] * inv));
 }
+// its grid
+inline dim3 combine_grid(int items, int R, int rows, int dims) { return dim3(items, R, (rows * (dims / 8) + 255) / 256); }
 
 bool encode(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
             const cuuint32_t* box) {

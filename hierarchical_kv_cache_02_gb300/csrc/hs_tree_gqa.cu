@@ -52,10 +52,10 @@ struct TcArgs {
 struct Control {
   PlanState plan;
   __align__(8) uint64_t full[11], empty[11];
-  uint64_t qfull[2], s[2], p[2], pv[2], v[2], mask[2][kMaskRing];
+  uint64_t qfull[2], s[2], p[2], pv[2], mask[2][kMaskRing];
   uint64_t fin;
   uint32_t valid[2][kMaskRing][4];
-  int vslot[2];
+  uint32_t vplace[2][kMaskRing];  // where a tile's values are: ring slot * 2 + phase
   uint32_t tmem, abort;
 };
 
@@ -74,14 +74,13 @@ struct Ring {
 // A place in a portion list, with what is needed of the portion.
 struct Cursor {
   const Portion* list;
-  int count, p, t, t0, t1, nodes_from;  // nodes_from: the first tile that holds nodes
+  int count, p, t, t0, t1;
   bool pairs;                           // shared: both groups take part (the last pair of row tiles may be single)
   __device__ __forceinline__ void fetch(const TcArgs& c) {
     if (p >= count) return;
     const Portion& P = list[p];
     t = t0 = uniform(P.t0);
     t1 = uniform(P.t1);
-    nodes_from = uniform((int)(((unsigned)P.n + 3u) & ~3u) / kTile);
     pairs = !c.shared || 2 * uniform(P.pair) + 1 < c.nmt;
   }
   __device__ __forceinline__ void open(const Portion* l, int n, const TcArgs& c) {
@@ -120,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ct.s[g], 1u);
       mbar_init(&ct.p[g], 128u);
       mbar_init(&ct.pv[g], 1u);
-      mbar_init(&ct.v[g], 1u);
       for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[g][i], kProducers);
     }
     mbar_init(&ct.fin, 1u);
@@ -140,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the only kernel that may start early is this call's own combine, which waits for this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
-  plan_start<kTile>(a, c.ws, &ct.plan);
+  bool go = plan_start<kTile>(a, c.ws, &ct.plan);
   tc_fence_after();
   const uint32_t tb = ct.tmem;
   // tensor memory: 128 columns of scores a group (their first 64 become the weights), then D of O a group
@@ -149,12 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ring<C::kRing> ring;             // producers and products
   int tiles0 = 0, tiles1 = 0;      // producers: tiles of each group loaded; products: finished
   int portions0 = 0, portions1 = 0;  // products: portions of each group begun
-  int nt = 0, nv = 0, nm = 0;      // softmax: tiles, tiles with nodes, tiles of the mask ring
+  int nt = 0, nm = 0;              // softmax: tiles, tiles of the mask ring
   int sent = 0;                    // producers: ring loads issued; first softmax thread: query loads
   bool ok = true;
   uint32_t bad = 0u;
 
-  while (plan_round<kTile>(a, c.ws, &ct.plan)) {
+  for (; go; go = plan_round<kTile>(a, c.ws, &ct.plan)) {
     const int ng = c.shared ? 1 : 2;  // portion lists
     // whether group g takes part in an item: the last pair of row tiles may be a single one
     auto present = [&](int g, const Portion& p) { return !c.shared || 2 * p.pair + g < c.nmt; };
@@ -201,8 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int now_row = g == 0 ? ahead0.row : ahead1.row;
             const bool boxed = c.seg != 0 && k0.t * kTile + 32 * pw + 32 <= P.n;
             const int x0 = P.head * a.kstride;
+            uint32_t vplace = 0u;
 #pragma unroll 1
             for (int val = 0; val < 2; ++val) {
+              vplace = (uint32_t)ring.slot * 2u + ring.phase;
               if (ok) ok = warp_wait_small(&ct.empty[ring.slot], ring.phase ^ 1u, abort);
               if (ok) {
                 const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 32 * pw * 128);
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int& n = g == 0 ? tiles0 : tiles1;
             if (ok && lane == 0) {
               ct.valid[g][n % kMaskRing][pw] = word;
+              if (pw == 0) ct.vplace[g][n % kMaskRing] = vplace;
               mbar_arrive(&ct.mask[g][n % kMaskRing]);
             }
             ++n;
@@ -255,11 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
       const uint32_t dv0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, C::kBlk));
       constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
-      auto land = [&](const Ring<C::kRing>& at) {
-        if (ok) ok = uniform_wait(&ct.full[at.slot], at.phase, abort);
-        // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      };
       int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
       Ring<C::kRing> v0, v1;     // where the values of the tile in hand are: of the group at hand, of the other
       Cursor k0, k1, p0, p1;     // next scores and next values of the group at hand, of the other
@@ -276,25 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           idle = 0;
           const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
           if (!c.shared || g == 0) vslot = v0.slot;
-          // nodes among the entries: the softmax looks at their values first (both groups together, so both are
-          // told before the first one's weights are waited for)
-          if (p0.t >= p0.nodes_from && (!c.shared || g == 0)) {
-            land(v0);
-            if (lane == 0) {
-              ct.vslot[g] = v0.slot;
-              mbar_arrive(&ct.v[g]);
-              if (c.shared && p0.pairs) {
-                ct.vslot[1] = v0.slot;
-                mbar_arrive(&ct.v[1]);
-              }
-            }
-            __syncwarp();
-          }
           if (here) {
             // the weights, and the values (shared: the first group's wait for these serves both)
             if (!c.shared || g == 0) {
               if (ok) ok = uniform_wait2(&ct.p[g], (uint32_t)(done & 1), &ct.full[v0.slot], v0.phase, abort);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as in land
+              // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             } else if (ok) {
               ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
             }
@@ -334,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = uniform_wait2(&ct.full[k_at.slot], k_at.phase, &ct.pv[g], (uint32_t)((done - 1) & 1), abort);
               else if (ok)
                 ok = uniform_wait(&ct.full[k_at.slot], k_at.phase, abort);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as in land
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as above
             } else if (ok && done > 0) {
               ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
             }
@@ -423,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t ctx = jw >= 0 ? 0u : (jw <= -32 ? 0xffffffffu : (1u << -jw) - 1u);
               w[x] &= ctx | (row_ok ? mask_bits(mw, mfirst, a.words, P.nn, jw) : 0u);
             }
-            if (ok) ok = mbar_wait_small(&ct.v[g], (uint32_t)(nv & 1), abort);
+            const uint32_t vp = ct.vplace[mg][nm % kMaskRing];
+            if (ok) ok = mbar_wait_small(&ct.full[vp >> 1], vp & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            ++nv;
-            const bool d = ok && clean_rows(smem + 2 * C::kSlot + ct.vslot[g] * C::kSlot, kTile, C::kCh, max(0, -j0),
+            const bool d = ok && clean_rows(smem + (2 + (vp >> 1)) * C::kSlot, kTile, C::kCh, max(0, -j0),
                                             min(kTile, P.nn - j0), both ? tid : row, both ? 256 : 128);
             if (bar_or(both ? 3 : 1 + g, both ? 256 : 128, d)) dirty = true;
           }
@@ -503,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && warp_ok) {
           const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
           const int wk = (c.shared ? 0 : g) * (int)gridDim.x + (int)blockIdx.x;
-          const long long prow = ((long long)wk * 2 + (P.t0 > 0 ? 0 : 1)) * c.ws.rows + (c.shared ? 128 * g : 0) + row;
+          const long long slot = ((long long)wk * 2 + (P.t0 > 0 ? 0 : 1)) * c.ws.rows;
+          const int srow = (c.shared ? 128 * g : 0) + row;
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
@@ -533,11 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
               } else {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) st_global_v8(c.ws.part + prow * D + 32 * x + 8 * y, o + 8 * y);
+                for (int y = 0; y < 4; ++y)
+                  st_global_v8(c.ws.part + slot * D + ((long long)(4 * x + y) * c.ws.rows + srow) * 8, o + 8 * y);
               }
             }
           }
-          if (row_ok && !whole) *(float2*)(c.ws.ml + prow * 2) = make_float2(m, l);
+          if (row_ok && !whole) *(float2*)(c.ws.ml + (slot + srow) * 2) = make_float2(m, l);
         }
         tc_fence_before();
       }
@@ -608,7 +593,7 @@ cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q
   if (e != cudaSuccess) return e;
   e = hs_launch_pdl(k_tree_gqa<D>, dim3(sms), dim3(kThreads), Shape<D>::kDyn, st, c, q, seg);
   if (e != cudaSuccess) return e;
-  return hs_launch_pdl(k_tree_combine<D>, dim3(p.items, c.a.R, (p.rows + 7) / 8), dim3(256), 0, st, cb);
+  return hs_launch_pdl(k_tree_combine<D>, combine_grid(p.items, c.a.R, p.rows, D), dim3(256), 0, st, cb);
 }
 
 }  // namespace

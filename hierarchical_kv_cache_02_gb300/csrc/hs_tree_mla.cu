@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the only kernel that may start early is this call's own combine, which waits for this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
-  plan_start<kTile>(a, c.ws, &ct.plan);
+  bool go = plan_start<kTile>(a, c.ws, &ct.plan);
   tc_fence_after();
   const uint32_t tb = ct.tmem;
 
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   uint32_t bad = 0u;
 
-  while (plan_round<kTile>(a, c.ws, &ct.plan)) {
+  for (; go; go = plan_round<kTile>(a, c.ws, &ct.plan)) {
     const Portion* list = ct.plan.port[0];
     const int count = ct.plan.nport[0];
     if (warp >= kWarpProd) {
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (ok && warp_ok) {
           const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
-          const long long prow = ((long long)blockIdx.x * 2 + (P.t0 > 0 ? 0 : 1)) * kRows + row;
+          const long long slot = ((long long)blockIdx.x * 2 + (P.t0 > 0 ? 0 : 1)) * kRows;
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
@@ -393,11 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       pack_bf16(o[8 * y + 4] * inv, o[8 * y + 5] * inv), pack_bf16(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
               } else {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) st_global_v8(c.ws.part + prow * kValue + dim + 8 * y, o + 8 * y);
+                for (int y = 0; y < 4; ++y)
+                  st_global_v8(c.ws.part + slot * kValue + ((dim / 8 + y) * kRows + row) * 8, o + 8 * y);
               }
             }
           }
-          if (row_ok && !whole && side == 0) *(float2*)(c.ws.ml + prow * 2) = make_float2(m, l);
+          if (row_ok && !whole && side == 0) *(float2*)(c.ws.ml + (slot + row) * 2) = make_float2(m, l);
         }
         tc_fence_before();
       }
@@ -491,6 +492,6 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   cudaError_t e = allow_smem(k_tree_mla, kDyn, done);
   if (e == cudaSuccess) e = hs_launch_pdl(k_tree_mla, dim3(num_sms), dim3(kThreads), kDyn, st, c, qm, seg);
   if (e == cudaSuccess)
-    e = hs_launch_pdl(k_tree_combine<kValue>, dim3(c.ws.items, cfg->num_requests, kRows / 8), dim3(256), 0, st, cb);
+    e = hs_launch_pdl(k_tree_combine<kValue>, combine_grid(c.ws.items, cfg->num_requests, kRows, kValue), dim3(256), 0, st, cb);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
