@@ -87,7 +87,7 @@ __device__ __forceinline__ const uint8_t* node_record(const TreeArgs& a, int r, 
 // of TT.  An item is the work of one accumulator over all tiles of a request (a KV head and one or two
 // groups of nodes, or a slice of the value dims); the tiles of all items of all requests form one
 // sequence, request by request and item by item, of which every worker takes an equal, contiguous
-// share.  (Each item begins with kBegin units of no tile, which stand for what a portion costs beside its tiles:
+// share.  (Each item begins with `begin` units of no tile, which stand for what a portion costs beside its tiles:
 // loading its queries, storing its result.)  Lengths live on the device alone, so each CTA finds its share
 // itself.  A worker's portion of an item that does not hold all its tiles becomes a partial: slot 0 of the worker when the portion
 // starts inside the item, else slot 1 (a worker has at most one of each); k_tree_combine joins them.
@@ -112,6 +112,7 @@ struct PlanState {  // shared memory
 
 struct WorkSplit {
   int items, np;         // per request; of them per KV head
+  int begin;             // units of an item before its tiles
   int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA
   long long* prefix;     // [R + 1] units (of one item) before each request, written by CTA 0
   float *part, *ml;      // [workers][2 slots][dims / 8][rows][8], [workers][2][rows][2]: maximum (base 2) and sum
@@ -145,10 +146,9 @@ struct Shares {
   }
 };
 
-constexpr int kBegin = 1;
 template <int TT>
-__device__ __forceinline__ long long units_of(int n, int nn) {
-  return nn == 0 ? 0 : tiles_of<TT>(n, nn) + kBegin;
+__device__ __forceinline__ long long units_of(const WorkSplit& ws, int n, int nn) {
+  return nn == 0 ? 0 : tiles_of<TT>(n, nn) + ws.begin;
 }
 
 // Worker g's next portions, by one thread; window[i] is request first + i.
@@ -159,7 +159,7 @@ __device__ __forceinline__ void plan_walk(const TreeArgs& a, const WorkSplit& ws
 #pragma unroll 1
   while (left > 0 && np < kPortions && i < kWindow && first + i < a.R) {
     const int n = s->wn[g][i], nn = s->wnn[g][i];
-    const long long U = units_of<TT>(n, nn);
+    const long long U = units_of<TT>(ws, n, nn);
     if (off >= U * ws.items) {
       off -= U * ws.items;
       ++i;
@@ -169,13 +169,13 @@ __device__ __forceinline__ void plan_walk(const TreeArgs& a, const WorkSplit& ws
     const long long u0 = off - item * U, u1 = min(U, u0 + left);
     left -= u1 - u0;
     off += u1 - u0;
-    if (u1 <= kBegin) continue;  // nothing but the item's first units
+    if (u1 <= ws.begin) continue;  // nothing but the item's first units
     Portion p;
     p.r = first + i;
     p.head = item / ws.np;
     p.pair = item - p.head * ws.np;
-    p.t0 = (int)max(0ll, u0 - kBegin);
-    p.t1 = (int)(u1 - kBegin);
+    p.t0 = (int)max(0ll, u0 - ws.begin);
+    p.t1 = (int)(u1 - ws.begin);
     p.n = n;
     p.len = s->wlen[g][i];
     p.nn = nn;
@@ -231,7 +231,7 @@ __device__ __forceinline__ bool plan_start(const TreeArgs& a, const WorkSplit& w
         s->wlen[g][lane] = len;
         s->wnn[g][lane] = (short)nn;
       }
-      const int U = (int)units_of<TT>(n, nn);  // 16 requests of 2^31 entries: below 2^30
+      const int U = (int)units_of<TT>(ws, n, nn);  // 16 requests of 2^31 entries: below 2^30
       int incl = U;
 #pragma unroll
       for (int o = 1; o < kWindow; o <<= 1) {
@@ -269,7 +269,7 @@ __device__ __forceinline__ bool plan_start(const TreeArgs& a, const WorkSplit& w
     for (int r = r0; r < r1; ++r) {
       if (pass == 0 || each > 1) {
         request_of(a, r, &n, &len, &nn, &bad);
-        U = units_of<TT>(n, nn);
+        U = units_of<TT>(ws, n, nn);
       }
       if (pass == 0) {
         mine += U;
@@ -444,6 +444,23 @@ __device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, uint64_t first,
   return v << (s - j0);
 }
 
+// What a row does not see, in its scores in tensor memory: -infinity.  (Apart from the loops over the scores, which
+// so have one form: code that a CTA meets for the first time costs about half a microsecond a kilobyte.)
+template <int WORDS>
+__device__ __forceinline__ void mask_scores(uint32_t ts, const uint32_t (&w)[WORDS]) {
+#pragma unroll 1
+  for (int x = 0; x < WORDS; ++x) {
+    float v[32];
+    tmem_ld32(ts + 32u * x, v);
+    uint32_t b = w[0];
+#pragma unroll
+    for (int i = 1; i < WORDS; ++i) b = x == i ? w[i] : b;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = (b >> j) & 1u ? v[j] : -INFINITY;
+    tmem_st32(ts + 32u * x, v);
+  }
+}
+
 // Takes infinite and NaN values out of the rows [y0, y1) of a tile of `blocks` 128-byte column blocks of `rows`
 // rows each (the swizzle moves bytes within a row's 128 only).  Thread `id` of `threads`; true: it found some.
 __device__ __forceinline__ bool clean_rows(uint8_t* tile, int rows, int blocks, int y0, int y1, int id, int threads) {
@@ -492,7 +509,7 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   if (blk >= DV / 8 || (!c.flat && x >= c.G * c.MT) || t >= nn) return;
   const Shares sh(total * c.ws.items, c.workers);
   const long long a = p0 * c.ws.items + item * U;
-  const int wf = sh.worker(a + kBegin), wl = sh.worker(a + U - 1);
+  const int wf = sh.worker(a + c.ws.begin), wl = sh.worker(a + U - 1);
   if (wf == wl) return;
   float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll

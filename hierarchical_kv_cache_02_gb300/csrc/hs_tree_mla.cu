@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && warp_ok) {
             float v[64];
             tmem_ld64(tb + lane_base + kScores, v);
-            if (!full) {
+            if (!full) {  // (here, not in tensor memory: the other lanes' scores are the next tile's, on their way)
 #pragma unroll
               for (int j = 0; j < 64; ++j) v[j] = (w[j >> 5] >> (j & 31)) & 1u ? v[j] : -INFINITY;
             }
@@ -314,14 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float s1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              float p0 = fast_exp2(fmaf(v[2 * j], a.qscale, -base)), p1 = fast_exp2(fmaf(v[2 * j + 1], a.qscale, -base));
-              if (!full) {
-                p0 = (w[j >> 4] >> ((2 * j) & 31)) & 1u ? p0 : 0.f;
-                p1 = (w[j >> 4] >> ((2 * j + 1) & 31)) & 1u ? p1 : 0.f;
-              }
-              pk[j] = pack_bf16(p0, p1);
-              sum += lo(pk[j]);  // the rounded weights, as the product takes them
-              s1 += hi(pk[j]);
+              float p0, p1;
+              fma2(p0, p1, v[2 * j], v[2 * j + 1], a.qscale, -base);
+              pk[j] = pack_bf16(fast_exp2(p0), fast_exp2(p1));
+              add2(sum, s1, lo(pk[j]), hi(pk[j]));  // the rounded weights, as the product takes them
             }
             sum = __shfl_sync(0xffffffffu, sum + s1, (lane & 15) + 16 * b);
             if (nt > 0) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
@@ -460,12 +456,14 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.ws.items = items_of(cfg, g->nodes);
   c.ws.np = 1;
   c.ws.groups = 1;
+  c.ws.begin = 1;
   c.ws.rows = kRows;
   hs_tree_workspace(g->d_workspace, cfg, num_sms, kRows, kValue, &c.ws.prefix, &c.ws.part, &c.ws.ml);
   if (c.a.qscale < 0.f) {
     c.negate = 1;
     c.a.qscale = -c.a.qscale;
   }
+  c.a.qscale = fmaxf(c.a.qscale, 1.17549435e-38f);  // times -infinity has to stay -infinity
   CUtensorMap qm, seg;
   memset(&seg, 0, sizeof(seg));
   const cuuint64_t rec = kDim * 2;

@@ -202,6 +202,7 @@ def test_scores_that_grow_and_fall_by_a_lot(cfg):
     check_tree(cfg, kv, [n], T, mask, q=q * 30)
     check_tree(cfg, kv, [n], T, mask, q=q * 0)
     check_tree(cfg, kv, [n], T, mask, q=q, scale=-0.25)
+    check_tree(cfg, kv, [n], T, mask, q=q, scale=0.0)
 
 
 def test_rows_beyond_32_bit_offsets():
