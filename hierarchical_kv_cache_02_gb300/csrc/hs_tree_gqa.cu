@@ -24,8 +24,11 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kProducers = 4;
-constexpr int kWarpMma = 8, kWarpProd = 9;
-constexpr int kThreads = (kWarpProd + kProducers) * 32;
+// Warps 0-7 are the softmax groups; the others stand where they share a quarter of the SM's issue slots with the
+// least: the products' warp (every cycle of it counts) beside warps 3 and 7, which have no rows when there are
+// few; the producers in the second and third quarter.  Warps 8 and 12 have nothing to do.
+constexpr int kWarpMma = 11, kThreads = 15 * 32;
+__device__ __forceinline__ int producer_of(int warp) { return warp == 9 || warp == 10 ? warp - 9 : warp == 13 || warp == 14 ? warp - 11 : -1; }
 constexpr int kMaskRing = 8;   // tiles of validity bits per group: more than the ring can run ahead
 constexpr float kLazy = 8.f;   // log2 headroom before the running maximum is raised
 constexpr size_t kSmemCap = 227 * 1024;
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == kWarpProd && lane == 0) {
+  if (warp == 9 && lane == 0) {
     prefetch_map(&qmap);
     if (c.seg != 0) prefetch_map(&segmap);
   }
@@ -162,10 +165,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K_g(i), V_g(i).  (Values loaded right behind their keys: the lookups and addresses serve both, and a
     // head's key and value are neighbours in memory.)
 
-    if (warp >= kWarpProd) {
+    const int pw = producer_of(warp);
+    if (pw >= 0) {
       // ---------------- producers: 32 entries of every tile each ----------------
       // lane y looks up entry y of the warp's 32
-      const int pw = warp - kWarpProd, crow = lane >> 3, cch = lane & 7;
+      const int crow = lane >> 3, cch = lane & 7;
       Lookahead ahead0 = {}, ahead1 = {};  // two variables, never exchanged: a move would wait for a load on its way
       Cursor k0, k1;
       k0.open(list_of(0), count_of(0), c);
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         swap_both(v0, v1);
         g ^= 1;
       }
-    } else {
+    } else if (warp < 8) {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
       const int g = warp >> 2, row = tid & 127;
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -533,15 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
-  if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (producer_of(warp) >= 0) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
-    if (warp >= kWarpProd) {
+    if (producer_of(warp) >= 0) {
 #pragma unroll 1
       for (int i = max(0, sent - C::kRing); i < sent; ++i)
         while (!mbar_try_wait(&ct.full[i % C::kRing], (uint32_t)((i / C::kRing) & 1)) && global_ns() - t0 < 1000000000ull) {
         }
-    } else if ((warp & 3) == 0 && warp < kWarpMma && sent > 0) {
+    } else if ((warp & 3) == 0 && warp < 8 && sent > 0) {
       while (!mbar_try_wait(&ct.qfull[warp >> 2], (uint32_t)((sent - 1) & 1)) && global_ns() - t0 < 1000000000ull) {
       }
     }

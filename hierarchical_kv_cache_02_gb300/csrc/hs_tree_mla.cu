@@ -29,8 +29,9 @@ __device__ __forceinline__ int part_from(int part) { return 4 * part; }
 __device__ __forceinline__ int part_blocks(int part) { return 4 + part; }
 constexpr int kBlk = 64 * 128;                    // bytes of one block of 64 rows
 constexpr int kBuf = kChunks * kBlk;              // a tile; also the queries
-constexpr int kProducers = 4, kWarpMma = 4, kWarpProd = 5;
-constexpr int kThreads = (kWarpProd + kProducers) * 32;
+// Warps 0-3 are the softmax; the products' warp shares a quarter of the SM's issue slots with one of them alone.
+constexpr int kProducers = 4, kWarpMma = 7, kThreads = 10 * 32;
+__device__ __forceinline__ int producer_of(int warp) { return warp >= 4 && warp <= 6 ? warp - 4 : warp == 9 ? 3 : -1; }
 constexpr int kMaskRing = 4;
 constexpr float kLazy = 8.f;                      // log2 headroom before the running maximum is raised
 constexpr size_t kDyn = 3 * (size_t)kBuf + kBlk + 1024;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == kWarpProd && lane == 0) {
+  if (warp == 4 && lane == 0) {
     prefetch_map(&qmap);
     if (c.seg != 0) prefetch_map(&segmap);
   }
@@ -105,9 +106,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (; go; go = plan_round<kTile>(a, c.ws, &ct.plan)) {
     const Portion* list = ct.plan.port[0];
     const int count = ct.plan.nport[0];
-    if (warp >= kWarpProd) {
+    const int pw = producer_of(warp);
+    if (pw >= 0) {
       // ---------------- producers: 16 entries of every tile each, looked up by lanes 0-15 ----------------
-      const int pw = warp - kWarpProd, crow = lane >> 3, cch = lane & 7;
+      const int crow = lane >> 3, cch = lane & 7;
       Lookahead ahead = {};
       ahead.at = count > 0 ? list[0].t0 : 0;
       int kp = 0, kt = ahead.at;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         vfirst = --vl == 0;
         if (vfirst && ++vp < n) vl = uniform(list[vp].t1 - list[vp].t0);
       }
-    } else {
+    } else if (warp < 4) {
       // ---------------- softmax: thread = row (lane & 15) of the warp's 16 ----------------
       // Lanes 0-15 hold the scores of even tiles and O's dims 0-255, lanes 16-31 those of odd tiles and
       // dims 256-511; what a row's two lanes have to agree on goes from the one with the scores to both.
@@ -415,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     warp_wait(&ct.fin, 0u, &never);
   }
   __syncthreads();
-  if (warp >= kWarpProd) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (producer_of(warp) >= 0) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
-    if (warp >= kWarpProd) {
+    if (producer_of(warp) >= 0) {
 #pragma unroll 1
       for (int i = max(0, sent - 4); i < sent; ++i)
         while (!mbar_try_wait(&ct.full[(i >> 1) & 1][i & 1], (uint32_t)((i >> 2) & 1)) && global_ns() - t0 < 1000000000ull) {
