@@ -461,14 +461,15 @@ __device__ __forceinline__ void mask_scores(uint32_t ts, const uint32_t (&w)[WOR
   }
 }
 
-// Takes infinite and NaN values out of the rows [y0, y1) of a tile of `blocks` 128-byte column blocks of `rows`
-// rows each (the swizzle moves bytes within a row's 128 only).  Thread `id` of `threads`; true: it found some.
-__device__ __forceinline__ bool clean_rows(uint8_t* tile, int rows, int blocks, int y0, int y1, int id, int threads) {
+// Takes infinite and NaN values out of the rows [y0, y1) of a tile of `blocks` 128-byte column blocks, `block`
+// bytes apart, with `group` bytes from 8 rows to the next (the swizzle moves bytes within a row's 128 only).
+// Thread `id` of `threads`; true: it found some.
+__device__ __forceinline__ bool clean_rows(uint8_t* tile, int block, int group, int blocks, int y0, int y1, int id, int threads) {
   bool found = false;
 #pragma unroll 1
   for (int i = id; i < (y1 - y0) * blocks * 8; i += threads) {
     const int x = i & 7, z = i >> 3, b = z % blocks, y = y0 + z / blocks;
-    uint4* at = (uint4*)(tile + b * (rows * 128) + y * 128 + 16 * x);
+    uint4* at = (uint4*)(tile + b * block + (y >> 3) * group + (y & 7) * 128 + 16 * x);
     const uint4 u = *at;
     if (bad_pair(u.x) || bad_pair(u.y) || bad_pair(u.z) || bad_pair(u.w)) {
       found = true;

@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t vp = ct.vplace[mg][nm % kMaskRing];
             if (ok) ok = mbar_wait_small(&ct.full[vp >> 1], vp & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            const bool d = ok && clean_rows(smem + (2 + (vp >> 1)) * C::kSlot, kTile, C::kCh, max(0, -j0),
+            const bool d = ok && clean_rows(smem + (2 + (vp >> 1)) * C::kSlot, kTile * 128, 1024, C::kCh, max(0, -j0),
                                             min(kTile, P.nn - j0), both ? tid : row, both ? 256 : 128);
             if (bar_or(both ? 3 : 1 + g, both ? 256 : 128, d)) dirty = true;
           }

@@ -25,10 +25,13 @@ constexpr int kTile = 64, kRows = 64, kDim = 576, kValue = 512;
 constexpr int kChunks = kDim / 64;                // 128-byte column blocks of a tile
 // A tile's blocks come and go in two parts: 0-3, the values' first half, and 4-8.
 constexpr int kParts = 2;
-__device__ __forceinline__ int part_from(int part) { return 4 * part; }
-__device__ __forceinline__ int part_blocks(int part) { return 4 + part; }
-constexpr int kBlk = 64 * 128;                    // bytes of one block of 64 rows
-constexpr int kBuf = kChunks * kBlk;              // a tile; also the queries
+__host__ __device__ constexpr int part_from(int part) { return 4 * part; }
+__host__ __device__ constexpr int part_blocks(int part) { return 4 + part; }
+constexpr int kBlk = 64 * 128;                    // bytes of one block of 64 rows of the queries or weights
+constexpr int kBuf = kChunks * kBlk;              // the queries; also a tile
+// A tile lies in groups of 8 records, a group's blocks one after the other: one copy brings 4 or 5 blocks of 16
+// records.  (Block by block, 9 copies a warp and tile, their issue alone took a third of the tile's time.)
+constexpr int kGroup = kChunks * 1024;
 // Warps 0-3 are the softmax; the products' warp shares a quarter of the SM's issue slots with one of them alone.
 constexpr int kProducers = 4, kWarpMma = 7, kThreads = 10 * 32;
 __device__ __forceinline__ int producer_of(int warp) { return warp >= 4 && warp <= 6 ? warp - 4 : warp == 9 ? 3 : -1; }
@@ -55,7 +58,8 @@ struct MlaControl {
 static_assert(kDyn + sizeof(MlaControl) <= 227 * 1024, "shared memory of a CTA");
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tree_mla(const MlaArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap) {
+    k_tree_mla(const MlaArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap0,
+               const __grid_constant__ CUtensorMap segmap1) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ MlaControl ct;
   const TreeArgs& a = c.a;
@@ -86,7 +90,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 4 && lane == 0) {
     prefetch_map(&qmap);
-    if (c.seg != 0) prefetch_map(&segmap);
+    if (c.seg != 0) {
+      prefetch_map(&segmap0);
+      prefetch_map(&segmap1);
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // the only kernel that may start early is this call's own combine, which waits for this one
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Portion& P = list[kp];
         const bool boxed = c.seg != 0 && kt * kTile + 16 * pw + 16 <= P.n;
         const int b = nt & 1;
-        const uint32_t dst = buf_u + (uint32_t)(b * kBuf + 16 * pw * 128);
+        const uint32_t dst = buf_u + (uint32_t)(b * kBuf + 2 * pw * kGroup);
         const int row = __shfl_sync(0xffffffffu, ahead.row, 0);
 #pragma unroll 1
         for (int part = 0; part < kParts; ++part) {
@@ -132,18 +139,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nch * 16 * 128));
             else mbar_arrive(full);
             __syncwarp();
-            if (lane < nch) tma_load_2d(dst + (uint32_t)((ch0 + lane) * kBlk), &segmap, 64 * (ch0 + lane), row, full);
+            if (lane == 0) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                tma_load_4d(dst + (uint32_t)(g * kGroup + ch0 * 1024), part == 0 ? &segmap0 : &segmap1, 0, 0, ch0, (row >> 3) + g, full);
+            }
           } else {
             // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int y = 4 * i + crow;
               const uint64_t src = __shfl_sync(0xffffffffu, ahead.now, y);
-              const uint32_t to = dst + (uint32_t)(ch0 * kBlk + y * 128 + ((cch ^ (y & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+              const uint32_t to = dst + (uint32_t)((y >> 3) * kGroup + ch0 * 1024 + (y & 7) * 128 + ((cch ^ (y & 7)) << 4)), n = src != 0ull ? 16u : 0u;
               const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + 128 * ch0 + 16 * cch : (const uint8_t*)a.q;
 #pragma unroll
               for (int h = 0; h < 5; ++h)
-                if (h < nch) cp_async16_zfill(to + h * kBlk, src != 0ull ? from + 128 * h : from, n);
+                if (h < nch) cp_async16_zfill(to + h * 1024, src != 0ull ? from + 128 * h : from, n);
             }
             cp_async_arrive_noinc(full);
           }
@@ -169,56 +180,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_o = umma_idesc_bf16(kRows, 256, 0, 1);
       const uint32_t dq = (uint32_t)uniform((int)umma_sdesc_lo(q_u, 16)), dk = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, 16));
       const uint32_t dp = (uint32_t)uniform((int)umma_sdesc_lo(p_u, 16));
-      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
-      const uint32_t dv = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, kBlk));
+      // V as it lies: blocks of 64 values 1 KB apart, 8 entries a group, the value dims contiguous
+      const uint32_t dv = (uint32_t)uniform((int)umma_sdesc_lo(buf_u, 1024));
       const int n = uniform(count);
       // the next scores' and the next values' place: portion, tiles left in it, whether it is its first tile;
-      // ahead: tiles whose scores were issued and whose values were not
-      int kp = 0, kl = 0, vp = 0, vl = 0, ahead = 0;
+      // ahead: tiles whose scores were issued and whose values were not; part: of the scores to come
+      int kp = 0, kl = 0, vp = 0, vl = 0, ahead = 0, part = 0;
       bool kfirst = true, vfirst = true;
       if (n > 0) kl = vl = uniform(list[0].t1 - list[0].t0);
       while (vp < n) {
+        const int i = nt + ahead, bs = i & 1;
+        const bool more = kp < n && ahead < 2;
         bool scores = ahead == 0;
-        if (kp < n && ahead == 1) {
-          const int i = nt + 1;
+        if (ahead != 0 && ok) {
+          ok = false;
 #pragma unroll 1
-          for (uint32_t x = 0; ok && x < (1u << 22); ++x) {
-            if (uniform_test(&ct.p, (uint32_t)(nt & 1))) break;
-            scores = uniform_test(&ct.full[i & 1][0], (uint32_t)((i >> 1) & 1));
-            if (scores) break;
+          for (uint32_t x = 0; x < (1u << 22); ++x) {
+            ok = uniform_test(&ct.p, (uint32_t)(nt & 1));
+            if (ok) break;
+            if (more) {
+              ok = scores = uniform_test(&ct.full[bs][part], (uint32_t)((i >> 1) & 1)) &&
+                            (!kfirst || part != 0 || uniform_test(&ct.qfull, (uint32_t)(nq & 1)));
+              if (ok) break;
+            }
+            if (__any_sync(0xffffffffu, *abort != 0u)) break;
           }
         }
         if (scores) {
-          const int i = nt + ahead, b = i & 1;
-          if (kfirst) {  // this portion's queries
+          if (kfirst && part == 0) {  // this portion's queries
             if (ok) ok = uniform_wait(&ct.qfull, (uint32_t)(nq & 1), abort);
             ++nq;
           }
-          const uint32_t to = tu + kScores + ((uint32_t)(16 * b) << 16);
-          const uint32_t y = dk + (uint32_t)(b * (kBuf >> 4));
+          if (ok) ok = uniform_wait(&ct.full[bs][part], (uint32_t)((i >> 1) & 1), abort);
+          // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc_fence_after();
+          const uint32_t to = tu + kScores + ((uint32_t)(16 * bs) << 16);
+          const uint32_t x = dq + part_from(part) * (kBlk >> 4), y = dk + (uint32_t)(bs * (kBuf >> 4)) + part_from(part) * 64;
+          if (ok && elect_one()) {
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            if (ok) ok = uniform_wait(&ct.full[b][part], (uint32_t)((i >> 1) & 1), abort);
-            // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_after();
-            if (ok && elect_one()) {
+            for (int h = 0; h < 4; ++h)
 #pragma unroll
-              for (int h = 4 * part; h < 4 + 5 * part; ++h)
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_lo<kGroup>(to, x + h * (kBlk >> 4) + 2 * ks, y + h * 64 + 2 * ks, id_s, (part | h | ks) != 0 ? 1u : 0u);
+            if (part == kParts - 1) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  umma_bf16_lo(to, dq + h * (kBlk >> 4) + 2 * ks, y + h * (kBlk >> 4) + 2 * ks, id_s, (h | ks) != 0 ? 1u : 0u);
-              if (part == kParts - 1) umma_commit(&ct.s[b]);
+              for (int ks = 0; ks < 4; ++ks) umma_bf16_lo<kGroup>(to, x + 4 * (kBlk >> 4) + 2 * ks, y + 4 * 64 + 2 * ks, id_s, 1u);
+              umma_commit(&ct.s[bs]);
             }
-            __syncwarp();
           }
+          __syncwarp();
+          if (++part < kParts) continue;
+          part = 0;
           ++ahead;
           kfirst = --kl == 0;
           if (kfirst && ++kp < n) kl = uniform(list[kp].t1 - list[kp].t0);
           continue;
         }
         const int b = nt & 1;
-        if (ok) ok = uniform_wait(&ct.p, (uint32_t)(nt & 1), abort);
         tc_fence_after();
         if (ok && elect_one()) {
           const uint32_t y = dv + (uint32_t)(b * (kBuf >> 4));
@@ -226,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_bf16_lo(tu + ((uint32_t)(16 * h) << 16), dp + 2 * ks, y + 4 * h * (kBlk >> 4) + 128 * ks, id_o,
-                           (!vfirst || ks != 0) ? 1u : 0u);
+              umma_bf16_lo<kGroup>(tu + ((uint32_t)(16 * h) << 16), dp + 2 * ks, y + 4 * h * 64 + ks * (2 * kGroup >> 4), id_o,
+                                   (!vfirst || ks != 0) ? 1u : 0u);
             umma_commit(&ct.empty[b][h]);
           }
           umma_commit(&ct.pv);
@@ -239,9 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (vfirst && ++vp < n) vl = uniform(list[vp].t1 - list[vp].t0);
       }
     } else if (warp < 4) {
-      // ---------------- softmax: thread = row (lane & 15) of the warp's 16 ----------------
-      // Lanes 0-15 hold the scores of even tiles and O's dims 0-255, lanes 16-31 those of odd tiles and
-      // dims 256-511; what a row's two lanes have to agree on goes from the one with the scores to both.
+      // ---------------- softmax: 16 rows a warp ----------------
+      // Scores (of even tiles in lanes 0-15 of tensor memory, of odd ones in 16-31) are read as four threads a row
+      // hold them, lane / 4 and lane / 4 + 8, so that all threads work on a tile; O a thread per row, lane & 15,
+      // dims 0-255 or 256-511.
       const int row = 16 * warp + (lane & 15), side = lane >> 4;
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
       auto load_q = [&](const Portion& P) {  // by the first thread
@@ -259,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         const uint64_t* mw = a.mask + ((int64_t)P.r * a.T + (row_ok ? t : 0)) * a.words;
         const uint64_t mfirst = mw[0];
-        float m = -INFINITY, l = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of rows lane / 4 and + 8; l: this thread's columns
         bool dirty = false;  // a node's value is infinite or NaN
         for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
           const int b = nt & 1;
@@ -270,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
           if (ok) ok = mbar_wait_small(&ct.mask[nt % kMaskRing], (uint32_t)((nt / kMaskRing) & 1), abort);
           ok = __all_sync(0xffffffffu, ok);
-          uint32_t w[2];
+          uint32_t w[2];  // of row lane & 15
 #pragma unroll
           for (int x = 0; x < 2; ++x) w[x] = ct.valid[nt % kMaskRing][2 * x] | (ct.valid[nt % kMaskRing][2 * x + 1] << 16);
           const bool full = !nodes && (w[0] & w[1]) == 0xffffffffu;
@@ -286,67 +306,78 @@ __global__ void __launch_bounds__(kThreads, 1)
             // added to the rows that see them at the end.  Their scores are done.
             for (int i = 0; i < kParts; ++i)
               if (ok) ok = mbar_wait_small(&ct.full[b][i], (uint32_t)((nt >> 1) & 1), abort);
-            const bool d = ok && clean_rows(smem + kBuf + kBlk + b * kBuf, kTile, kValue / 64, max(0, -j0), min(kTile, P.nn - j0), tid, 128);
+            const bool d = ok && clean_rows(smem + kBuf + kBlk + b * kBuf, 1024, kGroup, kValue / 64, max(0, -j0),
+                                             min(kTile, P.nn - j0), tid, 128);
             if (bar_or(1, 128, d)) dirty = true;
             ok = __all_sync(0xffffffffu, ok);
           }
-          float sum = 0.f;
-          uint32_t pk[32];
           if (ok && warp_ok) {
-            float v[64];
-            tmem_ld64(tb + lane_base + kScores, v);
-            if (!full) {  // (here, not in tensor memory: the other lanes' scores are the next tile's, on their way)
+            float v[32];
+            tmem_ld_16x64(tb + lane_base + kScores + ((uint32_t)(16 * b) << 16), v);
+            if (!full) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = (w[j >> 5] >> (j & 31)) & 1u ? v[j] : -INFINITY;
-            }
-            float mx = -INFINITY, my = -INFINITY;
+              for (int h = 0; h < 4; ++h) {  // row (lane / 4) + 8 (h & 1), 32 columns
+                const uint32_t bits = __shfl_sync(0xffffffffu, w[h >> 1], (lane >> 2) + 8 * (h & 1)) >> (2 * (lane & 3));
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-              mx = fmaxf(fmaxf(mx, v[j]), v[j + 1]);
-              my = fmaxf(fmaxf(my, v[j + 2]), v[j + 3]);
-            }
-            mx = fmaxf(mx, my) * a.qscale;
-            mx = __shfl_sync(0xffffffffu, mx, (lane & 15) + 16 * b);
-            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
-            const bool raise = mx > m + kLazy;
-            const bool any = __any_sync(0xffffffffu, raise);
-            const float mo = m;
-            if (raise) m = mx;
-            const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 0
-            float s1 = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float p0, p1;
-              fma2(p0, p1, v[2 * j], v[2 * j + 1], a.qscale, -base);
-              pk[j] = pack_bf16(fast_exp2(p0), fast_exp2(p1));
-              add2(sum, s1, lo(pk[j]), hi(pk[j]));  // the rounded weights, as the product takes them
-            }
-            sum = __shfl_sync(0xffffffffu, sum + s1, (lane & 15) + 16 * b);
-            if (nt > 0) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            if (any) {
-              const float al = (m == mo || mo == -INFINITY) ? 1.f : fast_exp2(mo - m);
-              l *= al;
-              if (tile != P.t0 && ok) {
-#pragma unroll 1
                 for (int x = 0; x < 8; ++x) {
-                  float o[32];
-                  tmem_ld32(tb + lane_base + 32u * x, o);
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] *= al;
-                  tmem_st32(tb + lane_base + 32u * x, o);
+                  const int j = 16 * (h >> 1) + 4 * (x >> 1) + 2 * (h & 1) + (x & 1);
+                  v[j] = (bits >> (8 * (x >> 1) + (x & 1))) & 1u ? v[j] : -INFINITY;
                 }
               }
             }
-            l += sum;
-            // P, K-major and swizzled like the queries: 64 entries are one 128-byte row
-            if (side == b) {
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                *(uint4*)(smem + kBuf + row * 128 + ((x ^ (row & 7)) << 4)) =
-                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+            for (int j = 0; j < 32; j += 4) {
+              mx[0] = fmaxf(fmaxf(mx[0], v[j]), v[j + 1]);
+              mx[1] = fmaxf(fmaxf(mx[1], v[j + 2]), v[j + 3]);
             }
+            bool any = false;
+            float al[2], base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+              mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.qscale;
+              const float mo = m[h];
+              if (mx[h] > mo + kLazy) {
+                m[h] = mx[h];
+                any = true;
+              }
+              al[h] = (m[h] == mo || mo == -INFINITY) ? 1.f : fast_exp2(mo - m[h]);
+              base[h] = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen so far: every weight is 0
+            }
+            any = __any_sync(0xffffffffu, any);
+            uint32_t pk[16];
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float p0, p1;
+              fma2(p0, p1, v[2 * j], v[2 * j + 1], a.qscale, -base[j & 1]);
+              pk[j] = pack_bf16(fast_exp2(p0), fast_exp2(p1));
+              add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], lo(pk[j]), hi(pk[j]));  // the rounded weights, as the product takes them
+            }
+            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
+            if (nt > 0) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (any && tile != P.t0 && ok) {
+              const float x0 = __shfl_sync(0xffffffffu, al[0], 4 * (lane & 7)), x1 = __shfl_sync(0xffffffffu, al[1], 4 * (lane & 7));
+              const float f = (lane & 8) != 0 ? x1 : x0;
+#pragma unroll 1
+              for (int x = 0; x < 8; ++x) {
+                float o[32];
+                tmem_ld32(tb + lane_base + 32u * x, o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= f;
+                tmem_st32(tb + lane_base + 32u * x, o);
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) l[h] = fmaf(l[h], al[h], sum[2 * h] + sum[2 * h + 1]);
+            // P, K-major and swizzled like the queries: 64 entries are one 128-byte row
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              stmatrix_x4(p_u + (uint32_t)(row * 128 + (((2 * x + side) ^ (row & 7)) << 4)), pk[4 * x], pk[4 * x + 1], pk[4 * x + 2],
+                          pk[4 * x + 3]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           } else if (ok && nt > 0) {
             ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);  // no phase of it may pass unseen
@@ -362,7 +393,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && warp_ok) {
           const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
           const long long slot = ((long long)blockIdx.x * 2 + (P.t0 > 0 ? 0 : 1)) * kRows;
-          const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          float mr = 0.f, lr = 0.f;  // of row lane & 15
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const float x = __shfl_sync(0xffffffffu, m[h], 4 * (lane & 7)), y = __shfl_sync(0xffffffffu, l[h], 4 * (lane & 7));
+            if (h == ((lane >> 3) & 1)) mr = x, lr = y;
+          }
+          const float inv = whole ? (lr == 0.f ? 0.f : 1.f / lr) : 1.f;
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
             float o[32];
@@ -396,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (row_ok && !whole && side == 0) *(float2*)(c.ws.ml + (slot + row) * 2) = make_float2(m, l);
+          if (row_ok && !whole && side == 0) *(float2*)(c.ws.ml + (slot + row) * 2) = make_float2(mr, lr);
         }
         tc_fence_before();
       }
@@ -466,15 +505,17 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
     c.a.qscale = -c.a.qscale;
   }
   c.a.qscale = fmaxf(c.a.qscale, 1.17549435e-38f);  // times -infinity has to stay -infinity
-  CUtensorMap qm, seg;
-  memset(&seg, 0, sizeof(seg));
+  CUtensorMap qm, seg[2];
+  memset(seg, 0, sizeof(seg));
   const cuuint64_t rec = kDim * 2;
   if (c.a.slot_pt == nullptr && c.a.locs == nullptr && c.a.kv.page_tokens % 16 == 0) {
     c.seg = 16;
     c.ctx_rows = (int)(c.a.kv.num_pages * c.a.kv.page_tokens);
-    const cuuint64_t size[2] = {kDim, (cuuint64_t)c.ctx_rows}, stride[1] = {rec};
-    const cuuint32_t box[2] = {64, 16};
-    if (!encode(&seg, c.a.kv.base, 2, size, stride, box)) c.seg = 0;
+    const cuuint64_t size[4] = {64, 8, kChunks, (cuuint64_t)c.ctx_rows / 8}, stride[3] = {rec, 128, 8 * rec};
+    for (int i = 0; i < kParts; ++i) {
+      const cuuint32_t box[4] = {64, 8, (cuuint32_t)part_blocks(i), 1};
+      if (!encode(&seg[i], c.a.kv.base, 4, size, stride, box)) c.seg = 0;
+    }
   }
   const cuuint64_t qsize[2] = {kDim, (cuuint64_t)cfg->num_requests * g->nodes * cfg->num_q_heads}, qstride[1] = {rec};
   const cuuint32_t qbox[2] = {64, kRows};
@@ -490,7 +531,7 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   cb.flat = kRows;
   static bool done[64];
   cudaError_t e = allow_smem(k_tree_mla, kDyn, done);
-  if (e == cudaSuccess) e = hs_launch_pdl(k_tree_mla, dim3(num_sms), dim3(kThreads), kDyn, st, c, qm, seg);
+  if (e == cudaSuccess) e = hs_launch_pdl(k_tree_mla, dim3(num_sms), dim3(kThreads), kDyn, st, c, qm, seg[0], seg[1]);
   if (e == cudaSuccess)
     e = hs_launch_pdl(k_tree_combine<kValue>, combine_grid(c.ws.items, cfg->num_requests, kRows, kValue), dim3(256), 0, st, cb);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
