@@ -146,6 +146,42 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// The same for a pair of CTAs (a cluster of two): A's rows are halved between them, and so are B's rows (the columns
+// of the accumulator); the even CTA issues for both, and a commit arrives on the barrier in both.
+template <uint32_t SB = 1024>
+__device__ __forceinline__ void umma2_bf16_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+               "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kSdescHi), "n"(sdesc_hi(SB))
+               : "memory");
+}
+__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {  // a shared address of this CTA, in CTA `rank`
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// On a barrier in any CTA of the cluster.  What it announces is this CTA's own shared memory, ordered before by
+// fence.proxy.async, and is read by the tensor cores alone: release at the CTA's scope.  (At the cluster's it
+// takes 1000 cycles more.)
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {  // every thread of both CTAs
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // 32 consecutive TMEM columns of this thread's lane
@@ -273,7 +309,7 @@ __device__ __forceinline__ bool uniform_wait2(uint64_t* bar, uint32_t parity, ui
   }
   return false;
 }
-__device__ __forceinline__ bool uniform_test(uint64_t* bar, uint32_t parity) {  // no wait
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {  // no wait
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -282,7 +318,7 @@ __device__ __forceinline__ bool uniform_test(uint64_t* bar, uint32_t parity) {  
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return __any_sync(0xffffffffu, ok != 0u);
+  return ok != 0u;
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 

@@ -113,7 +113,8 @@ struct PlanState {  // shared memory
 struct WorkSplit {
   int items, np;         // per request; of them per KV head
   int begin;             // units of an item before its tiles
-  int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA
+  int groups;            // workers of a CTA: worker w = group * gridDim.x + CTA; or
+  int pairs;             // 1: two neighbouring CTAs are one worker
   long long* prefix;     // [R + 1] units (of one item) before each request, written by CTA 0
   float *part, *ml;      // [workers][2 slots][dims / 8][rows][8], [workers][2][rows][2]: maximum (base 2) and sum
   int rows;              // accumulator rows of a portion
@@ -239,8 +240,8 @@ __device__ __forceinline__ bool plan_start(const TreeArgs& a, const WorkSplit& w
         if (lane >= o) incl += y;
       }
       const int total = __shfl_sync(0xffffffffu, incl, kWindow - 1);
-      const Shares sh((long long)total * ws.items, (int)gridDim.x * ws.groups);
-      const int w = g * (int)gridDim.x + (int)blockIdx.x;
+      const Shares sh((long long)total * ws.items, (int)(gridDim.x >> ws.pairs) * ws.groups);
+      const int w = g * (int)gridDim.x + (int)(blockIdx.x >> ws.pairs);
       const long long s0 = sh.start(w), left = g < ws.groups ? sh.start(w + 1) - s0 : 0;
       const long long off = s0 - (long long)(incl - U) * ws.items;
       const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < (long long)U * ws.items);
@@ -301,10 +302,10 @@ __device__ __forceinline__ bool plan_start(const TreeArgs& a, const WorkSplit& w
         total += s->scan[w];
       }
       run += incl - mine;
-      const Shares sh(total * ws.items, (int)gridDim.x * ws.groups);
+      const Shares sh(total * ws.items, (int)(gridDim.x >> ws.pairs) * ws.groups);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int w = g * (int)gridDim.x + (int)blockIdx.x;
+        const int w = g * (int)gridDim.x + (int)(blockIdx.x >> ws.pairs);
         const long long x = sh.start(w), left = g < ws.groups ? sh.start(w + 1) - x : 0;
         if (left > 0) s0[g] = x;
         if (tid == 0) s->left[g] = left;
