@@ -286,6 +286,17 @@ __device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, 
   return false;
 }
 
+__device__ __forceinline__ bool mbar_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                           volatile uint32_t* abort) {  // two at once: their latencies overlap
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 22); ++i) {
+    const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
+    if (x && y) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
 // A whole warp's wait whose result the compiler knows to be the same in all lanes.  The warp that issues the
 // products keeps to such values throughout: tcgen05.mma takes its operands from uniform registers, and where
 // they are not uniform to begin with each product costs their moves (57 cycles instead of 32 for one of

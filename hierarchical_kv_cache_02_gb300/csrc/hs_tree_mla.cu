@@ -29,10 +29,11 @@ constexpr int kQ = kChunks * kBlk;                // a CTA's queries
 constexpr int kKGroup = kChunks * 1024, kVGroup = 4 * 1024;
 constexpr int kKBuf = 4 * kKGroup, kVBuf = 8 * kVGroup;  // 32 whole records; 256 values of 64 records
 // Warps 0-3 are the softmax; the products' warp shares a quarter of the SM's issue slots with one of them alone.
-constexpr int kWarpMma = 7, kWarpPass = 8, kThreads = 10 * 32;
+constexpr int kWarpMma = 7, kPassKeys = 8, kPassValues = 10, kThreads = 11 * 32;
 __device__ __forceinline__ int key_producer(int warp) { return warp == 4 || warp == 5 ? warp - 4 : -1; }
 __device__ __forceinline__ int value_producer(int warp) { return warp == 6 ? 0 : warp == 9 ? 1 : -1; }
 constexpr int kMaskRing = 4;
+constexpr int kAhead = 4;                         // accumulators of scores
 constexpr float kLazy = 8.f;                      // log2 headroom before the running maximum is raised
 constexpr size_t kDyn = (size_t)kQ + kBlk + 2 * (kKBuf + kVBuf) + 1024;
 constexpr uint32_t kScores = 256;                 // first column of the scores, behind O's 256
@@ -48,8 +49,8 @@ struct MlaArgs {
 struct MlaControl {
   PlanState plan;
   __align__(8) uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t kpeer[2], vpeer[2], qpeer;  // even CTA: the same of the other CTA is full
-  uint64_t qfull, s[2], p, pv, mask[kMaskRing], fin;
+  uint64_t kready[2], vready[2], qready;  // even CTA: full in both
+  uint64_t qfull, s[kAhead], p, pv, mask[kMaskRing], fin;
   uint32_t valid[kMaskRing][2];
   float most[2][2][64], sums[2][64];
   uint32_t tmem, abort, dirty;
@@ -73,11 +74,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ct.vfull[b], 64u);
       mbar_init(&ct.kempty[b], 1u);
       mbar_init(&ct.vempty[b], 1u);
-      mbar_init(&ct.kpeer[b], 1u);
-      mbar_init(&ct.vpeer[b], 1u);
-      mbar_init(&ct.s[b], 1u);
+      mbar_init(&ct.kready[b], 2u);
+      mbar_init(&ct.vready[b], 2u);
     }
-    mbar_init(&ct.qpeer, 1u);
+    for (int i = 0; i < kAhead; ++i) mbar_init(&ct.s[i], 1u);
+    mbar_init(&ct.qready, 2u);
     mbar_init(&ct.qfull, 1u);
     mbar_init(&ct.p, 8u);
     mbar_init(&ct.pv, 1u);
@@ -225,45 +226,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (n > 0) kl = vl = uniform(list[0].t1 - list[0].t0);
       while (vp < n) {
         const int i = nt + ahead, bs = i & 1, b = nt & 1;
-        const bool more = kp < n && ahead < 2;
+        const bool more = kp < n && ahead < kAhead;
         bool scores = ahead == 0;
         if (ok) {
           ok = false;
-          const uint32_t fp = (uint32_t)((i >> 1) & 1), vq = (uint32_t)((nt >> 1) & 1);
+          const uint32_t kq = (uint32_t)((i >> 1) & 1), vq = (uint32_t)((nt >> 1) & 1);
 #pragma unroll 1
           for (uint32_t x = 0; x < (1u << 22); ++x) {
-            if (ahead != 0) {
-              const bool y0 = mbar_test(&ct.p, (uint32_t)(nt & 1)), y1 = mbar_test(&ct.vfull[b], vq),
-                         y2 = mbar_test(&ct.vpeer[b], vq);
-              ok = __any_sync(0xffffffffu, y0 && y1 && y2);
-              if (ok) break;
-            }
-            if (more) {
-              bool y0 = mbar_test(&ct.kfull[bs], fp), y1 = mbar_test(&ct.kpeer[bs], fp);
-              if (kfirst) {  // this portion's queries
-                y0 = y0 && mbar_test(&ct.qfull, (uint32_t)(nq & 1));
-                y1 = y1 && mbar_test(&ct.qpeer, (uint32_t)(nq & 1));
-              }
-              ok = scores = __any_sync(0xffffffffu, y0 && y1);
-              if (ok) break;
-            }
+            const bool y0 = mbar_test(&ct.p, (uint32_t)(nt & 1)), y1 = mbar_test(&ct.vready[b], vq),
+                       y2 = mbar_test(&ct.kready[bs], kq), y3 = !kfirst || mbar_test(&ct.qready, (uint32_t)(nq & 1));
+            ok = __any_sync(0xffffffffu, ahead != 0 && y0 && y1);
+            if (ok) break;
+            ok = scores = __any_sync(0xffffffffu, more && y2 && y3);
+            if (ok) break;
             if (__any_sync(0xffffffffu, *abort != 0u)) break;
           }
           if (!ok) scores = ahead == 0;
         }
-        // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_after();
         if (scores) {
           if (kfirst) ++nq;
-          const uint32_t to = tu + kScores + 32u * bs, y = dk + (uint32_t)(bs * (kKBuf >> 4));
+          const uint32_t to = tu + kScores + 32u * (i % kAhead), y = dk + (uint32_t)(bs * (kKBuf >> 4));
           if (ok && elect_one()) {
 #pragma unroll
             for (int h = 0; h < kChunks; ++h)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 umma2_bf16_lo<kKGroup>(to, dq + h * (kBlk >> 4) + 2 * ks, y + h * 64 + 2 * ks, id_s, (h | ks) != 0 ? 1u : 0u);
-            umma2_commit(&ct.s[bs]);
+            umma2_commit(&ct.s[i % kAhead]);
             umma2_commit(&ct.kempty[bs]);
           }
           __syncwarp();
@@ -289,30 +279,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         vfirst = --vl == 0;
         if (vfirst && ++vp < n) vl = uniform(list[vp].t1 - list[vp].t0);
       }
-    } else if (warp == kWarpMma) {
-      // ---------------- odd CTA: its queries and keys are there, passed on to the even one ----------------
-      const uint32_t kb = in_cta(smem_u32(&ct.kpeer[0]), 0), qb = in_cta(smem_u32(&ct.qpeer), 0);
+    } else if (warp == kPassKeys || warp == kPassValues) {
+      // ---------------- what the products take is there, passed on to the even CTA ----------------
+      // (Copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy.)
+      const bool keys = warp == kPassKeys;
+      uint64_t* full = keys ? ct.kfull : ct.vfull;
+      const uint32_t ready = in_cta(smem_u32(keys ? ct.kready : ct.vready), 0), qr = in_cta(smem_u32(&ct.qready), 0);
       for (int pi = 0; pi < count; ++pi) {
-        if (ok) ok = warp_wait_small(&ct.qfull, (uint32_t)(nq & 1), abort);
-        ++nq;
-        if (ok && lane == 0) cluster_arrive(qb);
+        if (keys) {
+          if (ok) ok = warp_wait_small(&ct.qfull, (uint32_t)(nq & 1), abort);
+          ++nq;
+          if (ok && lane == 0) cluster_arrive(qr);
+        }
         for (int tile = list[pi].t0; tile < list[pi].t1; ++tile, ++nt) {
-          if (ok) ok = warp_wait_small(&ct.kfull[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
+          if (ok) ok = warp_wait_small(&full[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (ok && lane == 0) cluster_arrive(kb + 8u * (nt & 1));
+          if (ok && lane == 0) cluster_arrive(ready + 8u * (nt & 1));
         }
       }
-    } else if (warp == kWarpPass) {
-      // ---------------- odd CTA: and its values ----------------
-      const uint32_t vb = in_cta(smem_u32(&ct.vpeer[0]), 0);
-      for (int pi = 0; rank != 0 && pi < count; ++pi) {
-        for (int tile = list[pi].t0; tile < list[pi].t1; ++tile, ++nt) {
-          if (ok) ok = warp_wait_small(&ct.vfull[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (ok && lane == 0) cluster_arrive(vb + 8u * (nt & 1));
-        }
-      }
-    } else {
+    } else if (warp < 4) {
       // ---------------- softmax: two threads a row, half of a tile's entries and half of the dims each ----------------
       const int row = tid & 63, half = tid >> 6;
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16, p_bar = in_cta(smem_u32(&ct.p), 0);
@@ -338,11 +323,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int b = nt & 1;
           const int j0 = (int)((long long)tile * kTile - n4);  // node of the tile's first entry
           const bool nodes = j0 + kTile > 0;
-          if (ok) ok = mbar_wait_small(&ct.s[b], (uint32_t)((nt >> 1) & 1), abort);
+          if (ok) ok = mbar_wait2(&ct.s[nt % kAhead], (uint32_t)((nt / kAhead) & 1), &ct.mask[nt % kMaskRing],
+                                  (uint32_t)((nt / kMaskRing) & 1), abort);
+          ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
-          if (ok) ok = mbar_wait_small(&ct.mask[nt % kMaskRing], (uint32_t)((nt / kMaskRing) & 1), abort);
-          ok = __all_sync(0xffffffffu, ok);
           uint32_t w = ct.valid[nt % kMaskRing][half];
           if (nodes) {
             // entries that are nodes: valid ones that this row sees
@@ -365,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool live = ok && warp_ok;
           float v[32], mx = -INFINITY;
           if (live) {
-            tmem_ld32(tb + lane_base + kScores + 32u * b, v);
+            tmem_ld32(tb + lane_base + kScores + 32u * (nt % kAhead), v);
             if (w != 0xffffffffu) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = (w >> j) & 1u ? v[j] : -INFINITY;
@@ -382,6 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pair_sync();
           if (live) {
             mx = fmaxf(mx, ct.most[b][half ^ 1][row]);
+            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
+            const bool done = nt == 0 || mbar_test(&ct.pv, (uint32_t)((nt - 1) & 1));
             const bool raise = mx > m + kLazy;
             const bool any = __any_sync(0xffffffffu, raise);
             const float mo = m;
@@ -396,8 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               pk[j] = pack_bf16(fast_exp2(p0), fast_exp2(p1));
               add2(sum, s1, lo(pk[j]), hi(pk[j]));  // the rounded weights, as the product takes them
             }
-            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
-            if (nt > 0) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+            if (!done) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (any) {
