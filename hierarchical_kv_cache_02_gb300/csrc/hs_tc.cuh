@@ -135,11 +135,12 @@ __device__ __forceinline__ void umma_bf16_lo(uint32_t d, uint32_t a, uint32_t b,
                "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kSdescHi), "n"(sdesc_hi(SB))
                : "memory");
 }
+template <uint32_t SB = 1024>
 __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                "mov.b64 y, {%2, %5};\n\t"
                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-               "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kSdescHi)
+               "r"(a), "r"(b), "r"(id), "r"(acc), "n"(sdesc_hi(SB))
                : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {

@@ -33,11 +33,15 @@ constexpr int kMaskRing = 8;   // tiles of validity bits per group: more than th
 constexpr float kLazy = 8.f;   // log2 headroom before the running maximum is raised
 constexpr size_t kSmemCap = 227 * 1024;
 
-template <int D>
+template <int D, bool SHARED>
 struct Shape {
   static constexpr int kCh = D / 64;                 // 64-value (128-byte) column blocks
   static constexpr int kBlk = kTile * 128;           // bytes of one block of a tile
   static constexpr int kSlot = kCh * kBlk;           // a K or V tile; also a Q tile
+  // How K and V lie: bytes from 8 records to the next 8, and from a 64-value block to the next.  Shared, a group's
+  // blocks one after the other, so that one copy brings all blocks of 16 or 32 records: their number is what copies
+  // cost there.  Unshared, block by block: memory bounds these, and copies of 128-byte rows use it better.
+  static constexpr int kGroup = SHARED ? kCh * 1024 : 1024, kBlock = SHARED ? 1024 : kTile * 128;
   static constexpr int kRing = D == 128 ? 5 : 11;
   static constexpr size_t kDyn = (size_t)(2 + kRing) * kSlot + 1024;
 };
@@ -101,10 +105,10 @@ struct Cursor {
   }
 };
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tree_gqa(const TcArgs c, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap segmap) {
-  using C = Shape<D>;
+  using C = Shape<D, SHARED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Control ct;
   const TreeArgs& a = c.a;
@@ -156,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t bad = 0u;
 
   for (; go; go = plan_round<kTile>(a, c.ws, &ct.plan)) {
-    const int ng = c.shared ? 1 : 2;  // portion lists
+    const int ng = SHARED ? 1 : 2;  // portion lists
     // whether group g takes part in an item: the last pair of row tiles may be a single one
-    auto present = [&](int g, const Portion& p) { return !c.shared || 2 * p.pair + g < c.nmt; };
+    auto present = [&](int g, const Portion& p) { return !SHARED || 2 * p.pair + g < c.nmt; };
     auto count_of = [&](int g) { return ct.plan.nport[g < ng ? g : 0]; };
     auto list_of = [&](int g) -> const Portion* { return ct.plan.port[g < ng ? g : 0]; };
     // The groups take turns: the products O_g(i) then S_g(i + 1), in the first turn S_g(0) alone; the ring's loads
@@ -209,15 +213,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               vplace = (uint32_t)ring.slot * 2u + ring.phase;
               if (ok) ok = warp_wait_small(&ct.empty[ring.slot], ring.phase ^ 1u, abort);
               if (ok) {
-                const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 32 * pw * 128);
+                const uint32_t dst = ring_u + (uint32_t)(ring.slot * C::kSlot + 4 * pw * C::kGroup);
                 uint64_t* full = &ct.full[ring.slot];
                 if (boxed) {
                   if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(32 * D * 2));
                   else mbar_arrive(full);
-                  const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row, (box * c.seg) & 31);
-                  if (box * c.seg < 32 && (lane & 3) < C::kCh)
-                    tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlk + box * c.seg * 128), &segmap, x0 + val * D + 64 * (lane & 3),
-                                row, full);
+                  if (SHARED) {
+                    __syncwarp();
+                    if (lane % c.seg == 0)
+                      tma_load_4d(dst + (uint32_t)((lane >> 3) * C::kGroup), &segmap, 0, 0, (x0 + val * D) >> 6, now_row >> 3, full);
+                    __syncwarp();
+                  } else {
+                    const int box = lane >> 2, row = __shfl_sync(0xffffffffu, now_row, (box * c.seg) & 31);
+                    if (box * c.seg < 32 && (lane & 3) < C::kCh)
+                      tma_load_2d(dst + (uint32_t)((lane & 3) * C::kBlock + box * c.seg * 128), &segmap, x0 + val * D + 64 * (lane & 3),
+                                  row, full);
+                  }
                 } else {
                   // 16 bytes a lane: rows 4 i .. 4 i + 3, swizzled as the boxes are
                   const int off = 2 * (x0 + val * D) + 16 * cch;
@@ -225,10 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int i = 0; i < 8; ++i) {
                     const int row = 4 * i + crow;
                     const uint64_t src = __shfl_sync(0xffffffffu, now, row);
-                    const uint32_t to = dst + (uint32_t)(row * 128 + ((cch ^ (row & 7)) << 4)), n = src != 0ull ? 16u : 0u;
+                    const uint32_t to = dst + (uint32_t)((row >> 3) * C::kGroup + (row & 7) * 128 + ((cch ^ (row & 7)) << 4)), n = src != 0ull ? 16u : 0u;
                     const uint8_t* from = src != 0ull ? (const uint8_t*)(uintptr_t)src + off : (const uint8_t*)a.q;
 #pragma unroll
-                    for (int b = 0; b < C::kCh; ++b) cp_async16_zfill(to + b * C::kBlk, src != 0ull ? from + 128 * b : from, n);
+                    for (int b = 0; b < C::kCh; ++b) cp_async16_zfill(to + b * C::kBlock, src != 0ull ? from + 128 * b : from, n);
                   }
                   cp_async_arrive_noinc(full);
                 }
@@ -257,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tu = (uint32_t)uniform((int)tb);
       const uint32_t id_s = umma_idesc_bf16(128, 128, 0, 0) | (c.negate ? kNegateA : 0u), id_o = umma_idesc_bf16(128, D, 0, 1);
       const uint32_t dq0 = (uint32_t)uniform((int)umma_sdesc_lo(q_u, 16)), dk0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, 16));
-      // V as it lies: 64-value blocks kBlk apart, 8 entries every 1 KB, the value dims contiguous
-      const uint32_t dv0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, C::kBlk));
+      // V as it lies: blocks of 64 values, 8 entries a group, the value dims contiguous
+      const uint32_t dv0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, C::kBlock));
       constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
       int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
       Ring<C::kRing> v0, v1;     // where the values of the tile in hand are: of the group at hand, of the other
@@ -274,11 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int done = g == 0 ? tiles0 : tiles1;  // tiles of this group finished
         if (due0 > 0) {
           idle = 0;
-          const bool here = g == 0 || p0.pairs, last_user = !c.shared || g == 1 || !p0.pairs;
-          if (!c.shared || g == 0) vslot = v0.slot;
+          const bool here = g == 0 || p0.pairs, last_user = !SHARED || g == 1 || !p0.pairs;
+          if (!SHARED || g == 0) vslot = v0.slot;
           if (here) {
             // the weights, and the values (shared: the first group's wait for these serves both)
-            if (!c.shared || g == 0) {
+            if (!SHARED || g == 0) {
               if (ok) ok = uniform_wait2(&ct.p[g], (uint32_t)(done & 1), &ct.full[v0.slot], v0.phase, abort);
               // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && elect_one()) {
               const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks) umma_bf16_ta(to, ts + 8u * ks, dv + 128 * ks, id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
+              for (int ks = 0; ks < 8; ++ks) umma_bf16_ta<C::kGroup>(to, ts + 8u * ks, dv + ks * (2 * C::kGroup >> 4), id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
               umma_commit(&ct.pv[g]);
               if (last_user) umma_commit(&ct.empty[vslot]);
             }
@@ -301,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (k0.left()) {
           idle = 0;
-          const bool here = g == 0 || k0.pairs, last_user = !c.shared || g == 1 || !k0.pairs;
+          const bool here = g == 0 || k0.pairs, last_user = !SHARED || g == 1 || !k0.pairs;
           const Ring<C::kRing> k_at = ring;
-          if (!c.shared || g == 0) {
+          if (!SHARED || g == 0) {
             kslot = ring.slot;
             ring.next();
             v0 = ring;
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++q;
             }
             // the keys; and the weights of the tile before share these columns: their product has to be complete
-            if (!c.shared || g == 0) {
+            if (!SHARED || g == 0) {
               if (ok && done > 0)
                 ok = uniform_wait2(&ct.full[k_at.slot], k_at.phase, &ct.pv[g], (uint32_t)((done - 1) & 1), abort);
               else if (ok)
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int b = 0; b < C::kCh; ++b)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                  umma_bf16_lo(ts, dq + b * kBlkStep + 2 * ks, dk + b * kBlkStep + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
+                  umma_bf16_lo<C::kGroup>(ts, dq + b * kBlkStep + 2 * ks, dk + b * (C::kBlock >> 4) + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
               umma_commit(&ct.s[g]);
               if (last_user) umma_commit(&ct.empty[kslot]);
             }
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_q = [&](const Portion& P) {  // by the group's first thread
         ++sent;
         mbar_arrive_expect_tx(&ct.qfull[g], (uint32_t)(C::kCh * c.G * c.MT * 128));
-        const int h = P.head, mt = c.shared ? 2 * P.pair + g : 0;
+        const int h = P.head, mt = SHARED ? 2 * P.pair + g : 0;
         for (int b = 0; b < C::kCh; ++b)
           tma_load_4d(q_u + (uint32_t)(g * C::kSlot + b * C::kBlk), &qmap, 64 * b, h * c.G, mt * c.MT, P.r, &ct.qfull[g]);
       };
@@ -375,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           nm += P.t1 - P.t0;
           continue;
         }
-        const bool both = c.shared && present(1, P);
-        const int h = P.head, mt = c.shared ? 2 * P.pair + g : 0, t = mt * c.MT + lt;
+        const bool both = SHARED && present(1, P);
+        const int h = P.head, mt = SHARED ? 2 * P.pair + g : 0, t = mt * c.MT + lt;
         const int n4 = (int)(((unsigned)P.n + 3u) & ~3u);
         const bool row_ok = row < c.G * c.MT && t < P.nn;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -392,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row == 0 && tile == P.t1 - 1) {  // the last scores of the portion are done: the next one's queries
             if (ok) next_q(pi + 1);
           }
-          const int mg = c.shared ? 0 : g;
+          const int mg = SHARED ? 0 : g;
           if (ok) ok = mbar_wait_small(&ct.mask[mg][nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
           ok = __all_sync(0xffffffffu, ok);
           uint32_t w[4];
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t vp = ct.vplace[mg][nm % kMaskRing];
             if (ok) ok = mbar_wait_small(&ct.full[vp >> 1], vp & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            const bool d = ok && clean_rows(smem + (2 + (vp >> 1)) * C::kSlot, kTile * 128, 1024, C::kCh, max(0, -j0),
+            const bool d = ok && clean_rows(smem + (2 + (vp >> 1)) * C::kSlot, C::kBlock, C::kGroup, C::kCh, max(0, -j0),
                                             min(kTile, P.nn - j0), both ? tid : row, both ? 256 : 128);
             if (bar_or(both ? 3 : 1 + g, both ? 256 : 128, d)) dirty = true;
           }
@@ -479,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (ok && warp_ok) {
           const bool whole = P.t0 == 0 && P.t1 == (int)tiles_of<kTile>(P.n, P.nn);
-          const int wk = (c.shared ? 0 : g) * (int)gridDim.x + (int)blockIdx.x;
+          const int wk = (SHARED ? 0 : g) * (int)gridDim.x + (int)blockIdx.x;
           const long long slot = ((long long)wk * 2 + (P.t0 > 0 ? 0 : 1)) * c.ws.rows;
-          const int srow = (c.shared ? 128 * g : 0) + row;
+          const int srow = (SHARED ? 128 * g : 0) + row;
           const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
@@ -578,14 +589,14 @@ bool plan_of(const hs_config* c, int T, int sms, Plan* p) {
   return true;
 }
 
-template <int D>
+template <int D, bool SHARED>
 cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q, const CUtensorMap& seg, const CombineArgs& cb,
                    cudaStream_t st) {
-  static_assert(Shape<D>::kDyn + sizeof(Control) <= kSmemCap, "shared memory of a CTA");
+  static_assert(Shape<D, SHARED>::kDyn + sizeof(Control) <= kSmemCap, "shared memory of a CTA");
   static bool done[64];
-  cudaError_t e = allow_smem(k_tree_gqa<D>, Shape<D>::kDyn, done);
+  cudaError_t e = allow_smem(k_tree_gqa<D, SHARED>, Shape<D, SHARED>::kDyn, done);
   if (e != cudaSuccess) return e;
-  e = hs_launch_pdl(k_tree_gqa<D>, dim3(sms), dim3(kThreads), Shape<D>::kDyn, st, c, q, seg);
+  e = hs_launch_pdl(k_tree_gqa<D, SHARED>, dim3(sms), dim3(kThreads), Shape<D, SHARED>::kDyn, st, c, q, seg);
   if (e != cudaSuccess) return e;
   return hs_launch_pdl(k_tree_combine<D>, combine_grid(p.items, c.a.R, p.rows, D), dim3(256), 0, st, cb);
 }
@@ -628,9 +639,12 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
     const int pt = c.a.kv.page_tokens;
     c.seg = pt % 32 == 0 ? 32 : pt % 16 == 0 ? 16 : 0;
     c.ctx_rows = (int)(c.a.kv.num_pages * pt);
+    // unshared: value, record; shared: value, record of a group, block, group
     const cuuint64_t rec = (cuuint64_t)c.a.kv.rec, size[2] = {rec / 2, (cuuint64_t)c.ctx_rows}, stride[1] = {rec};
-    const cuuint32_t box[2] = {64, (cuuint32_t)c.seg};
-    if (c.seg != 0 && !encode(&seg, c.a.kv.base, 2, size, stride, box)) c.seg = 0;
+    const cuuint64_t size4[4] = {64, 8, rec / 128, (cuuint64_t)c.ctx_rows / 8}, stride4[3] = {rec, 128, 8 * rec};
+    const cuuint32_t box[2] = {64, (cuuint32_t)c.seg}, box4[4] = {64, 8, (cuuint32_t)p.D / 64, (cuuint32_t)c.seg / 8};
+    if (c.seg != 0 && !(p.shared ? encode(&seg, c.a.kv.base, 4, size4, stride4, box4) : encode(&seg, c.a.kv.base, 2, size, stride, box)))
+      c.seg = 0;
   }
   const cuuint64_t row = (cuuint64_t)p.D * 2;
   const cuuint64_t qsize[4] = {(cuuint64_t)p.D, (cuuint64_t)cfg->num_q_heads, (cuuint64_t)g->nodes, (cuuint64_t)cfg->num_requests};
@@ -649,6 +663,7 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   cb.MT = p.MT;
   cb.per = p.shared ? 2 : 1;
   cb.np = p.np;
-  const cudaError_t e = p.D == 128 ? launch<128>(c, p, num_sms, qm, seg, cb, st) : launch<64>(c, p, num_sms, qm, seg, cb, st);
+  const auto run = p.D == 128 ? (p.shared ? launch<128, true> : launch<128, false>) : (p.shared ? launch<64, true> : launch<64, false>);
+  const cudaError_t e = run(c, p, num_sms, qm, seg, cb, st);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
