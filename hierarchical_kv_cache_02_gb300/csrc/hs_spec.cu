@@ -21,7 +21,7 @@ namespace {
 // A CTA takes a few tokens: their records' places and the sines and cosines, shared by all heads, first; then
 // units of two 16-byte vectors, two of them in flight per thread at 40 registers (six CTAs an SM).  Few tokens
 // spread over many CTAs, each with a share of every token's units.  16384 tokens of 32 + 8 + 8 heads of 128:
-// 67.5 us, 5.97 TB/s (four units in flight at 64 registers 73.6 us, one 68.1; 8 or 16 tokens a CTA 72 and 83 us, one 74).
+// 65.7 us, 6.1 TB/s (four units in flight at 64 registers 73.6 us, one 68.1; 8 or 16 tokens a CTA 72 and 83 us, one 74).
 
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 4;   // tokens of a CTA at most
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kAppThreads, 6) k_append_rotated(AppendArgs a)
       int64_t row = -1, pos = 0;
       if (live) {
         uint32_t bad = 0u;
-        pos = st + (t - c0);
+        pos = st + ((int64_t)t - c0);
         row = paged_row(a.kv, x, pos, (uint32_t)HS_DEVERR_APPEND, &bad);
         if (blockIdx.y == 0) report(a.kv.err, bad);
         if (a.rope_pos != nullptr) pos = given;
@@ -383,7 +383,7 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
   // 6.2 us).  A CTA's units stay below 2^16 (see Div).
   a.tokens = kAppTokens;
   while (a.tokens > 1 && (a.N < kMinCtas * a.tokens || units * a.tokens >= 65536)) a.tokens >>= 1;
-  const int ctas = (a.N + a.tokens - 1) / a.tokens;
+  const int ctas = (int)(((int64_t)a.N + a.tokens - 1) / a.tokens);
   int shares = 1;
   while (shares < 64 && (int64_t)ctas * shares < 2 * kSmsHint && units * a.tokens / shares > kAppFlight * kAppThreads / 4)
     shares *= 2;

@@ -11,7 +11,10 @@
 // by TMA where its pages allow, everything else row by row in 16-byte copies (TMA's gather of four rows measured
 // slower: its instructions leave a warp one lane at a time, 75 ns each).
 // Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
-// of one tile of rows 0.54 us at the tensor cores' rate.
+// of one tile of rows 0.54 us at the tensor cores' rate.  Measured: 4 requests x 131072 positions x 16 nodes x 32
+// heads 357 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.6 us (136 MB read, 3.4 TB/s: half of it the
+// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 94 us (812 TFLOP/s,
+// tensor cores active 41%: a turn of products, softmax and the hand-overs between them bounds it).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -40,7 +43,8 @@ struct Shape {
   static constexpr int kSlot = kCh * kBlk;           // a K or V tile; also a Q tile
   // How K and V lie: bytes from 8 records to the next 8, and from a 64-value block to the next.  Shared, a group's
   // blocks one after the other, so that one copy brings all blocks of 16 or 32 records: their number is what copies
-  // cost there.  Unshared, block by block: memory bounds these, and copies of 128-byte rows use it better.
+  // cost there (94 us instead of 100 on 8 ragged requests x 64 nodes in pages of 16).  Unshared, block by block: memory
+  // bounds these, and copies of 128-byte rows use it better (357 us instead of 397 on 4 x 131072 positions).
   static constexpr int kGroup = SHARED ? kCh * 1024 : 1024, kBlock = SHARED ? 1024 : kTile * 128;
   static constexpr int kRing = D == 128 ? 5 : 11;
   static constexpr size_t kDyn = (size_t)(2 + kRing) * kSlot + 1024;
@@ -623,8 +627,8 @@ int hs_tree_gqa_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.ws.items = p.items;
   c.ws.np = p.np;
   c.ws.groups = p.shared ? 1 : 2;
-  // unshared, the other group works while one changes its portion: 44.3 us with 0 and 45.2 with 1 on 16 requests x 8
-  // nodes over 2048 listed rows; shared, 105.9, 103.7, 102.0 and 104.9 us with 0 to 3 on 8 ragged requests x 64 nodes
+  // unshared, the other group works while one changes its portion: 40.2, 41.7 and 43.3 us with 0 to 2 on 16 requests
+  // x 8 nodes over 2048 listed rows; shared, 98.6, 96.3, 94.3 and 95.8 us with 0 to 3 on 8 ragged requests x 64 nodes
   c.ws.begin = p.shared ? 2 : 0;
   c.ws.rows = p.rows;
   hs_tree_workspace(g->d_workspace, cfg, p.workers, p.rows, p.D, &c.ws.prefix, &c.ws.part, &c.ws.ml);

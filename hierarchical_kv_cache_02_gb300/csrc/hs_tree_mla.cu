@@ -1,16 +1,22 @@
 // Tree attention over shared-latent records (576 values, the first 512 of them V) on the 5th-generation tensor
 // cores.
 //
-// The rows of a request are its (node, query head) pairs one after the other; an item is 64 of them, whatever the
-// head count.  A CTA holds their queries in shared memory (72 KB) and two tiles of 64 records (72 KB each): a
-// latent is key and value at once, so a tile is loaded once and stays from the scores to the value product.
-// Per tile S = Q K^T (64 x 64 x 576) and O += P V (64 x 512 x 64).  An accumulator of 64 rows takes 16 of every 32
-// lanes of tensor memory, so O's two halves of 256 dims share columns (lanes 0-15 and 16-31 of each
-// quarter), and so do the scores of even and odd tiles.  The scores of the next tile are issued before the
-// value product of the one at hand, so the softmax (one warpgroup, a thread per row) runs beside them.
-// 128 rows with half of the dims in an accumulator would use the tensor cores better, but their queries leave
-// 80 KB for records: not enough to load one tile while the values of another wait for its weights.
-// What bounds it: at full rate the products of a tile take 2176 cycles of a 64-row accumulator.
+// The rows of a request are its (node, query head) pairs one after the other; an item is 128 of them, whatever the
+// head count, and the work of two CTAs, a cluster on neighbouring SMs: each holds 64 rows' queries (72 KB), and the
+// products are the pair's (cta_group::2).  Per tile of 64 records
+//   S = Q K^T (128 x 64 x 576): a CTA holds the keys of 32 records, whole;
+//   O += P V (128 x 512 x 64): a CTA holds 256 of the values of all 64 records.
+// So a CTA loads 68 KB a tile, the keys free their memory as soon as the scores are done, and two tiles of each fit
+// beside the queries.  (One CTA for itself, 64 rows: a tile is key and value at once, 72 KB that stay from the
+// scores to the value product, and an accumulator of 64 rows runs the tensor cores at half their rate; two such tiles
+// fit: 97 us instead of 73 below.  128 rows of a CTA: their queries leave room for one tile.)
+// Rows 0-63 of an accumulator are the even CTA's, in both: its first half of columns in lanes 0-63 of tensor memory,
+// the second in 64-127.  So two threads share a row, half of a tile's entries and half of the dims each.
+// The even CTA's warp issues for both; what has landed in the odd one is passed on by an arrival on its barriers.
+// What bounds it: the products of a tile take about 1800 of its 2300 cycles; the rest is what the keys' two buffers
+// leave of the load's latency (1900 cycles under load).  Measured: 4 ragged requests of up to 32768 x 5 nodes x
+// 64 heads 73 us (705 TFLOP/s, tensor cores active 40%), 8 x 8 nodes over 2048 listed positions 45 us.  Keys that
+// come and go in two parts took 87 us (records fetched in two visits).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -527,7 +533,7 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.ws.np = 1;
   c.ws.groups = 1;
   c.ws.pairs = 1;
-  c.ws.begin = 2;
+  c.ws.begin = 2;  // 76.0, 74.2, 72.9 and 73.0 us with 0 to 3 on 4 ragged requests of up to 32768
   c.ws.rows = kRows;
   hs_tree_workspace(g->d_workspace, cfg, pairs, kRows, kValue, &c.ws.prefix, &c.ws.part, &c.ws.ml);
   if (c.a.qscale < 0.f) {

@@ -488,8 +488,9 @@ int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const 
  * one that was at position len[r] + path[r][i] before the call.  d_path int32 [num_requests][path_len],
  * node numbers with path[r][i] >= i (the nodes of a path ascend, so this holds for every tree whose
  * parents come first); another entry sets HS_DEVERR_LOC and is skipped, as is one whose position is
- * outside the cache; a count outside [0, path_len] sets HS_DEVERR_LOC and is clamped.  d_len int64, d_count
- * int32 [num_requests].  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_CUDA.
+ * outside the cache; a count outside [0, path_len] sets HS_DEVERR_LOC and is clamped.  Pages that two requests
+ * share must not hold records that this call moves or overwrites.  d_len int64, d_count int32
+ * [num_requests].  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_CUDA.
  */
 int hs_keep_path(const hs_config* cfg, const hs_paged_kv* kv, const int64_t* d_len, const int32_t* d_path, int path_len,
                  const int32_t* d_count, void* stream);
