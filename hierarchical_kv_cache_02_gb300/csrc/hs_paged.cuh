@@ -8,6 +8,8 @@
 // whole tiles, in 32 bits
 constexpr int32_t kMaxPositions = INT32_MAX - 65535;
 
+constexpr int kSmsHint = 152;  // to size grids by
+
 struct PagedRows {
   uint8_t* base;         // [num_pages][page_tokens][rec]
   const int32_t* table;  // [R][max_pages] or null: the identity

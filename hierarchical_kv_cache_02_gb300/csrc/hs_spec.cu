@@ -273,7 +273,6 @@ __global__ void __launch_bounds__(kKeepThreads) k_keep_path(PagedRows kv, const 
 // 2^256 / (2 pi), lowest word first
 constexpr uint64_t kOverTwoPi[4] = {0x7f9458eaf7aef158ull, 0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
 
-constexpr int kSmsHint = 152;  // to size grids by
 constexpr int kMinCtas = 456;
 
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }

@@ -493,18 +493,19 @@ struct CombineArgs {
   int flat;        // a shared latent: item i holds the rows [flat i, flat (i + 1)) of all node x head rows
 };
 
-// A thread holds 8 dims of a row, neighbouring threads neighbouring rows; items that one worker held whole are
-// written by it.
-template <int DV>
+// A thread holds W dims of a row, neighbouring threads neighbouring rows, with F partials on their way to it; items
+// that one worker held whole are written by it.  What it costs is round trips to what other SMs have just written,
+// about 1 us each, where there is little to join, and else the SMs' room for threads and loads: see launch_combine.
+template <int DV, int W, int F>
 __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kFlight = 4;  // partials in flight
   const int item = blockIdx.x, r = blockIdx.y, idx = blockIdx.z * 256 + threadIdx.x;
   const long long p0 = c.ws.prefix[r], U = c.ws.prefix[r + 1] - p0, total = c.ws.prefix[c.R];
   int nn = c.T;
   if (c.nodes != nullptr) nn = min(max(c.nodes[r], 0), c.T);
   if (U == 0) return;
-  const int rows = c.ws.rows, blk = idx / rows, row = idx - blk * rows, x = row & 127;
+  // the 8 / W threads of 8 dims of a row are neighbours
+  const int rows = c.ws.rows, part = idx % (8 / W), at = idx / (8 / W), blk = at / rows, row = at - blk * rows, x = row & 127;
   const int mt = c.flat ? 0 : (item % c.np) * c.per + (row >> 7);
   const int t = c.flat ? (item * c.flat + row) / c.Hq : mt * c.MT + x / c.G;
   const int h = c.flat ? (item * c.flat + row) % c.Hq : item / c.np * c.G + x % c.G;
@@ -513,53 +514,65 @@ __global__ void __launch_bounds__(256) k_tree_combine(CombineArgs c) {
   const long long a = p0 * c.ws.items + item * U;
   const int wf = sh.worker(a + c.ws.begin), wl = sh.worker(a + U - 1);
   if (wf == wl) return;
-  float M = -INFINITY, L = 0.f, acc[8];
+  float M = -INFINITY, L = 0.f, acc[W];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int i = 0; i < W; ++i) acc[i] = 0.f;
 #pragma unroll 1
-  for (int w0 = wf; w0 <= wl; w0 += kFlight) {
-    float2 ml[kFlight];
-    float4 lo4[kFlight], hi4[kFlight];
+  for (int w0 = wf; w0 <= wl; w0 += F) {
+    float2 ml[F];
+    float4 v[F][W / 4];
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) {  // the last one again where there are no more
-      const int w = min(w0 + j, wl);
+    for (int j = 0; j < F; ++j) {
+      const int w = w0 + j;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (w > wl) continue;
       const long long slot = ((long long)w * 2 + (w == wf ? 1 : 0)) * rows;
-      const float4* p = (const float4*)(c.ws.part + slot * DV + ((long long)blk * rows + row) * 8);
+      const float4* p = (const float4*)(c.ws.part + slot * DV + ((long long)blk * rows + row) * 8 + W * part);
       ml[j] = *(const float2*)(c.ws.ml + (slot + row) * 2);
-      lo4[j] = p[0];
-      hi4[j] = p[1];
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) v[j][i] = p[i];
     }
     float mn = M;
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) mn = fmaxf(mn, ml[j].x);
+    for (int j = 0; j < F; ++j) mn = fmaxf(mn, ml[j].x);
     const float al = M == mn ? 1.f : exp2f(M - mn);
     M = mn;
     L *= al;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= al;
+    for (int i = 0; i < W; ++i) acc[i] *= al;
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j) {
+    for (int j = 0; j < F; ++j) {
       // nothing seen: no part in the result; NaN scores alone: NaN
       const float wt = ml[j].x == -INFINITY ? (ml[j].y == 0.f ? 0.f : ml[j].y) : exp2f(ml[j].x - M);
-      if (w0 + j > wl || wt == 0.f) continue;
+      if (wt == 0.f) continue;
       L = fmaf(wt, ml[j].y, L);
-      acc[0] = fmaf(wt, lo4[j].x, acc[0]);
-      acc[1] = fmaf(wt, lo4[j].y, acc[1]);
-      acc[2] = fmaf(wt, lo4[j].z, acc[2]);
-      acc[3] = fmaf(wt, lo4[j].w, acc[3]);
-      acc[4] = fmaf(wt, hi4[j].x, acc[4]);
-      acc[5] = fmaf(wt, hi4[j].y, acc[5]);
-      acc[6] = fmaf(wt, hi4[j].z, acc[6]);
-      acc[7] = fmaf(wt, hi4[j].w, acc[7]);
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        acc[4 * i] = fmaf(wt, v[j][i].x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(wt, v[j][i].y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(wt, v[j][i].z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(wt, v[j][i].w, acc[4 * i + 3]);
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  *(uint4*)(c.out + (((int64_t)r * c.T + t) * c.Hq + h) * DV + 8 * blk) =
-      make_uint4(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv), pack(acc[4] * inv, acc[5] * inv),
-                 pack(acc[6] * inv, acc[7] * inv));
+  uint2* dst = (uint2*)(c.out + (((int64_t)r * c.T + t) * c.Hq + h) * DV + 8 * blk + W * part);
+  if (W == 8) {
+    *(uint4*)dst = make_uint4(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv), pack(acc[W - 4] * inv, acc[W - 3] * inv),
+                              pack(acc[W - 2] * inv, acc[W - 1] * inv));
+  } else {
+    *dst = make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
+  }
 }
-// its grid
-inline dim3 combine_grid(int items, int R, int rows, int dims) { return dim3(items, R, (rows * (dims / 8) + 255) / 256); }
+template <int DV>
+cudaError_t launch_combine(const CombineArgs& c, cudaStream_t st) {
+  auto ctas = [&](int w) { return (c.ws.rows * (DV / w) + 255) / 256; };
+  // Up to a CTA an SM it is latency: 12.6 us (the call) instead of 13.7 on 1 request x 4 nodes x 1000 positions.  More
+  // threads with fewer loads each else: 72.5 us instead of 74.3 on 4 requests x 5 nodes over shared latents.
+  if ((int64_t)c.ws.items * c.R * ctas(8) <= kSmsHint)
+    return hs_launch_pdl(k_tree_combine<DV, 4, 8>, dim3(c.ws.items, c.R, ctas(4)), dim3(256), 0, st, c);
+  return hs_launch_pdl(k_tree_combine<DV, 8, 4>, dim3(c.ws.items, c.R, ctas(8)), dim3(256), 0, st, c);
+}
 
 bool encode(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* stride,
             const cuuint32_t* box) {

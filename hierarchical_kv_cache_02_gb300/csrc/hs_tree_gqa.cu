@@ -602,7 +602,7 @@ cudaError_t launch(const TcArgs& c, const Plan& p, int sms, const CUtensorMap& q
   if (e != cudaSuccess) return e;
   e = hs_launch_pdl(k_tree_gqa<D, SHARED>, dim3(sms), dim3(kThreads), Shape<D, SHARED>::kDyn, st, c, q, seg);
   if (e != cudaSuccess) return e;
-  return hs_launch_pdl(k_tree_combine<D>, combine_grid(p.items, c.a.R, p.rows, D), dim3(256), 0, st, cb);
+  return launch_combine<D>(cb, st);
 }
 
 }  // namespace

@@ -567,7 +567,6 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   static bool done[64];
   cudaError_t e = allow_smem(k_tree_mla, kDyn, done);
   if (e == cudaSuccess) e = hs_launch_pdl(k_tree_mla, dim3(2 * pairs), dim3(kThreads), kDyn, st, c, qm, km, vm);
-  if (e == cudaSuccess)
-    e = hs_launch_pdl(k_tree_combine<kValue>, combine_grid(c.ws.items, cfg->num_requests, kRows, kValue), dim3(256), 0, st, cb);
+  if (e == cudaSuccess) e = launch_combine<kValue>(cb, st);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
