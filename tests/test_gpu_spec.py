@@ -192,6 +192,67 @@ def test_what_a_node_does_not_see_has_no_influence(cfg, bad):
     assert not bool(torch.isfinite(out[:, 1::2]).any())
 
 
+@pytest.mark.parametrize("cfg,dim", [(gqa(1), 3), (gqa(1), 127), (gqa(1, 8, 2, 64), 40), (gqa(1, 4, 2, 80), 79), (mla(1), 5),
+                                     (mla(1), 300), (mla(1), 511), (mla(1), 570)])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+def test_one_bad_value_of_a_node_stays_where_it_is(cfg, dim, bad):
+    """One infinite or NaN number in a node's value (shared latents: key and value at once), wherever it lies: rows that do
+    not see the node keep their bits; of the others a GQA row loses this dim alone."""
+    T, n = 11, 150
+    lat = cfg.layout == LAYOUT_MLA
+    kv = make_cache(cfg, n + T, 16, seed=dim)
+    parents = torch.tensor([[-1] + [max(-1, j - 2) for j in range(1, T)]])  # even nodes and odd nodes
+    mask = tree_mask(parents)
+    q, clean = check_tree(cfg, kv, [n], T, mask, seed=dim)
+    flat = kv.pages.view(-1, cfg.record_elems)
+    sick = 4
+    at = dim if lat else cfg.head_dim_qk + dim  # GQA: of the first KV head
+    flat[ref.row_of(kv.table.cpu(), 0, n + sick, kv.pages.shape[1], 0), at] = bad
+    out = kv.tree_attn(q, torch.tensor([n], dtype=torch.int64, device=DEV), mask.to(DEV))
+    sees = torch.tensor([(mask[0, i, 0].item() >> sick) & 1 for i in range(T)], dtype=torch.bool)
+    assert torch.equal(out[0, ~sees], clean[0, ~sees])
+    if lat:
+        assert not bool(torch.isfinite(out[0, sees]).any(dim=-1).all())
+    else:
+        G = cfg.num_q_heads // cfg.num_kv_heads
+        hit = out[0, sees][:, :G]
+        assert not bool(torch.isfinite(hit[..., dim]).any())
+        same = clean[0, sees].clone()
+        same[:, :G, dim] = hit[..., dim]
+        assert torch.equal(out[0, sees].nan_to_num(nan=7.0), same.nan_to_num(nan=7.0))
+
+
+def test_different_trees_at_once():
+    """Trees of every kernel on three streams at once, again and again over long contexts: always the bits of the first
+    call."""
+    forms = [(gqa(3), 8, 9000, 64, False), (gqa(3), 70, 4000, 16, False), (mla(3), 5, 6000, 64, False), (mla(3), 2, 6000, 16, True),
+             (gqa(3, 8, 2, 64), 5, 6000, 24, False), (gqa(3), 4, 6000, 64, True), (gqa(3, 4, 2, 80), 2, 300, 16, False)]
+    calls, first = [], []
+    for i, (cfg, T, n, page, listed) in enumerate(forms):
+        R = cfg.num_requests
+        kv = make_cache(cfg, n + T, page, seed=i)
+        q = randn((R, T, cfg.num_q_heads, cfg.head_dim_qk), i)
+        lens = torch.tensor([n, n // 3, n - 5], dtype=torch.int64, device=DEV)
+        mask = tree_mask(random_tree(R, T, seed=i)).to(DEV)
+        locs = None
+        if listed:
+            g = torch.Generator().manual_seed(i)
+            locs = torch.stack([torch.randperm(n // 3, generator=g)[:1500] for _ in range(R)]).to(torch.int32).to(DEV)
+        calls.append((kv, q, lens, mask, locs))
+        first.append(kv.tree_attn(q, lens, mask, locs=locs))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for turn in range(8):
+        outs = []
+        for i in range(3 * len(calls)):
+            kv, q, lens, mask, locs = calls[(i * 5 + turn) % len(calls)]
+            outs.append(((i * 5 + turn) % len(calls), kv.tree_attn(q, lens, mask, locs=locs, stream=streams[i % 3])))
+        torch.cuda.synchronize()
+        for which, out in outs:
+            assert torch.equal(out, first[which]), (turn, which)
+    assert all(c[0].errors() == 0 for c in calls)
+
+
 @pytest.mark.parametrize("cfg", [gqa(1), mla(1), gqa(1, 2, 1, 80)], ids=["gqa", "mla", "any"])
 def test_scores_that_grow_and_fall_by_a_lot(cfg):
     """Sharp softmaxes whose maximum moves through the context, and all scores equal."""
