@@ -12,9 +12,11 @@
 // slower: its instructions leave a warp one lane at a time, 75 ns each).
 // Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
 // of one tile of rows 0.54 us at the tensor cores' rate.  Measured: 4 requests x 131072 positions x 16 nodes x 32
-// heads 357 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.6 us (136 MB read, 3.4 TB/s: half of it the
-// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 94 us (812 TFLOP/s,
-// tensor cores active 41%: a turn of products, softmax and the hand-overs between them bounds it).
+// heads 358 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.5 us (136 MB read, 3.4 TB/s: half of it the
+// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 92 us (840 TFLOP/s,
+// tensor cores active 42%).  There a turn of a group is its products (two times 520 cycles) and what their hand-overs
+// take (500 from the value product's end to the scores, 450 from the scores to the other group's turn), 2050 of the 4100
+// cycles of a tile, in which its softmax takes 1870.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -68,6 +70,12 @@ struct Control {
   uint32_t valid[2][kMaskRing][4];
   uint32_t vplace[2][kMaskRing];  // where a tile's values are: ring slot * 2 + phase
   uint32_t tmem, abort;
+};
+
+// A number known when compiled, where another call passes an int.
+template <int N>
+struct Const {
+  __device__ __forceinline__ operator int() const { return N; }
 };
 
 template <int N>
@@ -275,94 +283,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V as it lies: blocks of 64 values, 8 entries a group, the value dims contiguous
       const uint32_t dv0 = (uint32_t)uniform((int)umma_sdesc_lo(ring_u, C::kBlock));
       constexpr uint32_t kSlotStep = C::kSlot >> 4, kBlkStep = C::kBlk >> 4;
-      int kslot = 0, vslot = 0;  // shared: the slots that both groups' products use, one after the other
-      Ring<C::kRing> v0, v1;     // where the values of the tile in hand are: of the group at hand, of the other
-      Cursor k0, k1, p0, p1;     // next scores and next values of the group at hand, of the other
-      k0.open(list_of(0), count_of(0), c);
-      k1.open(list_of(1), count_of(1), c);
-      p0 = k0;
-      p1 = k1;
-      int due0 = 0, due1 = 0, g = 0;  // scores done whose values are not
-      for (int idle = 0; idle < 2;) {
-        ++idle;
-        const uint32_t ts = tu + 128u * g, to = tu + 256u + (uint32_t)(D * g);
-        int done = g == 0 ? tiles0 : tiles1;  // tiles of this group finished
-        if (due0 > 0) {
-          idle = 0;
-          const bool here = g == 0 || p0.pairs, last_user = !SHARED || g == 1 || !p0.pairs;
-          if (!SHARED || g == 0) vslot = v0.slot;
-          if (here) {
-            // the weights, and the values (shared: the first group's wait for these serves both)
-            if (!SHARED || g == 0) {
-              if (ok) ok = uniform_wait2(&ct.p[g], (uint32_t)(done & 1), &ct.full[v0.slot], v0.phase, abort);
-              // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            } else if (ok) {
-              ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
-            }
-            tc_fence_after();
-            if (ok && elect_one()) {
-              const uint32_t dv = dv0 + (uint32_t)vslot * kSlotStep;
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks) umma_bf16_ta<C::kGroup>(to, ts + 8u * ks, dv + ks * (2 * C::kGroup >> 4), id_o, (p0.t != p0.t0 || ks != 0) ? 1u : 0u);
-              umma_commit(&ct.pv[g]);
-              if (last_user) umma_commit(&ct.empty[vslot]);
-            }
-            __syncwarp();
-            ++done;
-          }
-          --due0;
-          p0.next(c);
+      // O_g(i): the weights, and the values (shared: the first group's wait for these serves both)
+      auto values = [&](auto gc, const Cursor& p, const Ring<C::kRing>& v, int done) {
+        const int g = gc;  // a constant or not
+        const bool last_user = !SHARED || g == 1 || !p.pairs;
+        if (!SHARED || g == 0) {
+          if (ok) ok = uniform_wait2(&ct.p[g], (uint32_t)(done & 1), &ct.full[v.slot], v.phase, abort);
+          // copies of 16 bytes are generic-proxy writes; the tensor cores read through the async proxy
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else if (ok) {
+          ok = uniform_wait(&ct.p[g], (uint32_t)(done & 1), abort);
         }
-        if (k0.left()) {
-          idle = 0;
-          const bool here = g == 0 || k0.pairs, last_user = !SHARED || g == 1 || !k0.pairs;
-          const Ring<C::kRing> k_at = ring;
-          if (!SHARED || g == 0) {
-            kslot = ring.slot;
+        tc_fence_after();
+        if (ok && elect_one()) {
+          const uint32_t ts = tu + 128u * g, to = tu + 256u + (uint32_t)(D * g), dv = dv0 + (uint32_t)v.slot * kSlotStep;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16_ta<C::kGroup>(to, ts + 8u * ks, dv + ks * (2 * C::kGroup >> 4), id_o, (p.t != p.t0 || ks != 0) ? 1u : 0u);
+          umma_commit(&ct.pv[g]);
+          if (last_user) umma_commit(&ct.empty[v.slot]);
+        }
+        __syncwarp();
+      };
+      // S_g(i): the keys; and the weights of the tile before share its columns: their product has to be complete
+      auto scores = [&](auto gc, const Cursor& k, const Ring<C::kRing>& at, int done, int portions) {
+        const int g = gc;  // a constant or not
+        const bool last_user = !SHARED || g == 1 || !k.pairs;
+        if (ok && k.t == k.t0) ok = uniform_wait(&ct.qfull[g], (uint32_t)(portions & 1), abort);  // this portion's queries
+        if (!SHARED || g == 0) {
+          if (ok && done > 0)
+            ok = uniform_wait2(&ct.full[at.slot], at.phase, &ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+          else if (ok)
+            ok = uniform_wait(&ct.full[at.slot], at.phase, abort);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as above
+        } else if (ok && done > 0) {
+          ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
+        }
+        tc_fence_after();
+        if (ok && elect_one()) {
+          const uint32_t ts = tu + 128u * g, dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)at.slot * kSlotStep;
+#pragma unroll
+          for (int b = 0; b < C::kCh; ++b)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16_lo<C::kGroup>(ts, dq + b * kBlkStep + 2 * ks, dk + b * (C::kBlock >> 4) + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
+          umma_commit(&ct.s[g]);
+          if (last_user) umma_commit(&ct.empty[at.slot]);
+        }
+        __syncwarp();
+      };
+      // Shared, each group's turn is code of its own (91 us instead of 94 on 8 ragged requests x 64 nodes: exchanging the
+      // groups' state took a tenth of a turn); unshared, where memory bounds it, the code is common, as the start counts
+      // (40.5 us instead of 41.3 on 16 requests x 8 nodes over 2048 listed rows).
+      const Const<0> g0;
+      const Const<1> g1;
+      Ring<C::kRing> v0, v1;  // where the values of the tile in hand are
+      Cursor k0, p0;              // next scores and next values
+      k0.open(list_of(0), count_of(0), c);
+      p0 = k0;
+      bool due0 = false, due1 = false;  // scores done whose values are not
+      if (SHARED) {
+        while (due0 || k0.left()) {
+          const bool more = k0.left();
+          const Ring<C::kRing> at = ring;  // where the keys are
+          if (more) {
+            ring.next();
+            v1 = ring;
+            ring.next();
+          }
+          due1 = due0 && p0.pairs;
+          if (due0) values(g0, p0, v0, tiles0++);
+          const bool first = more && k0.t == k0.t0;
+          if (more) scores(g0, k0, at, tiles0, portions0);
+          if (due1) values(g1, p0, v0, tiles1++);
+          if (more && k0.pairs) scores(g1, k0, at, tiles1, portions1);
+          portions0 += first;
+          portions1 += first && k0.pairs;
+          if (due0) p0.next(c);
+          if (more) k0.next(c);
+          due0 = more;
+          v0 = v1;
+        }
+      } else {
+        // k0, p0, due0 and v0 are those of the group at hand, exchanged with the other's after its turn
+        Cursor k1, p1;
+        k1.open(list_of(1), count_of(1), c);
+        p1 = k1;
+        int g = 0;
+        for (int idle = 0; idle < 2;) {
+          ++idle;
+          int done = g == 0 ? tiles0 : tiles1;
+          if (due0) {
+            idle = 0;
+            values(g, p0, v0, done++);
+            p0.next(c);
+          }
+          due0 = k0.left();
+          if (due0) {
+            idle = 0;
+            const Ring<C::kRing> at = ring;
             ring.next();
             v0 = ring;
             ring.next();
+            const bool first = k0.t == k0.t0;
+            scores(g, k0, at, done, g == 0 ? portions0 : portions1);
+            if (g == 0) portions0 += first;
+            else portions1 += first;
+            k0.next(c);
           }
-          if (here) {
-            if (k0.t == k0.t0) {  // this portion's queries
-              int& q = g == 0 ? portions0 : portions1;
-              if (ok) ok = uniform_wait(&ct.qfull[g], (uint32_t)(q & 1), abort);
-              ++q;
-            }
-            // the keys; and the weights of the tile before share these columns: their product has to be complete
-            if (!SHARED || g == 0) {
-              if (ok && done > 0)
-                ok = uniform_wait2(&ct.full[k_at.slot], k_at.phase, &ct.pv[g], (uint32_t)((done - 1) & 1), abort);
-              else if (ok)
-                ok = uniform_wait(&ct.full[k_at.slot], k_at.phase, abort);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // as above
-            } else if (ok && done > 0) {
-              ok = uniform_wait(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
-            }
-            tc_fence_after();
-            if (ok && elect_one()) {
-              const uint32_t dq = dq0 + (uint32_t)g * kSlotStep, dk = dk0 + (uint32_t)kslot * kSlotStep;
-#pragma unroll
-              for (int b = 0; b < C::kCh; ++b)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  umma_bf16_lo<C::kGroup>(ts, dq + b * kBlkStep + 2 * ks, dk + b * (C::kBlock >> 4) + 2 * ks, id_s, (b | ks) != 0 ? 1u : 0u);
-              umma_commit(&ct.s[g]);
-              if (last_user) umma_commit(&ct.empty[kslot]);
-            }
-            __syncwarp();
-          }
-          ++due0;
-          k0.next(c);
+          if (g == 0) tiles0 = done;
+          else tiles1 = done;
+          swap_both(k0, k1);
+          swap_both(p0, p1);
+          swap_both(due0, due1);
+          swap_both(v0, v1);
+          g ^= 1;
         }
-        if (g == 0) tiles0 = done;
-        else tiles1 = done;
-        swap_both(k0, k1);
-        swap_both(p0, p1);
-        swap_both(due0, due1);
-        swap_both(v0, v1);
-        g ^= 1;
       }
     } else if (warp < 8) {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
