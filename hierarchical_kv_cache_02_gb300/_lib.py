@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -117,6 +118,12 @@ class hs_tree_args(ctypes.Structure):
         ("d_workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_int64),
     ]
+
+
+# the same two as bytes, for the calls of every step: packing them takes a fraction of filling a ctypes structure
+pack_append = struct.Struct("iPPPPqqPqqPiiiPqqPqqi0P")
+pack_tree = struct.Struct("PPPiPPifPPq")
+assert pack_append.size == ctypes.sizeof(hs_append_args) and pack_tree.size == ctypes.sizeof(hs_tree_args)
 
 
 _lock = threading.Lock()

@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .pool import HsConfig, _check, _dev_tensor, _fast_ptr, _fast_stream, _tree_args, _tree_nodes
+from .pool import HsConfig, _check, _dev_tensor, _fast_ptr, _fast_stream, _tree_args
 
 
 class RopeTable:
@@ -126,8 +126,10 @@ class PagedKV:
             max_pages = pages.shape[0] // R
         self.pages, self.table = pages, table
         self._err = torch.zeros((1,), dtype=torch.int32, device=pages.device)
+        self._r, self._r1 = (R,), (R + 1,)
         self._kv = _lib.hs_paged_kv(p, t, int(pages.shape[0]), int(pages.shape[1]), max_pages, self._err.data_ptr(),
                                     self.device)
+        self._c_ref, self._kv_ref = ctypes.byref(self._c), ctypes.byref(self._kv)
 
     def append(self, k, v, cu, start, rope: RopeTable | None = None, rope_pos=None, q=None, q_out=None,
                rotary_offset: int | None = None, stream=None):
@@ -146,22 +148,22 @@ class PagedKV:
             raise ValueError("k must be a tensor [N][Hkv][Dqk]")
         N, mla = int(k.shape[0]), c.layout == _lib.LAYOUT_MLA
         kp, kt, kh = _strided(k, N, c.num_kv_heads, c.head_dim_qk, "k", self.device)
-        vp, vt, vh = None, 0, 0
+        vp, vt, vh = 0, 0, 0
         if mla != (v is None):
             raise ValueError("a shared latent has no v" if mla else "v is missing")
         if v is not None:
             vp, vt, vh = _strided(v, N, c.num_kv_heads, c.head_dim_v, "v", self.device)
-        cup = _fast_ptr(cu, torch.int32, (c.num_requests + 1,), "cu", self.device)
-        sp = _fast_ptr(start, torch.int64, (c.num_requests,), "start", self.device)
-        rp = None if rope_pos is None else _fast_ptr(rope_pos, torch.int64, (N,), "rope_pos", self.device)
-        turns, rd, il = None, 0, 0
+        cup = _fast_ptr(cu, torch.int32, self._r1, "cu", self.device)
+        sp = _fast_ptr(start, torch.int64, self._r, "start", self.device)
+        rp = 0 if rope_pos is None else _fast_ptr(rope_pos, torch.int64, (N,), "rope_pos", self.device)
+        turns, rd, il = 0, 0, 0
         if rope is not None:
             if rope.device != self.device:
                 raise ValueError(f"rope must live on cuda:{self.device}")
             turns, rd, il = rope.turns.data_ptr(), rope.rotary_dim, int(rope.interleaved)
         if rotary_offset is None:
             rotary_offset = max(0, c.head_dim_qk - rd) if mla and rd else 0
-        qp, qt, qh, op, ot, oh, qd = None, 0, 0, None, 0, 0, 0
+        qp, qt, qh, op, ot, oh, qd = 0, 0, 0, 0, 0, 0, 0
         if q is not None:
             if not isinstance(q, torch.Tensor) or q.dim() != 3:
                 raise ValueError("q must be a tensor [N][Hq][Dqk or rotary_dim]")
@@ -175,10 +177,9 @@ class PagedKV:
             op, ot, oh = _strided(q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        a = _lib.hs_append_args(N, cup, sp, rp, kp, kt, kh, vp, vt, vh, turns, rd, int(rotary_offset), il, qp, qt, qh, op,
-                                ot, oh, qd)
-        _check("hs_append_rotated", self.lib.hs_append_rotated(ctypes.byref(self._c), ctypes.byref(self._kv),
-                                                               ctypes.byref(a), _fast_stream(torch, stream, self.device)))
+        a = _lib.pack_append.pack(N, cup, sp, rp, kp, kt, kh, vp, vt, vh, turns, rd, int(rotary_offset), il, qp, qt, qh, op, ot, oh, qd)
+        _check("hs_append_rotated", self.lib.hs_append_rotated(self._c_ref, self._kv_ref, a,
+                                                               _fast_stream(torch, stream, self.device)))
         return q_out
 
     def tree_attn(self, q, lens, mask, locs=None, nodes=None, out=None, scale=None, stream=None):
@@ -190,18 +191,15 @@ class PagedKV:
         import torch
 
         c = self.cfg
-        T = _tree_nodes(q)
-        lp = _fast_ptr(lens, torch.int64, (c.num_requests,), "lens", self.device)
-        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, T, mask, nodes, out, scale,
-                                    stream)
-        args.d_len = lp
+        lp, kp, k = _fast_ptr(lens, torch.int64, self._r, "lens", self.device), 0, 0
         if locs is not None:
             if locs.dim() != 2 or locs.shape[1] < 1:
                 raise ValueError("locs must be [R][k] with k >= 1")
-            args.d_locs = _fast_ptr(locs, torch.int32, (c.num_requests, locs.shape[1]), "locs", self.device)
-            args.top_k = int(locs.shape[1])
-        _check("hs_tree_attn", self.lib.hs_tree_attn(ctypes.byref(self._c), ctypes.byref(self._kv), ctypes.byref(args),
-                                                     _fast_stream(torch, stream, self.device)))
+            k = locs.shape[1]
+            kp = _fast_ptr(locs, torch.int32, (c.num_requests, k), "locs", self.device)
+        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, lp, kp, k, mask, nodes, out, scale,
+                                    stream)
+        _check("hs_tree_attn", self.lib.hs_tree_attn(self._c_ref, self._kv_ref, args, _fast_stream(torch, stream, self.device)))
         return out
 
     def keep_path(self, lens, path, count, stream=None):
@@ -209,14 +207,14 @@ class PagedKV:
         path int32 [R][P], ascending nodes; count int32 [R]."""
         import torch
 
-        R = self.cfg.num_requests
         if not isinstance(path, torch.Tensor) or path.dim() != 2:
             raise ValueError("path must be a tensor [R][P]")
-        lp = _fast_ptr(lens, torch.int64, (R,), "lens", self.device)
-        pp = _fast_ptr(path, torch.int32, (R, path.shape[1]), "path", self.device)
-        cp = _fast_ptr(count, torch.int32, (R,), "count", self.device)
-        _check("hs_keep_path", self.lib.hs_keep_path(ctypes.byref(self._c), ctypes.byref(self._kv), lp, pp,
-                                                     int(path.shape[1]), cp, _fast_stream(torch, stream, self.device)))
+        P = path.shape[1]
+        lp = _fast_ptr(lens, torch.int64, self._r, "lens", self.device)
+        pp = _fast_ptr(path, torch.int32, (self._r[0], P), "path", self.device)
+        cp = _fast_ptr(count, torch.int32, self._r, "count", self.device)
+        _check("hs_keep_path", self.lib.hs_keep_path(self._c_ref, self._kv_ref, lp, pp, P, cp,
+                                                     _fast_stream(torch, stream, self.device)))
 
     def errors(self, reset: bool = False) -> int:
         """The DEVERR_* bits that the calls so far recorded (synchronises the device)."""

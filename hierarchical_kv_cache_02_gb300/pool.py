@@ -121,36 +121,45 @@ def _fast_stream(torch, stream, device):
     return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _tree_args(torch, lib, c_cfg, cfg, device, sizes, q, T, mask, nodes, out, scale, stream):
-    """Check and marshal what both forms of the tree attention take; returns the C arguments, the
+def _tree_args(torch, lib, c_cfg, cfg, device, known, q, lens, locs, top_k, mask, nodes, out, scale, stream):
+    """Check and marshal what both forms of the tree attention take; returns the C arguments (packed), the
     output and the workspace.  The workspace is this call's own, allocated on the stream that uses it;
-    `sizes` keeps its bytes by T."""
-    R, Hq = cfg.num_requests, cfg.num_q_heads
-    qp = _fast_ptr(q, torch.bfloat16, (R, T, Hq, cfg.head_dim_qk), "q", device)
-    mp = _fast_ptr(mask, torch.int64, (R, T, (T + 63) // 64), "mask", device)
-    np_ = None if nodes is None else _fast_ptr(nodes, torch.int32, (R,), "nodes", device)
-    need = sizes.get(T)
-    if need is None:
+    `known` keeps its bytes and the tensors' shapes by T; lens and locs are addresses or 0."""
+    try:
+        T = q.shape[1]
+    except (AttributeError, IndexError):
+        T = _tree_nodes(q)
+    plan = known.get(T)
+    if plan is None:
+        T, R, Hq = _tree_nodes(q), cfg.num_requests, cfg.num_q_heads
         need = lib.hs_tree_attn_workspace(ctypes.byref(c_cfg), T, device)
         if need < 0:
             raise HsError("hs_tree_attn_workspace", int(need))
-        sizes[T] = need
+        plan = known[T] = (need, (R, T, Hq, cfg.head_dim_qk), (R, T, (T + 63) // 64), (R,), (R, T, Hq, cfg.head_dim_v),
+                           cfg.default_scale)
+    need, q_shape, mask_shape, nodes_shape, out_shape, s = plan
+    bf16 = torch.bfloat16
+    qp = _fast_ptr(q, bf16, q_shape, "q", device)
+    mp = _fast_ptr(mask, torch.int64, mask_shape, "mask", device)
+    np_ = 0 if nodes is None else _fast_ptr(nodes, torch.int32, nodes_shape, "nodes", device)
     ws = None
     if stream is None:
         if out is None:
-            out = torch.empty((R, T, Hq, cfg.head_dim_v), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty(out_shape, dtype=bf16, device=q.device)
         if need > 0:
             ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         with torch.cuda.stream(stream):
             if out is None:
-                out = torch.empty((R, T, Hq, cfg.head_dim_v), dtype=torch.bfloat16, device=q.device)
+                out = torch.empty(out_shape, dtype=bf16, device=q.device)
             if need > 0:
                 ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    op = _fast_ptr(out, torch.bfloat16, (R, T, Hq, cfg.head_dim_v), "out", device)
-    s = cfg.default_scale if scale is None else float(scale)
-    args = _lib.hs_tree_args(qp, None, None, 0, mp, np_, T, s, op, ws.data_ptr() if ws is not None else None, need)
-    return args, out, ws
+    op = _fast_ptr(out, bf16, out_shape, "out", device)
+    if scale is not None:
+        s = float(scale)
+        if not abs(s) <= 3.4e38:
+            raise ValueError("scale must be a finite 32-bit number")
+    return _lib.pack_tree.pack(qp, lens, locs, top_k, mp, np_, T, s, op, ws.data_ptr() if ws is not None else 0, need), out, ws
 
 
 class HsPool:
@@ -309,13 +318,11 @@ class HsPool:
         import torch
 
         c = self.cfg
-        T = _tree_nodes(q)
         lo = _fast_ptr(locs, torch.int32, (c.num_requests, c.top_k), "locs", self.device)
-        d = _fast_ptr(draft, torch.bfloat16, (c.num_requests, T, c.record_elems), "draft", self.device)
-        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, T, mask, nodes, out, scale,
-                                    stream)
-        args.d_locs, args.top_k = lo, c.top_k
-        _check("hs_pool_tree_attn", self.lib.hs_pool_tree_attn(self._h, int(layer), ctypes.byref(args), d,
+        args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, 0, lo, c.top_k, mask, nodes, out,
+                                    scale, stream)
+        d = _fast_ptr(draft, torch.bfloat16, (c.num_requests, q.shape[1], c.record_elems), "draft", self.device)
+        _check("hs_pool_tree_attn", self.lib.hs_pool_tree_attn(self._h, int(layer), args, d,
                                                                _fast_stream(torch, stream, self.device)))
         return out
 
