@@ -13,8 +13,8 @@
 // Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
 // of one tile of rows 0.54 us at the tensor cores' rate.  Measured: 4 requests x 131072 positions x 16 nodes x 32
 // heads 358 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.5 us (136 MB read, 3.4 TB/s: half of it the
-// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 92 us (840 TFLOP/s,
-// tensor cores active 42%).  There a turn of a group is its products (two times 520 cycles) and what their hand-overs
+// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 89.5 us (861 TFLOP/s,
+// tensor cores active 43%).  There a turn of a group is its products (two times 520 cycles) and what their hand-overs
 // take (500 from the value product's end to the scores, 450 from the scores to the other group's turn), 2050 of the 4100
 // cycles of a tile, in which its softmax takes 1870.
 #include <cuda_runtime.h>

@@ -15,7 +15,7 @@
 // The even CTA's warp issues for both; what has landed in the odd one is passed on by an arrival on its barriers.
 // What bounds it: the products of a tile take about 1800 of its 2300 cycles; the rest is what the keys' two buffers
 // leave of the load's latency (1900 cycles under load).  Measured: 4 ragged requests of up to 32768 x 5 nodes x
-// 64 heads 73 us (705 TFLOP/s, tensor cores active 40%), 8 x 8 nodes over 2048 listed positions 45 us.  Keys that
+// 64 heads 72.5 us (710 TFLOP/s, tensor cores active 40%), 8 x 8 nodes over 2048 listed positions 43.7 us.  Keys that
 // come and go in two parts took 87 us (records fetched in two visits).
 #include <cuda_runtime.h>
 #include <math.h>
