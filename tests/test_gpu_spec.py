@@ -166,6 +166,17 @@ def test_masks_of_any_pattern_and_nodes_in_use(cfg, T):
     assert torch.count_nonzero(out[0, 0]) == 0 and torch.count_nonzero(out[0, 2]) == 0
 
 
+@pytest.mark.parametrize("cfg,T", [(gqa(3), 4), (gqa(3), 70), (gqa(3, 8, 2, 64), 1), (gqa(3, 4, 2, 80), 2), (mla(3), 4), (gqa(40), 2),
+                                   (mla(40), 1)])
+def test_no_nodes_at_all(cfg, T):
+    """Nothing to do: every output row stays as it was, and the call after it works."""
+    R = cfg.num_requests
+    kv = make_cache(cfg, 64 + T, 16, seed=T)
+    mask = tree_mask(random_tree(R, T, seed=1))
+    check_tree(cfg, kv, [60] * R, T, mask, nodes=[0] * R)
+    check_tree(cfg, kv, [0] * R, T, mask, nodes=[0] * (R - 1) + [1])
+
+
 @pytest.mark.parametrize("cfg", [gqa(2), gqa(2, 8, 2, 64), gqa(2, 4, 2, 80), mla(2), mla(2, 16)],
                          ids=["gqa", "gqa64", "any", "mla", "mla16"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
