@@ -603,7 +603,7 @@ extern "C" int hs_device_usage(hs_pool* pool, int64_t* pages_in_use, int64_t* pa
 }
 
 extern "C" int hs_debug_stall_next(hs_pool* pool, int kernels) {
-  if (pool == nullptr || (kernels & ~(HS_STALL_ATTN | HS_STALL_RESOLVE | HS_STALL_FETCH)) != 0) return HS_ERR_ARG;
+  if (pool == nullptr || (kernels & ~(HS_STALL_ATTN | HS_STALL_RESOLVE | HS_STALL_FETCH | HS_STALL_TREE)) != 0) return HS_ERR_ARG;
   pool->debug_stall |= kernels;
   return HS_OK;
 }

@@ -254,26 +254,37 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The same with a limit of tries instead of a time (a try suspends the thread for a while; 2^22 of them take
-// a good part of a second at the least), for kernels whose code size counts.
-__device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
+// The limit of the waits below, about a second: every 64th try looks at the clock (its low word: a difference is right
+// while it is below 4 s), so a wait that succeeds soon never does.
+struct WaitLimit {
+  uint32_t tries = 0, t0 = 0;
+  __device__ __forceinline__ bool over() {
+    if ((++tries & 63u) != 0u) return false;
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    if (tries == 64u) t0 = t;
+    return t - t0 > 1000000000u;
   }
-  return false;
+};
+
+// mbar_wait_bounded for kernels whose code size counts
+__device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  WaitLimit limit;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (*abort != 0u || limit.over()) return false;
+  return true;
 }
 
 __device__ __forceinline__ bool mbar_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
                                            volatile uint32_t* abort) {  // two at once: their latencies overlap
+  WaitLimit limit;
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
+  for (;;) {
     const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
     if (x && y) return true;
-    if (*abort) return false;
+    if (*abort != 0u || limit.over()) return false;
   }
-  return false;
 }
 
 // A whole warp's wait whose result the compiler knows to be the same in all lanes.  The warp that issues the
@@ -281,23 +292,22 @@ __device__ __forceinline__ bool mbar_wait2(uint64_t* bar, uint32_t parity, uint6
 // they are not uniform to begin with each product costs their moves (57 cycles instead of 32 for one of
 // 64 x 64 x 16).
 __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  WaitLimit limit;
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
-    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, *abort != 0u)) return false;
-  }
-  return false;
+  while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) return false;
+  return true;
 }
 // Two at once: their latencies overlap.
 __device__ __forceinline__ bool uniform_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
                                               volatile uint32_t* abort) {
+  WaitLimit limit;
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 22); ++i) {
+  for (;;) {
     const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
     if (__any_sync(0xffffffffu, x && y)) return true;
-    if (__any_sync(0xffffffffu, *abort != 0u)) return false;
+    if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) return false;
   }
-  return false;
 }
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {  // no wait
   uint32_t ok;

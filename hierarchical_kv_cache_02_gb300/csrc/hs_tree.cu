@@ -237,6 +237,8 @@ extern "C" int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* a
   a.slot_shift = pool->slot_shift;
   a.draft = (const uint8_t*)d_draft;
   a.k = c.top_k;
+  a.stall = (pool->debug_stall & HS_STALL_TREE) != 0;  // test hook, consumed by this launch
+  pool->debug_stall &= ~HS_STALL_TREE;
   pool->last_res_layer = -1;  // an attention after this one waits for the whole stream
   return launch_tree(&c, args, a, pool->device, (cudaStream_t)stream);
 }

@@ -27,6 +27,7 @@ struct TreeArgs {
   int R, T, k, words, Hq, Hkv, dqk, dv;
   int kstride, voff;        // values: KV head g's key at g * kstride, its value voff further on
   float qscale;             // scale * log2(e)
+  int stall;                // test hook (hs_debug_stall_next): one arrival of a CTA's first tile is left out
 };
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }

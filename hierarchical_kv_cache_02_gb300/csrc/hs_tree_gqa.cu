@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && lane == 0) {
               ct.valid[g][n % kMaskRing][pw] = word;
               if (pw == 0) ct.vplace[g][n % kMaskRing] = vplace;
-              mbar_arrive(&ct.mask[g][n % kMaskRing]);
+              if (!(a.stall != 0 && n == 0 && pw == 1 && blockIdx.x == 0)) mbar_arrive(&ct.mask[g][n % kMaskRing]);
             }
             ++n;
           }

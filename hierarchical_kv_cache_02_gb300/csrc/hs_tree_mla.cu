@@ -237,15 +237,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) {
           ok = false;
           const uint32_t kq = (uint32_t)((i >> 1) & 1), vq = (uint32_t)((nt >> 1) & 1);
+          WaitLimit limit;
 #pragma unroll 1
-          for (uint32_t x = 0; x < (1u << 22); ++x) {
+          for (;;) {
             const bool y0 = mbar_test(&ct.p, (uint32_t)(nt & 1)), y1 = mbar_test(&ct.vready[b], vq),
                        y2 = mbar_test(&ct.kready[bs], kq), y3 = !kfirst || mbar_test(&ct.qready, (uint32_t)(nq & 1));
             ok = __any_sync(0xffffffffu, ahead != 0 && y0 && y1);
             if (ok) break;
             ok = scores = __any_sync(0xffffffffu, more && y2 && y3);
             if (ok) break;
-            if (__any_sync(0xffffffffu, *abort != 0u)) break;
+            if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) break;
           }
           if (!ok) scores = ahead == 0;
         }
@@ -419,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) cluster_arrive(p_bar);
+          if (lane == 0 && !(a.stall != 0 && nt == 0 && tid == 64 && blockIdx.x == 1)) cluster_arrive(p_bar);
         }
         // the portion's result: complete, or a partial
         if (ok) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);

@@ -217,7 +217,8 @@ class PagedKV:
                                                      _fast_stream(torch, stream, self.device)))
 
     def errors(self, reset: bool = False) -> int:
-        """The DEVERR_* bits that the calls so far recorded (synchronises the device)."""
+        """The DEVERR_* bits that the calls so far recorded (synchronises the device).  DEVERR_TIMEOUT: a tree
+        attention gave up waiting and its output is undefined; the cache is as it was."""
         import torch
 
         torch.cuda.synchronize(self.device)

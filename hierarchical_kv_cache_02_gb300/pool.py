@@ -372,7 +372,8 @@ class HsPool:
         """Test hook: the next launch of each kernel in `kernels` (STALL_ATTN, STALL_RESOLVE) leaves
         one barrier arrival out, so its bounded wait gives up and reports DEVERR_TIMEOUT.
         STALL_FETCH: one record a fetch CTA claimed is never marked as landed; the deciding CTA that
-        needs it gives up waiting, reports DEVERR_TIMEOUT and fetches it from the host itself."""
+        needs it gives up waiting, reports DEVERR_TIMEOUT and fetches it from the host itself.
+        STALL_TREE: the next tree_attn on the tensor cores, whose output is then undefined."""
         _check("hs_debug_stall_next", self.lib.hs_debug_stall_next(self._h, int(kernels)))
 
     def device_usage(self) -> dict:

@@ -361,9 +361,12 @@ int hs_release(hs_pool* pool, int req);
  *                      launch's first request never signal that the victims are chosen, so that
  *                      request's fetch CTAs give up waiting and install nothing.  Consumed by the
  *                      next resolve launch with fetch CTAs.
+ *   HS_STALL_TREE    : hs_pool_tree_attn on the tensor cores (an arrival of one CTA's first tile),
+ *                      consumed by the next hs_pool_tree_attn; the cache is not touched, so no reset
+ *                      is needed
  * Host-side only (takes effect at launch, also when the launch is captured).  Errors: HS_ERR_ARG.
  */
-enum { HS_STALL_ATTN = 1, HS_STALL_RESOLVE = 2, HS_STALL_FETCH = 4 };
+enum { HS_STALL_ATTN = 1, HS_STALL_RESOLVE = 2, HS_STALL_FETCH = 4, HS_STALL_TREE = 8 };
 int hs_debug_stall_next(hs_pool* pool, int kernels);
 
 /*
@@ -470,7 +473,10 @@ int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int cuda_device)
  * read); a node count outside [0, nodes] sets it and is clamped.  Scores, softmax sums and accumulators
  * are 32-bit; the weights enter the value product as bf16 for the shapes on the tensor cores, and the
  * output is rounded once to bf16.  The order of the sums depends on the lengths alone: equal calls give
- * equal bits.  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH (workspace too small), HS_ERR_CUDA.
+ * equal bits.  A bounded wait inside a kernel that gives up (about a second without progress, a stalled GPU) sets
+ * HS_DEVERR_TIMEOUT and leaves d_out undefined; the cache is only read, and the next call works.  With d_err NULL
+ * nothing reports that, nor any other error of the device's.
+ * Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH (workspace too small), HS_ERR_CUDA.
  */
 int hs_tree_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_tree_args* args, void* stream);
 
