@@ -173,11 +173,22 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {  // a
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// On a barrier in any CTA of the cluster.  What it announces is this CTA's own shared memory, ordered before by
-// fence.proxy.async, and is read by the tensor cores alone: release at the CTA's scope.  (At the cluster's it
-// takes 1000 cycles more.)
+// Hand-overs between the CTAs of a cluster.  The barrier is of any CTA; what the arriving thread did before (its stores,
+// its accesses to tensor memory behind tc_fence_before, copies that it waited for) is ordered before what the thread
+// does that sees the phase complete: both name the cluster's scope, as the default one reaches no further than the CTA.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool cluster_test(uint64_t* bar, uint32_t parity) {  // no wait
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
 }
 __device__ __forceinline__ void cluster_sync() {  // every thread of both CTAs
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -276,6 +287,14 @@ __device__ __forceinline__ bool mbar_wait_small(uint64_t* bar, uint32_t parity, 
   return true;
 }
 
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
+  WaitLimit limit;
+#pragma unroll 1
+  while (!cluster_test(bar, parity))
+    if (*abort != 0u || limit.over()) return false;
+  return true;
+}
+
 __device__ __forceinline__ bool mbar_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
                                            volatile uint32_t* abort) {  // two at once: their latencies overlap
   WaitLimit limit;
@@ -294,7 +313,7 @@ __device__ __forceinline__ bool mbar_wait2(uint64_t* bar, uint32_t parity, uint6
 __device__ __forceinline__ bool uniform_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort) {
   WaitLimit limit;
 #pragma unroll 1
-  while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
     if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) return false;
   return true;
 }
@@ -305,7 +324,7 @@ __device__ __forceinline__ bool uniform_wait2(uint64_t* bar, uint32_t parity, ui
 #pragma unroll 1
   for (;;) {
     const bool x = mbar_try_wait(bar, parity), y = mbar_try_wait(bar2, parity2);
-    if (__any_sync(0xffffffffu, x && y)) return true;
+    if (__all_sync(0xffffffffu, x && y)) return true;
     if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) return false;
   }
 }

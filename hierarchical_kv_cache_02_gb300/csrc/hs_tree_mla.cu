@@ -9,14 +9,16 @@
 // So a CTA loads 68 KB a tile, the keys free their memory as soon as the scores are done, and two tiles of each fit
 // beside the queries.  (One CTA for itself, 64 rows: a tile is key and value at once, 72 KB that stay from the
 // scores to the value product, and an accumulator of 64 rows runs the tensor cores at half their rate; two such tiles
-// fit: 97 us instead of 73 below.  128 rows of a CTA: their queries leave room for one tile.)
+// fit: 97 and 55 us on the two cases below.  128 rows of a CTA: their queries leave room for one tile.)
 // Rows 0-63 of an accumulator are the even CTA's, in both: its first half of columns in lanes 0-63 of tensor memory,
 // the second in 64-127.  So two threads share a row, half of a tile's entries and half of the dims each.
 // The even CTA's warp issues for both; what has landed in the odd one is passed on by an arrival on its barriers.
-// What bounds it: the products of a tile take about 1800 of its 2300 cycles; the rest is what the keys' two buffers
-// leave of the load's latency (1900 cycles under load).  Measured: 4 ragged requests of up to 32768 x 5 nodes x
-// 64 heads 72.5 us (710 TFLOP/s, tensor cores active 40%), 8 x 8 nodes over 2048 listed positions 43.7 us.  Keys that
-// come and go in two parts took 87 us (records fetched in two visits).
+// What bounds it: the chain from one value product to the next.  Its weights may be stored once the product before is
+// complete, and are handed to the even CTA by an arrival with release at the cluster's scope, which takes about 1000
+// cycles; a tile takes about 3000, its products 1800.  Measured: 4 ragged requests of up to 32768 x 5 nodes x 64 heads
+// 96.4 us (532 TFLOP/s), 8 x 8 nodes over 2048 listed positions 51.2 us.  (Arrivals with the default scope, the CTA's,
+// took 72.5 and 43.7 us, but order nothing for the other CTA.  The hand-over by a warp of its own: 105 and 52 us;
+// polls without ordering and a fence behind them: 122 and 59 us.)
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -57,6 +59,7 @@ struct MlaControl {
   __align__(8) uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t kready[2], vready[2], qready;  // even CTA: full in both
   uint64_t qfull, s[kAhead], p, pv, mask[kMaskRing], fin;
+  uint64_t told[2];  // the other CTA's softmax is through with a portion's nodes (two: it can be one portion ahead)
   uint32_t valid[kMaskRing][2];
   float most[2][2][64], sums[2][64];
   uint32_t tmem, abort, dirty;
@@ -90,6 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ct.pv, 1u);
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], 2u);
     mbar_init(&ct.fin, 1u);
+    for (int i = 0; i < 2; ++i) mbar_init(&ct.told[i], 4u);
     ct.abort = ct.dirty = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -119,6 +123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int nt = 0;                      // tiles so far, of each role
   int nq = 0;                      // portions so far (products); query loads (first softmax thread)
   int sent = 0;                    // producers: tiles whose copies were issued
+  int nd = 0;                      // softmax: portions with nodes
   bool ok = true;
   uint32_t bad = 0u;
 
@@ -240,11 +245,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           WaitLimit limit;
 #pragma unroll 1
           for (;;) {
-            const bool y0 = mbar_test(&ct.p, (uint32_t)(nt & 1)), y1 = mbar_test(&ct.vready[b], vq),
-                       y2 = mbar_test(&ct.kready[bs], kq), y3 = !kfirst || mbar_test(&ct.qready, (uint32_t)(nq & 1));
-            ok = __any_sync(0xffffffffu, ahead != 0 && y0 && y1);
+            const bool y0 = cluster_test(&ct.p, (uint32_t)(nt & 1)), y1 = cluster_test(&ct.vready[b], vq),
+                       y2 = cluster_test(&ct.kready[bs], kq), y3 = !kfirst || cluster_test(&ct.qready, (uint32_t)(nq & 1));
+            ok = __all_sync(0xffffffffu, ahead != 0 && y0 && y1);
             if (ok) break;
-            ok = scores = __any_sync(0xffffffffu, more && y2 && y3);
+            ok = scores = __all_sync(0xffffffffu, more && y2 && y3);
             if (ok) break;
             if (__any_sync(0xffffffffu, *abort != 0u || limit.over())) break;
           }
@@ -348,9 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                             min(kTile, P.nn - j0), tid, 128);
             if (bar_or(1, 128, d)) {
               dirty = true;
-              if (lane == 0)  // the other CTA's rows take their values from here, too
+              if (lane == 0)  // the other CTA's rows take their values from here, too; read there behind ct.told
                 asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(in_cta(smem_u32(&ct.dirty), (uint32_t)(rank ^ 1))) : "memory");
-              asm volatile("fence.acq_rel.cluster;" ::: "memory");
             }
             ok = __all_sync(0xffffffffu, ok);
           }
@@ -421,11 +425,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0 && !(a.stall != 0 && nt == 0 && tid == 64 && blockIdx.x == 1)) cluster_arrive(p_bar);
+          if (nodes && tile == P.t1 - 1 && lane == 0) cluster_arrive(in_cta(smem_u32(&ct.told[nd & 1]), (uint32_t)(rank ^ 1)));
         }
         // the portion's result: complete, or a partial
         if (ok) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+        if ((long long)P.t1 * kTile > n4) {  // it holds nodes: the other CTA has looked at its half of their values
+          if (ok) ok = cluster_wait(&ct.told[nd & 1], (uint32_t)((nd >> 1) & 1), abort);
+          ok = __all_sync(0xffffffffu, ok);
+          ++nd;
+        }
         ct.sums[half][row] = l;
         pair_sync();
         l += ct.sums[half ^ 1][row];
