@@ -402,6 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp < 8) {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
+      // (A warp comes together, by a vote or __syncwarp, behind each branch that its lanes may take apart: accesses to tensor memory
+      // are the whole warp's, and nothing else promises that it is whole there.)
       const int g = warp >> 2, row = tid & 127;
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tb + 128u * g + lane_base, to = tb + 256u + (uint32_t)(D * g) + lane_base;
@@ -470,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++nm;
           ++nt;
+          __syncwarp();
           if (ok && warp_ok) {
             // Scores 64 at a time: what a load from tensor memory costs is its wait.
             float mx = -INFINITY, my = -INFINITY;
@@ -492,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float al = (mn == m || m == -INFINITY) ? 1.f : fast_exp2(m - mn);
               m = mn;
               l *= al;
+              __syncwarp();
               if (tile != P.t0) {
 #pragma unroll 1
                 for (int x = 0; x < D / 32; ++x) {
@@ -537,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             float o[32];
+            __syncwarp();
             tmem_ld32(to + 32u * x, o);
             if (dirty && row_ok) {
               // values left out of the product (they would have reached every row): into the rows that see them
@@ -570,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && !whole) *(float2*)(c.ws.ml + (slot + srow) * 2) = make_float2(m, l);
         }
         tc_fence_before();
+        __syncwarp();
       }
     }
     if (!ok) *abort = 1u;
@@ -603,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   tc_fence_after();
   if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
 }

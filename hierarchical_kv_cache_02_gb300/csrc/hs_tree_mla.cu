@@ -311,6 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp < 4) {
       // ---------------- softmax: two threads a row, half of a tile's entries and half of the dims each ----------------
+      // (A warp comes together, by a vote or __syncwarp, behind each branch that its lanes may take apart: accesses to tensor memory
+      // are the whole warp's, and nothing else promises that it is whole there.)
       const int row = tid & 63, half = tid >> 6;
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16, p_bar = in_cta(smem_u32(&ct.p), 0);
       auto pair_sync = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + (warp & 1)) : "memory"); };
@@ -337,9 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool nodes = j0 + kTile > 0;
           if (ok) ok = mbar_wait2(&ct.s[nt % kAhead], (uint32_t)((nt / kAhead) & 1), &ct.mask[nt % kMaskRing],
                                   (uint32_t)((nt / kMaskRing) & 1), abort);
+          if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
-          if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
           uint32_t w = ct.valid[nt % kMaskRing][half];
           if (nodes) {
             // entries that are nodes: valid ones that this row sees
@@ -400,6 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (any) {
               const float al = (m == mo || mo == -INFINITY) ? 1.f : fast_exp2(mo - m);
               l *= al;
+              __syncwarp();
               if (tile != P.t0 && ok) {
 #pragma unroll 1
                 for (int x = 0; x < 8; ++x) {
@@ -447,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
             float o[32];
+            __syncwarp();
             tmem_ld32(tb + lane_base + 32u * x, o);
             const int dim = 256 * half + 32 * x;
             if (dirty && row_ok) {
@@ -480,6 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (row_ok && !whole && half == 0) *(float2*)(c.ws.ml + (slot + 64 * rank + row) * 2) = make_float2(m, l);
         }
         tc_fence_before();
+        __syncwarp();
       }
     }
     if (!ok) {  // the other CTA gives up, too
@@ -515,6 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   cluster_sync();  // neither CTA's memory is used by the other any more
   tc_fence_after();
   if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
