@@ -545,9 +545,10 @@ __global__ void __launch_bounds__(kJoinThreads, W == 8 ? 7 : 1) k_tree_combine(C
     for (int i = 0; i < W; ++i) acc[i] *= al;
 #pragma unroll
     for (int j = 0; j < F; ++j) {
-      // nothing seen: no part in the result; NaN scores alone: NaN
-      const float wt = ml[j].x == -INFINITY ? (ml[j].y == 0.f ? 0.f : ml[j].y) : exp2f(ml[j].x - M);
-      if (wt == 0.f) continue;
+      if (w0 + j > wl) continue;
+      // -infinity: nothing seen (sum 0), or NaN scores alone (NaN).  A weight of 0 counts all the same: what the row saw
+      // may be infinite or NaN, and what it saw nothing of holds zeros
+      const float wt = ml[j].x == -INFINITY ? ml[j].y : exp2f(ml[j].x - M);
       L = fmaf(wt, ml[j].y, L);
 #pragma unroll
       for (int i = 0; i < W / 4; ++i) {

@@ -31,3 +31,51 @@ def test_a_pairs_hand_overs_many_times(dims):
     for out in outs:
         assert torch.equal(out[:, ~sees], clean[:, ~sees])
         assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
+
+
+# what a node sees is bad in a value, or in a key (its score is NaN)
+@pytest.mark.parametrize("kind", ["value-inf", "value-nan", "key-nan"])
+@pytest.mark.parametrize("cfg", [gqa(1), gqa(1, 8, 2, 64), gqa(1, 4, 2, 80), mla(1), mla(1, 3, 128, 64)],
+                         ids=["gqa", "gqa64", "any", "mla", "any-latent"])
+@pytest.mark.parametrize("n", [60, 200, 600, 20000])
+@pytest.mark.parametrize("node", [False, True])
+def test_a_bad_entry_of_next_to_no_weight_is_seen(kind, cfg, n, node):
+    """One entry's weight is all there is in 32 bits (the others are below 2^-150 of it); a bad entry that has none makes
+    its dims, or with a NaN score its rows, infinite or NaN all the same, whether one worker holds the context or many."""
+    T, lat = 3, cfg.layout == 0
+    if lat and kind.startswith("value"):
+        pytest.skip("a latent's value is its key")
+    kv = make_cache(cfg, n + T, 16, seed=n)
+    flat, table, page = kv.pages.view(-1, cfg.record_elems), kv.table.cpu(), kv.pages.shape[1]
+    flat *= 0.125
+    D, Hkv, dim, col = cfg.head_dim_qk, cfg.num_kv_heads, 9, 9 if lat else 3
+    q = randn((1, T, cfg.num_q_heads, D), 5)
+    q[..., 0], q[..., col] = 8.0, -1.0
+    row = lambda p: ref.row_of(table, 0, p, page, 0)  # noqa: E731
+    for g in range(Hkv):  # scores of 8 * 512 / sqrt(D), 170 and more, against a few: 2^-245 at the most
+        flat[row(n - 3), g * (D + cfg.head_dim_v)] = 512.0
+    at = n + 1 if node else 7
+    key = 0 if lat else (Hkv - 1) * (D + cfg.head_dim_v)  # of the last KV head
+    where = {"value-inf": [(key + D + dim, "inf")], "value-nan": [(key + D + dim, "nan")], "key-nan": [(key + col, "nan")],
+             }[kind]
+    for e, _ in where:
+        flat[row(at), e] = 0.0
+    parents = torch.tensor([[-1, 0, 1]])
+    lens, mask = torch.tensor([n], dtype=torch.int64, device=DEV), tree_mask(parents)
+    _, clean = check_tree(cfg, kv, [n], T, mask, q=q)
+    for e, x in where:
+        flat[row(at), e] = float(x)
+    out = kv.tree_attn(q, lens, mask.to(DEV))
+    assert kv.errors() == 0
+    sees = torch.tensor([not node or i >= 1 for i in range(T)])
+    heads = torch.arange(cfg.num_q_heads) // (cfg.num_q_heads // Hkv) == Hkv - 1
+    assert torch.equal(out[0, ~sees], clean[0, ~sees]) and torch.equal(out[0, :, ~heads], clean[0, :, ~heads])
+    hit = out[0, sees][:, heads]
+    if kind == "key-nan":
+        assert bool(hit.isnan().all())
+        return
+    assert not bool(torch.isfinite(hit[..., dim]).any())
+    # the other dims: as without the entry, whose weight is nothing (its score was a few, it is that or -infinity)
+    hit, same = hit.clone(), clean[0, sees][:, heads].clone()
+    hit[..., dim] = same[..., dim] = 0
+    assert torch.equal(hit, same)
