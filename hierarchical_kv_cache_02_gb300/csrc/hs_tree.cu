@@ -79,10 +79,10 @@ __global__ void __launch_bounds__(kAnyWarps * 32) k_tree_any(TreeArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     s *= a.qscale;
-    if (s == -INFINITY) continue;  // weight 0 whatever the maximum
-    // NaN scores go on: fmaxf keeps the maximum, the weight is NaN
+    // -infinity: weight 0 whatever the maximum, but a value that is infinite or NaN counts.  NaN: fmaxf keeps the
+    // maximum, the weight is NaN
     const float mn = fmaxf(m, s);
-    const float al = m == mn ? 1.f : exp2f(m - mn), p = exp2f(s - mn);
+    const float al = m == mn ? 1.f : exp2f(m - mn), p = s == -INFINITY ? 0.f : exp2f(s - mn);
     m = mn;
     l = l * al + p;
 #pragma unroll

@@ -468,8 +468,9 @@ int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int cuda_device)
  * over the context's entries and the nodes j that i sees.  Every context record is read once for all
  * nodes and all query heads of its KV head.  Nothing visible gives zeros.  What a node does not see has no
  * influence on it, whatever its values (NaN and infinities included).  What it does see counts however small its
- * weight, even one that rounds to 0: an infinite or NaN value makes that dim of the output infinite or NaN, a NaN
- * score the whole row.  Positions outside
+ * weight, even one that is 0 (a score of -infinity) or rounds to it: an infinite or NaN value makes that dim of the
+ * output infinite or NaN, a NaN score the whole row.  A row whose visible scores are all -infinity
+ * gives zeros where the values are finite.  Positions outside
  * [0, max_pages * page_tokens) set HS_DEVERR_LOC, bad table entries HS_DEVERR_PAGE: such
  * entries are not seen.  A len < 0 sets HS_DEVERR_LOC and leaves neither context nor nodes (a list is still
  * read); a node count outside [0, nodes] sets it and is clamped.  Scores, softmax sums and accumulators

@@ -33,8 +33,8 @@ def test_a_pairs_hand_overs_many_times(dims):
         assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
 
 
-# what a node sees is bad in a value, or in a key (its score is NaN)
-@pytest.mark.parametrize("kind", ["value-inf", "value-nan", "key-nan"])
+# what a node sees is bad in a value, in a key (its score is NaN), or in both so that its score is -infinity
+@pytest.mark.parametrize("kind", ["value-inf", "value-nan", "key-nan", "minus-infinity"])
 @pytest.mark.parametrize("cfg", [gqa(1), gqa(1, 8, 2, 64), gqa(1, 4, 2, 80), mla(1), mla(1, 3, 128, 64)],
                          ids=["gqa", "gqa64", "any", "mla", "any-latent"])
 @pytest.mark.parametrize("n", [60, 200, 600, 20000])
@@ -57,7 +57,7 @@ def test_a_bad_entry_of_next_to_no_weight_is_seen(kind, cfg, n, node):
     at = n + 1 if node else 7
     key = 0 if lat else (Hkv - 1) * (D + cfg.head_dim_v)  # of the last KV head
     where = {"value-inf": [(key + D + dim, "inf")], "value-nan": [(key + D + dim, "nan")], "key-nan": [(key + col, "nan")],
-             }[kind]
+             "minus-infinity": [(key + col, "inf")] + ([] if lat else [(key + D + dim, "inf")])}[kind]
     for e, _ in where:
         flat[row(at), e] = 0.0
     parents = torch.tensor([[-1, 0, 1]])
