@@ -136,7 +136,7 @@ int check_tree(const hs_config* c, const hs_tree_args* g) {
       !hs_aligned(g->d_nodes, 4) || !hs_aligned(g->d_len, 8) || !hs_aligned(g->d_workspace, 16))
     return HS_ERR_ARG;
   if (g->nodes < 1 || g->nodes > HS_MAX_TREE_NODES) return HS_ERR_ARG;
-  if (!isfinite(g->scale)) return HS_ERR_ARG;
+  if (!isfinite(g->scale * kLog2e)) return HS_ERR_ARG;  // what the kernels multiply by
   return HS_OK;
 }
 

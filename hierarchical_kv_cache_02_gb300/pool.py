@@ -157,8 +157,8 @@ def _tree_args(torch, lib, c_cfg, cfg, device, known, q, lens, locs, top_k, mask
     op = _fast_ptr(out, bf16, out_shape, "out", device)
     if scale is not None:
         s = float(scale)
-        if not abs(s) <= 3.4e38:
-            raise ValueError("scale must be a finite 32-bit number")
+        if not abs(s) <= 2.35e38:  # times log2(e) it has to be a finite 32-bit number
+            raise ValueError("scale must be a number of magnitude 2.35e38 at most")
     return _lib.pack_tree.pack(qp, lens, locs, top_k, mp, np_, T, s, op, ws.data_ptr() if ws is not None else 0, need), out, ws
 
 

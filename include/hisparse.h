@@ -451,7 +451,7 @@ typedef struct {
   const int32_t* d_nodes;  /* [num_requests] nodes in use (0 .. nodes), or NULL: all of them.  Output rows
                               behind them are left as they were */
   int32_t nodes;           /* T, 1 .. HS_MAX_TREE_NODES */
-  float scale;
+  float scale;             /* magnitude below 2.35e38: scale * log2(e) is a finite 32-bit number */
   void* d_out;             /* bf16 [num_requests][nodes][num_q_heads][head_dim_v], 16-byte aligned */
   void* d_workspace;       /* hs_tree_attn_workspace bytes, 16-byte aligned; used by this call alone until
                               it is done: calls that may overlap need one each */

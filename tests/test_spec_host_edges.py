@@ -1,0 +1,14 @@
+"""More refusals of the speculative-decoding entry points on the host, before anything touches a device."""
+import ctypes
+
+import pytest
+
+from hierarchical_kv_cache_02_gb300 import _lib
+from test_spec_host import append, lib, paged, shape, tree  # noqa: F401 (lib: a fixture)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_a_scale_that_overflows_in_base_two(lib, scale):  # noqa: F811
+    """Scores are taken times scale * log2(e): where that is infinite, a score of 0 would be NaN."""
+    c, kv = shape(), paged()
+    assert lib.hs_tree_attn(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(tree(scale=scale)), None) == _lib.HS_ERR_ARG
