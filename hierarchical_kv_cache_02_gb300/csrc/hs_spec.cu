@@ -335,6 +335,8 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
     const bool by_token = (hq == 1 || hs >= d) && (n == 1 || ts >= (hq - 1) * hs + d);
     const bool by_head = (n == 1 || ts >= d) && (hq == 1 || hs >= (n - 1) * ts + d);
     if (!by_token && !by_head) return HS_ERR_ARG;
+    // in place, every thread reads what it writes only where both have the same strides
+    if (g.d_q == g.d_q_out && ((n > 1 && g.q_token_stride != ts) || (hq > 1 && g.q_head_stride != hs))) return HS_ERR_ARG;
     if (g.q_dim != cfg->head_dim_qk && (g.q_dim != g.rotary_dim || g.q_dim == 0)) return HS_ERR_ARG;
   }
   HsOnDevice on(kv->cuda_device);

@@ -12,3 +12,11 @@ def test_a_scale_that_overflows_in_base_two(lib, scale):  # noqa: F811
     """Scores are taken times scale * log2(e): where that is infinite, a score of 0 would be NaN."""
     c, kv = shape(), paged()
     assert lib.hs_tree_attn(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(tree(scale=scale)), None) == _lib.HS_ERR_ARG
+
+
+@pytest.mark.parametrize("change", [dict(q_out_token_stride=8192), dict(q_token_stride=8192), dict(q_head_stride=0),
+                                    dict(q_out_token_stride=128, q_out_head_stride=512)])
+def test_a_query_rotated_in_place_keeps_its_strides(lib, change):  # noqa: F811
+    """d_q_out may be d_q: then with the same strides, or a query would be overwritten before it is read."""
+    c, kv = shape(), paged()
+    assert lib.hs_append_rotated(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(append(**change)), None) == _lib.HS_ERR_ARG
