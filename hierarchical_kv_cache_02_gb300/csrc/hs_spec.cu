@@ -21,7 +21,10 @@ namespace {
 // A CTA takes a few tokens: their records' places and the sines and cosines, shared by all heads, first; then
 // units of two 16-byte vectors, two of them in flight per thread at 40 registers (six CTAs an SM).  Few tokens
 // spread over many CTAs, each with a share of every token's units.  16384 tokens of 32 + 8 + 8 heads of 128:
-// 65.7 us, 6.1 TB/s (four units in flight at 64 registers 73.6 us, one 68.1; 8 or 16 tokens a CTA 72 and 83 us, one 74).
+// 65.7 us, 6.1 TB/s (four units in flight at 64 registers 73.6 us, one 68.1; 8 or 16 tokens a CTA 72 and 83 us, one 74;
+// all loads issued before the places are known, into registers, 75: spills).  Latents, 8191 tokens of 576 and 64 queries'
+// 64 rotary values each: 31.3 us, 4.9 TB/s; 4 tokens are 2.3 rounds of a CTA's 512 units there, and 87 heads, which fill
+// three, move 4.66 TB/s where 64 heads move 4.03 (single calls, caches cold).
 
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 4;   // tokens of a CTA at most
@@ -381,7 +384,7 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
   a.angles = div(a.half);
   // kAppTokens tokens a CTA while that leaves three CTAs an SM, fewer else; then every token's units are shared by
   // several CTAs until the GPU is filled or a share is below a quarter of one round (16 tokens: 3.2 us; a CTA a token
-  // 6.2 us).  A CTA's units stay below 2^16 (see Div).
+  // 6.2 us).  A CTA of several tokens has fewer than 2^16 units (see Div; of one token nothing is divided by them).
   a.tokens = kAppTokens;
   while (a.tokens > 1 && (a.N < kMinCtas * a.tokens || units * a.tokens >= 65536)) a.tokens >>= 1;
   const int ctas = (int)(((int64_t)a.N + a.tokens - 1) / a.tokens);

@@ -2,8 +2,8 @@
 //
 // For node i of request r and query head h, over the context's entries and the nodes that i sees:
 //   s_e = scale <q, K(e)>,  o = sum_e 2^(s_e log2(e) - m) V(e) / sum_e 2^(s_e log2(e) - m).
-// A context record serves all T nodes and all query heads of its KV head, so the cache is read once:
-// at few rows (nodes x query heads of a KV head) device memory bounds it, at many the tensor cores.
+// On the tensor cores a context record serves many (node, query head) rows at once: at few rows device memory bounds
+// it, at many the products.  The kernel below, for every other shape, reads a record anew for each of them.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -14,7 +14,9 @@ namespace {
 
 // Any shape: a CTA per (node, query head, request), its four warps take the entries in turn and merge
 // their running maxima, sums and accumulators at the end.  A lane holds every 32nd group of 8 values of
-// a head (head dims up to 576 = 72 groups: at most three).
+// a head (head dims up to 576 = 72 groups: at most three).  Latency of its loads bounds it, each warp's one record after
+// the other: 16 requests x 8 nodes x 32 heads of 80 over 2048 listed positions 4.1 ms (plain torch products 0.70 ms, the
+// tensor cores' kernel with heads of 128 0.041 ms); 1 request x 4 nodes x 1000 positions 321 us (plain 638 us).
 constexpr int kAnyWarps = 4, kAnyGroups = 3;
 
 __global__ void __launch_bounds__(kAnyWarps * 32) k_tree_any(TreeArgs a) {

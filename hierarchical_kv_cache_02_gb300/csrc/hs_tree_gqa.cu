@@ -3,7 +3,8 @@
 // Rows of an accumulator are (node, query head of one KV head) pairs: MT = 128 / G nodes of G heads.  Per
 // tile of 128 entries S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128), both tcgen05.mma with the
 // accumulators in tensor memory; the weights P go back to tensor memory over their scores and enter the
-// second product from there.  Two softmax warpgroups, a thread per row, each with its own S and O:
+// second product from there, rounded to bf16, as the tensor cores take both operands of a product in one type and V is
+// bf16 (2^-8 of a weight at most; the sum that divides is of the rounded ones, so that weights still add up to 1).  Two softmax warpgroups, a thread per row, each with its own S and O:
 //   one tile of rows (T <= MT): each group is a worker of its own with its own share of the entries, so
 //     that one group's softmax runs beside the other's products;
 //   more rows: the groups take two tiles of rows over the same entries, which are loaded once for both.
@@ -12,8 +13,8 @@
 // slower: its instructions leave a warp one lane at a time, 75 ns each).
 // Device memory bounds it while MT-tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products
 // of one tile of rows 0.54 us at the tensor cores' rate.  Measured: 4 requests x 131072 positions x 16 nodes x 32
-// heads 358 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.5 us (136 MB read, 3.4 TB/s: half of it the
-// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 89.5 us (861 TFLOP/s,
+// heads 360 us (6.0 TB/s); 16 x 8 nodes over 2048 listed positions 40.8 us (136 MB read, 3.4 TB/s: half of it the
+// rows' latency, start and joining of the partials); 8 ragged requests of up to 16384 x 64 nodes 89.9 us (860 TFLOP/s,
 // tensor cores active 43%).  There a turn of a group is its products (two times 520 cycles) and what their hand-overs
 // take (500 from the value product's end to the scores, 450 from the scores to the other group's turn), 2050 of the 4100
 // cycles of a tile, in which its softmax takes 1870.

@@ -5,7 +5,8 @@
 // head count, and the work of two CTAs, a cluster on neighbouring SMs: each holds 64 rows' queries (72 KB), and the
 // products are the pair's (cta_group::2).  Per tile of 64 records
 //   S = Q K^T (128 x 64 x 576): a CTA holds the keys of 32 records, whole;
-//   O += P V (128 x 512 x 64): a CTA holds 256 of the values of all 64 records.
+//   O += P V (128 x 512 x 64): a CTA holds 256 of the values of all 64 records.  The weights P are rounded to bf16, as both
+//   operands of a product have one type and V is bf16 (2^-8 of a weight at most; the sum that divides is of the rounded).
 // So a CTA loads 68 KB a tile, the keys free their memory as soon as the scores are done, and two tiles of each fit
 // beside the queries.  (One CTA for itself, 64 rows: a tile is key and value at once, 72 KB that stay from the
 // scores to the value product, and an accumulator of 64 rows runs the tensor cores at half their rate; two such tiles
@@ -16,7 +17,7 @@
 // What bounds it: the chain from one value product to the next.  Its weights may be stored once the product before is
 // complete, and are handed to the even CTA by an arrival with release at the cluster's scope, which takes about 1000
 // cycles; a tile takes about 3000, its products 1800.  Measured: 4 ragged requests of up to 32768 x 5 nodes x 64 heads
-// 96.4 us (532 TFLOP/s), 8 x 8 nodes over 2048 listed positions 51.2 us.  (Arrivals with the default scope, the CTA's,
+// 96.0 us (534 TFLOP/s, tensor cores active 30%), 8 x 8 nodes over 2048 listed positions 50.7 us.  (Arrivals with the default scope, the CTA's,
 // took 72.5 and 43.7 us, but order nothing for the other CTA.  The hand-over by a warp of its own: 105 and 52 us;
 // polls without ordering and a fence behind them: 122 and 59 us.)
 #include <cuda_runtime.h>
@@ -550,7 +551,8 @@ int hs_tree_mla_launch(const hs_config* cfg, const hs_tree_args* g, const void* 
   c.ws.np = 1;
   c.ws.groups = 1;
   c.ws.pairs = 1;
-  c.ws.begin = 2;  // 76.0, 74.2, 72.9 and 73.0 us with 0 to 3 on 4 ragged requests of up to 32768
+  c.ws.begin = 2;  // 76.0, 74.2, 72.9 and 73.0 us with 0 to 3 on 4 ragged requests of up to 32768 (before hand-overs
+                   // between the CTAs had the cluster's scope)
   c.ws.rows = kRows;
   hs_tree_workspace(g->d_workspace, cfg, pairs, kRows, kValue, &c.ws.prefix, &c.ws.part, &c.ws.ml);
   if (c.a.qscale < 0.f) {

@@ -465,8 +465,12 @@ int64_t hs_tree_attn_workspace(const hs_config* cfg, int nodes, int cuda_device)
 /*
  * Attention of a tree of drafted tokens over a paged cache: for request r, node i and query head h,
  *   out[r][i][h] = sum_e softmax_e(scale * <q[r][i][h], K(e)>) V(e)
- * over the context's entries and the nodes j that i sees.  Every context record is read once for all
- * nodes and all query heads of its KV head.  Nothing visible gives zeros.  What a node does not see has no
+ * over the context's entries and the nodes j that i sees.  How often a context record is read: heads of 64 or 128
+ * (keys and values alike, G <= 128 query heads a KV head) once for every two tiles of floor(128 / G) nodes; latents of
+ * 576 values (512 of them V) once for every 128 (node, query head) rows; both run on the tensor cores.  Any other shape
+ * runs on CUDA cores and reads a record once for every node and query head: 3 to 11 times the time of plain
+ * matrix products on batches (80-value heads, 16 requests x 8 nodes over 2048 listed positions: 4.1 ms, where
+ * 128-value heads take 41 us).  Nothing visible gives zeros.  What a node does not see has no
  * influence on it, whatever its values (NaN and infinities included).  What it does see counts however small its
  * weight, even one that is 0 (a score of -infinity) or rounds to it: an infinite or NaN value makes that dim of the
  * output infinite or NaN, a NaN score the whole row.  A row whose visible scores are all -infinity
