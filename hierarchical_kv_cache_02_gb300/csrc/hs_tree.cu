@@ -139,6 +139,9 @@ int check_tree(const hs_config* c, const hs_tree_args* g) {
     return HS_ERR_ARG;
   if (g->nodes < 1 || g->nodes > HS_MAX_TREE_NODES) return HS_ERR_ARG;
   if (!isfinite(g->scale * kLog2e)) return HS_ERR_ARG;  // what the kernels multiply by
+  // outputs are written while other rows' queries are still read
+  const uintptr_t rows = (uintptr_t)c->num_requests * g->nodes * c->num_q_heads, q = (uintptr_t)g->d_q, o = (uintptr_t)g->d_out;
+  if (q < o + 2 * rows * c->head_dim_v && o < q + 2 * rows * c->head_dim_qk) return HS_ERR_ARG;
   return HS_OK;
 }
 

@@ -187,7 +187,7 @@ class PagedKV:
         context and each other.  q bf16 [R][T][Hq][Dqk]; lens int64 [R]; mask int64 [R][T][ceil(T/64)]
         (see tree_mask); locs int32 [R][k]: only these positions of the context (-1 = padding), else all
         of [0, lens[r]); nodes int32 [R]: nodes in use, output rows behind them are left as they were.
-        Returns out, bf16 [R][T][Hq][Dv]."""
+        Returns out, bf16 [R][T][Hq][Dv] (it may not overlap q)."""
         import torch
 
         c = self.cfg

@@ -314,7 +314,7 @@ class HsPool:
         q bf16 [R][T][Hq][Dqk]; locs int32 [R][k] (what resolve returned, shared by a request's nodes);
         draft bf16 [R][T][record_elems], the nodes' records (rotated, in no pool yet); mask int64
         [R][T][ceil(T/64)] (see tree_mask); nodes: int32 [R] nodes in use, rows behind them are left as
-        they were.  out: bf16 [R][T][Hq][Dv].  Not for pools with fetch_in_attention = 1."""
+        they were.  out: bf16 [R][T][Hq][Dv], apart from q.  Not for pools with fetch_in_attention = 1."""
         import torch
 
         c = self.cfg

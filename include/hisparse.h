@@ -452,7 +452,7 @@ typedef struct {
                               behind them are left as they were */
   int32_t nodes;           /* T, 1 .. HS_MAX_TREE_NODES */
   float scale;             /* magnitude below 2.35e38: scale * log2(e) is a finite 32-bit number */
-  void* d_out;             /* bf16 [num_requests][nodes][num_q_heads][head_dim_v], 16-byte aligned */
+  void* d_out;             /* bf16 [num_requests][nodes][num_q_heads][head_dim_v], 16-byte aligned; apart from d_q */
   void* d_workspace;       /* hs_tree_attn_workspace bytes, 16-byte aligned; used by this call alone until
                               it is done: calls that may overlap need one each */
   int64_t workspace_bytes;

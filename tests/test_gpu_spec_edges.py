@@ -5,7 +5,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import spec_ref as ref
-from hierarchical_kv_cache_02_gb300 import RopeTable, tree_mask
+from hierarchical_kv_cache_02_gb300 import HsError, RopeTable, tree_mask
 from test_gpu_spec import DEV, check_append, check_tree, gqa, make_cache, mla, randn, random_tree
 
 
@@ -133,3 +133,14 @@ def test_append_to_many_requests(R, most):
     inv = [1.0, 0.5, 0.25, 0.1, 1e-2, 1e-3, 1e-4, 1e-5]
     check_append(gqa(R, 2, 1, 24), sum(counts) + 7, counts, [r % 11 for r in range(R)], 5, RopeTable(16, inv_freq=inv), inv, False,
                  q_dim=16, off=8, lead=4)
+
+
+def test_an_output_over_the_queries_is_refused():
+    cfg, T = gqa(2), 4
+    kv = make_cache(cfg, 60, 16, seed=1)
+    both = randn((4, T, cfg.num_q_heads, cfg.head_dim_qk), 2)
+    q, lens, mask = both[:2], torch.tensor([50, 3], dtype=torch.int64, device=DEV), tree_mask(random_tree(2, T, 1)).to(DEV)
+    for out in (q, both[1:3]):
+        with pytest.raises(HsError):
+            kv.tree_attn(q, lens, mask, out=out)
+    assert torch.equal(kv.tree_attn(q, lens, mask, out=both[2:]), kv.tree_attn(q, lens, mask))  # right behind them

@@ -11,7 +11,15 @@ from test_spec_host import append, lib, paged, shape, tree  # noqa: F401 (lib: a
 def test_a_scale_that_overflows_in_base_two(lib, scale):  # noqa: F811
     """Scores are taken times scale * log2(e): where that is infinite, a score of 0 would be NaN."""
     c, kv = shape(), paged()
-    assert lib.hs_tree_attn(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(tree(scale=scale)), None) == _lib.HS_ERR_ARG
+    a = tree(scale=scale, d_out=1 << 40)
+    assert lib.hs_tree_attn(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(a), None) == _lib.HS_ERR_ARG
+
+
+@pytest.mark.parametrize("off", [0, 16, -16, 2 * 2 * 4 * 32 * 128 - 16, -(2 * 2 * 4 * 32 * 128 - 16)])
+def test_an_output_over_the_queries(lib, off):  # noqa: F811
+    """Rows are written while other rows' queries are still read: in place is refused."""
+    c, kv, q = shape(), paged(), 1 << 40
+    assert lib.hs_tree_attn(ctypes.byref(c), ctypes.byref(kv), ctypes.byref(tree(d_q=q, d_out=q + off)), None) == _lib.HS_ERR_ARG
 
 
 @pytest.mark.parametrize("change", [dict(q_out_token_stride=8192), dict(q_token_stride=8192), dict(q_head_stride=0),
