@@ -17,6 +17,8 @@ POLICY_LRU, POLICY_FIFO, POLICY_RANDOM, POLICY_SWAP_VANILLA = 0, 1, 2, 3
 LAYOUT_MLA, LAYOUT_GQA = 0, 1
 DEVERR_RANGE, DEVERR_DUP, DEVERR_CLOCK, DEVERR_APPEND, DEVERR_LOC, DEVERR_TIMEOUT = 1, 2, 4, 8, 16, 32
 DEVERR_PAGE, DEVERR_SLOTS = 64, 128
+WEIGHT_BF16, WEIGHT_FP32 = 0, 1
+MAX_AXES = 4
 STALL_ATTN, STALL_RESOLVE, STALL_FETCH, STALL_TREE = 1, 2, 4, 8  # hs_debug_stall_next (test hook for the bounded waits)
 
 # every entry point include/hisparse.h declares
@@ -25,7 +27,8 @@ EXPORTS = ("hs_record_bytes", "hs_pool_create", "hs_pool_destroy", "hs_pool_rese
            "hs_read_buffer", "hs_read_history", "hs_sparse_attn_noalloc", "hs_append_resolve",
            "hs_resolve_range", "hs_sparse_attn_range", "hs_reserve", "hs_release", "hs_host_usage",
            "hs_device_usage", "hs_debug_stall_next", "hs_rope_turns", "hs_append_rotated",
-           "hs_tree_attn_workspace", "hs_tree_attn", "hs_pool_tree_attn", "hs_keep_path")
+           "hs_tree_attn_workspace", "hs_tree_attn", "hs_pool_tree_attn", "hs_keep_path",
+           "hs_append_normed", "hs_evict_workspace", "hs_evict")
 
 
 class hs_config(ctypes.Structure):
@@ -104,6 +107,37 @@ class hs_append_args(ctypes.Structure):
     ]
 
 
+class hs_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("d_k_weight", ctypes.c_void_p),
+        ("k_weight_head_stride", ctypes.c_int64),
+        ("d_q_weight", ctypes.c_void_p),
+        ("q_weight_head_stride", ctypes.c_int64),
+        ("k_weight_type", ctypes.c_int32),
+        ("q_weight_type", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("axes", ctypes.c_int32),
+        ("d_axis", ctypes.c_void_p),
+    ]
+
+
+class hs_evict_args(ctypes.Structure):
+    _fields_ = [
+        ("d_len", ctypes.c_void_p),
+        ("d_weights", ctypes.c_void_p),
+        ("d_weights_out", ctypes.c_void_p),
+        ("d_len_out", ctypes.c_void_p),
+        ("d_first", ctypes.c_void_p),
+        ("capacity", ctypes.c_int64),
+        ("lists", ctypes.c_int32),
+        ("keep", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("recent", ctypes.c_int32),
+        ("d_workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class hs_tree_args(ctypes.Structure):
     _fields_ = [
         ("d_q", ctypes.c_void_p),
@@ -120,10 +154,13 @@ class hs_tree_args(ctypes.Structure):
     ]
 
 
-# the same two as bytes, for the calls of every step: packing them takes a fraction of filling a ctypes structure
+# the same as bytes, for the calls of every step: packing them takes a fraction of filling a ctypes structure
 pack_append = struct.Struct("iPPPPqqPqqPiiiPqqPqqi0P")
 pack_tree = struct.Struct("PPPiPPifPPq")
+pack_norm = struct.Struct("PqPqiifiP")
+pack_evict = struct.Struct("PPPPPqiiiiPq")
 assert pack_append.size == ctypes.sizeof(hs_append_args) and pack_tree.size == ctypes.sizeof(hs_tree_args)
+assert pack_norm.size == ctypes.sizeof(hs_norm_args) and pack_evict.size == ctypes.sizeof(hs_evict_args)
 
 
 _lock = threading.Lock()
@@ -176,6 +213,9 @@ def load(build_if_missing: bool = False):
             "hs_tree_attn": (I, [P, P, P, P]),
             "hs_pool_tree_attn": (I, [P, I, P, P, P]),
             "hs_keep_path": (I, [P, P, P, P, I, P, P]),
+            "hs_append_normed": (I, [P, P, P, P, P]),
+            "hs_evict_workspace": (I64, [P, I, I]),
+            "hs_evict": (I, [P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

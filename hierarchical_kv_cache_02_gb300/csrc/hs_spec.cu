@@ -7,7 +7,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "hs_paged.cuh"
+#include "hs_append.cuh"
 
 namespace {
 
@@ -30,12 +30,6 @@ constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 4;   // tokens of a CTA at most
 constexpr int kAppFlight = 2;   // units a thread loads before it stores
 
-// i / d by a multiplication with ceil(2^32 / d): exact while i * d < 2^32
-struct Div {
-  uint32_t d, m;
-  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1u ? i : __umulhi(i, m); }
-};
-
 struct AppendArgs {
   PagedRows kv;
   const int32_t* cu;
@@ -51,49 +45,6 @@ struct AppendArgs {
   Div all, kh, vh, qh, angles;                     // units of a token, of a head of each kind; pairs
 };
 
-struct Vec8 {
-  uint32_t w[4];
-};
-__device__ __forceinline__ Vec8 ld8(const uint16_t* p) {
-  const uint4 u = *(const uint4*)p;
-  return Vec8{{u.x, u.y, u.z, u.w}};
-}
-__device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
-  *(uint4*)p = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-}
-__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *(const uint32_t*)&v;
-}
-
-// four neighbouring pairs (cs: 16-byte aligned, as a multiple of four pairs)
-__device__ __forceinline__ void turn(Vec8& v, const float2* cs) {
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const float4 c = *(const float4*)(cs + i);
-    const float p0 = lo(v.w[i]), r0 = hi(v.w[i]), p1 = lo(v.w[i + 1]), r1 = hi(v.w[i + 1]);
-    v.w[i] = pack(p0 * c.x - r0 * c.y, r0 * c.x + p0 * c.y);
-    v.w[i + 1] = pack(p1 * c.z - r1 * c.w, r1 * c.z + p1 * c.w);
-  }
-}
-
-// Units of one head, two vectors of 8 values each.  Half form: unit u < half / 8 turns values 8u.. with their
-// partners half further on; the rest of the head, before and behind the rotary values, is copied, two vectors a
-// unit.  Interleaved: unit u holds values 16u.., each vector turned when it is a rotary one.
-int head_units(int dim, int half, int interleaved) {
-  return interleaved ? (dim + 15) / 16 : half / 8 + (dim - 2 * half + 15) / 16;
-}
-
-// One unit: where it reads and writes, and how it turns.
-struct Unit {
-  const uint16_t* src;  // null: nothing to do
-  uint16_t* dst;
-  int second;           // values to the second vector, 0: none
-  int cs, cs2;          // first pair of each vector in the table of sines and cosines, -1: copied
-};
-
 __global__ void __launch_bounds__(kAppThreads, 6) k_append_rotated(AppendArgs a) {
   extern __shared__ __align__(16) float2 s_cs[];   // [tokens][half] cosine and sine of each pair
   __shared__ int64_t s_row[kAppTokens], s_pos[kAppTokens];  // record row (-1: not stored), angle position
@@ -104,15 +55,7 @@ __global__ void __launch_bounds__(kAppThreads, 6) k_append_rotated(AppendArgs a)
   for (int w = tid >> 5; w < nt; w += kAppThreads / 32) {  // a warp a token
     const int lane = tid & 31, t = t0 + w;
     const int64_t given = a.rope_pos != nullptr ? a.rope_pos[t] : 0;
-    // the last request whose first token is not behind t: 32 places of the rest are looked at at a time
-    int x = 0, n = a.R;
-    while (n > 1) {
-      const int step = (n + 31) >> 5, at = lane * step;
-      const bool before = at < n && a.cu[x + at] <= t;
-      const int c = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0);
-      x += c * step;
-      n = min(step, n - c * step);
-    }
+    const int x = request_of_token(a.cu, a.R, t, lane);
     if (lane == 0) {
       const int c0 = a.cu[x], c1 = a.cu[x + 1];
       const int64_t st = a.start[x];
@@ -276,10 +219,6 @@ __global__ void __launch_bounds__(kKeepThreads) k_keep_path(PagedRows kv, const 
 // 2^256 / (2 pi), lowest word first
 constexpr uint64_t kOverTwoPi[4] = {0x7f9458eaf7aef158ull, 0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
 
-constexpr int kMinCtas = 456;
-
-bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
-
 }  // namespace
 
 extern "C" int hs_rope_turns(const double* h_inv_freq, int n, uint64_t* h_turns) {
@@ -312,36 +251,11 @@ extern "C" int hs_rope_turns(const double* h_inv_freq, int n, uint64_t* h_turns)
 
 extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, const hs_append_args* args,
                                  void* stream) {
-  int rc = hs_check_shape(cfg);
-  if (rc == HS_OK) rc = hs_check_paged(cfg, kv);
+  const int rc = check_append(cfg, kv, args);
   if (rc != HS_OK) return rc;
-  if (args == nullptr || args->num_tokens < 0) return HS_ERR_ARG;
   const hs_append_args& g = *args;
   const bool mla = cfg->layout == HS_LAYOUT_MLA;
   if (g.num_tokens == 0) return HS_OK;
-  if (g.d_cu == nullptr || g.d_start == nullptr || !hs_aligned(g.d_cu, 4) || !hs_aligned(g.d_start, 8) ||
-      !hs_aligned(g.d_rope_pos, 8))
-    return HS_ERR_ARG;
-  if (g.d_k == nullptr || (g.d_v == nullptr) != mla) return HS_ERR_ARG;
-  if (!hs_aligned(g.d_k, 16) || !stride_ok(g.k_token_stride) || !stride_ok(g.k_head_stride)) return HS_ERR_ARG;
-  if (!mla && (!hs_aligned(g.d_v, 16) || !stride_ok(g.v_token_stride) || !stride_ok(g.v_head_stride))) return HS_ERR_ARG;
-  if (g.rotary_dim < 0 || g.rotary_dim % 16 != 0 || g.rotary_offset < 0 || g.rotary_offset % 8 != 0 ||
-      g.rotary_offset > cfg->head_dim_qk - g.rotary_dim || (g.interleaved != 0 && g.interleaved != 1))
-    return HS_ERR_ARG;
-  if (g.rotary_dim > 0 && (g.d_turns == nullptr || !hs_aligned(g.d_turns, 8))) return HS_ERR_ARG;
-  if (g.d_q != nullptr) {
-    if (g.d_q_out == nullptr || !hs_aligned(g.d_q, 16) || !hs_aligned(g.d_q_out, 16) || !stride_ok(g.q_token_stride) ||
-        !stride_ok(g.q_head_stride) || !stride_ok(g.q_out_token_stride) || !stride_ok(g.q_out_head_stride))
-      return HS_ERR_ARG;
-    // no two queries may be written over each other: one stride has to step over all that the other spans
-    const int64_t n = g.num_tokens, hq = cfg->num_q_heads, ts = g.q_out_token_stride, hs = g.q_out_head_stride, d = g.q_dim;
-    const bool by_token = (hq == 1 || hs >= d) && (n == 1 || ts >= (hq - 1) * hs + d);
-    const bool by_head = (n == 1 || ts >= d) && (hq == 1 || hs >= (n - 1) * ts + d);
-    if (!by_token && !by_head) return HS_ERR_ARG;
-    // in place, every thread reads what it writes only where both have the same strides
-    if (g.d_q == g.d_q_out && ((n > 1 && g.q_token_stride != ts) || (hq > 1 && g.q_head_stride != hs))) return HS_ERR_ARG;
-    if (g.q_dim != cfg->head_dim_qk && (g.q_dim != g.rotary_dim || g.q_dim == 0)) return HS_ERR_ARG;
-  }
   HsOnDevice on(kv->cuda_device);
   if (!on.ok) return HS_ERR_CUDA;
   AppendArgs a{};
@@ -376,12 +290,11 @@ extern "C" int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, co
   a.kn = cfg->num_kv_heads * ku;
   a.vn = cfg->num_kv_heads * vu;
   const int units = a.kn + a.vn + cfg->num_q_heads * qu;
-  auto div = [](int d) { return Div{(uint32_t)(d > 0 ? d : 1), d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u}; };
-  a.all = div(units);
-  a.kh = div(ku);
-  a.vh = div(vu);
-  a.qh = div(qu);
-  a.angles = div(a.half);
+  a.all = div_by(units);
+  a.kh = div_by(ku);
+  a.vh = div_by(vu);
+  a.qh = div_by(qu);
+  a.angles = div_by(a.half);
   // kAppTokens tokens a CTA while that leaves three CTAs an SM, fewer else; then every token's units are shared by
   // several CTAs until the GPU is filled or a share is below a quarter of one round (16 tokens: 3.2 us; a CTA a token
   // 6.2 us).  A CTA of several tokens has fewer than 2^16 units (see Div; of one token nothing is divided by them).

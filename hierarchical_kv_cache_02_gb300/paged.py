@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from .pool import HsConfig, _check, _dev_tensor, _fast_ptr, _fast_stream, _tree_args
+from .pool import HsConfig, HsError, _check, _dev_tensor, _fast_ptr, _fast_stream, _tree_args
 
 
 class RopeTable:
@@ -24,10 +24,11 @@ class RopeTable:
 
     rotary_dim: rotated values of a head, a multiple of 16.  inv_freq: rotary_dim / 2 angles per position
     (radians); default theta ** (-2 j / rotary_dim).  interleaved: value 2j turns with 2j + 1, else j with
-    j + rotary_dim / 2."""
+    j + rotary_dim / 2.  axes: for positions with several axes (time, row and column of an image, say), the axis of each
+    of the rotary_dim / 2 pairs, numbers from 0 on, at most 4 of them; tokens then have a position for each axis."""
 
     def __init__(self, rotary_dim: int, theta: float = 10000.0, inv_freq=None, interleaved: bool = False,
-                 device: int = 0):
+                 device: int = 0, axes=None):
         import numpy as np
         import torch
 
@@ -42,7 +43,15 @@ class RopeTable:
         turns = np.empty((half,), dtype=np.uint64)
         _check("hs_rope_turns", _lib.load().hs_rope_turns(f.ctypes.data, half, turns.ctypes.data))
         self.rotary_dim, self.interleaved, self.device = int(rotary_dim), bool(interleaved), int(device)
+        self.axes, self.axis = 1, None
+        if axes is not None:
+            a = np.asarray(axes)
+            if a.shape != (half,) or a.dtype.kind not in "iu" or a.min() < 0 or a.max() >= _lib.MAX_AXES:
+                raise ValueError(f"axes must hold {half} numbers from 0 to {_lib.MAX_AXES - 1}")
+            self.axes = int(a.max()) + 1
         self.turns = torch.from_numpy(turns.view(np.int64)).to(f"cuda:{self.device}")
+        if self.axes > 1:
+            self.axis = torch.from_numpy(a.astype(np.uint8)).to(f"cuda:{self.device}")
 
 
 def tree_mask(parents):
@@ -97,6 +106,20 @@ def _strided(t, n, heads, dim, name, device, written=False):
     return t.data_ptr(), ts, hs
 
 
+def _weights(t, heads, dim, name, device):
+    """Pointer, head stride and type of a norm's weights [dim] or [heads][dim], bf16 or float32."""
+    import torch
+
+    if t is None:
+        return 0, 0, 0
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a torch.Tensor of bfloat16 or float32")
+    p = _fast_ptr(t, t.dtype, (dim,) if t.dim() == 1 else (heads, dim), name, device)
+    if p % 16:
+        raise ValueError(f"{name} must be aligned to 16 bytes")
+    return p, dim if t.dim() == 2 else 0, _lib.WEIGHT_FP32 if t.dtype is torch.float32 else _lib.WEIGHT_BF16
+
+
 class PagedKV:
     """pages bf16 [num_pages][page_tokens][record_elems] on a GPU; table int32 [R][max_pages]: position p
     of request r is row p % page_tokens of page table[r][p // page_tokens]; without a table request r owns
@@ -132,7 +155,7 @@ class PagedKV:
         self._c_ref, self._kv_ref = ctypes.byref(self._c), ctypes.byref(self._kv)
 
     def append(self, k, v, cu, start, rope: RopeTable | None = None, rope_pos=None, q=None, q_out=None,
-               rotary_offset: int | None = None, stream=None):
+               rotary_offset: int | None = None, stream=None, q_weight=None, k_weight=None, eps: float = 1e-6):
         """Store the records of N new tokens, their keys (and queries) rotated by their positions.
 
         k bf16 [N][Hkv][Dqk], v bf16 [N][Hkv][Dv] (shared latent: k [N][Dqk], v None): views with any
@@ -140,7 +163,11 @@ class PagedKV:
         r's, stored from position start[r] (int64 [R]) on; tokens outside cu are padding.  rope_pos int64
         [N]: the positions whose angles they get, when not those they are stored at.  q bf16
         [N][Hq][Dqk] or [N][Hq][rotary_dim] -> q_out (may be q).  rotary_offset: first rotated value of a
-        key; default 0, shared latent: the tail.  Returns q_out."""
+        key; default 0, shared latent: the tail.  Returns q_out.
+
+        With weights, heads are normed before they are rotated: x_i w_i / sqrt(mean(x^2) + eps).  q_weight, k_weight
+        bf16 or float32 [Dqk], or [Hq][Dqk] and [Hkv][Dqk] for weights of each head; shared latent: k_weight [Dv], over the
+        latent's values, no q_weight.  A table with axes takes rope_pos int64 [N][axes]."""
         import torch
 
         c = self.cfg
@@ -155,7 +182,10 @@ class PagedKV:
             vp, vt, vh = _strided(v, N, c.num_kv_heads, c.head_dim_v, "v", self.device)
         cup = _fast_ptr(cu, torch.int32, self._r1, "cu", self.device)
         sp = _fast_ptr(start, torch.int64, self._r, "start", self.device)
-        rp = 0 if rope_pos is None else _fast_ptr(rope_pos, torch.int64, (N,), "rope_pos", self.device)
+        several = rope is not None and rope.axes > 1
+        if several and rope_pos is None:
+            raise ValueError("a rope with several axes needs rope_pos")
+        rp = 0 if rope_pos is None else _fast_ptr(rope_pos, torch.int64, (N, rope.axes) if several else (N,), "rope_pos", self.device)
         turns, rd, il = 0, 0, 0
         if rope is not None:
             if rope.device != self.device:
@@ -177,10 +207,68 @@ class PagedKV:
             op, ot, oh = _strided(q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
         elif q_out is not None:
             raise ValueError("q_out without q")
+        normed = several or q_weight is not None or k_weight is not None
+        if normed:
+            b = self._norm_args(c, mla, rope, q, qd, q_weight, k_weight, eps)
         a = _lib.pack_append.pack(N, cup, sp, rp, kp, kt, kh, vp, vt, vh, turns, rd, int(rotary_offset), il, qp, qt, qh, op, ot, oh, qd)
-        _check("hs_append_rotated", self.lib.hs_append_rotated(self._c_ref, self._kv_ref, a,
-                                                               _fast_stream(torch, stream, self.device)))
+        if normed:
+            _check("hs_append_normed", self.lib.hs_append_normed(self._c_ref, self._kv_ref, a, b, _fast_stream(torch, stream, self.device)))
+        else:
+            _check("hs_append_rotated", self.lib.hs_append_rotated(self._c_ref, self._kv_ref, a,
+                                                                   _fast_stream(torch, stream, self.device)))
         return q_out
+
+    def _norm_args(self, c, mla, rope, q, qd, q_weight, k_weight, eps):
+        """What hs_append_normed takes beside the arguments of hs_append_rotated, packed."""
+        dim = c.head_dim_v if mla else c.head_dim_qk
+        kw, ks, kt = _weights(k_weight, c.num_kv_heads, dim, "k_weight", self.device)
+        if q_weight is not None and (mla or q is None or qd != c.head_dim_qk):
+            raise ValueError("q_weight needs whole query heads (and no shared latent)")
+        qw, qs, qt = _weights(q_weight, c.num_q_heads, dim, "q_weight", self.device)
+        if (qw or kw) and not (0.0 < eps < float("inf")):
+            raise ValueError("eps must be a positive number")
+        axis = rope.axis if rope is not None else None
+        return _lib.pack_norm.pack(kw, ks, qw, qs, kt, qt, float(eps), 1 if axis is None else rope.axes,
+                                   0 if axis is None else axis.data_ptr())
+
+    def evict(self, lens, weights, keep: int, first=0, recent: int = 0, weights_out=None, lens_out=None, stream=None):
+        """Cut every request of more than `keep` entries down to that many: its first `first` and last `recent` entries and, of
+        the others, those with the largest weights (of equal ones the earlier), in their order, become the entries [0, keep),
+        records and weights alike.
+
+        lens int64 [R]; weights float32 [R][lists][C], what prefix_attn sums up: lists 1 (a request's entries go together) or
+        Hkv (each KV head keeps its own).  first: a number, or int64 [R] on the device (a shared prefix stays whole:
+        pages of several requests must lie within it).  weights_out (default: weights, in place): the weights of what stays, 0
+        behind it up to lens.  Returns lens_out, min(lens, keep) (default: a new tensor; may be lens).  Keys keep the
+        rotation they were stored with: append the next tokens with rope_pos."""
+        import torch
+
+        c = self.cfg
+        if not isinstance(weights, torch.Tensor) or weights.dim() != 3 or weights.shape[1] not in (1, c.num_kv_heads):
+            raise ValueError("weights must be a tensor [R][1 or Hkv][C]")
+        shape = (c.num_requests, int(weights.shape[1]), int(weights.shape[2]))
+        lp = _fast_ptr(lens, torch.int64, self._r, "lens", self.device)
+        wp = _fast_ptr(weights, torch.float32, shape, "weights", self.device)
+        op = wp if weights_out is None else _fast_ptr(weights_out, torch.float32, shape, "weights_out", self.device)
+        keep, recent = int(keep), int(recent)
+        fp, f = 0, 0
+        if isinstance(first, torch.Tensor):
+            fp = _fast_ptr(first, torch.int64, self._r, "first", self.device)
+        else:
+            f = int(first)
+        if not 1 <= keep <= 2**31 - 65536 or recent < 0 or f < 0 or f + recent > keep:
+            raise ValueError("keep must be positive, first and recent together at most keep")
+        need = int(self.lib.hs_evict_workspace(self._c_ref, shape[1], keep))
+        if need < 0:
+            raise HsError("hs_evict_workspace", need)
+        with torch.cuda.stream(stream):  # None: the current one
+            ws = torch.empty((need,), dtype=torch.uint8, device=lens.device)
+            if lens_out is None:
+                lens_out = torch.empty(self._r, dtype=torch.int64, device=lens.device)
+        np_ = _fast_ptr(lens_out, torch.int64, self._r, "lens_out", self.device)
+        a = _lib.pack_evict.pack(lp, wp, op, np_, fp, shape[2], shape[1], keep, f, recent, ws.data_ptr(), need)
+        _check("hs_evict", self.lib.hs_evict(self._c_ref, self._kv_ref, a, _fast_stream(torch, stream, self.device)))
+        return lens_out
 
     def tree_attn(self, q, lens, mask, locs=None, nodes=None, out=None, scale=None, stream=None):
         """Attention of T drafted tokens a request, stored at positions [lens[r], lens[r] + T), over the

@@ -438,6 +438,33 @@ typedef struct {
  */
 int hs_append_rotated(const hs_config* cfg, const hs_paged_kv* kv, const hs_append_args* args, void* stream);
 
+#define HS_MAX_AXES 4
+enum { HS_WEIGHT_BF16 = 0, HS_WEIGHT_FP32 = 1 };
+
+typedef struct {
+  const void* d_k_weight;     /* weights of the keys' norm, 16-byte aligned, or NULL: keys are not normed.  GQA: head_dim_qk
+                                 of them, over a whole head; MLA: head_dim_v, over the latent's first head_dim_v
+                                 values (its V; the rotary tail is not normed) */
+  int64_t k_weight_head_stride; /* in values, a multiple of 8: KV head h's weights at h times it; 0: all heads' the same */
+  const void* d_q_weight;     /* likewise for the queries: head_dim_qk of them; NULL with MLA, without d_q and with
+                                 q_dim other than head_dim_qk */
+  int64_t q_weight_head_stride;
+  int32_t k_weight_type, q_weight_type; /* HS_WEIGHT_* */
+  float eps;                  /* > 0, finite; not looked at without weights */
+  int32_t axes;               /* axes of positions, 1 .. HS_MAX_AXES.  Above 1 d_rope_pos is int64 [N][axes] and not NULL */
+  const uint8_t* d_axis;      /* [rotary_dim / 2] the axis of each rotary pair, below axes; ignored with one axis */
+} hs_norm_args;
+
+/*
+ * hs_append_rotated with the norms of keys and queries on the way, and rotations by several axes of positions (rows and
+ * columns of images, say): a head x of d values becomes x_i w_i / sqrt(sum_j x_j^2 / d + eps), then its rotary pairs turn, pair j
+ * by position d_rope_pos[t][d_axis[j]].  Products, sums and the norm are 32-bit (squares above 3e38 overflow: the head becomes
+ * zeros), results are rounded once to bf16.  Values are stored as they are.  Otherwise, and in its errors, as hs_append_rotated;
+ * HS_ERR_ARG for bad hs_norm_args as well.  The argument checks know no length of the weights.
+ */
+int hs_append_normed(const hs_config* cfg, const hs_paged_kv* kv, const hs_append_args* args, const hs_norm_args* norm,
+                     void* stream);
+
 #define HS_MAX_TREE_NODES 256
 
 typedef struct {
@@ -507,6 +534,36 @@ int hs_pool_tree_attn(hs_pool* pool, int layer, const hs_tree_args* args, const 
  */
 int hs_keep_path(const hs_config* cfg, const hs_paged_kv* kv, const int64_t* d_len, const int32_t* d_path, int path_len,
                  const int32_t* d_count, void* stream);
+
+typedef struct {
+  const int64_t* d_len;     /* [num_requests] entries of each request */
+  const float* d_weights;   /* [num_requests][lists][capacity] accumulated weights of the entries */
+  float* d_weights_out;     /* the same of those that stay; d_weights itself, or apart from it */
+  int64_t* d_len_out;       /* [num_requests] min(len, keep); d_len itself, or apart from it */
+  const int64_t* d_first;   /* [num_requests] first entries that stay whatever their weight, or NULL: `first` for all */
+  int64_t capacity;         /* entries of a list, at most 2^31 - 65536 */
+  int32_t lists;            /* 1: a request's entries go together; num_kv_heads: each KV head has its own choice */
+  int32_t keep;             /* entries that a request keeps at most, 1 .. 2^31 - 65536 */
+  int32_t first, recent;    /* >= 0; first + recent <= keep: the first and last entries that stay */
+  void* d_workspace;        /* hs_evict_workspace bytes, 16-byte aligned, used by this call alone until it is done */
+  int64_t workspace_bytes;
+} hs_evict_args;
+
+/* Bytes of workspace; negative: an hs_status. */
+int64_t hs_evict_workspace(const hs_config* cfg, int lists, int keep);
+
+/*
+ * Evict by weight: of a request's len > keep entries the first `first`, the last `recent` and those of the others with
+ * the largest weights stay, keep in all; of equal weights the earlier entry stays; NaN counts as more than any number.
+ * They keep their order and become the entries [0, keep), records (with lists = num_kv_heads: each head's share of them) and
+ * weights alike; the weights of [keep, len) become 0, those behind len stay as they were.  A request with len <= keep stays as
+ * it is (its weights are copied when the output is another array).  A len outside [0, capacity] or the request's pages, or a
+ * d_first outside [0, keep - recent], sets HS_DEVERR_LOC and leaves the request and its weights alone (d_len_out is its d_len).
+ * Bad table entries set HS_DEVERR_PAGE and their moves are left out.  Records keep the rotation of the positions that they had.
+ * Pages that two requests share must lie within the first entries that stay of all of them.  Equal calls give equal bits.
+ * CAPTURABLE.  Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH, HS_ERR_CUDA.
+ */
+int hs_evict(const hs_config* cfg, const hs_paged_kv* kv, const hs_evict_args* args, void* stream);
 
 /* Host memory of the pool: pages mapped in some table, pages on the free list, pinned bytes held. */
 int hs_host_usage(hs_pool* pool, int64_t* pages_in_use, int64_t* pages_free, int64_t* bytes_pinned);
