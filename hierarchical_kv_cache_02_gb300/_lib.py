@@ -28,7 +28,7 @@ EXPORTS = ("hs_record_bytes", "hs_pool_create", "hs_pool_destroy", "hs_pool_rese
            "hs_resolve_range", "hs_sparse_attn_range", "hs_reserve", "hs_release", "hs_host_usage",
            "hs_device_usage", "hs_debug_stall_next", "hs_rope_turns", "hs_append_rotated",
            "hs_tree_attn_workspace", "hs_tree_attn", "hs_pool_tree_attn", "hs_keep_path",
-           "hs_append_normed", "hs_evict_workspace", "hs_evict")
+           "hs_append_normed", "hs_evict_workspace", "hs_evict", "hs_prefix_attn_workspace", "hs_prefix_attn")
 
 
 class hs_config(ctypes.Structure):
@@ -138,6 +138,24 @@ class hs_evict_args(ctypes.Structure):
     ]
 
 
+class hs_prefix_args(ctypes.Structure):
+    _fields_ = [
+        ("d_q", ctypes.c_void_p),
+        ("d_len", ctypes.c_void_p),
+        ("d_groups", ctypes.c_void_p),
+        ("d_prefix", ctypes.c_void_p),
+        ("groups", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("d_weights", ctypes.c_void_p),
+        ("capacity", ctypes.c_int64),
+        ("lists", ctypes.c_int32),
+        ("decay", ctypes.c_float),
+        ("d_out", ctypes.c_void_p),
+        ("d_workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class hs_tree_args(ctypes.Structure):
     _fields_ = [
         ("d_q", ctypes.c_void_p),
@@ -159,8 +177,10 @@ pack_append = struct.Struct("iPPPPqqPqqPiiiPqqPqqi0P")
 pack_tree = struct.Struct("PPPiPPifPPq")
 pack_norm = struct.Struct("PqPqiifiP")
 pack_evict = struct.Struct("PPPPPqiiiiPq")
+pack_prefix = struct.Struct("PPPPifPqifPPq")
 assert pack_append.size == ctypes.sizeof(hs_append_args) and pack_tree.size == ctypes.sizeof(hs_tree_args)
 assert pack_norm.size == ctypes.sizeof(hs_norm_args) and pack_evict.size == ctypes.sizeof(hs_evict_args)
+assert pack_prefix.size == ctypes.sizeof(hs_prefix_args)
 
 
 _lock = threading.Lock()
@@ -216,6 +236,8 @@ def load(build_if_missing: bool = False):
             "hs_append_normed": (I, [P, P, P, P, P]),
             "hs_evict_workspace": (I64, [P, I, I]),
             "hs_evict": (I, [P, P, P, P]),
+            "hs_prefix_attn_workspace": (I64, [P, P, I, I]),
+            "hs_prefix_attn": (I, [P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -150,6 +150,8 @@ class PagedKV:
         self.pages, self.table = pages, table
         self._err = torch.zeros((1,), dtype=torch.int32, device=pages.device)
         self._r, self._r1 = (R,), (R + 1,)
+        self._q_shape, self._o_shape = (R, cfg.num_q_heads, cfg.head_dim_qk), (R, cfg.num_q_heads, cfg.head_dim_v)
+        self._prefix_sizes = {}
         self._kv = _lib.hs_paged_kv(p, t, int(pages.shape[0]), int(pages.shape[1]), max_pages, self._err.data_ptr(),
                                     self.device)
         self._c_ref, self._kv_ref = ctypes.byref(self._c), ctypes.byref(self._kv)
@@ -288,6 +290,55 @@ class PagedKV:
         args, out, _ws = _tree_args(torch, self.lib, self._c, c, self.device, self._tree_sizes, q, lp, kp, k, mask, nodes, out, scale,
                                     stream)
         _check("hs_tree_attn", self.lib.hs_tree_attn(self._c_ref, self._kv_ref, args, _fast_stream(torch, stream, self.device)))
+        return out
+
+    def prefix_attn(self, q, lens, groups=None, prefix=None, weights=None, decay: float = 1.0, out=None, scale=None, stream=None):
+        """Attention of one new token a request over the positions [0, lens[r]), those that requests share read once.
+
+        q bf16 [R][Hq][Dqk]; lens int64 [R], the new tokens' own positions among them.  groups int32 [G + 1]
+        ascending and prefix int64 [G]: the requests [groups[g], groups[g + 1]) share the positions [0, prefix[g]), which
+        are read through the table's row of the first of them; the other requests share none.  weights float32
+        [R][lists][C], lists 1 or Hkv: takes weights * decay + the softmax weights, summed over the list's query heads, of the
+        positions that a request does not share (what evict goes by).  Returns out, bf16 [R][Hq][Dv] (it may not overlap q)."""
+        import torch
+
+        c = self.cfg
+        bf16 = torch.bfloat16
+        qp = _fast_ptr(q, bf16, self._q_shape, "q", self.device)
+        lp = _fast_ptr(lens, torch.int64, self._r, "lens", self.device)
+        if (groups is None) != (prefix is None):
+            raise ValueError("groups and prefix go together")
+        G, gp, pp = 0, 0, 0
+        if groups is not None:
+            if not isinstance(prefix, torch.Tensor) or prefix.dim() != 1 or prefix.shape[0] > c.num_requests:
+                raise ValueError("prefix must be a tensor [G] of at most R numbers")
+            G = prefix.shape[0]
+            gp = _fast_ptr(groups, torch.int32, (G + 1,), "groups", self.device)
+            pp = _fast_ptr(prefix, torch.int64, (G,), "prefix", self.device)
+        wp, cap, lists = 0, 0, 0
+        if weights is not None:
+            if not isinstance(weights, torch.Tensor) or weights.dim() != 3 or weights.shape[1] not in (1, c.num_kv_heads):
+                raise ValueError("weights must be a tensor [R][1 or Hkv][C]")
+            lists, cap = weights.shape[1], weights.shape[2]
+            wp = _fast_ptr(weights, torch.float32, (self._r[0], lists, cap), "weights", self.device)
+            if not abs(decay) < float("inf"):
+                raise ValueError("decay must be a finite number")
+        need = self._prefix_sizes.get((G, wp != 0))
+        if need is None:
+            need = int(self.lib.hs_prefix_attn_workspace(self._c_ref, self._kv_ref, G, int(wp != 0)))
+            if need < 0:
+                raise HsError("hs_prefix_attn_workspace", need)
+            self._prefix_sizes[G, wp != 0] = need
+        s = c.default_scale if scale is None else float(scale)
+        if not abs(s) <= 2.35e38:  # times log2(e) it has to be a finite 32-bit number
+            raise ValueError("scale must be a number of magnitude 2.35e38 at most")
+        with torch.cuda.stream(stream):  # None: the current one
+            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            if out is None:
+                out = torch.empty(self._o_shape, dtype=bf16, device=q.device)
+        op = _fast_ptr(out, bf16, self._o_shape, "out", self.device)
+        a = _lib.pack_prefix.pack(qp, lp, gp, pp, G, s, wp, cap, lists, float(decay), op, ws.data_ptr(), need)
+        _check("hs_prefix_attn", self.lib.hs_prefix_attn(self._c_ref, self._kv_ref, a, _fast_stream(torch, stream, self.device)))
         return out
 
     def keep_path(self, lens, path, count, stream=None):

@@ -536,6 +536,50 @@ int hs_keep_path(const hs_config* cfg, const hs_paged_kv* kv, const int64_t* d_l
                  const int32_t* d_count, void* stream);
 
 typedef struct {
+  const void* d_q;          /* bf16 [num_requests][num_q_heads][head_dim_qk], 16-byte aligned */
+  const int64_t* d_len;     /* [num_requests] positions a request sees, from 0 on (its new token's among them) */
+  const int32_t* d_groups;  /* [groups + 1] ascending: requests [groups[g], groups[g+1]) share positions; those outside
+                               [groups[0], groups[groups]) share none.  NULL with groups = 0 */
+  const int64_t* d_prefix;  /* [groups] positions that a group shares, any number */
+  int32_t groups;           /* 0 .. num_requests */
+  float scale;              /* magnitude below 2.35e38: scale * log2(e) is a finite 32-bit number */
+  float* d_weights;         /* [num_requests][lists][capacity] accumulated weights, or NULL */
+  int64_t capacity;         /* with d_weights: entries of a list, 1 .. 2^31 - 65536 */
+  int32_t lists;            /* with d_weights: 1 (all query heads together) or num_kv_heads (each KV head's query heads) */
+  float decay;              /* with d_weights: finite; what was accumulated is multiplied by it first */
+  void* d_out;              /* bf16 [num_requests][num_q_heads][head_dim_v], 16-byte aligned; apart from d_q */
+  void* d_workspace;        /* hs_prefix_attn_workspace bytes, 16-byte aligned; used by this call alone until it is
+                               done: calls that may overlap need one each */
+  int64_t workspace_bytes;
+} hs_prefix_args;
+
+/* Bytes of workspace a call needs, whatever the lengths; with weights (not 0) 4 bytes for each request, query head and position
+ * of its pages among them.  Of kv only page_tokens, max_pages and cuda_device matter.  Negative: an hs_status. */
+int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged_kv* kv, int groups, int weights);
+
+/*
+ * Attention of one new token a request (a decode step) over a paged cache whose requests share prefixes:
+ *   out[r][h] = sum_p softmax_p(scale * <q[r][h], K(p)>) V(p) over the positions p < len[r].
+ * The positions below d_prefix[g] are read once for all requests of group g, through the page table's row of its first one (a
+ * group of one request reads them as its own); later ones through each request's own row.  With
+ * d_weights, for every position p of a request that it does not share
+ *   weights[r][list][p] = decay * weights[r][list][p] + the softmax weights of p, summed over the list's query heads,
+ * from 32-bit scores and sums; those of shared positions, and behind len, stay as they are.
+ * Heads of 64 or 128 (keys and values alike, at most 128 query heads a KV head) run on the tensor cores; any other shape runs on
+ * CUDA cores and reads a record once for every query head and request.
+ * len 0: zeros.  A len outside [0, the request's pages] or, unless 0, below its group's prefix sets HS_DEVERR_LOC and gives zeros
+ * and no weights, one above capacity sets it and leaves the weights behind out; bounds of a group outside [0, num_requests] or
+ * descending, and a prefix outside the pages, set it, and the group shares nothing.  Bad table entries set HS_DEVERR_PAGE:
+ * such positions are not seen.  What a request does not see has no influence on it.  What it sees counts however small its weight:
+ * an infinite or NaN value makes that dim of the output infinite or NaN, a NaN score the whole row.  Scores, softmax sums and
+ * accumulators are 32-bit; on the tensor cores the weights enter the value product as bf16; the output is rounded once to
+ * bf16.  The order of the sums depends on lengths and groups alone: equal calls give equal bits.  A bounded wait inside a kernel
+ * that gives up (about a second without progress) sets HS_DEVERR_TIMEOUT and leaves d_out and d_weights undefined.  CAPTURABLE.
+ * Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH (workspace too small), HS_ERR_CUDA.
+ */
+int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_prefix_args* args, void* stream);
+
+typedef struct {
   const int64_t* d_len;     /* [num_requests] entries of each request */
   const float* d_weights;   /* [num_requests][lists][capacity] accumulated weights of the entries */
   float* d_weights_out;     /* the same of those that stay; d_weights itself, or apart from it */

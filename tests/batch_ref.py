@@ -73,3 +73,42 @@ def same(a, b):
     """Equal bit for bit, NaN included."""
     kind = {2: torch.int16, 4: torch.int32, 8: torch.int64}[a.element_size()]
     return a.shape == b.shape and a.dtype == b.dtype and torch.equal(a.contiguous().view(kind), b.contiguous().view(kind))
+
+
+def attention(cfg, rows, q, scale, own, only=None):
+    """rows[r]: [n][record] of what request r sees, the last own[r] of them its own; q [R][Hq][Dqk]; only: the
+    (request, head) pairs to compute, the others get no bound.
+
+    Returns (out, bound) [R][Hq][Dv], as spec_ref.tree's in every term, and for each request the softmax weights of its own rows
+    [Hq][own] with their bounds: a score is off by (Dqk + 2) 2^-24 |scale| sum |q K|, 2^x by 2^-21 relative, the normaliser
+    by as much and n 2^-24 for its sum."""
+    R, Hq, Dqk = q.shape
+    Hkv, Dv = cfg.num_kv_heads, cfg.head_dim_v
+    out = torch.zeros((R, Hq, Dv), dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(out)
+    weights = [torch.zeros((2, Hq, n), dtype=torch.float64, device=q.device) for n in own]
+    for r in range(R):
+        x = rows[r].double()
+        if x.shape[0] == 0:
+            continue
+        for h in range(Hq):
+            if only is not None and (r, h) not in only:
+                bound[r, h] = math.inf
+                weights[r][1, h] = math.inf
+                continue
+            if cfg.layout == 0:
+                k, v = x[:, :Dqk], x[:, :Dv]
+            else:
+                g = h // (Hq // Hkv) * (Dqk + Dv)
+                k, v = x[:, g:g + Dqk], x[:, g + Dqk:g + Dqk + Dv]
+            qq = q[r, h].double()
+            p = torch.softmax(k @ qq * scale, dim=0)
+            out[r, h] = p @ v
+            off = (Dqk + 2) * U_FP32 * abs(scale) * float((k.abs() @ qq.abs()).max())
+            w = U_BF16 + off + 2.0**-21 + k.shape[0] * U_FP32
+            bound[r, h] = U_BF16 * out[r, h].abs() + 2 * w * (1 + w) * (p @ v.abs()) * (1 + U_BF16)
+            e = 2 * (off + 2.0**-21) + k.shape[0] * U_FP32
+            if own[r]:
+                weights[r][0, h] = p[-own[r]:]
+                weights[r][1, h] = p[-own[r]:] * e * (1 + e) + 2.0**-126  # the last: exponents below the normal numbers'
+    return out, bound, weights

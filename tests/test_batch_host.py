@@ -29,6 +29,13 @@ def evict(**change):
     return _lib.hs_evict_args(**base)
 
 
+def prefix(**change):
+    base = dict(d_q=OK_PTR, d_len=OK_PTR, d_groups=OK_PTR, d_prefix=OK_PTR, groups=2, scale=0.1, d_weights=OK_PTR, capacity=64, lists=8, decay=1.0,
+                d_out=OK_PTR << 8, d_workspace=OK_PTR, workspace_bytes=1 << 40)
+    base.update(change)
+    return _lib.hs_prefix_args(**base)
+
+
 def ref(x):
     return ctypes.byref(x)
 
@@ -39,6 +46,8 @@ def test_bad_shapes(lib, change):
     assert lib.hs_append_normed(ref(c), ref(kv), ref(append()), ref(norm()), None) == _lib.HS_ERR_CONFIG
     assert lib.hs_evict(ref(c), ref(kv), ref(evict()), None) == _lib.HS_ERR_CONFIG
     assert lib.hs_evict_workspace(ref(c), 1, 8) == _lib.HS_ERR_CONFIG
+    assert lib.hs_prefix_attn(ref(c), ref(kv), ref(prefix()), None) == _lib.HS_ERR_CONFIG
+    assert lib.hs_prefix_attn_workspace(ref(c), ref(kv), 1, 0) == _lib.HS_ERR_CONFIG
 
 
 @pytest.mark.parametrize("change", BAD_PAGES)
@@ -46,6 +55,26 @@ def test_bad_pages(lib, change):
     c, kv = shape(), paged(**change)
     assert lib.hs_append_normed(ref(c), ref(kv), ref(append()), ref(norm()), None) == _lib.HS_ERR_ARG
     assert lib.hs_evict(ref(c), ref(kv), ref(evict()), None) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn(ref(c), ref(kv), ref(prefix()), None) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn_workspace(ref(c), ref(kv), 1, 0) == _lib.HS_ERR_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(d_q=None), dict(d_q=OK_PTR + 8), dict(d_len=None), dict(d_len=OK_PTR + 4), dict(d_groups=None), dict(d_groups=OK_PTR + 2),
+    dict(d_prefix=None), dict(d_prefix=OK_PTR + 4), dict(groups=-1), dict(groups=3), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(scale=2.5e38), dict(d_weights=OK_PTR + 2), dict(capacity=0), dict(capacity=1 << 31), dict(lists=2), dict(lists=0),
+    dict(decay=float("nan")), dict(decay=float("inf")), dict(d_out=None), dict(d_out=(OK_PTR << 8) + 8), dict(d_out=OK_PTR + 64),
+    dict(d_workspace=OK_PTR + 8)])
+def test_bad_prefixes(lib, change):
+    assert lib.hs_prefix_attn(ref(shape()), ref(paged()), ref(prefix(**change)), None) == _lib.HS_ERR_ARG
+
+
+def test_bad_workspaces_of_prefixes(lib):
+    c, kv = shape(), paged()
+    for groups in (-1, 3):
+        assert lib.hs_prefix_attn_workspace(ref(c), ref(kv), groups, 0) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn_workspace(ref(c), None, 0, 0) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn_workspace(None, ref(kv), 0, 0) == _lib.HS_ERR_ARG
 
 
 @pytest.mark.parametrize("change", [
@@ -94,3 +123,5 @@ def test_null_arguments(lib):
     assert lib.hs_append_normed(None, ref(kv), ref(append()), ref(norm()), None) == _lib.HS_ERR_ARG
     assert lib.hs_evict(ref(c), None, ref(evict()), None) == _lib.HS_ERR_ARG
     assert lib.hs_evict(ref(c), ref(kv), None, None) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn(ref(c), None, ref(prefix()), None) == _lib.HS_ERR_ARG
+    assert lib.hs_prefix_attn(ref(c), ref(kv), None, None) == _lib.HS_ERR_ARG
