@@ -206,7 +206,7 @@ int64_t score_cols(const hs_paged_kv* kv) {
   return up((int64_t)kv->max_pages * kv->page_tokens, 32) + 128;  // a last tile may reach beyond the positions
 }
 bool layout_of(const hs_config* c, const hs_paged_kv* kv, int groups, bool weigh, int sms, Layout* l) {
-  l->tc = c->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_plan(c, sms) : hs_prefix_plan{0};
+  l->tc = c->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_plan(c, sms) : hs_prefix_mla_plan(c, sms);
   l->parts = any_parts(c, sms);
   const int64_t rows = l->tc.rows > 0 ? l->tc.rows : (int64_t)c->num_requests * c->num_q_heads * l->parts;
   const int64_t heads = (int64_t)c->num_requests * c->num_q_heads;
@@ -296,7 +296,7 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
   }
   cudaStream_t st = (cudaStream_t)stream;
   if (l.tc.rows > 0) {
-    rc = hs_prefix_gqa_launch(cfg, &a, ws + l.units, ws + l.partials, sms, st);
+    rc = (cfg->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_launch : hs_prefix_mla_launch)(cfg, &a, ws + l.units, ws + l.partials, sms, st);
     if (rc != HS_OK) return rc;
   } else {
     float* part = (float*)(ws + l.partials);

@@ -384,4 +384,6 @@ struct hs_prefix_plan {
   int64_t rows;
 };
 hs_prefix_plan hs_prefix_gqa_plan(const hs_config* c, int num_sms);
+hs_prefix_plan hs_prefix_mla_plan(const hs_config* c, int num_sms);
 int hs_prefix_gqa_launch(const hs_config* c, const void* prefix_args, void* units, void* partials, int num_sms, cudaStream_t st);
+int hs_prefix_mla_launch(const hs_config* c, const void* prefix_args, void* units, void* partials, int num_sms, cudaStream_t st);
