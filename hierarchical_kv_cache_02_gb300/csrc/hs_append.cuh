@@ -8,13 +8,6 @@
 
 namespace {
 
-// i / d by a multiplication with ceil(2^32 / d): exact while i * d < 2^32
-struct Div {
-  uint32_t d, m;
-  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1u ? i : __umulhi(i, m); }
-};
-inline Div div_by(int d) { return Div{(uint32_t)(d > 0 ? d : 1), d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u}; }
-
 struct Vec8 {
   uint32_t w[4];
 };

@@ -10,6 +10,13 @@ constexpr int32_t kMaxPositions = INT32_MAX - 65535;
 
 constexpr int kSmsHint = 152;  // to size grids by
 
+// i / d by a multiplication with ceil(2^32 / d): exact while i * d < 2^32
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ uint32_t operator()(uint32_t i) const { return d == 1u ? i : __umulhi(i, m); }
+};
+inline Div div_by(int d) { return Div{(uint32_t)(d > 0 ? d : 1), d > 1 ? (uint32_t)((0x100000000ull + d - 1) / d) : 0u}; }
+
 struct PagedRows {
   uint8_t* base;         // [num_pages][page_tokens][rec]
   const int32_t* table;  // [R][max_pages] or null: the identity

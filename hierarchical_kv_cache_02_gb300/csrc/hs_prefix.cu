@@ -200,7 +200,7 @@ int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 struct Layout {  // of the workspace
   hs_prefix_plan tc;
   int parts;
-  int64_t units, partials, stats, scores, cols, end;
+  int64_t partials, stats, scores, cols, end;
 };
 int64_t score_cols(const hs_paged_kv* kv) {
   return up((int64_t)kv->max_pages * kv->page_tokens, 32) + 128;  // a last tile may reach beyond the positions
@@ -211,8 +211,7 @@ bool layout_of(const hs_config* c, const hs_paged_kv* kv, int groups, bool weigh
   const int64_t rows = l->tc.rows > 0 ? l->tc.rows : (int64_t)c->num_requests * c->num_q_heads * l->parts;
   const int64_t heads = (int64_t)c->num_requests * c->num_q_heads;
   l->cols = score_cols(kv);
-  l->units = 0;
-  l->partials = up((2 * ((int64_t)groups + c->num_requests + 1) + 1) * (int64_t)sizeof(long long), 32);
+  l->partials = up(hs_prefix_head_bytes(groups, c->num_requests), 32);
   l->stats = l->partials + up(rows * (c->head_dim_v + 4) * (int64_t)sizeof(float), 32);
   l->scores = l->stats + (weigh ? up(heads * (int64_t)sizeof(float2), 32) : 0);
   if (weigh && l->cols > (INT64_MAX / 8) / heads) return false;
@@ -284,7 +283,8 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
     a.voff = cfg->head_dim_qk;
   }
   a.qscale = g.scale * kLog2e;
-  a.ok = (int*)((long long*)(ws + l.units) + 2 * (g.groups + a.R + 1));
+  PrefixSplit none;
+  hs_prefix_head(ws, g.groups, &none, &a.ok);
   if (weigh) {
     a.weights = g.d_weights;
     a.cap = g.capacity;
@@ -296,7 +296,7 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
   }
   cudaStream_t st = (cudaStream_t)stream;
   if (l.tc.rows > 0) {
-    rc = (cfg->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_launch : hs_prefix_mla_launch)(cfg, &a, ws + l.units, ws + l.partials, sms, st);
+    rc = (cfg->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_launch : hs_prefix_mla_launch)(cfg, &a, ws, ws + l.partials, sms, st);
     if (rc != HS_OK) return rc;
   } else {
     float* part = (float*)(ws + l.partials);

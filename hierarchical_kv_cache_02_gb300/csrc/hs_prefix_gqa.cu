@@ -24,8 +24,8 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kProducers = 4;
 // Warps 0-7 are the softmax groups; the products' warp stands beside warps 3 and 7, which have no rows when there are few, the
-// producers in the second and third quarter of the SM.  Warps 8 and 12 have nothing to do.
-constexpr int kWarpMma = 11, kThreads = 15 * 32;
+// producers and the warp that finds the portions in the first three quarters of the SM.  Warp 12 has nothing to do.
+constexpr int kWarpMma = 11, kWarpPlan = 8, kThreads = 15 * 32;
 __device__ __forceinline__ int producer_of(int warp) { return warp == 9 || warp == 10 ? warp - 9 : warp == 13 || warp == 14 ? warp - 11 : -1; }
 constexpr int kMaskRing = 8;   // tiles of validity bits: more than the ring can run ahead
 constexpr float kLazy = 8.f;   // log2 headroom before the running maximum is raised
@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], kProducers);
     mbar_init(&ct.fin, 1u);
+    prefix_plan_init(&ct.plan, kProducers + 1 + 8);
     ct.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -112,51 +113,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the only kernel that may start early is this call's own join, which waits for this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
-  bool go = prefix_start(a, c.w, &ct.plan, (int)blockIdx.x);
+  prefix_start(a, c.w, &ct.plan, (int)blockIdx.x);
   tc_fence_after();
   const uint32_t tb = ct.tmem;
   // tensor memory: 128 columns of scores a group (their first 64 become the weights), then D of O a group
 
-  // state that runs on through the rounds, each used by one role
-  Ring<C::kRing> ring;             // producers and products
-  int tiles = 0;                   // producers: tiles loaded; softmax: tiles seen
-  int done0 = 0, done1 = 0;        // products: tasks of each group whose values were issued; softmax: done0 is this group's tasks
-  int begun0 = 0, begun1 = 0;      // products: portions of each group begun
-  int sent = 0;                    // producers: ring loads issued; first softmax thread: query loads
+  int sent = 0;  // producers: ring loads issued; first softmax thread: query loads
   bool ok = true;
   uint32_t bad = 0u;
-  // products: a group's task whose values are due, and where they are; two that are at one place share them
-  bool due0 = false, due1 = false;
-  int vslot0 = 0, vslot1 = 0;
-  uint32_t vphase0 = 0u, vphase1 = 0u;
-  bool vfirst0 = false, vfirst1 = false;
+  PrefixPlan* plan = &ct.plan;
 
-  for (; go; go = prefix_round(a, c.w, &ct.plan, (int)blockIdx.x)) {
-    const PPortion* list = ct.plan.port;
-    const int count = uniform(ct.plan.nport);
+  {
     const int pw = producer_of(warp);
     if (pw >= 0) {
       // ---------------- producers: 32 entries of every tile each, a lane's lookup of one ----------------
       const int crow = lane >> 3, cch = lane & 7;
-      int np = 0, nt = count > 0 ? list[0].t0 : 0;  // the place of the next lookup, a tile ahead of the copies
-      int page = -1, at = 0;                       // its page (-1: none) and place in it
+      Ring<C::kRing> ring;
+      int tiles = 0;               // loaded
+      int page = -1, at = 0;       // the next tile's entry: its page (-1: nothing seen there, -2: bad) and place in it
+      PPortion L = portion_take(plan, 0, false, &ok, abort);  // the lookups' portion, a tile ahead of the copies
+      int nl = 0, lt = L.t0;
       auto look = [&]() {
         page = -1;
-        if (np >= count) return;
-        const PPortion& P = list[np];
-        const int p = P.base + nt * kTile + 32 * pw + lane;
-        if (p >= P.p0 && p < P.p1) {
+        if (L.t0 == L.t1) return;
+        const int p = L.base + lt * kTile + 32 * pw + lane;
+        if (p >= L.p0 && p < L.p1) {
           const unsigned pg = (unsigned)p / (unsigned)a.kv.page_tokens;
           at = p - (int)(pg * (unsigned)a.kv.page_tokens);
-          page = a.kv.table != nullptr ? a.kv.table[(int64_t)P.lead * a.kv.max_pages + pg] : P.lead * a.kv.max_pages + (int)pg;
+          page = a.kv.table != nullptr ? a.kv.table[(int64_t)L.lead * a.kv.max_pages + pg] : L.lead * a.kv.max_pages + (int)pg;
           if (page < 0 || page >= a.kv.num_pages) page = -2;
         }
-        if (++nt == P.t1 && ++np < count) nt = list[np].t0;
+        if (++lt == L.t1) {
+          L = portion_take(plan, ++nl, false, &ok, abort);
+          lt = L.t0;
+        }
       };
+      PPortion P = L;
       look();
 #pragma unroll 1
-      for (int pi = 0; pi < count; ++pi) {
-        const PPortion& P = list[pi];
+      for (int pi = 0; P.t0 < P.t1; ++pi) {
+        if (lane == 0) mbar_arrive(&plan->empty[pi % kPrefixRing]);  // the lookups took it before
         const int x0 = P.head * a.kstride;
 #pragma unroll 1
         for (int t = P.t0; t < P.t1; ++t, ++tiles) {
@@ -203,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&ct.mask[tiles % kMaskRing]);
           }
         }
+        P = portion_take(plan, pi + 1, false, &ok, abort);
       }
     } else if (warp == kWarpMma) {
       // ---------------- products ----------------
@@ -248,9 +245,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
+      Ring<C::kRing> ring;
+      int done0 = 0, done1 = 0;    // tasks of each group whose values were issued
+      int begun0 = 0, begun1 = 0;  // portions of each group begun
+      // a group's task whose values are due, and where they are; two that are at one place share them
+      bool due0 = false, due1 = false;
+      int vslot0 = 0, vslot1 = 0;
+      uint32_t vphase0 = 0u, vphase1 = 0u;
+      bool vfirst0 = false, vfirst1 = false;
 #pragma unroll 1
-      for (int pi = 0; pi < count; ++pi) {
-        const int t0 = uniform(list[pi].t0), t1 = uniform(list[pi].t1), both = uniform(list[pi].both), first = uniform(list[pi].first);
+      for (int pi = 0;; ++pi) {
+        const PPortion P = portion_take(plan, pi, true, &ok, abort);
+        const int t0 = uniform(P.t0), t1 = uniform(P.t1), both = uniform(P.both), first = uniform(P.first);
+        if (t0 == t1) break;
 #pragma unroll 1
         for (int t = t0; t < t1; ++t) {
           const Ring<C::kRing> k = ring;  // where the keys are
@@ -280,10 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the rounds are apart by barriers, and a portion's results are stored within its round
       if (due0) values(0, vslot0, vphase0, vfirst0, !(due1 && vslot1 == vslot0), done0++);
       if (due1) values(1, vslot1, vphase1, vfirst1, true, done1++);
-      due0 = due1 = false;
     } else if (warp < 8) {
       // ---------------- softmax: group g, thread = row = TMEM lane ----------------
       // (A warp comes together, by a vote or __syncwarp, behind each branch that its lanes may take apart: accesses to tensor memory
@@ -293,19 +298,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ts = tb + 128u * g + lane_base, to = tb + 256u + (uint32_t)(D * g) + lane_base;
       const int lr = row / c.w.G, hq = row - lr * c.w.G;
       auto takes = [&](const PPortion& P) { return P.both || P.first == g || P.t1 - P.t0 > 1; };
+      int tiles = 0, done = 0;  // tiles so far, tasks of this group
       auto next_q = [&](int i) {  // the queries of the next portion this group takes part in, by the group's first thread
-        while (i < count && !takes(list[i])) ++i;
-        if (i >= count) return;
-        const PPortion& P = list[i];
-        ++sent;
-        mbar_arrive_expect_tx(&ct.qfull[g], (uint32_t)(C::kCh * c.w.G * (P.own ? 1 : c.w.MT) * 128));
-        const int r0 = P.r0 + (P.both && g == 1 ? c.w.MT : 0);
-        for (int b = 0; b < C::kCh; ++b)
-          tma_load_4d(q_u + (uint32_t)(g * C::kSlot + b * C::kBlk), P.own ? &qone : &qmany, 64 * b, P.head * c.w.G, r0, 0, &ct.qfull[g]);
+        for (;; ++i) {
+          if (!portion_wait(plan, i, abort)) return;
+          const PPortion& P = portion_at(plan, i);
+          if (P.t0 == P.t1) return;
+          if (!takes(P)) continue;
+          ++sent;
+          mbar_arrive_expect_tx(&ct.qfull[g], (uint32_t)(C::kCh * c.w.G * (P.own ? 1 : c.w.MT) * 128));
+          const int r0 = P.r0 + (P.both && g == 1 ? c.w.MT : 0);
+          for (int b = 0; b < C::kCh; ++b)
+            tma_load_4d(q_u + (uint32_t)(g * C::kSlot + b * C::kBlk), P.own ? &qone : &qmany, 64 * b, P.head * c.w.G, r0, 0, &ct.qfull[g]);
+          return;
+        }
       };
-      if (row == 0 && ok) next_q(0);
-      for (int pi = 0; pi < count; ++pi) {
-        const PPortion P = list[pi];
+      if (row == 0) next_q(0);
+      __syncwarp();
+#pragma unroll 1
+      for (int pi = 0;; ++pi) {
+        const PPortion P = portion_take(plan, pi, true, &ok, abort);
+        if (P.t0 == P.t1) break;
         if (!takes(P)) {
           tiles += P.t1 - P.t0;
           continue;
@@ -317,13 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.f, le = 0.f;
         for (int tile = P.t0 + off; tile < P.t1; tile += step) {
           const int nm = tiles + tile - P.t0;
-          if (ok) ok = mbar_wait2(&ct.s[g], (uint32_t)(done0 & 1), &ct.mask[nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
+          if (ok) ok = mbar_wait2(&ct.s[g], (uint32_t)(done & 1), &ct.mask[nm % kMaskRing], (uint32_t)((nm / kMaskRing) & 1), abort);
           tc_fence_after();
           if (row == 0 && tile + step >= P.t1) {  // the last scores of the portion are done: the next one's queries
             if (ok) next_q(pi + 1);
           }
           ok = __all_sync(0xffffffffu, ok);
-          ++done0;
+          ++done;
           __syncwarp();
           if (ok && warp_ok) {
             uint32_t w[4];
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ct.p[g]);
         }
         // the portion's partial sums
-        if (ok) ok = mbar_wait_small(&ct.pv[g], (uint32_t)((done0 - 1) & 1), abort);
+        if (ok) ok = mbar_wait_small(&ct.pv[g], (uint32_t)((done - 1) & 1), abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok && warp_ok) {
@@ -424,8 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
       }
+    } else if (warp == kWarpPlan) {
+      prefix_walk(a, c.w, plan, (int)blockIdx.x, abort);
     }
-    if (!ok) *abort = 1u;
     __syncwarp();
   }
   if (!ok) {
@@ -472,13 +486,15 @@ bool split_of(const hs_config* c, int sms, PrefixSplit* w) {
   w->flat = 0;
   w->G = G;
   w->MT = 128 / G < c->num_requests ? 128 / G : c->num_requests;
-  w->per = 2;
-  w->tile = kTile;
-  w->cost = 2;
-  w->cost2 = 3;
+  w->mt = div_by(w->MT);
+  w->pairs = 1;
+  w->tile_shift = 7;
+  w->cost = div_by(2);
+  w->cost2 = div_by(3);
   w->begin = 1;
   w->copies = 2;
   w->most = 256;
+  w->group_rows = 3 * c->num_q_heads;
   w->workers = sms;
   return true;
 }
@@ -491,27 +507,25 @@ cudaError_t launch(const GqaArgs& c, const CUtensorMap& qm, const CUtensorMap& q
   if (e != cudaSuccess) return e;
   e = hs_launch_pdl(k_prefix_gqa<D, W>, dim3(c.w.workers), dim3(kThreads), Shape<D>::kDyn, st, c, qm, q1, seg);
   if (e != cudaSuccess) return e;
-  return hs_launch_pdl(k_prefix_join<D>, dim3((c.a.Hq * (D / 8) + kPrefixJoinThreads - 1) / kPrefixJoinThreads, c.a.R),
-                       dim3(kPrefixJoinThreads), 0, st, c.a, c.w);
+  return launch_join<D>(c.a, c.w, st);
 }
 
 }  // namespace
 
-// Rows of partials: a request's own segment has 2 Hq of them; a group of n requests 2 Hq min(n, MT) for every two row tiles, of
-// which there are at most n / (2 MT) + 1, so at most 3 Hq n in all; and what keeps the workers' apart.
+// Rows of partials: a request's own segment takes 2 Hq of them; a group of n requests 2 Hq min(n, MT) for every two row tiles, of
+// which there are at most n / (2 MT) + 1, so at most 3 Hq n; and what keeps the workers' apart.
 hs_prefix_plan hs_prefix_gqa_plan(const hs_config* c, int num_sms) {
   PrefixSplit w;
   if (!split_of(c, num_sms, &w)) return {0};
-  return {5ll * c->num_requests * c->num_q_heads + (int64_t)w.workers * w.most};
+  return {(w.group_rows + 2ll * c->num_q_heads) * c->num_requests + (int64_t)w.workers * w.most};
 }
 
-int hs_prefix_gqa_launch(const hs_config* cfg, const void* prefix_args, void* units, void* partials, int num_sms, cudaStream_t st) {
+int hs_prefix_gqa_launch(const hs_config* cfg, const void* prefix_args, void* head, void* partials, int num_sms, cudaStream_t st) {
   GqaArgs c{};
   c.a = *(const PrefixArgs*)prefix_args;
   if (!split_of(cfg, num_sms, &c.w)) return HS_ERR_CONFIG;
-  const int V = c.a.ngroups + c.a.R + 1, D = c.a.dqk;
-  c.w.units = (long long*)units;
-  c.w.rows = c.w.units + V;
+  const int D = c.a.dqk;
+  hs_prefix_head(head, c.a.ngroups, &c.w, &c.a.ok);
   c.w.part = (float*)partials;
   c.w.ml = c.w.part + hs_prefix_gqa_plan(cfg, num_sms).rows * D;
   if (c.a.qscale < 0.f) {

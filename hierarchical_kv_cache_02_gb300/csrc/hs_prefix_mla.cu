@@ -30,7 +30,7 @@ constexpr int kQ = kChunks * kBlk;                // a CTA's queries
 constexpr int kKGroup = kChunks * 1024, kVGroup = 4 * 1024;
 constexpr int kKBuf = 4 * kKGroup, kVBuf = 8 * kVGroup;  // 32 whole records; 256 values of 64 records
 // Warps 0-3 are the softmax; the products' warp shares a quarter of the SM's issue slots with one of them alone.
-constexpr int kWarpMma = 7, kPassKeys = 8, kPassValues = 10, kThreads = 11 * 32;
+constexpr int kWarpMma = 7, kPassKeys = 8, kPassValues = 10, kWarpPlan = 11, kThreads = 12 * 32;
 __device__ __forceinline__ int key_producer(int warp) { return warp == 4 || warp == 5 ? warp - 4 : -1; }
 __device__ __forceinline__ int value_producer(int warp) { return warp == 6 ? 0 : warp == 9 ? 1 : -1; }
 constexpr int kMaskRing = 4;
@@ -57,24 +57,28 @@ struct MlaControl {
   float2 sums[2][64];
   uint32_t tmem, abort;
 };
+static_assert(kTile == 64, "the split's tiles");
 static_assert(kDyn + sizeof(MlaControl) <= 227 * 1024, "shared memory of a CTA");
 
-// A producer lane's lookup of its entry of each tile of a portion list, a tile ahead of the copies.
+// A producer lane's lookup of its entry of each tile, a tile ahead of the copies.
 struct Lookup {
-  int np = 0, nt = 0;       // portion and tile of the next lookup
-  int page = -1, at = 0;    // its page (-1: nothing seen there, -2: bad) and the place in it
-  __device__ __forceinline__ void next(const PrefixArgs& a, const PPortion* list, int count, int mine) {
+  PPortion L;               // the next lookup's portion
+  int nl = 0, lt;           // its number, the tile
+  int page = -1, at = 0;    // what was found: the page (-1: nothing seen there, -2: bad) and the place in it
+  __device__ __forceinline__ void next(const PrefixArgs& a, PrefixPlan* plan, int mine, bool* ok, volatile uint32_t* abort) {
     page = -1;
-    if (np >= count) return;
-    const PPortion& P = list[np];
-    const int p = P.base + nt * kTile + mine;
-    if (p >= P.p0 && p < P.p1) {
+    if (L.t0 == L.t1) return;
+    const int p = L.base + lt * kTile + mine;
+    if (p >= L.p0 && p < L.p1) {
       const unsigned pg = (unsigned)p / (unsigned)a.kv.page_tokens;
       at = p - (int)(pg * (unsigned)a.kv.page_tokens);
-      page = a.kv.table != nullptr ? a.kv.table[(int64_t)P.lead * a.kv.max_pages + pg] : P.lead * a.kv.max_pages + (int)pg;
+      page = a.kv.table != nullptr ? a.kv.table[(int64_t)L.lead * a.kv.max_pages + pg] : L.lead * a.kv.max_pages + (int)pg;
       if (page < 0 || page >= a.kv.num_pages) page = -2;
     }
-    if (++nt == P.t1 && ++np < count) nt = list[np].t0;
+    if (++lt == L.t1) {
+      L = portion_take(plan, ++nl, false, ok, abort);
+      lt = L.t0;
+    }
   }
 };
 
@@ -107,6 +111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ct.pv, 1u);
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], 2u);
     mbar_init(&ct.fin, 1u);
+    prefix_plan_init(&ct.plan, rank == 0 ? 11 : 10);  // the warps that read it: not the odd CTA's products' one
     ct.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -129,35 +134,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   const int worker = (int)blockIdx.x >> 1;
-  bool go = prefix_start(a, c.w, &ct.plan, worker);
+  prefix_start(a, c.w, &ct.plan, worker);
   tc_fence_after();
   const uint32_t tb = ct.tmem;
 
-  // state that runs on through the rounds
-  int nt = 0;                      // tiles so far, of each role
-  int nq = 0;                      // portions so far (products); query loads (first softmax thread)
-  int sent = 0;                    // producers: tiles whose copies were issued
+  int nt = 0;    // tiles so far, of each role
+  int nq = 0;    // portions so far (products); query loads (first softmax thread)
+  int sent = 0;  // producers: tiles whose copies were issued
   bool ok = true;
   uint32_t bad = 0u;
+  PrefixPlan* plan = &ct.plan;
 
-  for (; go; go = prefix_round(a, c.w, &ct.plan, worker)) {
-    const PPortion* list = ct.plan.port;
-    const int count = ct.plan.nport;
+  {
     if (key_producer(warp) >= 0) {
       // ---------------- keys: 16 whole records of this CTA's 32 of a tile, looked up by lanes 0-15 ----------------
       const int first = 16 * key_producer(warp), crow = lane >> 3, cch = lane & 7;
       Lookup ahead;
-      ahead.nt = count > 0 ? list[0].t0 : 0;
-      int kp = 0, kt = ahead.nt;
-      ahead.next(a, list, count, 32 * rank + first + (lane & 15));
+      ahead.L = portion_take(plan, 0, false, &ok, abort);
+      ahead.lt = ahead.L.t0;
+      PPortion P = ahead.L;
+      ahead.next(a, plan, 32 * rank + first + (lane & 15), &ok, abort);
+      int kt = P.t0;
 #pragma unroll 1
-      while (kp < count) {
-        const PPortion& P = list[kp];
+      for (int pi = 0; P.t0 < P.t1;) {
+        if (kt == P.t0 && lane == 0) mbar_arrive(&plan->empty[pi % kPrefixRing]);  // the lookups took it before
         if (ahead.page == -2) bad |= (uint32_t)HS_DEVERR_PAGE;
         const bool seen = ahead.page >= 0;
         const int row = seen ? ahead.page * a.kv.page_tokens + ahead.at : c.ctx_rows;
         const int e0 = P.base + kt * kTile + 32 * rank + first;
-        ahead.next(a, list, count, 32 * rank + first + (lane & 15));
+        ahead.next(a, plan, 32 * rank + first + (lane & 15), &ok, abort);
         const int b = nt & 1;
         const uint32_t dst = k_u + (uint32_t)(b * kKBuf + (first >> 3) * kKGroup);
         uint64_t* full = &ct.kfull[b];
@@ -186,24 +191,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++nt;
         if (++kt == P.t1) {
-          ++kp;
-          if (kp < count) kt = list[kp].t0;
+          P = portion_take(plan, ++pi, false, &ok, abort);
+          kt = P.t0;
         }
       }
     } else if (value_producer(warp) >= 0) {
       // ---------------- values: this CTA's 256 of 32 records of every tile, a lane's lookup each ----------------
       const int half = value_producer(warp), crow = lane >> 3, cch = lane & 7;
       Lookup ahead;
-      ahead.nt = count > 0 ? list[0].t0 : 0;
-      int kp = 0, kt = ahead.nt;
-      ahead.next(a, list, count, 32 * half + lane);
+      ahead.L = portion_take(plan, 0, false, &ok, abort);
+      ahead.lt = ahead.L.t0;
+      PPortion P = ahead.L;
+      ahead.next(a, plan, 32 * half + lane, &ok, abort);
+      int kt = P.t0;
 #pragma unroll 1
-      while (kp < count) {
-        const PPortion& P = list[kp];
+      for (int pi = 0; P.t0 < P.t1;) {
+        if (kt == P.t0 && lane == 0) mbar_arrive(&plan->empty[pi % kPrefixRing]);  // the lookups took it before
         const bool seen = ahead.page >= 0;
         const int row = seen ? ahead.page * a.kv.page_tokens + ahead.at : c.ctx_rows;
         const int e0 = P.base + kt * kTile + 32 * half;
-        ahead.next(a, list, count, 32 * half + lane);
+        ahead.next(a, plan, 32 * half + lane, &ok, abort);
         const int b = nt & 1;
         const uint32_t dst = v_u + (uint32_t)(b * kVBuf + 4 * half * kVGroup);
         uint64_t* full = &ct.vfull[b];
@@ -236,8 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++nt;
         if (++kt == P.t1) {
-          ++kp;
-          if (kp < count) kt = list[kp].t0;
+          P = portion_take(plan, ++pi, false, &ok, abort);
+          kt = P.t0;
         }
       }
     } else if (warp == kWarpMma && rank == 0) {
@@ -250,15 +257,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t dp = (uint32_t)uniform((int)umma_sdesc_lo(p_u, 16));
       // V as it lies: blocks of 64 values 1 KB apart, 8 entries a group, the value dims contiguous
       const uint32_t dv = (uint32_t)uniform((int)umma_sdesc_lo(v_u, 1024));
-      const int n = uniform(count);
-      // the next scores' and the next values' place: portion, tiles left in it, whether it is its first tile;
+      // the next scores' and the next values' place: portion, tiles left in it (0: no more), whether it is its first tile;
       // ahead: tiles whose scores were issued and whose values were not
-      int kp = 0, kl = 0, vp = 0, vl = 0, ahead = 0;
+      int kp = 0, vp = 0, ahead = 0;
+      auto tiles_of = [&](int i) {
+        const PPortion P = portion_take(plan, i, false, &ok, abort);
+        return uniform(P.t1 - P.t0);
+      };
+      int kl = tiles_of(0), vl = kl;
       bool kfirst = true, vfirst = true;
-      if (n > 0) kl = vl = uniform(list[0].t1 - list[0].t0);
-      while (vp < n) {
+      while (vl > 0) {
         const int i = nt + ahead, bs = i & 1, b = nt & 1;
-        const bool more = kp < n && ahead < kAhead;
+        const bool more = kl > 0 && ahead < kAhead;
         bool scores = ahead == 0;
         if (ok) {
           ok = false;
@@ -292,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           ++ahead;
           kfirst = --kl == 0;
-          if (kfirst && ++kp < n) kl = uniform(list[kp].t1 - list[kp].t0);
+          if (kfirst) kl = tiles_of(++kp);
           continue;
         }
         if (ok && elect_one()) {
@@ -310,7 +320,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++nt;
         --ahead;
         vfirst = --vl == 0;
-        if (vfirst && ++vp < n) vl = uniform(list[vp].t1 - list[vp].t0);
+        if (vfirst) {
+          if (lane == 0) mbar_arrive(&plan->empty[vp % kPrefixRing]);
+          vl = tiles_of(++vp);  // the scores' place is there already
+        }
       }
     } else if (warp == kPassKeys || warp == kPassValues) {
       // ---------------- what the products take is there, passed on to the even CTA ----------------
@@ -318,13 +331,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool keys = warp == kPassKeys;
       uint64_t* full = keys ? ct.kfull : ct.vfull;
       const uint32_t ready = in_cta(smem_u32(keys ? ct.kready : ct.vready), 0), qr = in_cta(smem_u32(&ct.qready), 0);
-      for (int pi = 0; pi < count; ++pi) {
+#pragma unroll 1
+      for (int pi = 0;; ++pi) {
+        const PPortion P = portion_take(plan, pi, true, &ok, abort);
+        if (P.t0 == P.t1) break;
         if (keys) {
           if (ok) ok = warp_wait_small(&ct.qfull, (uint32_t)(nq & 1), abort);
           ++nq;
           if (ok && lane == 0) cluster_arrive(qr);
         }
-        for (int tile = list[pi].t0; tile < list[pi].t1; ++tile, ++nt) {
+        for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
           if (ok) ok = warp_wait_small(&full[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (ok && lane == 0) cluster_arrive(ready + 8u * (nt & 1));
@@ -337,14 +353,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row = tid & 63, half = tid >> 6;
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16, p_bar = in_cta(smem_u32(&ct.p), 0);
       auto pair_sync = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + (warp & 1)) : "memory"); };
-      auto load_q = [&](const PPortion& P) {  // by the first thread
+      auto load_q = [&](int i) {  // of portion i, by the first thread
+        if (!portion_wait(plan, i, abort)) return;
+        const PPortion& P = portion_at(plan, i);
+        if (P.t0 == P.t1) return;
         mbar_arrive_expect_tx(&ct.qfull, (uint32_t)kQ);
         for (int b = 0; b < kChunks; ++b) tma_load_2d(q_u + (uint32_t)(b * kBlk), &qmap, 64 * b, P.r0 + 64 * rank, &ct.qfull);
         ++nq;
       };
-      if (tid == 0 && count > 0 && ok) load_q(list[0]);
-      for (int pi = 0; pi < count; ++pi) {
-        const PPortion P = list[pi];
+      if (tid == 0) load_q(0);
+      __syncwarp();
+#pragma unroll 1
+      for (int pi = 0;; ++pi) {
+        const PPortion P = portion_take(plan, pi, true, &ok, abort);
+        if (P.t0 == P.t1) break;
         const bool row_ok = 64 * rank + row < P.cnt;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         float m = -INFINITY, l = 0.f, le = 0.f;  // the sums: of this thread's entries
@@ -352,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int b = nt & 1;
           if (ok) ok = mbar_wait2(&ct.s[nt % kAhead], (uint32_t)((nt / kAhead) & 1), &ct.mask[nt % kMaskRing],
                                   (uint32_t)((nt / kMaskRing) & 1), abort);
-          if (tid == 0 && tile == P.t1 - 1 && pi + 1 < count && ok) load_q(list[pi + 1]);  // the last scores are done
+          if (tid == 0 && tile == P.t1 - 1 && ok) load_q(pi + 1);  // the last scores are done
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           const uint32_t w = ct.valid[nt % kMaskRing][half];
@@ -463,6 +485,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
       }
+    } else if (warp == kWarpPlan) {
+      prefix_walk(a, c.w, plan, worker, abort);
+      if (*abort != 0u) ok = false;
     }
     if (!ok) {  // the other CTA gives up, too
       *abort = 1u;
@@ -505,16 +530,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- host ------------------------------------------------------------------------------------------
 
-void split_of(int num_sms, PrefixSplit* w) {
+void split_of(const hs_config* c, int num_sms, PrefixSplit* w) {
   w->heads = 1;
   w->flat = 1;
   w->G = w->MT = 1;
-  w->per = 1;
-  w->tile = kTile;
-  w->cost = w->cost2 = 1;
+  w->mt = div_by(1);
+  w->pairs = 0;
+  w->tile_shift = 6;
+  w->cost = w->cost2 = div_by(1);
   w->begin = 2;
   w->copies = 1;
   w->most = kRows;
+  w->group_rows = 2 * c->num_q_heads;
   w->workers = num_sms / 2;
 }
 
@@ -524,8 +551,7 @@ cudaError_t launch(const MlaArgs& c, const CUtensorMap& qm, const CUtensorMap& k
   cudaError_t e = allow_smem(k_prefix_mla<W>, kDyn, done);
   if (e == cudaSuccess) e = hs_launch_pdl(k_prefix_mla<W>, dim3(2 * c.w.workers), dim3(kThreads), kDyn, st, c, qm, km, vm);
   if (e != cudaSuccess) return e;
-  return hs_launch_pdl(k_prefix_join<kValue>, dim3((c.a.Hq * (kValue / 8) + kPrefixJoinThreads - 1) / kPrefixJoinThreads, c.a.R),
-                       dim3(kPrefixJoinThreads), 0, st, c.a, c.w);
+  return launch_join<kValue>(c.a, c.w, st);
 }
 
 }  // namespace
@@ -537,13 +563,11 @@ hs_prefix_plan hs_prefix_mla_plan(const hs_config* c, int num_sms) {
   return {4ll * c->num_requests * c->num_q_heads + (int64_t)(num_sms / 2) * kRows};
 }
 
-int hs_prefix_mla_launch(const hs_config* cfg, const void* prefix_args, void* units, void* partials, int num_sms, cudaStream_t st) {
+int hs_prefix_mla_launch(const hs_config* cfg, const void* prefix_args, void* head, void* partials, int num_sms, cudaStream_t st) {
   MlaArgs c{};
   c.a = *(const PrefixArgs*)prefix_args;
-  split_of(num_sms, &c.w);
-  const int V = c.a.ngroups + c.a.R + 1;
-  c.w.units = (long long*)units;
-  c.w.rows = c.w.units + V;
+  split_of(cfg, num_sms, &c.w);
+  hs_prefix_head(head, c.a.ngroups, &c.w, &c.a.ok);
   c.w.part = (float*)partials;
   c.w.ml = c.w.part + hs_prefix_mla_plan(cfg, num_sms).rows * kValue;
   if (c.a.qscale < 0.f) {
