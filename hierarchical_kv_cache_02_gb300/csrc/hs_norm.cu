@@ -14,12 +14,19 @@
 
 namespace {
 
-// A head lies over a group of 4 to 32 neighbouring lanes (a power of two), a unit of two vectors each, so that the sum of its
-// squares is a few shuffles; heads of more than 32 units (the latent's 36) have a second unit a lane.  The heads of
-// a kind (keys, values, queries) of all tokens of a CTA stand one behind the other, 32 / group of them a warp.
+// A head lies over a group of 1 to 32 neighbouring lanes (a power of two), a unit of two vectors each, so that the sum of its
+// squares is a few shuffles; heads of more than 32 units (the latent's 36) have a second unit a lane.  The heads of a kind
+// (keys, values, queries) stand one behind the other, 32 / group of them a warp, and a warp does the same heads of one token
+// after the other, so that places and weights are found once: what a token costs then is its loads, about 110 instructions a
+// warp, its stores.  The loads go to shared memory, kAhead tokens ahead, each lane's to places of its own (in registers there is
+// room for two tokens: 91 us instead of XX on 16384 tokens of 32 + 8 + 8 heads of 128).  A CTA takes a run of tokens,
+// finds their records' places first and the sines and cosines a few tokens ahead.
 
-constexpr int kThreads = 256;
-constexpr int kTokens = 4;  // tokens of a CTA at most
+constexpr int kMaxWarps = 12;
+constexpr int kRun = 64;    // tokens of a CTA at most
+constexpr int kStage = 8;   // tokens whose angles are at hand; two stages
+constexpr int kCtas = 2;    // CTAs of kMaxWarps an SM
+constexpr int kAhead = 8;   // units of a lane on their way
 
 struct Kind {
   const uint16_t* src;
@@ -31,7 +38,9 @@ struct Kind {
   const void* w;       // weights [norm] or [heads][norm]
   int64_t whs;
   int wide;            // weights of 32 bits, else bf16
-  int first;           // the kind's first warp task
+  float per;           // 1 / norm
+  int first;           // the kind's first warp among a token's
+  int head_rec, to;    // keys and values: where a head's begin in the record
 };
 
 struct NormArgs {
@@ -43,10 +52,10 @@ struct NormArgs {
   const uint8_t* axis;  // of each pair, or null: 0
   uint16_t* q_out;
   int64_t ots, ohs;
-  int R, N, dqk, dv, half, interleaved, axes;
+  int R, N, half, interleaved, axes;
   float eps;
-  Kind kind[3];         // keys, values, queries
-  int tasks, per_cta, tokens;
+  Kind kind[3];         // keys, values (a latent: the values behind its normed ones, where they are apart), queries
+  int tasks, run;       // warps of a token, tokens of a CTA
   Div angles;
 };
 
@@ -75,161 +84,223 @@ __device__ __forceinline__ Place place_of(const Kind& k, int u, int interleaved)
   return p;
 }
 
-__device__ __forceinline__ float squares(const Vec8& v) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s = fmaf(hi(v.w[i]), hi(v.w[i]), fmaf(lo(v.w[i]), lo(v.w[i]), s));
-  return s;
+// Two 32-bit values at a time.
+struct Two {
+  float x, y;
+};
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
-__device__ __forceinline__ void widen(const Vec8& v, float (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = lo(v.w[i]);
-    x[2 * i + 1] = hi(v.w[i]);
-  }
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+      "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
 }
-__device__ __forceinline__ Vec8 narrow(const float (&x)[8]) {
-  return Vec8{{pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7])}};
-}
-// times r and the weights from value d on
-__device__ __forceinline__ void scale(float (&x)[8], const Kind& k, int h, int d, float r) {
+__device__ __forceinline__ Two wide(uint32_t w) { return Two{lo(w), hi(w)}; }
+
+// 8 weights from value d on
+__device__ __forceinline__ void weights(const Kind& k, int h, int d, Two (&w)[4]) {
   const int64_t at = (int64_t)h * k.whs + d;
-  float w[8];
   if (k.wide) {
     const float4 a = *(const float4*)((const float*)k.w + at), b = *(const float4*)((const float*)k.w + at + 4);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    w[0] = Two{a.x, a.y}, w[1] = Two{a.z, a.w}, w[2] = Two{b.x, b.y}, w[3] = Two{b.z, b.w};
   } else {
-    widen(ld8((const uint16_t*)k.w + at), w);
-  }
+    const Vec8 v = ld8((const uint16_t*)k.w + at);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    for (int i = 0; i < 4; ++i) w[i] = wide(v.w[i]);
+  }
 }
-// the four pairs (x0, x1), (x2, x3), ... by c, s of each
-__device__ __forceinline__ void turn_inside(float (&x)[8], const float2* cs) {
+// the four pairs of neighbours by their cosines and sines
+__device__ __forceinline__ void turn_inside(Two (&x)[4], const float* c, const float* s) {
+  const float4 cc = *(const float4*)c, ss = *(const float4*)s;
+  const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 c = cs[i];
-    const float p = x[2 * i], r = x[2 * i + 1];
-    x[2 * i] = p * c.x - r * c.y;
-    x[2 * i + 1] = r * c.x + p * c.y;
+    const Two p = x[i];
+    x[i].x = p.x * cv[i] - p.y * sv[i];
+    x[i].y = p.y * cv[i] + p.x * sv[i];
   }
 }
 
-// PER: units of a lane.  FLIGHT: heads whose loads are on their way at once.
-template <int PER, int FLIGHT>
-__global__ void __launch_bounds__(kThreads) k_append_normed(const __grid_constant__ NormArgs a) {
-  extern __shared__ __align__(16) float2 s_cs[];  // [tokens][half] cosine and sine of each pair
-  __shared__ int64_t s_row[kTokens], s_pos[kTokens][HS_MAX_AXES];
-  __shared__ int s_live[kTokens];
+// What a lane does of every token: unit p of its head.
+struct Mine {
+  Place at;
+  bool there;
+  Two wx[4], wy[4];  // weights of its two vectors
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ Vec8 lds8(uint32_t at) {
+  Vec8 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "r"(at) : "memory");
+  return v;
+}
+
+// PER: units of a lane.
+template <int PER>
+__global__ void __launch_bounds__(32 * kMaxWarps, PER == 1 ? kCtas : 1) k_append_normed(const __grid_constant__ NormArgs a) {
+  constexpr int kDepth = kAhead / PER;           // tokens on their way
+  extern __shared__ __align__(16) float s_cs[];  // [2][2][kStage][half]: stage, cosines and sines; then the warps' rings
+  __shared__ int64_t s_row[kRun], s_pos[kRun][HS_MAX_AXES];
+  __shared__ uint8_t s_live[kRun];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int t0 = blockIdx.x * a.run, nt = min(a.run, a.N - t0), half = a.half;
+  const int task = (int)blockIdx.y * warps + warp;
+  const int kn = (task >= a.kind[1].first) + (task >= a.kind[2].first);
+  const Kind& k = a.kind[kn];
+  const int u0 = lane & ((1 << k.lanes) - 1), h = ((task - k.first) * 32 + lane) >> k.lanes;
+  const bool on = task < a.tasks && h < (int)k.heads.d;
+  const int norm = k.norm, lanes = 1 << k.lanes, to = h * k.head_rec + k.to;
+  const float per = k.per;
+  const int64_t ts = k.ts;
+  const uint16_t* src = k.src + (int64_t)t0 * ts + (int64_t)h * k.hs;
   hs_pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.N - t0);
-  for (int w = warp; w < nt; w += kThreads / 32) {  // a warp a token
+  Mine mine[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    Mine& m = mine[p];
+    m.there = on && u0 + 32 * p < k.units;
+    m.at = place_of(k, u0 + 32 * p, a.interleaved);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m.wx[i] = m.wy[i] = Two{1.f, 1.f};
+    if (m.there && m.at.d < norm) weights(k, h, m.at.d, m.wx);
+    if (m.there && m.at.second != 0 && m.at.d + m.at.second < norm) weights(k, h, m.at.d + m.at.second, m.wy);
+  }
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_cs + 4 * kStage * half) + (uint32_t)(warp * kAhead * 1024 + lane * 16);
+  auto load = [&](int t) {
+    if (t < nt) {
+      const uint16_t* from = src + (int64_t)t * ts;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        const uint32_t to = ring + (uint32_t)((t % kDepth * PER + p) * 1024);
+        if (mine[p].there) copy16(to, from + mine[p].at.d);
+        if (mine[p].there && mine[p].at.second != 0) copy16(to + 512u, from + mine[p].at.d + mine[p].at.second);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int t = 0; t < kDepth; ++t) load(t);
+  for (int w = tid; w < nt; w += blockDim.x) {  // a thread a token
     const int t = t0 + w;
-    const int64_t given = a.rope_pos != nullptr && lane < a.axes ? a.rope_pos[(int64_t)t * a.axes + lane] : 0;
-    const int x = request_of_token(a.cu, a.R, t, lane);
+    int x = 0;
+    for (int n = a.R; n > 1;) {  // the last request whose first token is not behind t
+      const int before = n >> 1;
+      if (a.cu[x + before] <= t) x += before;
+      n -= before;
+    }
     const int c0 = a.cu[x], c1 = a.cu[x + 1];
     const bool live = c0 <= t && t < c1;
     const int64_t pos = a.start[x] + ((int64_t)t - c0);
-    if (lane == 0) {
-      uint32_t bad = 0u;
-      s_row[w] = live ? paged_row(a.kv, x, pos, (uint32_t)HS_DEVERR_APPEND, &bad) : -1;
-      s_live[w] = live;
-      if (blockIdx.y == 0) report(a.kv.err, bad);
-    }
-    if (lane < a.axes) s_pos[w][lane] = a.rope_pos != nullptr ? given : pos;
+    uint32_t bad = 0u;
+    s_row[w] = live ? paged_row(a.kv, x, pos, (uint32_t)HS_DEVERR_APPEND, &bad) : -1;
+    s_live[w] = live;
+    if (blockIdx.y == 0) report(a.kv.err, bad);
+    for (int i = 0; i < a.axes; ++i) s_pos[w][i] = a.rope_pos != nullptr ? a.rope_pos[(int64_t)t * a.axes + i] : pos;
   }
   __syncthreads();
-  for (uint32_t i = tid; i < (uint32_t)(nt * a.half); i += kThreads) {
-    const uint32_t t = a.angles(i), j = i - t * a.angles.d;
-    const int x = a.axis != nullptr ? min((int)a.axis[j], a.axes - 1) : 0;
-    const uint64_t turns = (uint64_t)s_pos[t][x] * a.turns[j];
-    float s, c;
-    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-    s_cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int end = min(a.tasks, (int)(blockIdx.y + 1) * a.per_cta);
-#pragma unroll 1
-  for (int task0 = (int)blockIdx.y * a.per_cta + warp; task0 < end; task0 += FLIGHT * (kThreads / 32)) {
-    Vec8 x[FLIGHT][PER], y[FLIGHT][PER];
-    float sum[FLIGHT];
-    // the loads of all heads in hand
+  auto one = [&](int t, const float* c, const float* s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    Vec8 rx[PER], ry[PER];
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      const int task = task0 + f * (kThreads / 32);
-      sum[f] = 0.f;
-      if (task >= end) continue;
-      const int kn = (task >= a.kind[1].first) + (task >= a.kind[2].first);
-      const Kind& k = a.kind[kn];
-      const uint32_t slot = (uint32_t)(task - k.first) * 32u + lane, row = slot >> k.lanes, t = k.heads(row), h = row - t * k.heads.d;
-      const bool on = t < (uint32_t)nt && (kn == 2 ? s_live[t] != 0 : s_row[t] >= 0);
+    for (int p = 0; p < PER; ++p) {
+      const uint32_t from = ring + (uint32_t)((t % kDepth * PER + p) * 1024);
+      rx[p] = lds8(from);
+      ry[p] = lds8(from + 512u);
+    }
+    Two r = {1.f, 1.f};
+    if (norm != 0) {
+      Two sum = {0.f, 0.f};
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
-        const int u = (int)(slot & ((1u << k.lanes) - 1u)) + (p << 5);
-        if (!on || u >= k.units) continue;
-        const Place at = place_of(k, u, a.interleaved);
-        const uint16_t* src = k.src + (int64_t)(t0 + (int)t) * k.ts + (int64_t)h * k.hs + at.d;
-        x[f][p] = ld8(src);
-        if (at.second != 0) y[f][p] = ld8(src + at.second);
+        const Mine& m = mine[p];
+        if (m.there && m.at.d < norm)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = fma(wide(rx[p].w[i]), wide(rx[p].w[i]), sum);
+        if (m.there && m.at.second != 0 && m.at.d + m.at.second < norm)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum = fma(wide(ry[p].w[i]), wide(ry[p].w[i]), sum);
       }
+      float all = sum.x + sum.y;
+#pragma unroll 1
+      for (int o = 1; o < lanes; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      r.x = r.y = rsqrtf(fmaf(all, per, a.eps));
     }
+    if (kn == 2 ? !s_live[t] : s_row[t] < 0) {
+      load(t + kDepth);
+      return;
+    }
+    uint16_t* dst = kn == 2 ? a.q_out + (int64_t)(t0 + t) * a.ots + (int64_t)h * a.ohs
+                            : (uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + to;
 #pragma unroll
-    for (int f = 0; f < FLIGHT; ++f) {
-      const int task = task0 + f * (kThreads / 32);
-      if (task >= end) continue;
-      const int kn = (task >= a.kind[1].first) + (task >= a.kind[2].first);
-      const Kind& k = a.kind[kn];
-      const uint32_t slot = (uint32_t)(task - k.first) * 32u + lane, row = slot >> k.lanes, t = k.heads(row), h = row - t * k.heads.d;
-      const bool on = t < (uint32_t)nt && (kn == 2 ? s_live[t] != 0 : s_row[t] >= 0);
-      float r = 1.f;
-      if (k.norm != 0) {  // the same for the whole warp
+    for (int p = 0; p < PER; ++p) {
+      const Mine& m = mine[p];
+      if (!m.there) continue;
+      Vec8 x = rx[p], y = ry[p];
+      if (norm != 0 || m.at.j >= 0 || m.at.j2 >= 0) {
+        Two v[4], w[4];
 #pragma unroll
-        for (int p = 0; p < PER; ++p) {
-          const int u = (int)(slot & ((1u << k.lanes) - 1u)) + (p << 5);
-          if (!on || u >= k.units) continue;
-          const Place at = place_of(k, u, a.interleaved);
-          if (at.d < k.norm) sum[f] += squares(x[f][p]);
-          if (at.second != 0 && at.d + at.second < k.norm) sum[f] += squares(y[f][p]);
+        for (int i = 0; i < 4; ++i) {
+          v[i] = wide(x.w[i]);
+          w[i] = wide(y.w[i]);
         }
-#pragma unroll 1
-        for (int o = 1; o < 1 << k.lanes; o <<= 1) sum[f] += __shfl_xor_sync(0xffffffffu, sum[f], o);
-        r = rsqrtf(sum[f] / (float)k.norm + a.eps);
-      }
-      if (!on) continue;
-      uint16_t* dst = kn == 2 ? a.q_out + (int64_t)(t0 + (int)t) * a.ots + (int64_t)h * a.ohs
-                              : (uint16_t*)(a.kv.base + s_row[t] * a.kv.rec) + (int)h * (a.dqk + a.dv) + (kn == 1 ? a.dqk : 0);
-      const float2* cs = s_cs + t * a.half;
+        if (m.at.d < norm)
 #pragma unroll
-      for (int p = 0; p < PER; ++p) {
-        const int u = (int)(slot & ((1u << k.lanes) - 1u)) + (p << 5);
-        if (u >= k.units) continue;
-        const Place at = place_of(k, u, a.interleaved);
-        if (k.norm != 0 || at.j >= 0 || at.j2 >= 0) {
-          float v[8], w[8];
-          widen(x[f][p], v);
-          widen(y[f][p], w);
-          if (at.d < k.norm) scale(v, k, h, at.d, r);
-          if (at.second != 0 && at.d + at.second < k.norm) scale(w, k, h, at.d + at.second, r);
-          if (a.interleaved) {
-            if (at.j >= 0) turn_inside(v, cs + at.j);
-            if (at.j2 >= 0) turn_inside(w, cs + at.j2);
-          } else if (at.j >= 0) {
+          for (int i = 0; i < 4; ++i) v[i] = mul(v[i], mul(r, m.wx[i]));
+        if (m.at.d + m.at.second < norm)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 c = cs[at.j + i];
-              const float v0 = v[i], w0 = w[i];
-              v[i] = v0 * c.x - w0 * c.y;
-              w[i] = w0 * c.x + v0 * c.y;
+          for (int i = 0; i < 4; ++i) w[i] = mul(w[i], mul(r, m.wy[i]));
+        if (a.interleaved) {
+          if (m.at.j >= 0) turn_inside(v, c + m.at.j, s + m.at.j);
+          if (m.at.j2 >= 0) turn_inside(w, c + m.at.j2, s + m.at.j2);
+        } else if (m.at.j >= 0) {
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float4 cc = *(const float4*)(c + m.at.j + 2 * i), ss = *(const float4*)(s + m.at.j + 2 * i);
+            const Two ck[2] = {{cc.x, cc.y}, {cc.z, cc.w}}, sk[2] = {{ss.x, ss.y}, {ss.z, ss.w}};
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const Two b = v[i + n], e = w[i + n];
+              v[i + n] = fma(e, Two{-sk[n].x, -sk[n].y}, mul(b, ck[n]));
+              w[i + n] = fma(b, sk[n], mul(e, ck[n]));
             }
           }
-          x[f][p] = narrow(v);
-          y[f][p] = narrow(w);
         }
-        st8(dst + at.d, x[f][p]);
-        if (at.second != 0) st8(dst + at.d + at.second, y[f][p]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x.w[i] = pack(v[i].x, v[i].y);
+          y.w[i] = pack(w[i].x, w[i].y);
+        }
       }
+      st8(dst + m.at.d, x);
+      if (m.at.second != 0) st8(dst + m.at.d + m.at.second, y);
     }
+    load(t + kDepth);  // into the place that was read, by the lane that read it
+  };
+#pragma unroll 1
+  for (int b = 0; b < nt; b += kStage) {
+    // the angles of this stage; the stage before last has been read by all
+    float* c = s_cs + (b / kStage & 1) * 2 * kStage * half;
+    float* s = c + kStage * half;
+    const int m = min(kStage, nt - b);
+    for (uint32_t i = tid; i < (uint32_t)(m * half); i += blockDim.x) {
+      const uint32_t t = a.angles(i), j = i - t * a.angles.d;
+      const int x = a.axis != nullptr ? min((int)a.axis[j], a.axes - 1) : 0;
+      const uint64_t turns = (uint64_t)s_pos[b + t][x] * a.turns[j];
+      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s[i], &c[i]);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t < m; ++t) one(b + t, c + t * half, s + t * half);
   }
 }
 
@@ -275,51 +346,55 @@ extern "C" int hs_append_normed(const hs_config* cfg, const hs_paged_kv* kv, con
   a.ohs = g.q_out_head_stride;
   a.R = cfg->num_requests;
   a.N = g.num_tokens;
-  a.dqk = cfg->head_dim_qk;
-  a.dv = mla ? 0 : cfg->head_dim_v;
   a.half = g.rotary_dim / 2;
   a.interleaved = g.interleaved;
   a.axes = n.axes;
   a.eps = n.eps;
   a.angles = div_by(a.half);
-  int most = 0, heads = 0;  // units of a head, heads of a token
+  const int dqk = cfg->head_dim_qk, dv = cfg->head_dim_v;
+  // a latent's normed values and its rotary tail are heads of their own: the first are 32 units then
+  const bool apart = mla && n.d_k_weight != nullptr && g.rotary_offset >= dv && dv < dqk;
+  int most = 0;  // units of a head
   for (int x = 0; x < 3; ++x) {
     Kind& k = a.kind[x];
-    const int H = x == 0 ? cfg->num_kv_heads : x == 1 ? (mla ? 0 : cfg->num_kv_heads) : (g.d_q != nullptr ? cfg->num_q_heads : 0);
-    k.src = (const uint16_t*)(x == 0 ? g.d_k : x == 1 ? g.d_v : g.d_q);
-    k.ts = x == 0 ? g.k_token_stride : x == 1 ? g.v_token_stride : g.q_token_stride;
-    k.hs = x == 0 ? g.k_head_stride : x == 1 ? g.v_head_stride : g.q_head_stride;
-    k.dim = x == 0 ? a.dqk : x == 1 ? a.dv : g.q_dim;
-    k.half = x == 1 ? 0 : a.half;
-    k.off = x == 0 || (x == 2 && g.q_dim == cfg->head_dim_qk) ? g.rotary_offset : 0;
+    const bool tail = x == 1 && apart;
+    const int H = x == 0 || tail ? cfg->num_kv_heads : x == 1 ? (mla ? 0 : cfg->num_kv_heads) : (g.d_q != nullptr ? cfg->num_q_heads : 0);
+    k.src = (const uint16_t*)(x == 0 ? g.d_k : x == 1 ? (tail ? (const uint16_t*)g.d_k + dv : g.d_v) : g.d_q);
+    k.ts = x == 0 || tail ? g.k_token_stride : x == 1 ? g.v_token_stride : g.q_token_stride;
+    k.hs = x == 0 || tail ? g.k_head_stride : x == 1 ? g.v_head_stride : g.q_head_stride;
+    k.dim = x == 0 ? (apart ? dv : dqk) : x == 1 ? (tail ? dqk - dv : dv) : g.q_dim;
+    k.half = (x == 0 && apart) || (x == 1 && !tail) ? 0 : a.half;
+    k.off = tail ? g.rotary_offset - dv : x == 0 || (x == 2 && g.q_dim == dqk) ? g.rotary_offset : 0;
     k.w = x == 0 ? n.d_k_weight : x == 2 ? n.d_q_weight : nullptr;
     k.wide = (x == 0 ? n.k_weight_type : n.q_weight_type) == HS_WEIGHT_FP32;
     k.whs = x == 0 ? n.k_weight_head_stride : n.q_weight_head_stride;
-    k.norm = k.w == nullptr ? 0 : mla ? cfg->head_dim_v : k.dim;
+    k.norm = k.w == nullptr ? 0 : mla ? dv : k.dim;
+    k.per = k.norm > 0 ? 1.f / (float)k.norm : 0.f;
+    k.head_rec = mla ? dqk : dqk + dv;
+    k.to = tail ? dv : x == 1 ? dqk : 0;
     k.heads = div_by(H);
     k.units = H > 0 ? head_units(k.dim, k.half, a.interleaved) : 0;
     k.lanes = log2_up(k.units < 32 ? k.units : 32);
     if (k.units > most) most = k.units;
-    heads += H;
   }
-  auto tasks_of = [&](int x, int tokens) {
-    const Kind& k = a.kind[x];
-    return k.units == 0 ? 0 : (int)((((int64_t)tokens * k.heads.d << k.lanes) + 31) >> 5);
-  };
-  auto tasks = [&](int tokens) { return tasks_of(0, tokens) + tasks_of(1, tokens) + tasks_of(2, tokens); };
-  // as many tokens a CTA, and as many CTAs a token, as in hs_append_rotated
-  a.tokens = kTokens;
-  while (a.tokens > 1 && a.N < kMinCtas * a.tokens) a.tokens >>= 1;
-  a.kind[1].first = tasks_of(0, a.tokens);
-  a.kind[2].first = a.kind[1].first + tasks_of(1, a.tokens);
-  a.tasks = tasks(a.tokens);
-  const int ctas = (int)(((int64_t)a.N + a.tokens - 1) / a.tokens);
-  int shares = 1;
-  while (shares < 64 && (int64_t)ctas * shares < 2 * kSmsHint && a.tasks / shares > kThreads / 32) shares *= 2;
-  a.per_cta = (a.tasks + shares - 1) / shares;
-  const size_t smem = (size_t)a.tokens * a.half * sizeof(float2);
-  const dim3 grid(ctas, shares), block(kThreads);
-  const cudaError_t e = most > 32 ? hs_launch_pdl(k_append_normed<2, 1>, grid, block, smem, (cudaStream_t)stream, a)
-                                  : hs_launch_pdl(k_append_normed<1, 2>, grid, block, smem, (cudaStream_t)stream, a);
+  for (int x = 0; x < 3; ++x) {
+    a.kind[x].first = a.tasks;
+    if (a.kind[x].units > 0) a.tasks += (int)((((int64_t)a.kind[x].heads.d << a.kind[x].lanes) + 31) >> 5);
+  }
+  // the warps of a token over as few CTAs as hold them, evenly; runs so long that the CTAs fill the SMs once
+  const int shares = (a.tasks + kMaxWarps - 1) / kMaxWarps, warps = (a.tasks + shares - 1) / shares;
+  const int64_t room = (int64_t)kSmsHint * (kCtas * kMaxWarps / warps);
+  const int64_t run = ((int64_t)a.N * shares + room - 1) / room;
+  a.run = run < 1 ? 1 : run > kRun ? kRun : (int)run;
+  const size_t smem = 4 * (size_t)kStage * a.half * sizeof(float) + (size_t)warps * kAhead * 1024;
+  static bool done[64];
+  if (kv->cuda_device >= 64 || !done[kv->cuda_device]) {
+    const int top = 4 * kStage * 288 * (int)sizeof(float) + kMaxWarps * kAhead * 1024;
+    if (hs_raise_smem_limit(k_append_normed<1>, top) != cudaSuccess || hs_raise_smem_limit(k_append_normed<2>, top) != cudaSuccess) return HS_ERR_CUDA;
+    if (kv->cuda_device < 64) done[kv->cuda_device] = true;
+  }
+  const dim3 grid((unsigned)(((int64_t)a.N + a.run - 1) / a.run), shares), block(32 * warps);
+  const cudaError_t e = most > 32 ? hs_launch_pdl(k_append_normed<2>, grid, block, smem, (cudaStream_t)stream, a)
+                                  : hs_launch_pdl(k_append_normed<1>, grid, block, smem, (cudaStream_t)stream, a);
   return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }

@@ -151,10 +151,20 @@ class PagedKV:
         self._err = torch.zeros((1,), dtype=torch.int32, device=pages.device)
         self._r, self._r1 = (R,), (R + 1,)
         self._q_shape, self._o_shape = (R, cfg.num_q_heads, cfg.head_dim_qk), (R, cfg.num_q_heads, cfg.head_dim_v)
-        self._prefix_sizes = {}
+        self._prefix_sizes, self._evict_sizes = {}, {}
+        self._scale = cfg.default_scale
         self._kv = _lib.hs_paged_kv(p, t, int(pages.shape[0]), int(pages.shape[1]), max_pages, self._err.data_ptr(),
                                     self.device)
         self._c_ref, self._kv_ref = ctypes.byref(self._c), ctypes.byref(self._kv)
+
+    def _empty(self, shape, dtype, stream):
+        """A tensor of this cache's device, allocated on the stream that uses it."""
+        import torch
+
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.pages.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.pages.device)
 
     def append(self, k, v, cu, start, rope: RopeTable | None = None, rope_pos=None, q=None, q_out=None,
                rotary_offset: int | None = None, stream=None, q_weight=None, k_weight=None, eps: float = 1e-6):
@@ -260,13 +270,15 @@ class PagedKV:
             f = int(first)
         if not 1 <= keep <= 2**31 - 65536 or recent < 0 or f < 0 or f + recent > keep:
             raise ValueError("keep must be positive, first and recent together at most keep")
-        need = int(self.lib.hs_evict_workspace(self._c_ref, shape[1], keep))
-        if need < 0:
-            raise HsError("hs_evict_workspace", need)
-        with torch.cuda.stream(stream):  # None: the current one
-            ws = torch.empty((need,), dtype=torch.uint8, device=lens.device)
-            if lens_out is None:
-                lens_out = torch.empty(self._r, dtype=torch.int64, device=lens.device)
+        need = self._evict_sizes.get((shape[1], keep))
+        if need is None:
+            need = int(self.lib.hs_evict_workspace(self._c_ref, shape[1], keep))
+            if need < 0:
+                raise HsError("hs_evict_workspace", need)
+            self._evict_sizes[shape[1], keep] = need
+        if lens_out is None:
+            lens_out = self._empty(self._r, torch.int64, stream)
+        ws = self._empty((need,), torch.uint8, stream)
         np_ = _fast_ptr(lens_out, torch.int64, self._r, "lens_out", self.device)
         a = _lib.pack_evict.pack(lp, wp, op, np_, fp, shape[2], shape[1], keep, f, recent, ws.data_ptr(), need)
         _check("hs_evict", self.lib.hs_evict(self._c_ref, self._kv_ref, a, _fast_stream(torch, stream, self.device)))
@@ -329,15 +341,16 @@ class PagedKV:
             if need < 0:
                 raise HsError("hs_prefix_attn_workspace", need)
             self._prefix_sizes[G, wp != 0] = need
-        s = c.default_scale if scale is None else float(scale)
-        if not abs(s) <= 2.35e38:  # times log2(e) it has to be a finite 32-bit number
-            raise ValueError("scale must be a number of magnitude 2.35e38 at most")
-        with torch.cuda.stream(stream):  # None: the current one
-            ws = torch.empty((need,), dtype=torch.uint8, device=q.device)
-            if out is None:
-                out = torch.empty(self._o_shape, dtype=bf16, device=q.device)
+        s = self._scale
+        if scale is not None:
+            s = float(scale)
+            if not abs(s) <= 2.35e38:  # times log2(e) it has to be a finite 32-bit number
+                raise ValueError("scale must be a number of magnitude 2.35e38 at most")
+        if out is None:
+            out = self._empty(self._o_shape, bf16, stream)
+        ws = self._empty((need,), torch.uint8, stream)
         op = _fast_ptr(out, bf16, self._o_shape, "out", self.device)
-        a = _lib.pack_prefix.pack(qp, lp, gp, pp, G, s, wp, cap, lists, float(decay), op, ws.data_ptr(), need)
+        a = _lib.pack_prefix.pack(qp, lp, gp, pp, G, s, wp, cap, lists, decay, op, ws.data_ptr(), need)
         _check("hs_prefix_attn", self.lib.hs_prefix_attn(self._c_ref, self._kv_ref, a, _fast_stream(torch, stream, self.device)))
         return out
 
