@@ -26,7 +26,7 @@ constexpr int kMaxWarps = 12;
 constexpr int kRun = 64;    // tokens of a CTA at most
 constexpr int kStage = 8;   // tokens whose angles are at hand; two stages
 constexpr int kCtas = 2;    // CTAs of kMaxWarps an SM
-constexpr int kAhead = 8;   // units of a lane on their way
+constexpr int kAhead = 4;   // units of a lane on their way
 
 struct Kind {
   const uint16_t* src;
@@ -219,20 +219,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, PER == 1 ? kCtas : 1) k_append
     }
     Two r = {1.f, 1.f};
     if (norm != 0) {
-      Two sum = {0.f, 0.f};
+      Two sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
       for (int p = 0; p < PER; ++p) {
         const Mine& m = mine[p];
         if (m.there && m.at.d < norm)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum = fma(wide(rx[p].w[i]), wide(rx[p].w[i]), sum);
+          for (int i = 0; i < 4; ++i) sum[i] = fma(wide(rx[p].w[i]), wide(rx[p].w[i]), sum[i]);
         if (m.there && m.at.second != 0 && m.at.d + m.at.second < norm)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum = fma(wide(ry[p].w[i]), wide(ry[p].w[i]), sum);
+          for (int i = 0; i < 4; ++i) sum[i] = fma(wide(ry[p].w[i]), wide(ry[p].w[i]), sum[i]);
       }
-      float all = sum.x + sum.y;
-#pragma unroll 1
-      for (int o = 1; o < lanes; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      float all = ((sum[0].x + sum[1].x) + (sum[2].x + sum[3].x)) + ((sum[0].y + sum[1].y) + (sum[2].y + sum[3].y));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+        if (o < lanes) all += __shfl_xor_sync(0xffffffffu, all, o);
       r.x = r.y = rsqrtf(fmaf(all, per, a.eps));
     }
     if (kn == 2 ? !s_live[t] : s_row[t] < 0) {
