@@ -489,9 +489,9 @@ bool split_of(const hs_config* c, int sms, PrefixSplit* w) {
   w->mt = div_by(w->MT);
   w->pairs = 1;
   w->tile_shift = 7;
-  w->cost = div_by(2);
-  w->cost2 = div_by(3);
-  w->begin = 1;
+  w->cost = div_by(4);
+  w->cost2 = div_by(6);
+  w->begin = 3;
   w->copies = 2;
   w->most = 256;
   w->group_rows = 3 * c->num_q_heads;

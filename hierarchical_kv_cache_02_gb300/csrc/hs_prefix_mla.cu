@@ -9,9 +9,8 @@
 //   operands of a product have one type and V is bf16 (2^-8 of a weight at most; the sum that divides is of the rounded).
 // Rows 0-63 of an accumulator are the even CTA's, in both: its first half of columns in lanes 0-63 of tensor memory, the second
 // in 64-127.  So two threads share a row, half of a tile's entries and half of the dims each.  The even CTA's warp issues for
-// both; what has landed in the odd one is passed on by an arrival on its barriers.
-// What bounds it: the chain from one value product to the next, whose weights are handed to the even CTA by an arrival with
-// release at the cluster's scope; a tile takes about 3000 cycles, its products 1800, whatever the rows in use.
+// both; what has landed in the odd one, and its weights, are passed on by warps of their own, by arrivals with release at the
+// cluster's scope on the even one's barriers.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -36,7 +35,7 @@ __device__ __forceinline__ int value_producer(int warp) { return warp == 6 ? 0 :
 constexpr int kMaskRing = 4;
 constexpr int kAhead = 4;                         // accumulators of scores
 constexpr float kLazy = 8.f;                      // log2 headroom before the running maximum is raised
-constexpr size_t kDyn = (size_t)kQ + kBlk + 2 * (kKBuf + kVBuf) + 1024;
+constexpr size_t kDyn = (size_t)kQ + 2 * kBlk + 2 * (kKBuf + kVBuf);  // from a 1 KB boundary on
 constexpr uint32_t kScores = 256;                 // first column of the scores, behind O's 256
 
 struct MlaArgs {
@@ -51,7 +50,7 @@ struct MlaControl {
   PrefixPlan plan;
   __align__(8) uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t kready[2], vready[2], qready;  // even CTA: full in both
-  uint64_t qfull, s[kAhead], p, pv, mask[kMaskRing], fin;
+  uint64_t qfull, s[kAhead], p[2], podd[2], pv[2], mask[kMaskRing], fin;  // p: even CTA; podd: odd CTA, its own warps'
   uint32_t valid[kMaskRing][2];
   float most[2][2][64];
   float2 sums[2][64];
@@ -92,8 +91,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const PrefixArgs& a = c.a;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int rank = uniform((int)cluster_rank());
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t q_u = smem_u32(smem), p_u = q_u + kQ, k_u = p_u + kBlk, v_u = k_u + 2 * kKBuf;
+  uint8_t* smem = smem_raw;
+  const uint32_t q_u = smem_u32(smem), p_u = q_u + kQ, k_u = p_u + 2 * kBlk, v_u = k_u + 2 * kKBuf;
+  if ((q_u & 1023u) != 0u) {  // all of a CTA's memory is used: there is no room to round up, and none is needed
+    if (tid == 0) report(a.kv.err, (uint32_t)HS_DEVERR_TIMEOUT);
+    return;
+  }
   volatile uint32_t* abort = &ct.abort;
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -107,11 +110,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kAhead; ++i) mbar_init(&ct.s[i], 1u);
     mbar_init(&ct.qready, 2u);
     mbar_init(&ct.qfull, 1u);
-    mbar_init(&ct.p, 8u);
-    mbar_init(&ct.pv, 1u);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ct.p[i], 5u);
+      mbar_init(&ct.podd[i], 4u);
+      mbar_init(&ct.pv[i], 1u);
+    }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], 2u);
     mbar_init(&ct.fin, 1u);
-    prefix_plan_init(&ct.plan, rank == 0 ? 11 : 10);  // the warps that read it: not the odd CTA's products' one
+    prefix_plan_init(&ct.plan, 11);  // the warps that read it
     ct.abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -276,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           WaitLimit limit;
 #pragma unroll 1
           for (;;) {
-            const bool y0 = cluster_test(&ct.p, (uint32_t)(nt & 1)), y1 = cluster_test(&ct.vready[b], vq),
+            const bool y0 = cluster_test(&ct.p[b], vq), y1 = cluster_test(&ct.vready[b], vq),
                        y2 = cluster_test(&ct.kready[bs], kq), y3 = !kfirst || cluster_test(&ct.qready, (uint32_t)(nq & 1));
             ok = __all_sync(0xffffffffu, ahead != 0 && y0 && y1);
             if (ok) break;
@@ -311,10 +317,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma2_bf16_lo<kVGroup>(tu + 128u * h, dp + 2 * ks, y + 2 * h * 64 + ks * (2 * kVGroup >> 4), id_o,
+              umma2_bf16_lo<kVGroup>(tu + 128u * h, dp + (uint32_t)(b * (kBlk >> 4)) + 2 * ks, y + 2 * h * 64 + ks * (2 * kVGroup >> 4), id_o,
                                      (!vfirst || ks != 0) ? 1u : 0u);
           umma2_commit(&ct.vempty[b]);
-          umma2_commit(&ct.pv);
+          umma2_commit(&ct.pv[b]);
         }
         __syncwarp();
         ++nt;
@@ -323,6 +329,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (vfirst) {
           if (lane == 0) mbar_arrive(&plan->empty[vp % kPrefixRing]);
           vl = tiles_of(++vp);  // the scores' place is there already
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ---------------- the odd CTA's weights, passed on to the even one ----------------
+      // (Its softmax does not wait for that: an arrival with release at the cluster's scope takes 0.8 us, half of a tile's time.)
+      const uint32_t p_bar = in_cta(smem_u32(ct.p), 0);
+#pragma unroll 1
+      for (int pi = 0;; ++pi) {
+        const PPortion P = portion_take(plan, pi, true, &ok, abort);
+        if (P.t0 == P.t1) break;
+#pragma unroll 1
+        for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
+          if (ok) ok = warp_wait_small(&ct.podd[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
+          tc_fence_after();
+          tc_fence_before();
+          if (ok && lane == 0) cluster_arrive(p_bar + 8u * (nt & 1));
         }
       }
     } else if (warp == kPassKeys || warp == kPassValues) {
@@ -343,7 +365,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
           if (ok) ok = warp_wait_small(&full[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (ok && lane == 0) cluster_arrive(ready + 8u * (nt & 1));
+          if (ok && lane == 0) {
+            if (rank == 0) mbar_arrive(&(keys ? ct.kready : ct.vready)[nt & 1]);
+            else cluster_arrive(ready + 8u * (nt & 1));
+          }
         }
       }
     } else if (warp < 4) {
@@ -351,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (A warp comes together, by a vote or __syncwarp, behind each branch that its lanes may take apart: accesses to tensor memory
       // are the whole warp's, and nothing else promises that it is whole there.)
       const int row = tid & 63, half = tid >> 6;
-      const uint32_t lane_base = (uint32_t)(warp * 32) << 16, p_bar = in_cta(smem_u32(&ct.p), 0);
+      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
       auto pair_sync = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + (warp & 1)) : "memory"); };
       auto load_q = [&](int i) {  // of portion i, by the first thread
         if (!portion_wait(plan, i, abort)) return;
@@ -398,8 +423,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pair_sync();
           if (live) {
             mx = fmaxf(mx, ct.most[b][half ^ 1][row]);
-            // the value product before this tile's: O may be rescaled, and P rewritten, once it is complete
-            const bool done = nt == 0 || mbar_test(&ct.pv, (uint32_t)((nt - 1) & 1));
             const bool raise = mx > m + kLazy;
             const bool any = __any_sync(0xffffffffu, raise);
             const float mo = m;
@@ -425,7 +448,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; j += 8) st_global_v8(keep + j, v + j);
             }
             if (W) __syncwarp();
-            if (!done) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+            // P's place is free once the product two tiles before is complete; O may be rescaled once the last one is
+            if (nt > 1) ok = mbar_wait_small(&ct.pv[b], (uint32_t)(((nt >> 1) - 1) & 1), abort);
+            if (any && tile != P.t0 && ok) ok = mbar_wait_small(&ct.pv[b ^ 1], (uint32_t)(((nt - 1) >> 1) & 1), abort);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (any) {
@@ -449,19 +474,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // P, K-major and swizzled like the queries: 64 entries are one 128-byte row
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              *(uint4*)(smem + kQ + row * 128 + (((4 * half + x) ^ (row & 7)) << 4)) =
+              *(uint4*)(smem + kQ + b * kBlk + row * 128 + (((4 * half + x) ^ (row & 7)) << 4)) =
                   make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          } else if (ok && nt > 0) {
-            ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);  // no phase of it may pass unseen
+          } else if (ok && nt > 1) {
+            ok = mbar_wait_small(&ct.pv[b], (uint32_t)(((nt >> 1) - 1) & 1), abort);  // no phase of it may pass unseen
             ok = __all_sync(0xffffffffu, ok);
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) cluster_arrive(p_bar);
+          if (lane == 0) mbar_arrive(rank == 0 ? &ct.p[b] : &ct.podd[b]);
         }
         // the portion's partial sums
-        if (ok) ok = mbar_wait_small(&ct.pv, (uint32_t)((nt - 1) & 1), abort);
+        if (ok) ok = mbar_wait_small(&ct.pv[(nt - 1) & 1], (uint32_t)(((nt - 1) >> 1) & 1), abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         ct.sums[half][row] = make_float2(l, le);
