@@ -20,6 +20,7 @@ struct EvictArgs {
   const int64_t* first_of;  // [R] or null: first
   int64_t cap;              // entries of a list of weights
   int R, lists, keep, first, recent;
+  int page_shift;           // log2 of the tokens of a page, -1: no power of two
   int2* move;               // [R][lists][keep]: source and destination row of entry i, where they differ
   float* w_tmp;             // [R][lists][keep]
   int2* meta;               // [R][lists]: entries that stay, first of them that moves
@@ -27,12 +28,14 @@ struct EvictArgs {
 
 // ---- the choice ----------------------------------------------------------------------------------
 //
-// The m-th largest weight by radix selection (11, 11 and 10 bits) over keys that order as the weights do, then one ordered
-// pass that gives every entry that stays its place.  A warp takes a contiguous run of entries in that pass, so two barriers
-// are enough; the weights wait in shared memory where they fit.
+// The m-th largest weight by radix selection, 11 bits at a time, over keys that order as the weights do, less the smallest of them
+// (weights crowd into a few exponents: without that most of a warp's counts meet in the same bins); then one ordered pass that
+// gives every entry that stays its place.  A warp takes a contiguous run of entries in that pass, so two barriers are enough; the
+// weights and the request's pages wait in shared memory where they fit.
 
 constexpr int kPickThreads = 1024, kBins = 2048;
-constexpr int kCached = 48 * 1024;  // weights kept in shared memory at most
+constexpr int kCached = 44 * 1024;  // weights kept in shared memory at most
+constexpr int kPages = 4 * 1024;    // entries of the page table, likewise
 
 // orders as the weights: NaN above everything, -0 as 0
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -41,9 +44,23 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, int cached) {
-  extern __shared__ float s_w[];
+// paged_row of a position within the pages, whose first table entries are at hand
+__device__ __forceinline__ int row_of(const PagedRows& c, int shift, const int32_t* first, int count, int r, int p, uint32_t* bad) {
+  const int pg = shift >= 0 ? p >> shift : (int)((unsigned)p / (unsigned)c.page_tokens);
+  int page;
+  if (pg < count) page = first[pg];
+  else page = c.table != nullptr ? c.table[(int64_t)r * c.max_pages + pg] : r * c.max_pages + pg;
+  if ((unsigned)page >= (unsigned)c.num_pages) {
+    *bad |= (uint32_t)HS_DEVERR_PAGE;
+    return -1;
+  }
+  return page * c.page_tokens + (p - pg * c.page_tokens);  // below 2^31, as all rows are
+}
+
+__global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, int cached, int pages) {
+  extern __shared__ float s_w[];  // weights, then the page table
   __shared__ int s_hist[kBins], s_warp[32], s_eq[32], s_bin, s_want, s_hole;
+  __shared__ uint32_t s_min, s_max;
   hs_pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int list = blockIdx.x, r = blockIdx.y;
@@ -62,24 +79,45 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
   }
   const int n = (int)n64, f = (int)f64, to = n - a.recent;  // the weights decide in [f, to)
   const bool in_smem = n <= cached;
-  if (in_smem)
-    for (int i = tid; i < n; i += kPickThreads) s_w[i] = w[i];
-  if (tid == 0) s_hole = n;
+  int32_t* s_pages = (int32_t*)(s_w + cached);
+  if (tid == 0) {
+    s_hole = n;
+    s_min = 0xffffffffu;
+    s_max = 0u;
+  }
+  __syncthreads();
+  for (int i = tid; i < pages; i += kPickThreads) s_pages[i] = a.kv.table[(int64_t)r * a.kv.max_pages + i];
+  uint32_t least = 0xffffffffu, most = 0u;
+  for (int i = tid; i < n; i += kPickThreads) {
+    const float x = w[i];
+    if (in_smem) s_w[i] = x;
+    if (i >= f && i < to) {
+      least = min(least, key_of(x));
+      most = max(most, key_of(x));
+    }
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    atomicMin(&s_min, least);
+    atomicMax(&s_max, most);
+  }
   const float* src = in_smem ? s_w : w;
-  uint32_t limit = 0xffffffffu, mask = 0u;  // the key of the last one chosen, the bits of it that are known
-  int want = a.keep - f - a.recent;         // of those with the known bits, how many stay
+  uint32_t limit = 0xffffffffu;      // the key of the last one chosen
+  int want = a.keep - f - a.recent;  // of those at it, how many stay
   if (want > 0) {
-    limit = 0u;
+    __syncthreads();
+    limit = s_min;  // the least key of those that are counted; `shift`: log2 of the keys of a bin
+    uint32_t span = s_max - limit;
+    int shift = max(0, 21 - __clz(span));
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-      __syncthreads();
+    for (;;) {
       s_hist[tid] = 0;
       s_hist[tid + kPickThreads] = 0;
       __syncthreads();
       for (int i = f + tid; i < to; i += kPickThreads) {
-        const uint32_t k = key_of(src[i]);
-        if ((k & mask) == limit) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+        const uint32_t k = key_of(src[i]) - limit;
+        if (k <= span) atomicAdd(&s_hist[k >> shift], 1);
       }
       __syncthreads();
       // entries in the bins above a thread's two
@@ -92,9 +130,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
       }
       if (lane == 0) s_warp[warp] = incl;
       __syncthreads();
-      int above = lane > warp ? s_warp[lane] : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+      int above = __reduce_add_sync(0xffffffffu, lane > warp ? s_warp[lane] : 0);
       above += incl - h0 - h1;
       if (above < want && want <= above + h1) {
         s_bin = 2 * tid + 1;
@@ -104,14 +140,17 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
         s_want = want - above - h1;
       }
       __syncthreads();
-      limit |= (uint32_t)s_bin << shift;
-      mask |= (uint32_t)(bins - 1) << shift;
+      limit += (uint32_t)s_bin << shift;
       want = s_want;
+      if (shift == 0) break;
+      span = (1u << shift) - 1u;
+      shift = max(0, shift - 11);
     }
   }
   // places: those that stay for sure (more weight, or first or recent), and the first `want` of those at the limit
   const int run = ((n + 31) / 32 + 31) / 32 * 32, p0 = warp * run, p1 = min(n, p0 + run);
   int sure = 0, eq = 0, hole = n;
+  uint32_t bits = 0u;
   __syncthreads();
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -144,11 +183,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
           if (in_smem) w_out[rank] = x;
           else a.w_tmp[at * a.keep + rank] = x;
           if (rank != p) {
-            uint32_t err = 0u;
-            const int64_t from = paged_row(a.kv, r, p, (uint32_t)HS_DEVERR_LOC, &err);
-            const int64_t dst = paged_row(a.kv, r, rank, (uint32_t)HS_DEVERR_LOC, &err);
-            a.move[at * a.keep + rank] = make_int2((int)from, (int)dst);
-            report(a.kv.err, err);
+            a.move[at * a.keep + rank] = make_int2(row_of(a.kv, a.page_shift, s_pages, pages, r, p, &bits), row_of(a.kv, a.page_shift, s_pages, pages, r, rank, &bits));
           }
         } else {
           hole = min(hole, p);
@@ -161,6 +196,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) hole = min(hole, __shfl_xor_sync(0xffffffffu, hole, o));
   if (lane == 0) atomicMin(&s_hole, hole);
+  report(a.kv.err, bits);
   __syncthreads();
   if (!in_smem)
     for (int i = tid; i < a.keep; i += kPickThreads) w_out[i] = a.w_tmp[at * a.keep + i];
@@ -264,16 +300,20 @@ extern "C" int hs_evict(const hs_config* cfg, const hs_paged_kv* kv, const hs_ev
   a.keep = g.keep;
   a.first = g.first;
   a.recent = g.recent;
+  a.page_shift = -1;
+  for (int x = 0; x < 31; ++x)
+    if (kv->page_tokens == 1 << x) a.page_shift = x;
   a.meta = (int2*)g.d_workspace;
   a.move = (int2*)((uint8_t*)g.d_workspace + meta_bytes(cfg, g.lists));
   a.w_tmp = (float*)(a.move + (int64_t)a.R * a.lists * a.keep);
   const int cached = (int)(g.capacity < kCached ? g.capacity : kCached);
+  const int pages = kv->d_table == nullptr ? 0 : kv->max_pages < kPages ? kv->max_pages : kPages;
   static bool done[64];
   if (kv->cuda_device >= 64 || !done[kv->cuda_device]) {
-    if (hs_raise_smem_limit(k_evict_pick, kCached * (int)sizeof(float)) != cudaSuccess) return HS_ERR_CUDA;
+    if (hs_raise_smem_limit(k_evict_pick, (kCached + kPages) * 4) != cudaSuccess) return HS_ERR_CUDA;
     if (kv->cuda_device < 64) done[kv->cuda_device] = true;
   }
-  cudaError_t e = hs_launch_pdl(k_evict_pick, dim3(a.lists, a.R), dim3(kPickThreads), cached * sizeof(float), (cudaStream_t)stream, a, cached);
+  cudaError_t e = hs_launch_pdl(k_evict_pick, dim3(a.lists, a.R), dim3(kPickThreads), (cached + pages) * 4, (cudaStream_t)stream, a, cached, pages);
   if (e != cudaSuccess) return HS_ERR_CUDA;
   // as wide a slice as still gives every SM two CTAs
   const int64_t share = a.kv.rec / a.lists;
