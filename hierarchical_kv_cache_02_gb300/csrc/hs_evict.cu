@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
   __shared__ int s_hist[kBins], s_warp[32], s_eq[32], s_bin, s_want, s_hole;
   __shared__ uint32_t s_min, s_max;
   hs_pdl_wait();
+  // the only kernel that may start early is this call's own second one, which waits for this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int list = blockIdx.x, r = blockIdx.y;
   const int64_t n64 = a.len[r], f64 = a.first_of != nullptr ? a.first_of[r] : a.first;

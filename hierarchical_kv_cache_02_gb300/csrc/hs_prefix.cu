@@ -20,27 +20,32 @@ namespace {
 // group of 8 values of a head (head dims up to 576 = 72 groups: at most three).  It reads a record once for every query head, and
 // a shared one for every request.
 
+constexpr int kAnyJoinThreads = 256;
 constexpr int kAnyWarps = 4, kAnyGroups = 3, kAnyParts = 64;
 
-__global__ void __launch_bounds__(1024) k_prefix_check(const PrefixArgs a) {
+// What the tensor cores' kernels find out on their way: whether the groups are sound, and the requests.
+__global__ void __launch_bounds__(1024) k_prefix_check(const PrefixArgs a, PrefixRequest* of) {
   hs_pdl_wait();
   const int tid = threadIdx.x;
   const bool ok = __syncthreads_and(bounds_ok(a, tid, 1024)) != 0;
   uint32_t bad = ok ? 0u : (uint32_t)HS_DEVERR_LOC;
   if (ok)
     for (int g = tid; g < a.ngroups; g += 1024) group_segment(a, g, &bad);
-  if (tid == 0) *a.ok = ok;
+  for (int r = tid; r < a.R; r += 1024) {
+    int g;
+    const Segment shared = shared_segment(a, r, ok, &g), own = own_segment(a, r, shared.p1, &bad);
+    of[r] = PrefixRequest{0, own.p0, own.p1, g, shared.r0, shared.nr, 0};
+  }
   report(a.kv.err, bad);
 }
 
-__global__ void __launch_bounds__(kAnyWarps * 32) k_prefix_any(const PrefixArgs a, float* part, float* ml, int parts) {
+__global__ void __launch_bounds__(kAnyWarps * 32) k_prefix_any(const PrefixArgs a, const PrefixRequest* of, float* part, float* ml, int parts) {
   __shared__ float s_acc[kAnyWarps][kAnyGroups * 32 * 8];
   __shared__ float s_m[kAnyWarps], s_l[kAnyWarps];
   hs_pdl_wait();
   const int h = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t bad = 0u;
-  int g;
-  const Segment sg = shared_segment(a, r, *a.ok != 0, &g), own = own_segment(a, r, sg.p1, &bad);
+  const PrefixRequest own = of[r];
   // parts of whole groups of 32 positions
   const int chunks = (int)(((unsigned)own.p1 + 31u) >> 5), each = (chunks + parts - 1) / parts;
   const int64_t e0 = 32 * (int64_t)each * blockIdx.z;
@@ -64,7 +69,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) k_prefix_any(const PrefixArgs 
   }
   float m = -INFINITY, l = 0.f;
   for (int64_t p = e0 + warp; p < e1; p += kAnyWarps) {
-    const int64_t at = paged_row(a.kv, p < own.p0 ? sg.lead : r, p, (uint32_t)HS_DEVERR_LOC, &bad);
+    const int64_t at = paged_row(a.kv, p < own.p0 ? own.r0 : r, p, (uint32_t)HS_DEVERR_LOC, &bad);
     float s = -INFINITY;
     const uint16_t* kp = (const uint16_t*)(a.kv.base + at * a.kv.rec) + koff;
     if (at >= 0) {
@@ -136,9 +141,9 @@ __global__ void __launch_bounds__(kAnyWarps * 32) k_prefix_any(const PrefixArgs 
   if (threadIdx.x == 0) *(float4*)(ml + 4 * to) = make_float4(M, L, L, 0.f);
 }
 
-__global__ void __launch_bounds__(kPrefixJoinThreads) k_prefix_any_join(const PrefixArgs a, const float* part, const float* ml, int parts) {
+__global__ void __launch_bounds__(kAnyJoinThreads) k_prefix_any_join(const PrefixArgs a, const float* part, const float* ml, int parts) {
   hs_pdl_wait();
-  const int vecs = a.dv >> 3, at = blockIdx.x * kPrefixJoinThreads + threadIdx.x, r = blockIdx.y;
+  const int vecs = a.dv >> 3, at = blockIdx.x * kAnyJoinThreads + threadIdx.x, r = blockIdx.y;
   if (at >= a.Hq * vecs) return;
   const int h = at / vecs, d = 8 * (at - h * vecs);
   const long long row = ((long long)r * a.Hq + h) * parts;
@@ -149,27 +154,41 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) k_prefix_any_join(const Pr
 
 // ---- weights -------------------------------------------------------------------------------------
 
-constexpr int kWeighThreads = 256;
+constexpr int kWeighThreads = 256, kWeighEach = 4;
 
-// CTAs share a request's list; a thread takes every so many-th position and sums over the list's query heads.
-__global__ void __launch_bounds__(kWeighThreads) k_prefix_weigh(const PrefixArgs a) {
+// CTAs share a request's list; a thread takes kWeighEach positions at a time and sums over the list's query heads.  A round trip
+// for the request's place, one for the statistics, one for the scores: 4.6 us XX
+__global__ void __launch_bounds__(kWeighThreads) k_prefix_weigh(const PrefixArgs a, const PrefixRequest* of) {
+  __shared__ float2 s_stats[1024];
   hs_pdl_wait();
   const int list = blockIdx.y, r = blockIdx.z, heads = a.Hq / a.lists;
-  uint32_t bad = 0u;
-  int g;
-  const Segment sg = shared_segment(a, r, *a.ok != 0, &g), own = own_segment(a, r, sg.p1, &bad);
-  if (own.p1 > a.cap && threadIdx.x == 0 && blockIdx.x == 0 && list == 0) report(a.kv.err, (uint32_t)HS_DEVERR_LOC);
-  const int end = (int)min((int64_t)own.p1, a.cap);
-  float* w = a.weights + ((int64_t)r * a.lists + list) * a.cap;
+  const PrefixRequest q = of[r];
+  if (q.p1 > a.cap && threadIdx.x == 0 && blockIdx.x == 0 && list == 0) report(a.kv.err, (uint32_t)HS_DEVERR_LOC);
+  const int64_t end = min((int64_t)q.p1, a.cap), each = (int64_t)gridDim.x * kWeighThreads * kWeighEach;
+  int64_t p = q.p0 + (int64_t)blockIdx.x * kWeighThreads * kWeighEach + threadIdx.x;
+  if (p - threadIdx.x >= end) return;  // the whole CTA
   const int64_t h0 = (int64_t)r * a.Hq + list * heads;
-  for (int64_t p = own.p0 + (int64_t)blockIdx.x * kWeighThreads + threadIdx.x; p < end; p += (int64_t)gridDim.x * kWeighThreads) {
-    float sum = 0.f;
-#pragma unroll 4
-    for (int h = 0; h < heads; ++h) {
-      const float2 st = a.stats[h0 + h];
-      sum = fmaf(exp2f(a.scores[(h0 + h) * a.score_cols + p] - st.x), st.y, sum);
+  for (int h = threadIdx.x; h < heads; h += kWeighThreads) s_stats[h] = a.stats[h0 + h];
+  __syncthreads();
+  float* w = a.weights + ((int64_t)r * a.lists + list) * a.cap;
+  for (; p < end; p += each) {
+    float sum[kWeighEach], old[kWeighEach];
+#pragma unroll
+    for (int x = 0; x < kWeighEach; ++x) {
+      sum[x] = 0.f;
+      old[x] = p + x * kWeighThreads < end ? w[p + x * kWeighThreads] : 0.f;
     }
-    w[p] = fmaf(a.decay, w[p], sum);
+    const float* s = a.scores + h0 * a.score_cols + p;
+#pragma unroll 4
+    for (int h = 0; h < heads; ++h, s += a.score_cols) {
+      const float2 st = s_stats[h];
+#pragma unroll
+      for (int x = 0; x < kWeighEach; ++x)
+        if (p + x * kWeighThreads < end) sum[x] = fmaf(exp2f(s[x * kWeighThreads] - st.x), st.y, sum[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < kWeighEach; ++x)
+      if (p + x * kWeighThreads < end) w[p + x * kWeighThreads] = fmaf(a.decay, old[x], sum[x]);
   }
 }
 
@@ -283,8 +302,8 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
     a.voff = cfg->head_dim_qk;
   }
   a.qscale = g.scale * kLog2e;
-  PrefixSplit none;
-  hs_prefix_head(ws, g.groups, &none, &a.ok);
+  PrefixSplit head;
+  hs_prefix_head(ws, g.groups, &head);
   if (weigh) {
     a.weights = g.d_weights;
     a.cap = g.capacity;
@@ -301,20 +320,20 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
   } else {
     float* part = (float*)(ws + l.partials);
     float* ml = part + (int64_t)a.R * a.Hq * l.parts * a.dv;
-    cudaError_t e = hs_launch_pdl(k_prefix_check, dim3(1), dim3(1024), 0, st, a);
+    cudaError_t e = hs_launch_pdl(k_prefix_check, dim3(1), dim3(1024), 0, st, a, head.of);
     if (e == cudaSuccess)
-      e = hs_launch_pdl(k_prefix_any, dim3(a.Hq, a.R, l.parts), dim3(kAnyWarps * 32), 0, st, a, part, ml, l.parts);
+      e = hs_launch_pdl(k_prefix_any, dim3(a.Hq, a.R, l.parts), dim3(kAnyWarps * 32), 0, st, a, (const PrefixRequest*)head.of, part, ml, l.parts);
     if (e == cudaSuccess)
-      e = hs_launch_pdl(k_prefix_any_join, dim3((a.Hq * (a.dv / 8) + kPrefixJoinThreads - 1) / kPrefixJoinThreads, a.R),
-                        dim3(kPrefixJoinThreads), 0, st, a, (const float*)part, (const float*)ml, l.parts);
+      e = hs_launch_pdl(k_prefix_any_join, dim3((a.Hq * (a.dv / 8) + kAnyJoinThreads - 1) / kAnyJoinThreads, a.R),
+                        dim3(kAnyJoinThreads), 0, st, a, (const float*)part, (const float*)ml, l.parts);
     if (e != cudaSuccess) return HS_ERR_CUDA;
   }
   if (weigh) {
     // a few CTAs an SM in all; the positions that there are is known on the device alone
-    const int64_t lists = (int64_t)a.R * a.lists, most = (a.cap + kWeighThreads - 1) / kWeighThreads;
+    const int64_t lists = (int64_t)a.R * a.lists, most = (a.cap + kWeighThreads * kWeighEach - 1) / (kWeighThreads * kWeighEach);
     int64_t ctas = (8ll * sms + lists - 1) / lists;
     ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
-    if (hs_launch_pdl(k_prefix_weigh, dim3((unsigned)ctas, a.lists, a.R), dim3(kWeighThreads), 0, st, a) != cudaSuccess) return HS_ERR_CUDA;
+    if (hs_launch_pdl(k_prefix_weigh, dim3((unsigned)ctas, a.lists, a.R), dim3(kWeighThreads), 0, st, a, (const PrefixRequest*)head.of) != cudaSuccess) return HS_ERR_CUDA;
   }
   return HS_OK;
 }

@@ -18,7 +18,6 @@ struct PrefixArgs {
   float* scores;          // [R][Hq][score_cols], in units of log2, with weights
   int64_t score_cols;
   float2* stats;          // [R][Hq] maximum and 1 / sum of each row, with weights
-  int* ok;                // whether the groups' bounds ascend within [0, R], written by the first kernel
   int R, ngroups, Hq, Hkv, dqk, dv, lists;
   int kstride, voff;      // values: KV head g's key at g * kstride, its value voff further on
   float qscale;           // scale * log2(e)
@@ -250,10 +249,7 @@ __device__ __forceinline__ void prefix_start(const PrefixArgs& a, const PrefixSp
     }
     sh = Shares(total, w.workers);
     start = sh.start(worker);
-    if (blockIdx.x == 0 && tid == 0) {
-      w.units[G] = total;
-      *a.ok = ok;
-    }
+    if (blockIdx.x == 0 && tid == 0) w.units[G] = total;
     if (blockIdx.x != 0 && !(start >= before && start < before + mine)) break;
   }
   __syncthreads();
@@ -370,8 +366,6 @@ __device__ __forceinline__ PPortion portion_take(PrefixPlan* s, int i, bool done
 
 // ---- joining ---------------------------------------------------------------------------------------
 
-constexpr int kPrefixJoinThreads = 256;
-
 // The running sum of a row's partials: 8 of its dims, maximum, sums of rounded and of exact weights.
 struct Joined {
   float m = -INFINITY, l = 0.f, le = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -436,33 +430,47 @@ struct Pieces {
 // A CTA joins the rows of a request that are together in all partials: the G of a KV head, or (flat) one.  Its first threads find
 // the partials' places, kPrefixList at a time; then a thread takes 8 dims of a row from every `slices`-th partial, kPrefixAhead of
 // them on their way at a time, and the slices are summed in order.
+// What it costs is a chain of round trips, and instructions met for the first time: it starts while the attention still runs, and
+// goes through the first of them once on made-up numbers (16.9 us instead of XX for the call on 2 x 1000 positions).
 constexpr int kPrefixAhead = 4, kPrefixList = 64;
 
-template <int DV>
-__global__ void __launch_bounds__(kPrefixJoinThreads, 3) k_prefix_join(const PrefixArgs a, const PrefixSplit w, int slices) {
+template <int DV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const PrefixArgs a, const PrefixSplit w, int slices) {
   constexpr int vecs = DV >> 3;
   __shared__ Pieces s_piece[2];  // of its own segment, of its group's
   __shared__ long long s_share[2];
   __shared__ int s_row[kPrefixList];
-  __shared__ float s_acc[kPrefixJoinThreads][8];
-  __shared__ float4 s_ml[kPrefixJoinThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float s_acc[THREADS][8];
+  __shared__ float4 s_ml[THREADS];
   const int tid = threadIdx.x, r = blockIdx.x, rows = w.flat ? 1 : w.G, h0 = blockIdx.y * rows, units = rows * vecs;
-  if (tid < 2) {  // a thread a segment
-    const PrefixRequest q = w.of[r];
-    const Shares sh(w.units[a.ngroups], w.workers);
-    const bool group = tid == 1;
-    const Segment sg = !group ? Segment{r, r, 1, q.p0, q.p1} : Segment{q.r0, q.r0, q.nr, 0, q.g >= 0 ? q.p0 : 0};
-    s_piece[tid].n = 0;
-    if (q.p1 > 0) s_piece[tid].of(a, w, sh, sg, group, !group ? q.units : q.g > 0 ? w.units[q.g] : 0, r, h0);
-    if (!group) {
-      s_share[0] = sh.per;
-      s_share[1] = sh.more;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass != 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      // only this call's own last kernel may start early, which waits for this one
+      if (a.weights != nullptr) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    if (tid < 2) {  // a thread a segment
+      PrefixRequest q{0, 0, 64, -1, r, 1, 0};
+      long long total = 4 * w.workers;
+      if (pass != 0) {
+        q = w.of[r];
+        total = w.units[a.ngroups];
+      }
+      const Shares sh(total, w.workers);
+      const bool group = tid == 1;
+      const Segment sg = !group ? Segment{r, r, 1, q.p0, q.p1} : Segment{q.r0, q.r0, q.nr, 0, q.g >= 0 ? q.p0 : 0};
+      s_piece[tid].n = 0;
+      if (q.p1 > 0) s_piece[tid].of(a, w, sh, sg, group, !group ? q.units : q.g > 0 ? w.units[q.g] : 0, r, h0);
+      if (!group) {
+        s_share[0] = sh.per;
+        s_share[1] = sh.more;
+      }
     }
   }
-  const int u0 = units * slices <= kPrefixJoinThreads ? tid % units : tid, slice = units * slices <= kPrefixJoinThreads ? tid / units : 0;
+  const int u0 = units * slices <= THREADS ? tid % units : tid, slice = units * slices <= THREADS ? tid / units : 0;
 #pragma unroll 1
-  for (int ub = 0; ub < units; ub += kPrefixJoinThreads) {  // more than one turn: more rows than threads, one slice
+  for (int ub = 0; ub < units; ub += THREADS) {  // more than one turn: more rows than threads, one slice
     const int u = ub + u0, x = u / vecs, vec = u - x * vecs;
     const bool on = u < units && slice < slices;
     Joined sum;
@@ -513,12 +521,18 @@ __global__ void __launch_bounds__(kPrefixJoinThreads, 3) k_prefix_join(const Pre
   }
 }
 
-template <int DV>
-cudaError_t launch_join(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t st) {
+template <int DV, int THREADS>
+cudaError_t launch_join_by(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t st) {
   const int rows = w.flat ? 1 : w.G, units = rows * (DV / 8);
   int slices = 1;
-  while (2 * slices * units <= kPrefixJoinThreads) slices *= 2;
-  return hs_launch_pdl(k_prefix_join<DV>, dim3(a.R, a.Hq / rows), dim3(kPrefixJoinThreads), 0, st, a, w, slices);
+  while (2 * slices * units <= THREADS) slices *= 2;
+  return hs_launch_pdl(k_prefix_join<DV, THREADS>, dim3(a.R, a.Hq / rows), dim3(THREADS), 0, st, a, w, slices);
+}
+template <int DV>
+cudaError_t launch_join(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t st) {
+  // as many threads as the SMs hold at once: few CTAs have twice as many, for twice as many slices
+  const bool few = (int64_t)a.R * (a.Hq / (w.flat ? 1 : w.G)) <= kSmsHint;
+  return few ? launch_join_by<DV, 512>(a, w, st) : launch_join_by<DV, 256>(a, w, st);
 }
 
 }  // namespace
@@ -529,13 +543,12 @@ cudaError_t launch_join(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t 
 struct hs_prefix_plan {
   int64_t rows;
 };
-// The start of the workspace: units of the groups, the groups' soundness, the requests.
+// The start of the workspace: units of the groups, the requests.
 inline int64_t hs_prefix_head_bytes(int64_t groups, int64_t requests) {
-  return ((groups + 2) * (int64_t)sizeof(long long) + 15) / 16 * 16 + requests * (int64_t)sizeof(PrefixRequest);
+  return ((groups + 1) * (int64_t)sizeof(long long) + 15) / 16 * 16 + requests * (int64_t)sizeof(PrefixRequest);
 }
-inline void hs_prefix_head(void* ws, int groups, PrefixSplit* w, int** ok) {
+inline void hs_prefix_head(void* ws, int groups, PrefixSplit* w) {
   w->units = (long long*)ws;
-  *ok = (int*)(w->units + groups + 1);
   w->of = (PrefixRequest*)((uint8_t*)ws + hs_prefix_head_bytes(groups, 0));
 }
 hs_prefix_plan hs_prefix_gqa_plan(const hs_config* c, int num_sms);

@@ -525,7 +525,7 @@ int hs_prefix_gqa_launch(const hs_config* cfg, const void* prefix_args, void* he
   c.a = *(const PrefixArgs*)prefix_args;
   if (!split_of(cfg, num_sms, &c.w)) return HS_ERR_CONFIG;
   const int D = c.a.dqk;
-  hs_prefix_head(head, c.a.ngroups, &c.w, &c.a.ok);
+  hs_prefix_head(head, c.a.ngroups, &c.w);
   c.w.part = (float*)partials;
   c.w.ml = c.w.part + hs_prefix_gqa_plan(cfg, num_sms).rows * D;
   if (c.a.qscale < 0.f) {

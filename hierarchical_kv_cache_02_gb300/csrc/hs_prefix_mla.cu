@@ -592,7 +592,7 @@ int hs_prefix_mla_launch(const hs_config* cfg, const void* prefix_args, void* he
   MlaArgs c{};
   c.a = *(const PrefixArgs*)prefix_args;
   split_of(cfg, num_sms, &c.w);
-  hs_prefix_head(head, c.a.ngroups, &c.w, &c.a.ok);
+  hs_prefix_head(head, c.a.ngroups, &c.w);
   c.w.part = (float*)partials;
   c.w.ml = c.w.part + hs_prefix_mla_plan(cfg, num_sms).rows * kValue;
   if (c.a.qscale < 0.f) {
