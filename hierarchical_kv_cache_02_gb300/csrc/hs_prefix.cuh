@@ -117,7 +117,9 @@ struct PrefixSplit {
   int workers;
   long long* units;      // [ngroups + 1] before each group's segment and in all, written by the first CTA
   struct PrefixRequest* of; // [R], likewise
-  float *part, *ml;      // [rows][dv], [rows][4]: maximum (base 2), sum of rounded weights, of exact ones
+  int together;          // rows that a CTA of the join takes: they are neighbours in all their partials
+  float *part, *ml;      // of each copy of a portion [dv / 8][rows][8], so that neighbouring rows are stored side by side; and
+                         // [rows][4]: maximum (base 2), sum of rounded weights, of exact ones
 };
 
 // What the join has to know of a request.
@@ -396,17 +398,17 @@ struct Joined {
 
 // The partials of an item, or of one row of it: where each worker's are.
 struct Pieces {
-  long long item, base;    // units before the item; its first row of partials, plus the row's place in it
+  long long item, base;    // units before the item; its first row of partials
   Div cost;
-  int begin, tiles, first, copies, stride, n;  // first worker, partials a worker, rows between them, partials in all
-  // of row (r, h), or of the first of the G rows of h's KV head, where they are together
+  int begin, tiles, first, copies, stride, row, n;  // first worker, partials a worker, rows of each, the row's place in them, partials in all
+  // of row (r, h), h the first of a KV head's where rows are not flat
   __device__ __forceinline__ void of(const PrefixArgs& a, const PrefixSplit& w, const Shares& sh, const Segment& sg, bool group, long long units,
                                      int r, int h) {
     n = 0;
     const Shape1 sp = shape_of(a, w, sg);
     if (sp.tiles == 0) return;
     const int j = r - sg.r0, flat = j * a.Hq + h, mt = w.flat ? flat >> 7 : (int)w.mt((uint32_t)j);
-    const int row = w.flat ? flat & 127 : (j - mt * w.MT) * w.G;
+    row = w.flat ? flat & 127 : (j - mt * w.MT) * w.G;
     const int head = w.flat ? 0 : h / w.G, pair = mt >> w.pairs;
     const bool both = w.pairs && 2 * pair + 1 < sp.nmt;
     begin = w.begin;
@@ -415,11 +417,11 @@ struct Pieces {
     stride = w.copies == 2 ? sp.rows >> 1 : sp.rows;
     copies = both ? 1 : w.copies;
     item = units + head * sp.head + (long long)pair * sp.item;
-    base = rows_before(a, w, group, sg.r0) + (long long)(head * sp.np + pair) * sp.rows + row + (both ? (mt & 1) * stride : 0);
+    base = rows_before(a, w, group, sg.r0) + (long long)(head * sp.np + pair) * sp.rows + (both ? (mt & 1) * stride : 0);
     first = sh.worker(item + begin);
     n = copies * (sh.worker(item + begin + (long long)(sp.tiles - 1) * (int)cost.d) - first + 1);
   }
-  // the row of partial i, -1: its worker has no tile (or too few for a second copy)
+  // the first row of partial i, -1: its worker has no tile (or too few for a second copy)
   __device__ __forceinline__ int at(const PrefixSplit& w, const Shares& sh, int i) const {
     const int wk = first + (copies == 2 ? i >> 1 : i), copy = copies == 2 ? i & 1 : 0;
     const int t0 = tile_at(sh.start(wk) - item, begin, cost, tiles), t1 = tile_at(sh.start(wk + 1) - item, begin, cost, tiles);
@@ -427,7 +429,7 @@ struct Pieces {
   }
 };
 
-// A CTA joins the rows of a request that are together in all partials: the G of a KV head, or (flat) one.  Its first threads find
+// A CTA joins rows of a request that are together in all partials: the G of a KV head, or (flat) up to four.  Its first threads find
 // the partials' places, kPrefixList at a time; then a thread takes 8 dims of a row from every `slices`-th partial, kPrefixAhead of
 // them on their way at a time, and the slices are summed in order.
 // What it costs is a chain of round trips, and instructions met for the first time: it starts while the attention still runs, and
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
   __shared__ int s_row[kPrefixList];
   __shared__ float s_acc[THREADS][8];
   __shared__ float4 s_ml[THREADS];
-  const int tid = threadIdx.x, r = blockIdx.x, rows = w.flat ? 1 : w.G, h0 = blockIdx.y * rows, units = rows * vecs;
+  const int tid = threadIdx.x, r = blockIdx.x, rows = w.together, h0 = blockIdx.y * rows, units = rows * vecs;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass != 0) {
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
       const Shares sh(total, w.workers);
       const bool group = tid == 1;
       const Segment sg = !group ? Segment{r, r, 1, q.p0, q.p1} : Segment{q.r0, q.r0, q.nr, 0, q.g >= 0 ? q.p0 : 0};
-      s_piece[tid].n = 0;
+      s_piece[tid].n = s_piece[tid].row = s_piece[tid].stride = 0;
       if (q.p1 > 0) s_piece[tid].of(a, w, sh, sg, group, !group ? q.units : q.g > 0 ? w.units[q.g] : 0, r, h0);
       if (!group) {
         s_share[0] = sh.per;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
   const int u0 = units * slices <= THREADS ? tid % units : tid, slice = units * slices <= THREADS ? tid / units : 0;
 #pragma unroll 1
   for (int ub = 0; ub < units; ub += THREADS) {  // more than one turn: more rows than threads, one slice
-    const int u = ub + u0, x = u / vecs, vec = u - x * vecs;
+    const int u = ub + u0, vec = u / rows, x = u - vec * rows;  // neighbouring threads: neighbouring rows
     const bool on = u < units && slice < slices;
     Joined sum;
 #pragma unroll 1
@@ -488,6 +490,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
       }
       __syncthreads();
       if (!on) continue;
+      const int row0 = s_piece[0].row + x, row1 = s_piece[1].row + x;
+      const int at0 = (vec * s_piece[0].stride + row0) * 8, at1 = (vec * s_piece[1].stride + row1) * 8;
 #pragma unroll 1
       for (int i0 = slice; i0 < m; i0 += kPrefixAhead * slices) {
         float4 l[kPrefixAhead], y[kPrefixAhead][2];
@@ -497,8 +501,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
           const int i = i0 + k * slices;
           row[k] = i < m ? s_row[i] : -1;
           if (row[k] >= 0) {
-            const float* p = w.part + (long long)(row[k] + x) * DV + 8 * vec;
-            l[k] = *(const float4*)(w.ml + 4ll * (row[k] + x));
+            const bool mine = c0 + i < own;
+            const float* p = w.part + (long long)row[k] * DV + (mine ? at0 : at1);
+            l[k] = *(const float4*)(w.ml + 4ll * (row[k] + (mine ? row0 : row1)));
             y[k][0] = *(const float4*)p;
             y[k][1] = *(const float4*)(p + 4);
           }
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const Pr
 
 template <int DV, int THREADS>
 cudaError_t launch_join_by(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t st) {
-  const int rows = w.flat ? 1 : w.G, units = rows * (DV / 8);
+  const int rows = w.together, units = rows * (DV / 8);
   int slices = 1;
   while (2 * slices * units <= THREADS) slices *= 2;
   return hs_launch_pdl(k_prefix_join<DV, THREADS>, dim3(a.R, a.Hq / rows), dim3(THREADS), 0, st, a, w, slices);
@@ -531,7 +536,7 @@ cudaError_t launch_join_by(const PrefixArgs& a, const PrefixSplit& w, cudaStream
 template <int DV>
 cudaError_t launch_join(const PrefixArgs& a, const PrefixSplit& w, cudaStream_t st) {
   // as many threads as the SMs hold at once: few CTAs have twice as many, for twice as many slices
-  const bool few = (int64_t)a.R * (a.Hq / (w.flat ? 1 : w.G)) <= kSmsHint;
+  const bool few = (int64_t)a.R * (a.Hq / w.together) <= kSmsHint;
   return few ? launch_join_by<DV, 512>(a, w, st) : launch_join_by<DV, 256>(a, w, st);
 }
 

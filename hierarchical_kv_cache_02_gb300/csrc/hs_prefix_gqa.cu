@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok && warp_ok) {
-          const long long to_row = P.row + (long long)(P.both ? g : off) * P.stride + row;
+          const long long first = P.row + (long long)(P.both ? g : off) * P.stride;  // of this copy
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
             float o[32];
@@ -428,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(to + 32u * x, o);
             if (row_ok) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) st_global_v8(c.w.part + to_row * D + 32 * x + 8 * y, o + 8 * y);
+              for (int y = 0; y < 4; ++y) st_global_v8(c.w.part + first * D + ((4 * x + y) * P.stride + row) * 8, o + 8 * y);
             }
           }
-          if (row_ok) *(float4*)(c.w.ml + 4 * to_row) = make_float4(m, l, le, 0.f);
+          if (row_ok) *(float4*)(c.w.ml + 4 * (first + row)) = make_float4(m, l, le, 0.f);
         }
         tiles += P.t1 - P.t0;
         tc_fence_before();
@@ -495,6 +495,7 @@ bool split_of(const hs_config* c, int sms, PrefixSplit* w) {
   w->copies = 2;
   w->most = 256;
   w->group_rows = 3 * c->num_q_heads;
+  w->together = G;
   w->workers = sms;
   return true;
 }

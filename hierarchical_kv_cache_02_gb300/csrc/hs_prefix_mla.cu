@@ -59,6 +59,21 @@ struct MlaControl {
 static_assert(kTile == 64, "the split's tiles");
 static_assert(kDyn + sizeof(MlaControl) <= 227 * 1024, "shared memory of a CTA");
 
+// A box into this CTA's memory whose bytes are counted by a barrier of either CTA of the pair (bar: a cluster's address)
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// Whether a tile comes in whole boxes, in both CTAs: then they are counted by the even one's barriers, and nothing has to be
+// passed on.
+__device__ __forceinline__ bool direct(const MlaArgs& c, const PPortion& P, int tile) {
+  const int e0 = P.base + tile * kTile;
+  return c.seg != 0 && e0 >= P.p0 && e0 + kTile <= P.p1;
+}
+
 // A producer lane's lookup of its entry of each tile, a tile ahead of the copies.
 struct Lookup {
   PPortion L;               // the next lookup's portion
@@ -155,6 +170,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (key_producer(warp) >= 0) {
       // ---------------- keys: 16 whole records of this CTA's 32 of a tile, looked up by lanes 0-15 ----------------
       const int first = 16 * key_producer(warp), crow = lane >> 3, cch = lane & 7;
+      const uint32_t kready = in_cta(smem_u32(ct.kready), 0);
       Lookup ahead;
       ahead.L = portion_take(plan, 0, false, &ok, abort);
       ahead.lt = ahead.L.t0;
@@ -174,7 +190,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint64_t* full = &ct.kfull[b];
         if (ok) ok = warp_wait_small(&ct.kempty[b], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
         if (ok) {
-          if (c.seg != 0 && e0 >= P.p0 && e0 + 16 <= P.p1) {
+          if (direct(c, P, kt)) {
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive_expect_tx(&ct.kready[b], 4u * kKGroup);  // of both CTAs
+              tma_load_pair(dst, &kmap, 0, 0, 0, row >> 3, kready + 8u * b);
+            }
+            __syncwarp();
+            mbar_arrive(full);
+          } else if (c.seg != 0 && e0 >= P.p0 && e0 + 16 <= P.p1) {
             if (lane == 0) mbar_arrive_expect_tx(full, 2u * kKGroup);
             else mbar_arrive(full);
             __syncwarp();
@@ -204,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (value_producer(warp) >= 0) {
       // ---------------- values: this CTA's 256 of 32 records of every tile, a lane's lookup each ----------------
       const int half = value_producer(warp), crow = lane >> 3, cch = lane & 7;
+      const uint32_t vready = in_cta(smem_u32(ct.vready), 0);
       Lookup ahead;
       ahead.L = portion_take(plan, 0, false, &ok, abort);
       ahead.lt = ahead.L.t0;
@@ -220,14 +244,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int b = nt & 1;
         const uint32_t dst = v_u + (uint32_t)(b * kVBuf + 4 * half * kVGroup);
         uint64_t* full = &ct.vfull[b];
-        if (ok) ok = warp_wait_small(&ct.vempty[b], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
         const uint32_t word = __ballot_sync(0xffffffffu, seen);
+        // ahead of the wait: the softmax begins with the scores, before the values' place is free.  (What is overwritten is
+        // of four tiles before, whose product was complete before the last tile's place was.)
+        if (ok && lane == 0) {
+          ct.valid[nt % kMaskRing][half] = word;
+          mbar_arrive(&ct.mask[nt % kMaskRing]);
+        }
+        if (ok) ok = warp_wait_small(&ct.vempty[b], (uint32_t)(((nt >> 1) & 1) ^ 1), abort);
         if (ok) {
-          if (lane == 0) {
-            ct.valid[nt % kMaskRing][half] = word;
-            mbar_arrive(&ct.mask[nt % kMaskRing]);
-          }
-          if (c.seg != 0 && e0 >= P.p0 && e0 + 32 <= P.p1) {
+          if (direct(c, P, kt)) {
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&ct.vready[b], 8u * kVGroup);  // of both CTAs
+            __syncwarp();
+            if ((lane & 15) == 0) tma_load_pair(dst + (uint32_t)((lane >> 3) * kVGroup), &vmap, 0, 0, 4 * rank, row >> 3, vready + 8u * b);
+            __syncwarp();
+            mbar_arrive(full);
+          } else if (c.seg != 0 && e0 >= P.p0 && e0 + 32 <= P.p1) {
             if (lane == 0) mbar_arrive_expect_tx(full, 4u * kVGroup);
             else mbar_arrive(full);
             __syncwarp();
@@ -365,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int tile = P.t0; tile < P.t1; ++tile, ++nt) {
           if (ok) ok = warp_wait_small(&full[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (ok && lane == 0) {
+          if (ok && lane == 0 && !direct(c, P, tile)) {
             if (rank == 0) mbar_arrive(&(keys ? ct.kready : ct.vready)[nt & 1]);
             else cluster_arrive(ready + 8u * (nt & 1));
           }
@@ -494,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l += ct.sums[half ^ 1][row].x;
         le += ct.sums[half ^ 1][row].y;
         if (ok && warp_ok) {
-          const long long to_row = P.row + 64 * rank + row;
+          const int mine = 64 * rank + row;
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
             float o[32];
@@ -502,10 +534,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld32(tb + lane_base + 32u * x, o);
             if (row_ok) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) st_global_v8(c.w.part + to_row * kValue + 256 * half + 32 * x + 8 * y, o + 8 * y);
+              for (int y = 0; y < 4; ++y) st_global_v8(c.w.part + P.row * kValue + ((32 * half + 4 * x + y) * P.stride + mine) * 8, o + 8 * y);
             }
           }
-          if (row_ok && half == 0) *(float4*)(c.w.ml + 4 * to_row) = make_float4(m, l, le, 0.f);
+          if (row_ok && half == 0) *(float4*)(c.w.ml + 4 * (P.row + mine)) = make_float4(m, l, le, 0.f);
         }
         tc_fence_before();
         __syncwarp();
@@ -534,6 +566,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (kpw >= 0 || vpw >= 0) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
+    if (c.seg != 0 && (kpw >= 0 || vpw >= 0))  // what the even CTA's barriers count may be of copies that were never made: time enough for those that were
+      while (global_ns() - t0 < 1000000ull) {
+      }
     if (kpw >= 0 || vpw >= 0) {
       uint64_t* full = kpw >= 0 ? ct.kfull : ct.vfull;
 #pragma unroll 1
@@ -563,10 +598,11 @@ void split_of(const hs_config* c, int num_sms, PrefixSplit* w) {
   w->pairs = 0;
   w->tile_shift = 6;
   w->cost = w->cost2 = div_by(1);
-  w->begin = 2;
+  w->begin = 3;
   w->copies = 1;
   w->most = kRows;
   w->group_rows = 2 * c->num_q_heads;
+  w->together = c->num_q_heads % 4 == 0 ? 4 : 1;  // items begin at multiples of 128 rows
   w->workers = num_sms / 2;
 }
 
