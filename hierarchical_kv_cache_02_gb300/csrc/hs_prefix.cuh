@@ -177,7 +177,7 @@ struct PrefixPlan {  // shared memory
   long long off, left;  // units into segment cur, units to take
   int cur, ok;          // ok: the groups' bounds are sound
   Segment seg;          // segment cur
-  long long scan[16];
+  long long scan[32];   // of each warp of the CTA
 };
 __device__ __forceinline__ void prefix_plan_init(PrefixPlan* s, int readers) {
   for (int i = 0; i < kPrefixRing; ++i) {
@@ -434,7 +434,7 @@ struct Pieces {
 // them on their way at a time, and the slices are summed in order.
 // What it costs is a chain of round trips, and instructions met for the first time: it starts while the attention still runs, and
 // goes through the first of them once on made-up numbers (16.9 us instead of XX for the call on 2 x 1000 positions).
-constexpr int kPrefixAhead = 4, kPrefixList = 64;
+constexpr int kPrefixAhead = 3, kPrefixList = 64;
 
 template <int DV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) k_prefix_join(const PrefixArgs a, const PrefixSplit w, int slices) {

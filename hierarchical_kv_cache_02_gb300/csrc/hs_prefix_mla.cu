@@ -50,10 +50,12 @@ struct MlaControl {
   PrefixPlan plan;
   __align__(8) uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t kready[2], vready[2], qready;  // even CTA: full in both
-  uint64_t qfull, s[kAhead], p[2], podd[2], pv[2], mask[kMaskRing], fin;  // p: even CTA; podd: odd CTA, its own warps'
+  uint64_t qfull, s[kAhead], p[2], podd[2], pv[2], pair[2], mask[kMaskRing], fin;  // p: even CTA; podd: odd CTA, its own warps'
   uint32_t valid[kMaskRing][2];
-  float most[2][2][64];
-  float2 sums[2][64];
+  union {
+    float most[2][2][64];
+    float2 sums[2][64];  // at a portion's end
+  };
   uint32_t tmem, abort;
 };
 static_assert(kTile == 64, "the split's tiles");
@@ -129,6 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ct.p[i], 5u);
       mbar_init(&ct.podd[i], 4u);
       mbar_init(&ct.pv[i], 1u);
+      mbar_init(&ct.pair[i], 2u);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], 2u);
     mbar_init(&ct.fin, 1u);
@@ -409,7 +412,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // are the whole warp's, and nothing else promises that it is whole there.)
       const int row = tid & 63, half = tid >> 6;
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-      auto pair_sync = [&]() { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + (warp & 1)) : "memory"); };
+      uint64_t* pair = &ct.pair[warp & 1];
+      uint32_t met = 0u;
+      auto pair_sync = [&]() {  // the two warps of 32 rows; like every wait it gives up
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair);
+        if (ok) ok = mbar_wait_small(pair, met, abort);
+        met ^= 1u;
+        ok = __all_sync(0xffffffffu, ok);
+      };
       auto load_q = [&](int i) {  // of portion i, by the first thread
         if (!portion_wait(plan, i, abort)) return;
         const PPortion& P = portion_at(plan, i);
@@ -525,6 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_sync();
         l += ct.sums[half ^ 1][row].x;
         le += ct.sums[half ^ 1][row].y;
+        pair_sync();  // the next tile's maxima take their place
         if (ok && warp_ok) {
           const int mine = 64 * rank + row;
 #pragma unroll 1
