@@ -220,6 +220,8 @@ def check_evict(cfg, lens, keep, first=0, recent=0, heads=False, page=16, seed=0
     (mla(1, 2, 8, 8), [70000], 20000, dict(first=100, recent=1000)),
     (mla(2, 2, 8, 8), [70000, 49153], 49152, {}),
     (gqa(2, 4, 4, 8), [60000, 50000], 30001, dict(heads=True, slack=11)),
+    (mla(1, 2, 8, 8), [9100], 4000, dict(page=2, recent=4)),
+    (gqa(2, 2, 1, 8), [6000, 5000], 4500, dict(page=1, first=4200)),
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict(cfg, lens, keep, more, in_place):

@@ -110,6 +110,7 @@ def test_prefixes(shape, R, groups, prefix, lens, page, lists):
     (gqa(40), [0, 40], 3000, 300, 64), (gqa(70), [0, 66], 5000, 200, 16), (gqa(33, 8, 2, 64), [2, 9, 30], 900, 1100, 32),
     (gqa(300, 4, 2), [0, 130, 290], 700, 90, 16), (gqa(700, 2, 1), [0], 0, 150, 16), (gqa(600, 2, 1, 64), [0, 600], 40, 60, 32),
     (gqa(3), [0, 2], 20000, 9000, 16), (gqa(5, 32, 8, 64), [0, 5], 9000, 3, 128), (gqa(130, 20, 4), [0, 60, 128], 333, 140, 48),
+    (gqa(1500, 2, 1), list(range(0, 1401, 2)), 90, 40, 16), (gqa(1100, 2, 1, 80), list(range(3, 1100, 3)), 50, 30, 16), (mla(1100, 4), list(range(1, 1001, 4)), 70, 40, 32),
     (mla(20), [0, 17], 3000, 300, 64), (mla(5), [0, 2], 9000, 4000, 16), (mla(90, 16), [0, 40, 90], 700, 100, 16), (mla(300, 4), [0, 200], 90, 40, 32),
 ])
 @pytest.mark.parametrize("weigh", [False, True])
@@ -177,6 +178,58 @@ def test_a_value_that_is_infinite_reaches_who_sees_it(cfg):
         keep = torch.ones((cfg.num_q_heads, dv), dtype=torch.bool, device=DEV)
         keep[:G, 3] = False
         assert ref.same(out[1][keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("cfg", [gqa(4), gqa(4, 8, 2, 64), mla(4), gqa(4, 4, 2, 80)], ids=["gqa", "gqa64", "mla", "any"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_score_that_is_no_number_reaches_who_sees_it(cfg, bad):
+    """In a key that a group shares, in one of a request's own, and in the only one that a request sees."""
+    groups, prefix, lens = [0, 2], [150], [170, 330, 260, 1]
+    kv, q, clean, _ = check(cfg, groups, prefix, lens)
+    flat, t = kv.pages.view(-1, cfg.record_elems), kv.table.cpu()
+    G = cfg.num_q_heads // cfg.num_kv_heads
+    for r, p, who in ((0, 20, (0, 1)), (1, 300, (1,)), (2, 70, (2,)), (3, 0, (3,))):
+        row = row_of(t, r, p, 16, 0)
+        keep = flat[row].clone()
+        flat[row, :G] = bad  # of the first KV head
+        out = kv.prefix_attn(q, torch.tensor(lens, device=DEV), groups=torch.tensor(groups, dtype=torch.int32, device=DEV),
+                             prefix=torch.tensor(prefix, device=DEV))
+        flat[row] = keep
+        for x in range(4):
+            if x not in who:
+                assert ref.same(out[x], clean[x])
+            elif bad != bad:
+                assert bool(torch.isnan(out[x, :G]).all())
+            assert ref.same(out[x, G:], clean[x, G:])
+    assert kv.errors() == 0
+
+
+@pytest.mark.parametrize("cfg", [gqa(3), gqa(3, 8, 2, 64), mla(3), gqa(3, 4, 2, 80)], ids=["gqa", "gqa64", "mla", "any"])
+def test_records_beyond_32_bits(cfg):
+    """The same records in a small cache and in pages at both ends of one of 9 GB give the same bits throughout."""
+    R, page, most = cfg.num_requests, 16, 208
+    near = make_cache(cfg, most, page, 3)
+    n = 9 * 10**9 // (2 * page * cfg.record_elems)
+    pages = torch.empty((n, page, cfg.record_elems), dtype=torch.bfloat16, device=DEV)
+    count = near.table.numel()
+    ids = torch.cat([torch.arange(n - count + 4, n), torch.arange(4)])[torch.randperm(count, generator=torch.Generator().manual_seed(1))].to(DEV)
+    pages[ids] = near.pages[near.table.flatten().long()]
+    far = PagedKV(cfg, pages, ids.to(torch.int32).view_as(near.table))
+    D, Dv, latent = cfg.head_dim_qk, cfg.head_dim_v, cfg.layout == 0
+    k = torch.randn((R, cfg.num_kv_heads, D), generator=gen(1), device=DEV).to(torch.bfloat16)
+    q = torch.randn((R, cfg.num_q_heads, D), generator=gen(2), device=DEV).to(torch.bfloat16)
+    lens, cu = [180, 200, 77], torch.arange(R + 1, dtype=torch.int32, device=DEV)
+    groups, prefix = torch.tensor([0, 2], dtype=torch.int32, device=DEV), torch.tensor([64], device=DEV)
+    got = []
+    for kv in (near, far):
+        lt, acc = torch.tensor(lens, device=DEV), torch.zeros((R, 1, most), device=DEV)
+        kv.append(k, None if latent else k[..., :Dv], cu, lt - 1, rope=RopeTable(16), k_weight=torch.ones(Dv if latent else D, device=DEV))
+        out = kv.prefix_attn(q, lt, groups=groups, prefix=prefix, weights=acc)
+        kv.evict(lt, acc, 100, first=64, recent=8, lens_out=lt)
+        got.append((out, lt, acc, kv.pages[kv.table.flatten().long()]))
+        assert kv.errors() == 0
+    for a, b in zip(*got):
+        assert ref.same(a, b)
 
 
 @pytest.mark.parametrize("cfg", [gqa(5), mla(5), gqa(5, 4, 2, 80)], ids=["gqa", "mla", "any"])
