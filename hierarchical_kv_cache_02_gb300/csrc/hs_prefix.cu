@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kAnyJoinThreads) k_prefix_any_join(const Prefi
 constexpr int kWeighThreads = 256, kWeighEach = 4;
 
 // CTAs share a request's list; a thread takes kWeighEach positions at a time and sums over the list's query heads.  A round trip
-// for the request's place, one for the statistics, one for the scores: 4.6 us XX
+// for the request's place, one for the statistics, one for the scores (one position at a time: 73.6 us instead of 70.5 for 16 requests of up
+// to 8192 positions, 32 query heads, attention included).
 __global__ void __launch_bounds__(kWeighThreads) k_prefix_weigh(const PrefixArgs a, const PrefixRequest* of) {
   __shared__ float2 s_stats[1024];
   hs_pdl_wait();
@@ -333,7 +334,9 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
     const int64_t lists = (int64_t)a.R * a.lists, most = (a.cap + kWeighThreads * kWeighEach - 1) / (kWeighThreads * kWeighEach);
     int64_t ctas = (8ll * sms + lists - 1) / lists;
     ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
-    if (hs_launch_pdl(k_prefix_weigh, dim3((unsigned)ctas, a.lists, a.R), dim3(kWeighThreads), 0, st, a, (const PrefixRequest*)head.of) != cudaSuccess) return HS_ERR_CUDA;
+    if (hs_launch_pdl(k_prefix_weigh, dim3((unsigned)ctas, a.lists, a.R), dim3(kWeighThreads), 0, st, a, (const PrefixRequest*)head.of) !=
+        cudaSuccess)
+      return HS_ERR_CUDA;
   }
   return HS_OK;
 }

