@@ -172,12 +172,14 @@ struct PPortion {
 constexpr int kPrefixRing = 8;
 
 struct PrefixPlan {  // shared memory
-  PPortion port[kPrefixRing];
+  union {
+    PPortion port[kPrefixRing];
+    long long scan[32];  // of each warp of the CTA, before the first portion
+  };
   uint64_t full[kPrefixRing], empty[kPrefixRing];
   long long off, left;  // units into segment cur, units to take
   int cur, ok;          // ok: the groups' bounds are sound
   Segment seg;          // segment cur
-  long long scan[32];   // of each warp of the CTA
 };
 __device__ __forceinline__ void prefix_plan_init(PrefixPlan* s, int readers) {
   for (int i = 0; i < kPrefixRing; ++i) {

@@ -134,18 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int crow = lane >> 3, cch = lane & 7;
       Ring<C::kRing> ring;
       int tiles = 0;               // loaded
-      int page = -1, at = 0;       // the next tile's entry: its page (-1: nothing seen there, -2: bad) and place in it
+      int page = 0, at = -1;       // the next tile's entry: its page, looked at only when it is used, and place in it (-1: nothing seen)
       PPortion L = portion_take(plan, 0, false, &ok, abort);  // the lookups' portion, a tile ahead of the copies
       int nl = 0, lt = L.t0;
       auto look = [&]() {
-        page = -1;
+        at = -1;
         if (L.t0 == L.t1) return;
         const int p = L.base + lt * kTile + 32 * pw + lane;
         if (p >= L.p0 && p < L.p1) {
           const unsigned pg = (unsigned)p / (unsigned)a.kv.page_tokens;
           at = p - (int)(pg * (unsigned)a.kv.page_tokens);
           page = a.kv.table != nullptr ? a.kv.table[(int64_t)L.lead * a.kv.max_pages + pg] : L.lead * a.kv.max_pages + (int)pg;
-          if (page < 0 || page >= a.kv.num_pages) page = -2;
         }
         if (++lt == L.t1) {
           L = portion_take(plan, ++nl, false, &ok, abort);
@@ -160,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x0 = P.head * a.kstride;
 #pragma unroll 1
         for (int t = P.t0; t < P.t1; ++t, ++tiles) {
-          if (page == -2) bad |= (uint32_t)HS_DEVERR_PAGE;
-          const bool seen = page >= 0;
+          const bool seen = at >= 0 && (unsigned)page < (unsigned)a.kv.num_pages;
+          if (at >= 0 && !seen) bad |= (uint32_t)HS_DEVERR_PAGE;
           const int row = seen ? page * a.kv.page_tokens + at : c.ctx_rows;
           const int e0 = P.base + t * kTile + 32 * pw;
           const bool boxed = c.seg != 0 && e0 >= P.p0 && e0 + 32 <= P.p1;

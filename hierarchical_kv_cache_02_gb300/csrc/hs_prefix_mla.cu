@@ -80,25 +80,28 @@ __device__ __forceinline__ bool direct(const MlaArgs& c, const PPortion& P, int 
   return c.seg != 0 && e0 >= P.p0 && e0 + kTile <= P.p1;
 }
 
-// A producer lane's lookup of its entry of each tile, a tile ahead of the copies.
+// A producer lane's lookup of its entry of each tile, a tile ahead of the copies.  What the table says is looked at only when it is
+// used: until then nothing waits for it.
 struct Lookup {
   PPortion L;               // the next lookup's portion
   int nl = 0, lt;           // its number, the tile
-  int page = -1, at = 0;    // what was found: the page (-1: nothing seen there, -2: bad) and the place in it
+  int page = 0, at = -1;    // what was found: the page, and the place in it (-1: nothing seen there)
   __device__ __forceinline__ void next(const PrefixArgs& a, PrefixPlan* plan, int mine, bool* ok, volatile uint32_t* abort) {
-    page = -1;
+    at = -1;
     if (L.t0 == L.t1) return;
     const int p = L.base + lt * kTile + mine;
     if (p >= L.p0 && p < L.p1) {
       const unsigned pg = (unsigned)p / (unsigned)a.kv.page_tokens;
       at = p - (int)(pg * (unsigned)a.kv.page_tokens);
       page = a.kv.table != nullptr ? a.kv.table[(int64_t)L.lead * a.kv.max_pages + pg] : L.lead * a.kv.max_pages + (int)pg;
-      if (page < 0 || page >= a.kv.num_pages) page = -2;
     }
     if (++lt == L.t1) {
       L = portion_take(plan, ++nl, false, ok, abort);
       lt = L.t0;
     }
+  }
+  __device__ __forceinline__ int row(const PrefixArgs& a) const {  // -1: nothing seen, -2: a bad page
+    return at < 0 ? -1 : (unsigned)page < (unsigned)a.kv.num_pages ? page * a.kv.page_tokens + at : -2;
   }
 };
 
@@ -187,9 +190,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int pi = 0; P.t0 < P.t1;) {
         if (kt == P.t0 && lane == 0) mbar_arrive(&plan->empty[pi % kPrefixRing]);  // the lookups took it before
-        if (ahead.page == -2) bad |= (uint32_t)HS_DEVERR_PAGE;
-        const bool seen = ahead.page >= 0;
-        const int row = seen ? ahead.page * a.kv.page_tokens + ahead.at : c.ctx_rows;
+        const int found = ahead.row(a);
+        if (found == -2) bad |= (uint32_t)HS_DEVERR_PAGE;
+        const bool seen = found >= 0;
+        const int row = seen ? found : c.ctx_rows;
         const int e0 = P.base + kt * kTile + 32 * rank + first;
         ahead.next(a, plan, 32 * rank + first + (lane & 15), &ok, abort);
         const int b = nt & 1;
@@ -244,8 +248,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int pi = 0; P.t0 < P.t1;) {
         if (kt == P.t0 && lane == 0) mbar_arrive(&plan->empty[pi % kPrefixRing]);  // the lookups took it before
-        const bool seen = ahead.page >= 0;
-        const int row = seen ? ahead.page * a.kv.page_tokens + ahead.at : c.ctx_rows;
+        const int found = ahead.row(a);
+        const bool seen = found >= 0;
+        const int row = seen ? found : c.ctx_rows;
         const int e0 = P.base + kt * kTile + 32 * half;
         ahead.next(a, plan, 32 * half + lane, &ok, abort);
         const int b = nt & 1;
