@@ -3,8 +3,8 @@
 // Of the n entries of a request, `keep` stay: its first f, its last c, and of the others the keep - f - c with the largest
 // weights, the earlier of equal ones.  They keep their order and move to the front.  Two kernels: the choice, a CTA for
 // each list of weights (a request's, or one of its KV heads'), and the moves, which device memory bounds: a record's
-// share that moves is read once and written once.  16 requests from 8192 to 4096 entries, 8 KV heads of 128 each by itself: 64 us, the
-// choice 17 and the moves 45, 6.4 TB/s; one request from 2049 to 2048: 9.9 us.
+// share that moves is read once and written once.  16 requests from 8192 to 4096 entries, 8 KV heads of 128 each by itself: 63 us, the
+// choice 16 and the moves 45, 6.4 TB/s; one request from 2049 to 2048: 9.7 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,8 +29,8 @@ struct EvictArgs {
 
 // ---- the choice ----------------------------------------------------------------------------------
 //
-// The m-th largest weight by radix selection, 11 bits at a time, over keys that order as the weights do, less the smallest of them
-// (weights crowd into a few exponents: without that most of a warp's counts meet in the same bins); then one ordered pass that
+// The m-th largest weight by radix selection, 11 bits at a time until a bin stays whole, over keys that order as the weights do, less
+// the smallest of them (weights crowd into a few exponents: without that most of a warp's counts meet in the same bins); then one ordered pass that
 // gives every entry that stays its place.  A warp takes a contiguous run of entries in that pass, so two barriers are enough; the
 // weights and the request's pages wait in shared memory where they fit.
 
@@ -60,7 +60,7 @@ __device__ __forceinline__ int row_of(const PagedRows& c, int shift, const int32
 
 __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, int cached, int pages) {
   extern __shared__ float s_w[];  // weights, then the page table
-  __shared__ int s_hist[kBins], s_warp[32], s_eq[32], s_bin, s_want, s_hole;
+  __shared__ int s_hist[kBins], s_warp[32], s_eq[32], s_bin, s_want, s_all, s_hole;
   __shared__ uint32_t s_min, s_max;
   hs_pdl_wait();
   // the only kernel that may start early is this call's own second one, which waits for this one
@@ -138,14 +138,17 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictArgs a, 
       if (above < want && want <= above + h1) {
         s_bin = 2 * tid + 1;
         s_want = want - above;
+        s_all = want == above + h1;
       } else if (above + h1 < want && want <= above + h1 + h0) {
         s_bin = 2 * tid;
         s_want = want - above - h1;
+        s_all = want == above + h1 + h0;
       }
       __syncthreads();
       limit += (uint32_t)s_bin << shift;
       want = s_want;
-      if (shift == 0) break;
+      if (s_all != 0) want = n;  // all of the bin stay: those above its first key, and those at it
+      if (shift == 0 || s_all != 0) break;
       span = (1u << shift) - 1u;
       shift = max(0, shift - 11);
     }
