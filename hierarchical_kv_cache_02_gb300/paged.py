@@ -213,8 +213,7 @@ class PagedKV:
             if qd != c.head_dim_qk and (qd != rd or qd == 0):
                 raise ValueError("the last dim of q must be head_dim_qk or rotary_dim")
             if q_out is None:
-                with torch.cuda.stream(stream):  # None: the current one
-                    q_out = torch.empty((N, c.num_q_heads, qd), dtype=torch.bfloat16, device=q.device)
+                q_out = self._empty((N, c.num_q_heads, qd), torch.bfloat16, stream)
             qp, qt, qh = _strided(q, N, c.num_q_heads, qd, "q", self.device)
             op, ot, oh = _strided(q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
         elif q_out is not None:

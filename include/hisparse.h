@@ -565,15 +565,15 @@ int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged_kv* kv, in
  * d_weights, for every position p of a request that it does not share
  *   weights[r][list][p] = decay * weights[r][list][p] + the softmax weights of p, summed over the list's query heads,
  * from 32-bit scores and sums; those of shared positions, and behind len, stay as they are.
- * Heads of 64 or 128 (keys and values alike, at most 128 query heads a KV head) run on the tensor cores; any other shape runs on
- * CUDA cores and reads a record once for every query head and request.
+ * Heads of 64 or 128 (keys and values alike, at most 128 query heads a KV head) and shared latents of 576 with 512 values run on
+ * the tensor cores; any other shape runs on CUDA cores and reads a record once for every query head and request.
  * len 0: zeros.  A len outside [0, the request's pages] or, unless 0, below its group's prefix sets HS_DEVERR_LOC and gives zeros
  * and no weights, one above capacity sets it and leaves the weights behind out; bounds of a group outside [0, num_requests] or
  * descending, and a prefix outside the pages, set it, and the group shares nothing.  Bad table entries set HS_DEVERR_PAGE:
  * such positions are not seen.  What a request does not see has no influence on it.  What it sees counts however small its weight:
- * an infinite or NaN value makes that dim of the output infinite or NaN, a NaN score the whole row.  Scores, softmax sums and
- * accumulators are 32-bit; on the tensor cores the weights enter the value product as bf16; the output is rounded once to
- * bf16.  The order of the sums depends on lengths and groups alone: equal calls give equal bits.  A bounded wait inside a kernel
+ * an infinite or NaN value makes that dim of the output infinite or NaN, a score that is NaN or +infinity the whole row NaN.  A row
+ * whose scores are all -infinity gives zeros where the values are finite.  Scores, softmax sums and accumulators are 32-bit; on the
+ * tensor cores the weights enter the value product as bf16; the output is rounded once to bf16.  The order of the sums depends on lengths and groups alone: equal calls give equal bits.  A bounded wait inside a kernel
  * that gives up (about a second without progress) sets HS_DEVERR_TIMEOUT and leaves d_out and d_weights undefined.  CAPTURABLE.
  * Errors: HS_ERR_ARG, HS_ERR_CONFIG, HS_ERR_SCRATCH (workspace too small), HS_ERR_CUDA.
  */

@@ -205,6 +205,27 @@ def test_a_score_that_is_no_number_reaches_who_sees_it(cfg, bad):
 
 
 @pytest.mark.parametrize("cfg", [gqa(3), gqa(3, 8, 2, 64), mla(3), gqa(3, 4, 2, 80)], ids=["gqa", "gqa64", "mla", "any"])
+def test_scores_of_both_infinities(cfg):
+    """Of one key: +infinity makes a row NaN, -infinity is a weight of zero; alone it gives zeros."""
+    lens, sick, D = [70, 300, 1], 40, cfg.head_dim_qk
+    q = torch.randn((3, cfg.num_q_heads, D), generator=gen(1), device=DEV).to(torch.bfloat16)
+    q[..., D - 1] = torch.where(torch.arange(cfg.num_q_heads, device=DEV) % 2 == 0, 1.0, -1.0).to(torch.bfloat16)
+    kv = make_cache(cfg, 300, 16, 5)
+    flat, t = kv.pages.view(-1, cfg.record_elems), kv.table.cpu()
+    width = cfg.record_elems // cfg.num_kv_heads
+    for r, p in ((0, sick), (2, 0)):  # of every KV head; of a latent a value behind those of V
+        flat[row_of(t, r, p, 16, 0), D - 1 :: width] = float("inf")
+    out = kv.prefix_attn(q, torch.tensor(lens, device=DEV), groups=torch.tensor([0, 2], dtype=torch.int32, device=DEV),
+                         prefix=torch.tensor([60], device=DEV))
+    rows = [flat[torch.tensor([row_of(t, 0 if p < 60 and r < 2 else r, p, 16, 0) for p in range(n) if r == 2 or p != sick], device=DEV)]
+            for r, n in enumerate(lens)]
+    want, bound, _ = ref.attention(cfg, rows[:2] + [rows[2][:0]], q, cfg.default_scale, [0] * 3)
+    assert bool(torch.isnan(out[:, ::2]).all())
+    assert bool(((out.double() - want).abs() <= bound)[:, 1::2].all()) and torch.count_nonzero(out[2, 1::2]) == 0
+    assert kv.errors() == 0
+
+
+@pytest.mark.parametrize("cfg", [gqa(3), gqa(3, 8, 2, 64), mla(3), gqa(3, 4, 2, 80)], ids=["gqa", "gqa64", "mla", "any"])
 def test_records_beyond_32_bits(cfg):
     """The same records in a small cache and in pages at both ends of one of 9 GB give the same bits throughout."""
     R, page, most = cfg.num_requests, 16, 208
