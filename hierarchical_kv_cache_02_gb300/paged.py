@@ -74,15 +74,16 @@ def tree_mask(parents):
     return (bits.view(R, T, words, 64) << torch.arange(64, device=parents.device)).sum(dim=3)
 
 
-def _strided(t, n, heads, dim, name, device, written=False):
+def _strided(torch, t, n, heads, dim, name, device, written=False):
     """Pointer, token stride and head stride of a bf16 [n][heads][dim] view ([n][dim] when heads is 1)."""
-    import torch
-
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == (n, heads, dim) and t.get_device() == device:
-        ts, hs, vs = t.stride()
-        p = t.data_ptr()
-        if vs == 1 and n > 1 and heads > 1 and not (ts | hs | p >> 1) & 7 and (not written or ts >= (heads - 1) * hs + dim):
-            return p, ts, hs  # what most calls pass; the rest is looked at one by one
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == (n, heads, dim) and t.get_device() == device:
+            ts, hs, vs = t.stride()
+            p = t.data_ptr()
+            if vs == 1 and n > 1 and heads > 1 and not (ts | hs | p >> 1) & 7 and (not written or ts >= (heads - 1) * hs + dim):
+                return p, ts, hs  # what most calls pass; the rest is looked at one by one
+    except AttributeError:
+        pass
 
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -106,18 +107,17 @@ def _strided(t, n, heads, dim, name, device, written=False):
     return t.data_ptr(), ts, hs
 
 
-def _weights(t, heads, dim, name, device):
+def _weights(torch, t, heads, dim, name, device):
     """Pointer, head stride and type of a norm's weights [dim] or [heads][dim], bf16 or float32."""
-    import torch
-
     if t is None:
         return 0, 0, 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(t, torch.Tensor) or (t.dtype is not torch.bfloat16 and t.dtype is not torch.float32):
         raise TypeError(f"{name} must be a torch.Tensor of bfloat16 or float32")
-    p = _fast_ptr(t, t.dtype, (dim,) if t.dim() == 1 else (heads, dim), name, device)
-    if p % 16:
+    several = t.dim() == 2
+    p = _fast_ptr(t, t.dtype, (heads, dim) if several else (dim,), name, device)
+    if p & 15:
         raise ValueError(f"{name} must be aligned to 16 bytes")
-    return p, dim if t.dim() == 2 else 0, _lib.WEIGHT_FP32 if t.dtype is torch.float32 else _lib.WEIGHT_BF16
+    return p, dim if several else 0, _lib.WEIGHT_FP32 if t.dtype is torch.float32 else _lib.WEIGHT_BF16
 
 
 class PagedKV:
@@ -186,12 +186,12 @@ class PagedKV:
         if not isinstance(k, torch.Tensor) or k.dim() < 2:
             raise ValueError("k must be a tensor [N][Hkv][Dqk]")
         N, mla = int(k.shape[0]), c.layout == _lib.LAYOUT_MLA
-        kp, kt, kh = _strided(k, N, c.num_kv_heads, c.head_dim_qk, "k", self.device)
+        kp, kt, kh = _strided(torch, k, N, c.num_kv_heads, c.head_dim_qk, "k", self.device)
         vp, vt, vh = 0, 0, 0
         if mla != (v is None):
             raise ValueError("a shared latent has no v" if mla else "v is missing")
         if v is not None:
-            vp, vt, vh = _strided(v, N, c.num_kv_heads, c.head_dim_v, "v", self.device)
+            vp, vt, vh = _strided(torch, v, N, c.num_kv_heads, c.head_dim_v, "v", self.device)
         cup = _fast_ptr(cu, torch.int32, self._r1, "cu", self.device)
         sp = _fast_ptr(start, torch.int64, self._r, "start", self.device)
         several = rope is not None and rope.axes > 1
@@ -214,13 +214,13 @@ class PagedKV:
                 raise ValueError("the last dim of q must be head_dim_qk or rotary_dim")
             if q_out is None:
                 q_out = self._empty((N, c.num_q_heads, qd), torch.bfloat16, stream)
-            qp, qt, qh = _strided(q, N, c.num_q_heads, qd, "q", self.device)
-            op, ot, oh = _strided(q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
+            qp, qt, qh = _strided(torch, q, N, c.num_q_heads, qd, "q", self.device)
+            op, ot, oh = _strided(torch, q_out, N, c.num_q_heads, qd, "q_out", self.device, written=True)
         elif q_out is not None:
             raise ValueError("q_out without q")
         normed = several or q_weight is not None or k_weight is not None
         if normed:
-            b = self._norm_args(c, mla, rope, q, qd, q_weight, k_weight, eps)
+            b = self._norm_args(torch, c, mla, rope, q, qd, q_weight, k_weight, eps)
         a = _lib.pack_append.pack(N, cup, sp, rp, kp, kt, kh, vp, vt, vh, turns, rd, int(rotary_offset), il, qp, qt, qh, op, ot, oh, qd)
         if normed:
             _check("hs_append_normed", self.lib.hs_append_normed(self._c_ref, self._kv_ref, a, b, _fast_stream(torch, stream, self.device)))
@@ -229,13 +229,13 @@ class PagedKV:
                                                                    _fast_stream(torch, stream, self.device)))
         return q_out
 
-    def _norm_args(self, c, mla, rope, q, qd, q_weight, k_weight, eps):
+    def _norm_args(self, torch, c, mla, rope, q, qd, q_weight, k_weight, eps):
         """What hs_append_normed takes beside the arguments of hs_append_rotated, packed."""
         dim = c.head_dim_v if mla else c.head_dim_qk
-        kw, ks, kt = _weights(k_weight, c.num_kv_heads, dim, "k_weight", self.device)
+        kw, ks, kt = _weights(torch, k_weight, c.num_kv_heads, dim, "k_weight", self.device)
         if q_weight is not None and (mla or q is None or qd != c.head_dim_qk):
             raise ValueError("q_weight needs whole query heads (and no shared latent)")
-        qw, qs, qt = _weights(q_weight, c.num_q_heads, dim, "q_weight", self.device)
+        qw, qs, qt = _weights(torch, q_weight, c.num_q_heads, dim, "q_weight", self.device)
         if (qw or kw) and not (0.0 < eps < float("inf")):
             raise ValueError("eps must be a positive number")
         axis = rope.axis if rope is not None else None
