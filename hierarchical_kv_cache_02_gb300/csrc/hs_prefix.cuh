@@ -42,7 +42,7 @@ __device__ __forceinline__ bool bounds_ok(const PrefixArgs& a, int g, int step) 
   for (; g < a.ngroups; g += step) ok = ok && a.groups[g] >= 0 && a.groups[g] <= a.groups[g + 1] && a.groups[g + 1] <= a.R;
   return ok;
 }
-// Requests and prefix of group g, with sound bounds.  A group of one shares nothing: its prefix counts as the request's own.
+// Requests and prefix of group g, with sound bounds.
 __device__ __forceinline__ Segment group_segment(const PrefixArgs& a, int g, uint32_t* bad) {
   const int64_t p = a.prefix[g];
   const bool out = p < 0 || p > positions_of(a);
@@ -51,7 +51,7 @@ __device__ __forceinline__ Segment group_segment(const PrefixArgs& a, int g, uin
   s.r0 = s.lead = a.groups[g];
   s.nr = a.groups[g + 1] - s.r0;
   s.p0 = 0;
-  s.p1 = s.nr >= 2 && !out ? (int)p : 0;
+  s.p1 = s.nr >= 1 && !out ? (int)p : 0;
   return s;
 }
 // The group of request r, -1: none.

@@ -310,7 +310,7 @@ class PagedKV:
         ascending and prefix int64 [G]: the requests [groups[g], groups[g + 1]) share the positions [0, prefix[g]), which
         are read through the table's row of the first of them; the other requests share none.  weights float32
         [R][lists][C], lists 1 or Hkv: takes weights * decay + the softmax weights, summed over the list's query heads, of the
-        positions that a request does not share (what evict goes by).  Returns out, bf16 [R][Hq][Dv] (it may not overlap q)."""
+        positions behind a request's prefix (what evict goes by).  Returns out, bf16 [R][Hq][Dv] (it may not overlap q)."""
         import torch
 
         c = self.cfg

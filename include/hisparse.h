@@ -560,9 +560,9 @@ int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged_kv* kv, in
 /*
  * Attention of one new token a request (a decode step) over a paged cache whose requests share prefixes:
  *   out[r][h] = sum_p softmax_p(scale * <q[r][h], K(p)>) V(p) over the positions p < len[r].
- * The positions below d_prefix[g] are read once for all requests of group g, through the page table's row of its first one (a
- * group of one request reads them as its own); later ones through each request's own row.  With
- * d_weights, for every position p of a request that it does not share
+ * The positions below d_prefix[g] are read once for all requests of group g, through the page table's row of its first one; later
+ * ones through each request's own row.  With d_weights, for every position p of a request behind its group's prefix (of a group of
+ * one request, too)
  *   weights[r][list][p] = decay * weights[r][list][p] + the softmax weights of p, summed over the list's query heads,
  * from 32-bit scores and sums; those of shared positions, and behind len, stay as they are.
  * Heads of 64 or 128 (keys and values alike, at most 128 query heads a KV head) and shared latents of 576 with 512 values run on

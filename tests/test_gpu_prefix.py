@@ -16,8 +16,7 @@ def shared_of(R, groups, prefix):
     lead, pre = list(range(R)), [0] * R
     for g, p in enumerate(prefix):
         for r in range(groups[g], groups[g + 1]):
-            if groups[g + 1] - groups[g] > 1:
-                lead[r], pre[r] = groups[g], p
+            lead[r], pre[r] = groups[g], p
     return lead, pre
 
 
