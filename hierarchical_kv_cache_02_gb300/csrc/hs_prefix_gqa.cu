@@ -13,7 +13,7 @@
 // Device memory bounds it while row tiles are few: 64 KB a tile and SM at 6.8 TB/s are 1.46 us, the products of one row tile
 // 0.56 us at the tensor cores' rate.  With two row tiles it is each group's chain: softmax 1770 cycles, of which the powers are 1030 (8
 // a number), then 1690 until the next scores are there (P's arrival to the value product's issue 250, the products 530 each).
-// 16 requests over 32768 shared positions (32 / 8 heads of 128): 50 us, 4.2 TB/s; 64 over 131072: 151 us, 4.5 TB/s and 0.9 PFLOP/s.
+// 16 requests over 32768 shared positions (32 / 8 heads of 128): 50 us, 4.2 TB/s; 64 over 131072: 149 us, 4.6 TB/s and 0.9 PFLOP/s.
 // What was slower: two threads a row (54 and 177 us: 16 warps, the halves' maxima exchanged); a part of the powers as polynomials; the
 // weights handed over in two parts (no gain); scores 64 entries at a time (200).
 #include <cuda_runtime.h>
@@ -494,7 +494,7 @@ bool split_of(const hs_config* c, int sms, PrefixSplit* w) {
   w->tile_shift = 7;
   w->cost = div_by(4);
   w->cost2 = div_by(6);
-  w->begin = 3;
+  w->begin = 5;  // measured: 151.7 us for 64 requests over 131072 with 3, 148.3 with 5, 152.3 with 8
   w->copies = 2;
   w->most = 256;
   w->group_rows = 3 * c->num_q_heads;
