@@ -56,9 +56,11 @@ struct MlaControl {
   uint64_t kready[2], vready[2], qready;  // even CTA: full in both
   uint64_t qfull, s[kAhead], p[2], podd[2], pv[2], pair[2], mask[kMaskRing], fin;  // p: even CTA; podd: odd CTA, its own warps'
   uint32_t valid[kMaskRing][2];
+  // Of the same shape, [..][half][row], so that a row's bytes are the same in both: pair_sync joins the two warps of 32 rows alone,
+  // and the other two may be a portion's end ahead.
   union {
-    float most[2][2][64];
-    float2 sums[2][64];  // at a portion's end
+    float most[2][2][64];  // of a tile, by turns
+    float sums[2][2][64];  // at a portion's end: of the rounded weights, of the exact ones
   };
   uint32_t tmem, abort;
 };
@@ -541,10 +543,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) ok = mbar_wait_small(&ct.pv[(nt - 1) & 1], (uint32_t)(((nt - 1) >> 1) & 1), abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        ct.sums[half][row] = make_float2(l, le);
+        ct.sums[0][half][row] = l;
+        ct.sums[1][half][row] = le;
         pair_sync();
-        l += ct.sums[half ^ 1][row].x;
-        le += ct.sums[half ^ 1][row].y;
+        l += ct.sums[0][half ^ 1][row];
+        le += ct.sums[1][half ^ 1][row];
         pair_sync();  // the next tile's maxima take their place
         if (ok && warp_ok) {
           const int mine = 64 * rank + row;
