@@ -28,7 +28,7 @@ EXPORTS = ("hs_record_bytes", "hs_pool_create", "hs_pool_destroy", "hs_pool_rese
            "hs_resolve_range", "hs_sparse_attn_range", "hs_reserve", "hs_release", "hs_host_usage",
            "hs_device_usage", "hs_debug_stall_next", "hs_rope_turns", "hs_append_rotated",
            "hs_tree_attn_workspace", "hs_tree_attn", "hs_pool_tree_attn", "hs_keep_path",
-           "hs_append_normed", "hs_evict_workspace", "hs_evict", "hs_prefix_attn_workspace", "hs_prefix_attn")
+           "hs_append_normed", "hs_evict_workspace", "hs_evict", "hs_prefix_attn_workspace", "hs_prefix_attn", "hs_debug_stall_prefix")
 
 
 class hs_config(ctypes.Structure):
@@ -238,6 +238,7 @@ def load(build_if_missing: bool = False):
             "hs_evict": (I, [P, P, P, P]),
             "hs_prefix_attn_workspace": (I64, [P, P, I, I]),
             "hs_prefix_attn": (I, [P, P, P, P]),
+            "hs_debug_stall_prefix": (I, []),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

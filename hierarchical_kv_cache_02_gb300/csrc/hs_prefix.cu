@@ -239,6 +239,8 @@ bool layout_of(const hs_config* c, const hs_paged_kv* kv, int groups, bool weigh
   return true;
 }
 
+thread_local int stall_next;  // test hook, of the calling thread
+
 int check_prefix(const hs_config* c, const hs_prefix_args* g) {
   if (g == nullptr || g->d_q == nullptr || g->d_len == nullptr || g->d_out == nullptr) return HS_ERR_ARG;
   if (!hs_aligned(g->d_q, 16) || !hs_aligned(g->d_len, 8) || !hs_aligned(g->d_out, 16) || !hs_aligned(g->d_groups, 4) ||
@@ -268,6 +270,11 @@ extern "C" int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged
   if (sms < 1) return HS_ERR_CUDA;
   Layout l;
   return layout_of(cfg, kv, groups, weights != 0, sms, &l) ? l.end : (int64_t)HS_ERR_ARG;
+}
+
+extern "C" int hs_debug_stall_prefix(void) {
+  stall_next = 1;
+  return HS_OK;
 }
 
 extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_prefix_args* args, void* stream) {
@@ -316,6 +323,8 @@ extern "C" int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const
   }
   cudaStream_t st = (cudaStream_t)stream;
   if (l.tc.rows > 0) {
+    a.stall = stall_next;  // consumed by this launch
+    stall_next = 0;
     rc = (cfg->layout == HS_LAYOUT_GQA ? hs_prefix_gqa_launch : hs_prefix_mla_launch)(cfg, &a, ws, ws + l.partials, sms, st);
     if (rc != HS_OK) return rc;
   } else {

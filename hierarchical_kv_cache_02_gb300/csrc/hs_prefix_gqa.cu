@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t word = __ballot_sync(0xffffffffu, seen);
           if (ok && lane == 0) {
             ct.valid[tiles % kMaskRing][pw] = word;
-            mbar_arrive(&ct.mask[tiles % kMaskRing]);
+            if (!(a.stall != 0 && tiles == 0 && pw == 1)) mbar_arrive(&ct.mask[tiles % kMaskRing]);
           }
         }
         P = portion_take(plan, pi + 1, false, &ok, abort);

@@ -353,6 +353,11 @@ class PagedKV:
         _check("hs_prefix_attn", self.lib.hs_prefix_attn(self._c_ref, self._kv_ref, a, _fast_stream(torch, stream, self.device)))
         return out
 
+    def debug_stall_next(self):
+        """Test hook: this thread's next prefix_attn on the tensor cores leaves one barrier arrival out, so its bounded waits give up
+        and DEVERR_TIMEOUT is reported; its outputs are then undefined."""
+        _check("hs_debug_stall_prefix", self.lib.hs_debug_stall_prefix())
+
     def keep_path(self, lens, path, count, stream=None):
         """The record of node path[r][i] moves to position lens[r] + i for i < count[r].  lens int64 [R];
         path int32 [R][P], ascending nodes; count int32 [R]."""

@@ -579,6 +579,14 @@ int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged_kv* kv, in
  */
 int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_prefix_args* args, void* stream);
 
+/*
+ * Test hook for the bounded waits of hs_prefix_attn (not for production use), as hs_debug_stall_next is for a pool's: the calling
+ * thread's next hs_prefix_attn on the tensor cores leaves out an arrival of every CTA's first tile, so that waits run
+ * to their limit of about a second.  The call sets HS_DEVERR_TIMEOUT, its d_out and d_weights are undefined; the cache stays as it is
+ * and the context usable.  Host-side only (takes effect at launch, also when the launch is captured).
+ */
+int hs_debug_stall_prefix(void);
+
 typedef struct {
   const int64_t* d_len;     /* [num_requests] entries of each request */
   const float* d_weights;   /* [num_requests][lists][capacity] accumulated weights of the entries */
