@@ -390,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok) ok = warp_wait_small(&ct.podd[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           tc_fence_after();
           tc_fence_before();
-          if (ok && lane == 0) cluster_arrive(p_bar + 8u * (nt & 1));
+          if (ok && lane == 0 && !(a.stall != 0 && nt == 0)) cluster_arrive(p_bar + 8u * (nt & 1));
         }
       }
     } else if (warp == kPassKeys || warp == kPassValues) {
@@ -590,15 +590,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (kpw >= 0 || vpw >= 0) asm volatile("cp.async.wait_all;" ::: "memory");
   if (*abort != 0u && lane == 0) {
     const uint64_t t0 = global_ns();
-    if (c.seg != 0 && (kpw >= 0 || vpw >= 0))  // what the even CTA's barriers count may be of copies that were never made: time enough for those that were
-      while (global_ns() - t0 < 1000000ull) {
-      }
     if (kpw >= 0 || vpw >= 0) {
       uint64_t* full = kpw >= 0 ? ct.kfull : ct.vfull;
 #pragma unroll 1
       for (int i = max(0, sent - 2); i < sent; ++i)
         while (!mbar_try_wait(&full[i & 1], (uint32_t)((i >> 1) & 1)) && global_ns() - t0 < 1000000000ull) {
         }
+      // The boxes that the even CTA's barriers count, into both CTAs: the odd one waits for it below.  A tile's place is free when
+      // both CTAs' copies two tiles before were used, so the odd one's may be of two tiles that this one made none for; then their
+      // barriers never complete, and the limit is the time that they have.
+      uint64_t* ready = kpw >= 0 ? ct.kready : ct.vready;
+      if (rank == 0 && c.seg != 0) {
+#pragma unroll 1
+        for (int i = max(0, sent - 2); i < sent + 2; ++i)
+          while (!mbar_try_wait(&ready[i & 1], (uint32_t)((i >> 1) & 1)) && global_ns() - t0 < 1000000000ull) {
+          }
+      }
     } else if (warp == 0 && nq > 0) {
       while (!mbar_try_wait(&ct.qfull, (uint32_t)((nq - 1) & 1)) && global_ns() - t0 < 1000000000ull) {
       }

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 import batch_ref as ref
 from hierarchical_kv_cache_02_gb300 import DEVERR_TIMEOUT
-from test_gpu_batch import DEV, gqa
+from test_gpu_batch import DEV, gqa, mla
 from test_gpu_prefix import check
 
 CASES = [
@@ -17,6 +17,9 @@ CASES = [
     pytest.param(lambda R: gqa(R), 7, id="gqa-records"),
     pytest.param(lambda R: gqa(R, 28, 4, 64), 32, id="gqa64-boxes"),
     pytest.param(lambda R: gqa(R, 128, 1), 16, id="gqa-two-row-tiles"),
+    pytest.param(lambda R: mla(R), 16, id="latent-boxes"),
+    pytest.param(lambda R: mla(R), 7, id="latent-records"),
+    pytest.param(lambda R: mla(R, 24), 64, id="latent-few-rows"),
 ]
 
 
