@@ -22,7 +22,7 @@ struct PrefixArgs {
   int kstride, voff;      // values: KV head g's key at g * kstride, its value voff further on
   float qscale;           // scale * log2(e)
   float decay;
-  int stall;              // test hook (hs_debug_stall_prefix): one arrival of a CTA's first tile is left out
+  int stall;              // test hook (hs_debug_stall_prefix): arrivals that a barrier of a worker's first tile waits for in vain
 };
 
 // ---- segments ------------------------------------------------------------------------------------

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ct.p[g], 128u);
       mbar_init(&ct.pv[g], 1u);
     }
-    for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], kProducers);
+    for (int i = 0; i < kMaskRing; ++i) mbar_init(&ct.mask[i], kProducers + (i == 0 ? a.stall : 0));
     mbar_init(&ct.fin, 1u);
     prefix_plan_init(&ct.plan, kProducers + 1 + 8);
     ct.abort = 0u;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t word = __ballot_sync(0xffffffffu, seen);
           if (ok && lane == 0) {
             ct.valid[tiles % kMaskRing][pw] = word;
-            if (!(a.stall != 0 && tiles == 0 && pw == 1)) mbar_arrive(&ct.mask[tiles % kMaskRing]);
+            mbar_arrive(&ct.mask[tiles % kMaskRing]);
           }
         }
         P = portion_take(plan, pi + 1, false, &ok, abort);

@@ -137,7 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ct.qready, 2u);
     mbar_init(&ct.qfull, 1u);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ct.p[i], 5u);
+      mbar_init(&ct.p[i], 5u + (i == 0 ? (uint32_t)a.stall : 0u));
       mbar_init(&ct.podd[i], 4u);
       mbar_init(&ct.pv[i], 1u);
       mbar_init(&ct.pair[i], 2u);
@@ -390,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok) ok = warp_wait_small(&ct.podd[nt & 1], (uint32_t)((nt >> 1) & 1), abort);
           tc_fence_after();
           tc_fence_before();
-          if (ok && lane == 0 && !(a.stall != 0 && nt == 0)) cluster_arrive(p_bar + 8u * (nt & 1));
+          if (ok && lane == 0) cluster_arrive(p_bar + 8u * (nt & 1));
         }
       }
     } else if (warp == kPassKeys || warp == kPassValues) {

@@ -354,8 +354,8 @@ class PagedKV:
         return out
 
     def debug_stall_next(self):
-        """Test hook: this thread's next prefix_attn on the tensor cores leaves one barrier arrival out, so its bounded waits give up
-        and DEVERR_TIMEOUT is reported; its outputs are then undefined."""
+        """Test hook: this thread's next prefix_attn on the tensor cores has a barrier wait for an arrival that nothing makes, so its
+        bounded waits give up and DEVERR_TIMEOUT is reported; its outputs are then undefined."""
         _check("hs_debug_stall_prefix", self.lib.hs_debug_stall_prefix())
 
     def keep_path(self, lens, path, count, stream=None):

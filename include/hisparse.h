@@ -581,9 +581,9 @@ int hs_prefix_attn(const hs_config* cfg, const hs_paged_kv* kv, const hs_prefix_
 
 /*
  * Test hook for the bounded waits of hs_prefix_attn (not for production use), as hs_debug_stall_next is for a pool's: the calling
- * thread's next hs_prefix_attn on the tensor cores leaves out an arrival of every CTA's first tile, so that waits run
- * to their limit of about a second.  The call sets HS_DEVERR_TIMEOUT, its d_out and d_weights are undefined; the cache stays as it is
- * and the context usable.  Host-side only (takes effect at launch, also when the launch is captured).
+ * thread's next hs_prefix_attn on the tensor cores has a barrier of every worker's first tile wait for an arrival that nothing
+ * makes, so that waits run to their limit of about a second.  The call sets HS_DEVERR_TIMEOUT, its d_out and d_weights are
+ * undefined; the cache stays as it is and the context usable.  Host-side only (takes effect at launch, also when the launch is captured).
  */
 int hs_debug_stall_prefix(void);
 

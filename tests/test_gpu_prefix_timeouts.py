@@ -1,5 +1,6 @@
-"""The bounded waits of the attention over shared prefixes, exercised without any GPU fault: a test hook leaves one barrier
-arrival out, the waits for it run to their limit of about a second, and the call reports it and leaves everything usable."""
+"""The bounded waits of the attention over shared prefixes, exercised without any GPU fault: a test hook has a
+barrier wait for an arrival that nothing makes, the waits run to their limit of about a second, and the call reports it and
+leaves everything usable."""
 import time
 
 import pytest
