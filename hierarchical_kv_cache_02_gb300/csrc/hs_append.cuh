@@ -1,5 +1,4 @@
-// What the appends to a paged cache have in common: vectors of bf16 and their rotation, units of a head, the request of
-// a token, the checks of their arguments.
+// What the appends to a paged cache have in common: vectors of bf16, units of a head, the checks of their arguments.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,46 +24,12 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *(const uint32_t*)&v;
 }
 
-// four neighbouring pairs (cs: 16-byte aligned, as a multiple of four pairs)
-__device__ __forceinline__ void turn(Vec8& v, const float2* cs) {
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const float4 c = *(const float4*)(cs + i);
-    const float p0 = lo(v.w[i]), r0 = hi(v.w[i]), p1 = lo(v.w[i + 1]), r1 = hi(v.w[i + 1]);
-    v.w[i] = pack(p0 * c.x - r0 * c.y, r0 * c.x + p0 * c.y);
-    v.w[i + 1] = pack(p1 * c.z - r1 * c.w, r1 * c.z + p1 * c.w);
-  }
-}
-
 // Units of one head, two vectors of 8 values each.  Half form: unit u < half / 8 turns values 8u.. with their
 // partners half further on; the rest of the head, before and behind the rotary values, is copied, two vectors a
 // unit.  Interleaved: unit u holds values 16u.., each vector turned when it is a rotary one.
 inline int head_units(int dim, int half, int interleaved) {
   return interleaved ? (dim + 15) / 16 : half / 8 + (dim - 2 * half + 15) / 16;
 }
-
-// One unit: where it reads and writes, and how it turns.
-struct Unit {
-  const uint16_t* src;  // null: nothing to do
-  uint16_t* dst;
-  int second;           // values to the second vector, 0: none
-  int cs, cs2;          // first pair of each vector in the table of sines and cosines, -1: copied
-};
-
-// The last request whose first token is not behind t, by a whole warp: 32 places of the rest are looked at at a time.
-__device__ __forceinline__ int request_of_token(const int32_t* cu, int R, int t, int lane) {
-  int x = 0, n = R;
-  while (n > 1) {
-    const int step = (n + 31) >> 5, at = lane * step;
-    const bool before = at < n && cu[x + at] <= t;
-    const int c = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0);
-    x += c * step;
-    n = min(step, n - c * step);
-  }
-  return x;
-}
-
-constexpr int kMinCtas = 456;
 
 inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 

@@ -29,6 +29,7 @@ namespace {
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 4;   // tokens of a CTA at most
 constexpr int kAppFlight = 2;   // units a thread loads before it stores
+constexpr int kMinCtas = 456;
 
 struct AppendArgs {
   PagedRows kv;
@@ -44,6 +45,38 @@ struct AppendArgs {
   int kn, vn, per_cta, tokens;                     // units of a token's keys and values, units and tokens of a CTA
   Div all, kh, vh, qh, angles;                     // units of a token, of a head of each kind; pairs
 };
+
+// four neighbouring pairs (cs: 16-byte aligned, as a multiple of four pairs)
+__device__ __forceinline__ void turn(Vec8& v, const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float4 c = *(const float4*)(cs + i);
+    const float p0 = lo(v.w[i]), r0 = hi(v.w[i]), p1 = lo(v.w[i + 1]), r1 = hi(v.w[i + 1]);
+    v.w[i] = pack(p0 * c.x - r0 * c.y, r0 * c.x + p0 * c.y);
+    v.w[i + 1] = pack(p1 * c.z - r1 * c.w, r1 * c.z + p1 * c.w);
+  }
+}
+
+// One unit: where it reads and writes, and how it turns.
+struct Unit {
+  const uint16_t* src;  // null: nothing to do
+  uint16_t* dst;
+  int second;           // values to the second vector, 0: none
+  int cs, cs2;          // first pair of each vector in the table of sines and cosines, -1: copied
+};
+
+// The last request whose first token is not behind t, by a whole warp: 32 places of the rest are looked at at a time.
+__device__ __forceinline__ int request_of_token(const int32_t* cu, int R, int t, int lane) {
+  int x = 0, n = R;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const bool before = at < n && cu[x + at] <= t;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0);
+    x += c * step;
+    n = min(step, n - c * step);
+  }
+  return x;
+}
 
 __global__ void __launch_bounds__(kAppThreads, 6) k_append_rotated(AppendArgs a) {
   extern __shared__ __align__(16) float2 s_cs[];   // [tokens][half] cosine and sine of each pair
