@@ -1,4 +1,4 @@
-// Attention of one new token a request over a paged cache, the prefixes that requests share read once for all of them, and the
+// Attention of one new token a request over a paged cache, the prefixes that requests share read for many of them at a time, and the
 // weights it gives to what they do not share.
 //
 // For request r, query head h, over the positions p below its length:

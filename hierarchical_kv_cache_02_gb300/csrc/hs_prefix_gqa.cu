@@ -1,4 +1,4 @@
-// Attention of one new token a request over GQA records, shared prefixes read once, on the 5th-generation tensor cores.
+// Attention of one new token a request over GQA records, shared prefixes read once for 2 MT requests, on the 5th-generation tensor cores.
 //
 // Rows of an accumulator are (request, query head of one KV head) pairs: MT = 128 / G requests of G heads for a prefix, one
 // request's G heads for what it has for itself.  Per tile of 128 entries S = Q K^T (128 x 128 x D) and O += P V (128 x D x 128),
@@ -494,7 +494,7 @@ bool split_of(const hs_config* c, int sms, PrefixSplit* w) {
   w->tile_shift = 7;
   w->cost = div_by(4);
   w->cost2 = div_by(6);
-  w->begin = 5;  // measured: 151.7 us for 64 requests over 131072 with 3, 148.3 with 5, 152.3 with 8
+  w->begin = 5;  // measured on heads of 128 alone: 151.7 us for 64 requests over 131072 with 3, 148.3 with 5, 152.3 with 8
   w->copies = 2;
   w->most = 256;
   w->group_rows = 3 * c->num_q_heads;

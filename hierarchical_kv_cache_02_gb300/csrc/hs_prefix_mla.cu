@@ -1,5 +1,5 @@
 // Attention of one new token a request over shared-latent records (576 values, the first 512 of them V), shared prefixes read
-// once, on the 5th-generation tensor cores.
+// once for 128 rows, on the 5th-generation tensor cores.
 //
 // The rows of a segment are its requests' query heads one after the other; an item is 128 of them, whatever the head count, and
 // the work of two CTAs, a cluster on neighbouring SMs: each holds 64 rows' queries (72 KB), and the products are the pair's
@@ -14,7 +14,7 @@
 // The products bound it from below: 18 MFLOP a tile and pair are 0.72 us at the tensor cores' rate.  A tile takes 1.28 us, the chain
 // of its softmax: scores read and their maximum 530 cycles, the two threads' exchange 280, powers 390, the weights' place and the
 // rescaling's votes 460, weights stored and handed over 500.  (With half the products, or half the values loaded, it takes 2 and 0 us
-// less.)  8 requests of 64 heads over 32768 shared positions: 58 us, 0.64 PFLOP/s.
+// less.)  8 requests of 64 heads over 32768 shared positions: 59 us, 0.62 PFLOP/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -304,13 +304,14 @@ class PagedKV:
         return out
 
     def prefix_attn(self, q, lens, groups=None, prefix=None, weights=None, decay: float = 1.0, out=None, scale=None, stream=None):
-        """Attention of one new token a request over the positions [0, lens[r]), those that requests share read once.
+        """Attention of one new token a request over the positions [0, lens[r]), those that requests share read for many at a time.
 
         q bf16 [R][Hq][Dqk]; lens int64 [R], the new tokens' own positions among them.  groups int32 [G + 1]
         ascending and prefix int64 [G]: the requests [groups[g], groups[g + 1]) share the positions [0, prefix[g]), which
         are read through the table's row of the first of them; the other requests share none.  weights float32
         [R][lists][C], lists 1 or Hkv: takes weights * decay + the softmax weights, summed over the list's query heads, of the
-        positions behind a request's prefix (what evict goes by).  Returns out, bf16 [R][Hq][Dv] (it may not overlap q)."""
+        positions behind a request's prefix (what evict goes by); the call's workspace then holds 4 bytes for each request, query
+        head and position of the table.  Returns out, bf16 [R][Hq][Dv] (it may not overlap q)."""
         import torch
 
         c = self.cfg
@@ -374,7 +375,7 @@ class PagedKV:
 
     def errors(self, reset: bool = False) -> int:
         """The DEVERR_* bits that the calls so far recorded (synchronises the device).  DEVERR_TIMEOUT: a tree
-        attention gave up waiting and its output is undefined; the cache is as it was."""
+        or prefix attention gave up waiting, its output and the weights it sums up are undefined; the cache is as it was."""
         import torch
 
         torch.cuda.synchronize(self.device)

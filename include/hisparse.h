@@ -554,14 +554,15 @@ typedef struct {
 } hs_prefix_args;
 
 /* Bytes of workspace a call needs, whatever the lengths; with weights (not 0) 4 bytes for each request, query head and position
- * of its pages among them.  Of kv only page_tokens, max_pages and cuda_device matter.  Negative: an hs_status. */
+ * of its pages among them, shared ones too (64 requests of 32 heads and 131072 positions: 1.07 GB).  Of kv only page_tokens, max_pages and cuda_device matter.  Negative: an hs_status. */
 int64_t hs_prefix_attn_workspace(const hs_config* cfg, const hs_paged_kv* kv, int groups, int weights);
 
 /*
  * Attention of one new token a request (a decode step) over a paged cache whose requests share prefixes:
  *   out[r][h] = sum_p softmax_p(scale * <q[r][h], K(p)>) V(p) over the positions p < len[r].
- * The positions below d_prefix[g] are read once for all requests of group g, through the page table's row of its first one; later
- * ones through each request's own row.  With d_weights, for every position p of a request behind its group's prefix (of a group of
+ * The positions below d_prefix[g] are read for many requests of group g at a time, through the page table's row of its first one: once
+ * for every two tiles of floor(128 / query heads a KV head) requests, over shared latents once for every 128 (request, query head)
+ * rows.  Later ones are read through each request's own row.  With d_weights, for every position p of a request behind its group's prefix (of a group of
  * one request, too)
  *   weights[r][list][p] = decay * weights[r][list][p] + the softmax weights of p, summed over the list's query heads,
  * from 32-bit scores and sums; those of shared positions, and behind len, stay as they are.
